@@ -2,6 +2,10 @@
 DeltaNet, KDA and Gated DeltaNet-2 forward, the backward, Residual Linear
 Attention / Residual DeltaNet, plus the single-token recurrent decode step.
 
+Around them: the RMS norm with the residual's addition (also in 8 bits), the
+short causal convolution with a carried state and the selective state space scan, for
+sequences, single tokens and gradients (``mixer``).
+
 The computation lives in CUDA kernels behind the C ABI of include/ldn.h
 (lib/libldn.so, built by ``build.build()``); this package holds the ctypes
 binding (``_native``) and the seeded synthetic workloads (``workloads``).
@@ -15,3 +19,20 @@ from ._native import (  # noqa: F401
     ldn_chunk_fwd, ldn_chunk_fwd_noalloc, ldn_chunk_fwd_select, ldn_chunk_fwd_ws, ldn_chunk_fwd_workspace_size, ldn_chunk_fwd_select_ws, ldn_chunk_fwd_split_segments, ldn_chunk_fwd_variant, ldn_decode_step, ldn_get_device_status, ldn_prologue, ldn_rmsnorm_gated,
     ldn_status_string, ldn_version, load,
 )
+from ._native import (  # noqa: F401
+    ldn_add_rmsnorm, ldn_add_rmsnorm_backward, ldn_add_rmsnorm_backward_workspace_size, ldn_add_rmsnorm_e4m3,
+    ldn_short_conv, ldn_short_conv_backward, ldn_short_conv_backward_workspace_size, ldn_short_conv_step,
+    ldn_ssm_backward, ldn_ssm_backward_workspace_size, ldn_ssm_scan, ldn_ssm_scan_workspace_size, ldn_ssm_step,
+)
+_MIXER = ("add_rmsnorm", "add_rmsnorm_backward", "add_rmsnorm_e4m3", "selective_scan", "selective_scan_backward",
+          "selective_scan_step", "short_conv", "short_conv_backward", "short_conv_step")
+
+
+def __getattr__(name):
+    # the torch layer of these is imported at first use: importing the package needs no torch
+    if name in _MIXER:
+        from . import mixer
+        for n in _MIXER:
+            globals()[n] = getattr(mixer, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

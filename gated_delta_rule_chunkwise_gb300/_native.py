@@ -10,11 +10,12 @@ Two layers:
     ``ldn_chunk_fwd_gdn2``, ``ldn_decode_step_gdn2``, ``ldn_backward``,
     ``ldn_backward_workspace_size``, ``ldn_rla_fwd``, ``ldn_rla_fwd_ws``,
     ``ldn_rla_fwd_workspace_size``, ``ldn_prologue``,
-    ``ldn_rmsnorm_gated``,
+    ``ldn_rmsnorm_gated``, ``ldn_add_rmsnorm*``, ``ldn_short_conv*``, ``ldn_ssm_*``,
     ``ldn_get_device_status``, ``ldn_status_string``, ``ldn_version``: the C
     entry points under the same names, taking raw integer pointers;
   * ``chunk_fwd``, ``decode_step``, ``chunk_fwd_gdn2``, ``decode_step_gdn2``, ``backward`` and
-    ``rla_fwd``:
+    ``rla_fwd``, and (module ``mixer``) ``add_rmsnorm``, ``add_rmsnorm_e4m3``, ``short_conv``,
+    ``short_conv_step``, ``selective_scan``, ``selective_scan_step`` and their ``*_backward``:
     the same calls on torch CUDA tensors,
     with shape / dtype checks and allocation of outputs and of the split
     variant's workspace (torch is used for device memory and the current
@@ -50,6 +51,7 @@ class LdnError(RuntimeError):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
 _SIGNATURES = {
     "ldn_chunk_fwd": ([_P] * 8 + [_I] * 8 + [_P], _I),
     "ldn_chunk_fwd_variant": ([_P] * 8 + [_I] * 9 + [_P], _I),
@@ -70,6 +72,21 @@ _SIGNATURES = {
     "ldn_decode_step_gdn2": ([_P] * 8 + [_I] * 5 + [_P], _I),
     "ldn_prologue": ([_P] * 6 + [_I] + [_P] * 9 + [_I] * 7 + [ctypes.c_float, _P], _I),
     "ldn_rmsnorm_gated": ([_P] * 4 + [_I] * 5 + [ctypes.c_float, _P], _I),
+    "ldn_add_rmsnorm": ([_P] * 5 + [_L] + [_I] * 3 + [ctypes.c_float, _P], _I),
+    "ldn_add_rmsnorm_e4m3": ([_P] * 6 + [_L] + [_I] * 4 + [ctypes.c_float, _P], _I),
+    "ldn_add_rmsnorm_backward": ([_P] * 7 + [_L] + [_I] * 3 + [ctypes.c_float, _P, ctypes.c_size_t, _P], _I),
+    "ldn_add_rmsnorm_backward_workspace_size": ([_L, _I], ctypes.c_size_t),
+    "ldn_short_conv": ([_P, _L] + [_P] * 6 + [_I] * 6 + [_P], _I),
+    "ldn_short_conv_step": ([_P, _L] + [_P] * 5 + [_I] * 5 + [_P], _I),
+    "ldn_short_conv_backward": ([_P, _L] + [_P] * 10 + [_I] * 6 + [_P, ctypes.c_size_t, _P], _I),
+    "ldn_short_conv_backward_workspace_size": ([_I] * 4, ctypes.c_size_t),
+    "ldn_ssm_scan": ([_P, _L, _P, _L, _P, _P, _L, _P, _L, _P, _P, _L] + [_P] * 6 + [_I] * 7 +
+                     [_P, ctypes.c_size_t, _P], _I),
+    "ldn_ssm_scan_workspace_size": ([_I] * 5, ctypes.c_size_t),
+    "ldn_ssm_step": ([_P, _L, _P, _L, _P, _P, _L, _P, _L, _P, _P, _L] + [_P] * 4 + [_I] * 6 + [_P], _I),
+    "ldn_ssm_backward": ([_P, _L, _P, _L, _P, _P, _L, _P, _L, _P, _P, _L] + [_P] * 14 + [_I] * 7 +
+                         [_P, ctypes.c_size_t, _P], _I),
+    "ldn_ssm_backward_workspace_size": ([_I] * 5, ctypes.c_size_t),
     "ldn_get_device_status": ([_P], _I),
     "ldn_status_string": ([_I], ctypes.c_char_p),
     "ldn_version": ([], _I),
@@ -187,6 +204,76 @@ def ldn_prologue(q_in, k_in, v_in, conv_q, conv_k, conv_v, width, beta_logit, ga
 
 def ldn_rmsnorm_gated(o, g, weight, y, B, T, H, dv, dtype, eps, stream):
     return load().ldn_rmsnorm_gated(o, g, weight, y, B, T, H, dv, dtype, eps, stream)
+
+
+def ldn_add_rmsnorm(x, residual, weight, y, residual_out, rows, D, dtype, residual_dtype, eps, stream):
+    return load().ldn_add_rmsnorm(x, residual, weight, y, residual_out, rows, D, dtype, residual_dtype, eps, stream)
+
+
+def ldn_add_rmsnorm_e4m3(x, residual, weight, q, scale, residual_out, rows, D, group, dtype, residual_dtype, eps,
+                         stream):
+    return load().ldn_add_rmsnorm_e4m3(x, residual, weight, q, scale, residual_out, rows, D, group, dtype,
+                                       residual_dtype, eps, stream)
+
+
+def ldn_add_rmsnorm_backward(dy, s, weight, dsum, dx, dresidual, dweight, rows, D, dtype, residual_dtype, eps,
+                             workspace, workspace_bytes, stream):
+    return load().ldn_add_rmsnorm_backward(dy, s, weight, dsum, dx, dresidual, dweight, rows, D, dtype,
+                                           residual_dtype, eps, workspace, workspace_bytes, stream)
+
+
+def ldn_add_rmsnorm_backward_workspace_size(rows, D):
+    return load().ldn_add_rmsnorm_backward_workspace_size(rows, D)
+
+
+def ldn_short_conv(x, ldx, weight, bias, state, lens, y, state_out, B, T, C, width, activation, dtype, stream):
+    return load().ldn_short_conv(x, ldx, weight, bias, state, lens, y, state_out, B, T, C, width, activation, dtype,
+                                 stream)
+
+
+def ldn_short_conv_step(x, ldx, weight, bias, state, y, state_out, B, C, width, activation, dtype, stream):
+    return load().ldn_short_conv_step(x, ldx, weight, bias, state, y, state_out, B, C, width, activation, dtype,
+                                      stream)
+
+
+def ldn_short_conv_backward(x, ldx, weight, bias, state, lens, dy, dstate_out, dx, dweight, dbias, dstate, B, T, C,
+                            width, activation, dtype, workspace, workspace_bytes, stream):
+    return load().ldn_short_conv_backward(x, ldx, weight, bias, state, lens, dy, dstate_out, dx, dweight, dbias,
+                                          dstate, B, T, C, width, activation, dtype, workspace, workspace_bytes,
+                                          stream)
+
+
+def ldn_short_conv_backward_workspace_size(B, T, C, width):
+    return load().ldn_short_conv_backward_workspace_size(B, T, C, width)
+
+
+def ldn_ssm_scan(u, ldu, delta, ld_delta, A, Bm, ldb, Cm, ldc, Dskip, z, ldz, delta_bias, h0, lens, y, h_final,
+                 states, B, T, D, N, G, delta_softplus, dtype, workspace, workspace_bytes, stream):
+    return load().ldn_ssm_scan(u, ldu, delta, ld_delta, A, Bm, ldb, Cm, ldc, Dskip, z, ldz, delta_bias, h0, lens, y,
+                               h_final, states, B, T, D, N, G, delta_softplus, dtype, workspace, workspace_bytes,
+                               stream)
+
+
+def ldn_ssm_scan_workspace_size(B, T, D, N, G):
+    return load().ldn_ssm_scan_workspace_size(B, T, D, N, G)
+
+
+def ldn_ssm_step(u, ldu, delta, ld_delta, A, Bm, ldb, Cm, ldc, Dskip, z, ldz, delta_bias, h, h_out, y, B, D, N, G,
+                 delta_softplus, dtype, stream):
+    return load().ldn_ssm_step(u, ldu, delta, ld_delta, A, Bm, ldb, Cm, ldc, Dskip, z, ldz, delta_bias, h, h_out, y,
+                               B, D, N, G, delta_softplus, dtype, stream)
+
+
+def ldn_ssm_backward(u, ldu, delta, ld_delta, A, Bm, ldb, Cm, ldc, Dskip, z, ldz, delta_bias, states, lens, dy,
+                     dh_final, du, ddelta, dA, dB, dC, dD, dz, ddelta_bias, dh0, B, T, D, N, G, delta_softplus, dtype,
+                     workspace, workspace_bytes, stream):
+    return load().ldn_ssm_backward(u, ldu, delta, ld_delta, A, Bm, ldb, Cm, ldc, Dskip, z, ldz, delta_bias, states,
+                                   lens, dy, dh_final, du, ddelta, dA, dB, dC, dD, dz, ddelta_bias, dh0, B, T, D, N,
+                                   G, delta_softplus, dtype, workspace, workspace_bytes, stream)
+
+
+def ldn_ssm_backward_workspace_size(B, T, D, N, G):
+    return load().ldn_ssm_backward_workspace_size(B, T, D, N, G)
 
 
 def ldn_get_device_status(stream):

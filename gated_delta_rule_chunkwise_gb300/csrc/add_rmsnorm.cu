@@ -1,0 +1,329 @@
+// RMS norm with the residual's addition, and its gradient.
+//
+//   s = x + r (stored in the residual's type),  rstd = 1 / sqrt(mean_c s_c^2 + eps),
+//   y = s rstd w,   as the element type or in e4m3 with scales:
+//   scale = max(max_group |y|, 2^-100) / 448,  q = e4m3(y / scale), saturating;
+//   a group is 128 consecutive channels or the whole row.
+// The norm is taken of s AS STORED: a bf16 residual stream rounds the sum once, and that
+// value is what the next block adds to and what the gradient reads back.
+//
+//   ds = dsum + rstd (w dy - s rstd^2 mean_c(w dy s)),  dw = sum over rows of dy s rstd.
+//
+// Both directions move every byte once and are bound by HBM: a row lives in registers (8
+// consecutive channels a thread and vector), two block sums a row.  Arithmetic is fp32.
+#include <cuda_fp8.h>
+
+#include "mixer_common.cuh"
+
+namespace ldn {
+namespace {
+
+constexpr int kE = 8;   // channels per thread and vector
+constexpr float kE4m3Max = 448.f;
+
+template <int NV>
+__device__ __forceinline__ void block_sum(float *v, float *sm, int nwarps)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) sm[i * 32 + warp] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float t = lane < nwarps ? sm[i * 32 + lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        v[i] = t;
+    }
+}
+
+__device__ __forceinline__ float block_max(float v, float *sm, int nwarps)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (lane == 0) sm[warp] = v;
+    __syncthreads();
+    float t = lane < nwarps ? sm[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+    return t;
+}
+
+template <int N, bool VEC>
+__device__ __forceinline__ void store_e4m3(uint8_t *p, const float *v, int valid)
+{
+    static_assert(N == 8, "two words");
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i], v[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2], v[4 * i + 3]), __NV_SATFINITE,
+                                                     __NV_E4M3);
+        w[i] = lo | (hi << 16);
+    }
+    if constexpr (VEC) {
+        if (valid > 0) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < valid) p[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+    }
+}
+
+// Rounds to the stored type and back.
+__device__ __forceinline__ float as_stored(float x, const float *) { return x; }
+__device__ __forceinline__ float as_stored(float x, const __nv_bfloat16 *)
+{
+    return __bfloat162float(__float2bfloat16_rn(x));
+}
+
+// EIGHT: 0 = y in TIn, 1 = e4m3 with a scale per row, 2 = per 128 channels.
+template <typename TIn, typename TRes, int EIGHT, int VPT, bool VEC>
+__global__ void __launch_bounds__(1024)
+add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__restrict__ w, void *__restrict__ y,
+                   float *__restrict__ scale, TRes *r_out, int D, float eps)
+{
+    __shared__ float sm[64];
+    const size_t row = blockIdx.x;
+    const int nt = blockDim.x, nwarps = nt >> 5;
+    const TIn *xr = x + row * D;
+    float v[VPT][kE], ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int c = (k * nt + (int)threadIdx.x) * kE, valid = D - c;
+        load_n<kE, VEC>(xr + c, v[k], valid);
+        if (r) {
+            float q[kE];
+            load_n<kE, VEC>(r + row * D + c, q, valid);
+#pragma unroll
+            for (int i = 0; i < kE; ++i) v[k][i] = as_stored(v[k][i] + q[i], r);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int c = (k * nt + (int)threadIdx.x) * kE;
+        if (r) store_n<kE, VEC>(r_out + row * D + c, v[k], D - c);
+#pragma unroll
+        for (int i = 0; i < kE; ++i) ss = fmaf(v[k][i], v[k][i], ss);
+    }
+    block_sum<1>(&ss, sm, nwarps);
+    const float rstd = rsqrtf(ss / (float)D + eps);
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int c = (k * nt + (int)threadIdx.x) * kE, valid = D - c;
+        float g[kE];
+        load_n<kE, false>(w + c, g, valid);
+#pragma unroll
+        for (int i = 0; i < kE; ++i) v[k][i] *= rstd * g[i];
+        if constexpr (EIGHT == 0) {
+            store_n<kE, VEC>((TIn *)y + row * D + c, v[k], valid);
+        } else {
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < kE; ++i) m = fmaxf(m, fabsf(v[k][i]));
+            if constexpr (EIGHT == 2) {
+                // 128 channels are the 8-channel vectors of 16 neighbouring lanes
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                m = fmaxf(m, 0x1p-100f);
+                const float up = kE4m3Max / m;
+#pragma unroll
+                for (int i = 0; i < kE; ++i) v[k][i] *= up;
+                store_e4m3<kE, VEC>((uint8_t *)y + row * D + c, v[k], valid);
+                if ((threadIdx.x & 15) == 0 && valid > 0)
+                    scale[row * (size_t)((D + 127) / 128) + c / 128] = m / kE4m3Max;
+            } else {
+                top = fmaxf(top, m);
+            }
+        }
+    }
+    if constexpr (EIGHT == 1) {
+        top = fmaxf(block_max(top, sm + 32, nwarps), 0x1p-100f);
+        const float up = kE4m3Max / top;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * nt + (int)threadIdx.x) * kE;
+#pragma unroll
+            for (int i = 0; i < kE; ++i) v[k][i] *= up;
+            store_e4m3<kE, VEC>((uint8_t *)y + row * D + c, v[k], D - c);
+        }
+        if (threadIdx.x == 0) scale[row] = top / kE4m3Max;
+    }
+}
+
+// A block walks rows blockIdx.x, + gridDim.x, ...; the columns' share of dw stays in
+// registers over all of them and goes to `part` [gridDim.x][D] once.
+template <typename TIn, typename TRes, int VPT, bool VEC>
+__global__ void __launch_bounds__(1024)
+add_rmsnorm_bwd_kernel(const TIn *__restrict__ dy, const TRes *__restrict__ s, const float *__restrict__ w,
+                       const TRes *__restrict__ dsum, TIn *__restrict__ dx, TRes *__restrict__ dres,
+                       float *__restrict__ part, long long rows, int D, float eps)
+{
+    __shared__ float sm[2][64];
+    const int nt = blockDim.x, nwarps = nt >> 5;
+    float acc[VPT][kE], g[VPT][kE];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int c = (k * nt + (int)threadIdx.x) * kE;
+        load_n<kE, false>(w + c, g[k], D - c);
+#pragma unroll
+        for (int i = 0; i < kE; ++i) acc[k][i] = 0.f;
+    }
+    int turn = 0;
+    for (long long row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
+        float sv[VPT][kE], gy[VPT][kE], sums[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * nt + (int)threadIdx.x) * kE, valid = D - c;
+            load_n<kE, VEC>(s + row * D + c, sv[k], valid);
+            load_n<kE, VEC>(dy + row * D + c, gy[k], valid);
+        }
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int i = 0; i < kE; ++i) {
+                sums[0] = fmaf(sv[k][i], sv[k][i], sums[0]);
+                sums[1] = fmaf(g[k][i] * gy[k][i], sv[k][i], sums[1]);
+            }
+        block_sum<2>(sums, sm[turn], nwarps);   // two buffers: the next row's sums pass no reader of these
+        const float rstd = rsqrtf(sums[0] / (float)D + eps);
+        const float m = rstd * rstd * (sums[1] / (float)D);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * nt + (int)threadIdx.x) * kE, valid = D - c;
+            float d[kE];
+            if (dsum) load_n<kE, VEC>(dsum + row * D + c, d, valid);
+            else
+#pragma unroll
+                for (int i = 0; i < kE; ++i) d[i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kE; ++i) {
+                acc[k][i] = fmaf(gy[k][i], sv[k][i] * rstd, acc[k][i]);
+                d[i] = fmaf(rstd, g[k][i] * gy[k][i] - sv[k][i] * m, d[i]);
+            }
+            if (dx) store_n<kE, VEC>(dx + row * D + c, d, valid);
+            if (dres) store_n<kE, VEC>(dres + row * D + c, d, valid);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int c = (k * nt + (int)threadIdx.x) * kE;
+        store_n<kE, false>(part + (size_t)blockIdx.x * D + c, acc[k], D - c);
+    }
+}
+
+// out[c] = sum over n rows of part[n][c]; 8 rows in flight per block of 32 x 8 threads.
+__global__ void __launch_bounds__(256) column_sum_kernel(const float *__restrict__ part, float *__restrict__ out,
+                                                         int n, int D)
+{
+    __shared__ float sm[8][33];
+    const int c = blockIdx.x * 32 + threadIdx.x, y = threadIdx.y;
+    float t = 0.f;
+    if (c < D)
+        for (int i = y; i < n; i += 8) t += part[(size_t)i * D + c];
+    sm[y][threadIdx.x] = t;
+    __syncthreads();
+    if (y == 0 && c < D) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) t += sm[i][threadIdx.x];
+        out[c] = t;
+    }
+}
+
+// Threads for D channels at VPT vectors of 8 each, in whole warps.
+int norm_threads(int D, int vpt) { return std::min(1024, (((D + kE * vpt - 1) / (kE * vpt) + 31) / 32) * 32); }
+
+// Vectors per thread: the fewest that fit 1024 threads, but two from 4096 channels on.
+int norm_vpt(int D) { return D < 4096 ? 1 : D <= 16384 ? 2 : 4; }
+
+template <typename TIn, typename TRes, int EIGHT, int VPT>
+void norm_run(const AddNormArgs &a, bool vec, cudaStream_t st)
+{
+    const dim3 grid((unsigned)a.rows), block(norm_threads(a.D, VPT));
+    if (vec)
+        add_rmsnorm_kernel<TIn, TRes, EIGHT, VPT, true><<<grid, block, 0, st>>>(
+            (const TIn *)a.x, (const TRes *)a.residual, a.weight, a.y, a.scale, (TRes *)a.residual_out, a.D, a.eps);
+    else
+        add_rmsnorm_kernel<TIn, TRes, EIGHT, VPT, false><<<grid, block, 0, st>>>(
+            (const TIn *)a.x, (const TRes *)a.residual, a.weight, a.y, a.scale, (TRes *)a.residual_out, a.D, a.eps);
+}
+
+template <typename TIn, typename TRes>
+void norm_pick(const AddNormArgs &a, bool vec, cudaStream_t st)
+{
+    const int v = norm_vpt(a.D);
+    const int e = !a.scale ? 0 : a.group ? 2 : 1;
+#define LDN_NORM(E, V) norm_run<TIn, TRes, E, V>(a, vec, st)
+    if (e == 0) v == 1 ? LDN_NORM(0, 1) : v == 2 ? LDN_NORM(0, 2) : LDN_NORM(0, 4);
+    if (e == 1) v == 1 ? LDN_NORM(1, 1) : v == 2 ? LDN_NORM(1, 2) : LDN_NORM(1, 4);
+    if (e == 2) v == 1 ? LDN_NORM(2, 1) : v == 2 ? LDN_NORM(2, 2) : LDN_NORM(2, 4);
+#undef LDN_NORM
+}
+
+bool vec16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+template <typename TIn, typename TRes, int VPT>
+void norm_bwd_run(const AddNormBwdArgs &a, int grid, bool vec, cudaStream_t st)
+{
+    const dim3 block(norm_threads(a.D, VPT));
+    if (vec)
+        add_rmsnorm_bwd_kernel<TIn, TRes, VPT, true><<<grid, block, 0, st>>>(
+            (const TIn *)a.dy, (const TRes *)a.s, a.weight, (const TRes *)a.dsum, (TIn *)a.dx, (TRes *)a.dres,
+            a.part, a.rows, a.D, a.eps);
+    else
+        add_rmsnorm_bwd_kernel<TIn, TRes, VPT, false><<<grid, block, 0, st>>>(
+            (const TIn *)a.dy, (const TRes *)a.s, a.weight, (const TRes *)a.dsum, (TIn *)a.dx, (TRes *)a.dres,
+            a.part, a.rows, a.D, a.eps);
+}
+
+template <typename TIn, typename TRes>
+void norm_bwd_pick(const AddNormBwdArgs &a, int grid, bool vec, cudaStream_t st)
+{
+    const int v = norm_vpt(a.D);
+    v == 1   ? norm_bwd_run<TIn, TRes, 1>(a, grid, vec, st)
+    : v == 2 ? norm_bwd_run<TIn, TRes, 2>(a, grid, vec, st)
+             : norm_bwd_run<TIn, TRes, 4>(a, grid, vec, st);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const AddNormArgs &a, cudaStream_t st)
+{
+    const bool vec = a.D % kE == 0 && vec16(a.x) && vec16(a.residual) && vec16(a.residual_out) && vec16(a.y);
+    if (a.dtype == LDN_F32) norm_pick<float, float>(a, vec, st);
+    else if (a.res_dtype == LDN_F32) norm_pick<__nv_bfloat16, float>(a, vec, st);
+    else norm_pick<__nv_bfloat16, __nv_bfloat16>(a, vec, st);
+    return cudaGetLastError();
+}
+
+// Blocks of the gradient's row walk: enough to fill the SMs (2048 threads each), no more than
+// rows.  A fixed 152 SMs, so that the workspace's size needs no device.
+int add_rmsnorm_bwd_blocks(long long rows, int D)
+{
+    const int per = std::max(1, 1024 / norm_threads(D, norm_vpt(D)));
+    return (int)std::min<long long>(rows, 152LL * per);
+}
+
+cudaError_t launch_add_rmsnorm_bwd(const AddNormBwdArgs &a, cudaStream_t st)
+{
+    const bool vec = a.D % kE == 0 && vec16(a.dy) && vec16(a.s) && vec16(a.dsum) && vec16(a.dx) && vec16(a.dres);
+    const int grid = add_rmsnorm_bwd_blocks(a.rows, a.D);
+    if (grid > 0) {
+        if (a.dtype == LDN_F32) norm_bwd_pick<float, float>(a, grid, vec, st);
+        else if (a.res_dtype == LDN_F32) norm_bwd_pick<__nv_bfloat16, float>(a, grid, vec, st);
+        else norm_bwd_pick<__nv_bfloat16, __nv_bfloat16>(a, grid, vec, st);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    column_sum_kernel<<<(a.D + 31) / 32, dim3(32, 8), 0, st>>>(a.part, a.dweight, grid, a.D);
+    return cudaGetLastError();
+}
+
+}  // namespace ldn

@@ -62,6 +62,94 @@ struct RmsNormArgs {
     float eps;
 };
 
+// RMS norm with the residual's addition (add_rmsnorm.cu).  scale set: e4m3 output.
+struct AddNormArgs {
+    const void *x, *residual;
+    const float *weight;
+    void *y;
+    float *scale;
+    void *residual_out;
+    long long rows;
+    int D, group, dtype, res_dtype;
+    float eps;
+};
+struct AddNormBwdArgs {
+    const void *dy, *s;
+    const float *weight;
+    const void *dsum;
+    void *dx, *dres;
+    float *dweight, *part;   // part [add_rmsnorm_bwd_blocks][D]
+    long long rows;
+    int D, dtype, res_dtype;
+    float eps;
+};
+cudaError_t launch_add_rmsnorm(const AddNormArgs &a, cudaStream_t stream);
+cudaError_t launch_add_rmsnorm_bwd(const AddNormBwdArgs &a, cudaStream_t stream);
+int add_rmsnorm_bwd_blocks(long long rows, int D);
+
+// Short causal convolution with a carried state (short_conv.cu).  Rows of x are ldx elements
+// apart, sequences T rows; y, dy, dx and the states are contiguous.
+struct ConvArgs {
+    const void *x;
+    long long ldx;
+    const float *w, *bias;
+    const void *state;
+    void *state_out;
+    const int *lens;
+    void *y;
+    int B, T, C, W, act, dtype;
+};
+struct ConvBwdArgs {
+    const void *x;
+    long long ldx;
+    const float *w, *bias;
+    const void *state;
+    const int *lens;
+    const void *dy, *dstate_out;
+    void *dx;
+    float *dw, *db;
+    void *dstate;
+    float *part;
+    int B, T, C, W, act, dtype;
+};
+cudaError_t launch_short_conv(const ConvArgs &a, cudaStream_t stream);
+cudaError_t launch_short_conv_step(const ConvArgs &a, cudaStream_t stream);
+cudaError_t launch_short_conv_bwd(const ConvBwdArgs &a, cudaStream_t stream);
+size_t short_conv_bwd_workspace_bytes(int B, int T, int C, int W);
+
+// Selective state space scan (ssm_scan.cu, ssm_backward.cu).  u, delta, z [B][T][D] and
+// Bm, Cm [B][T][G][N] with rows ld* elements apart.
+struct SsmArgs {
+    const void *u, *delta, *Bm, *Cm, *z;
+    long long ldu, ldd, ldb, ldc, ldz;
+    const float *A, *Dskip, *bias, *h0;
+    const int *lens;
+    void *y;
+    float *h_final, *states;   // states: entering every kSsmChunk tokens, [B][chunks][D][N]
+    float *ws;                 // segment states and sums of steps, or null
+    size_t ws_bytes;
+    int B, T, D, N, G, softplus, dtype;
+};
+struct SsmBwdArgs {
+    const void *u, *delta, *Bm, *Cm, *z;
+    long long ldu, ldd, ldb, ldc, ldz;
+    const float *A, *Dskip, *bias, *states;
+    const int *lens;
+    const void *dy;
+    const float *dh_final;
+    void *du, *ddelta, *dB, *dC, *dz;
+    float *dA, *dD, *dbias, *dh0;
+    float *ws;
+    int B, T, D, N, G, softplus, dtype;
+};
+constexpr int kSsmChunk = 32;
+bool ssm_supported_n(int N);
+size_t ssm_scan_workspace_bytes(int B, int T, int D, int N, int G);
+cudaError_t launch_ssm_scan(const SsmArgs &a, cudaStream_t stream);
+cudaError_t launch_ssm_step(const SsmArgs &a, cudaStream_t stream);   // h0 -> h_final, one token
+size_t ssm_backward_workspace_bytes(int B, int T, int D, int N, int G);
+cudaError_t launch_ssm_backward(const SsmBwdArgs &a, cudaStream_t stream);
+
 // Split variant: workspace bytes per (b, h, chunk) -- [Q~ ; -W] (32 KiB), [P U' ; U']
 // per 64-column slice of dv (16 KiB each), K~ (16 KiB), e^{g_C} per key channel
 // (512 B); layout described in include/ldn.h.

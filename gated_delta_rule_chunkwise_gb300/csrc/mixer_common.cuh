@@ -1,0 +1,136 @@
+// Device helpers shared by the operators around a token mixer: the RMS norm with the
+// residual's addition (add_rmsnorm.cu), the short convolution (short_conv.cu) and the
+// selective scan (ssm_scan.cu, ssm_backward.cu).
+#pragma once
+#include "ldn_internal.cuh"
+
+namespace ldn {
+
+// N consecutive elements, widened to fp32.  Vectors of 8 / 16 bytes when VEC (the address is
+// then a multiple of the vector), single elements otherwise; elements at and past `valid`
+// read as zero (VEC vectors are wholly inside or wholly outside).
+template <int N, bool VEC>
+__device__ __forceinline__ void load_n(const float *p, float *v, int valid = N)
+{
+    if constexpr (VEC) {
+        static_assert(N % 4 == 0, "float4 loads");
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 x = valid > 0 ? *reinterpret_cast<const float4 *>(p + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = i < valid ? p[i] : 0.f;
+    }
+}
+
+__device__ __forceinline__ void bf16x2_widen(uint32_t u, float *v)
+{
+    v[0] = __uint_as_float(u << 16);   // a bf16 is the upper half of its fp32
+    v[1] = __uint_as_float(u & 0xffff0000u);
+}
+
+template <int N, bool VEC>
+__device__ __forceinline__ void load_n(const __nv_bfloat16 *p, float *v, int valid = N)
+{
+    if constexpr (VEC && N == 8) {
+        const uint4 u = valid > 0 ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+        bf16x2_widen(u.x, v); bf16x2_widen(u.y, v + 2); bf16x2_widen(u.z, v + 4); bf16x2_widen(u.w, v + 6);
+    } else if constexpr (VEC) {
+        static_assert(N == 4, "8- or 16-byte loads");
+        const uint2 u = valid > 0 ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0, 0);
+        bf16x2_widen(u.x, v); bf16x2_widen(u.y, v + 2);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = i < valid ? __bfloat162float(p[i]) : 0.f;
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16x2_pack(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// N consecutive results, each rounded once to the element type; nothing at and past `valid`.
+template <int N, bool VEC>
+__device__ __forceinline__ void store_n(float *p, const float *v, int valid = N)
+{
+    if constexpr (VEC) {
+        if (valid > 0)
+#pragma unroll
+            for (int i = 0; i < N; i += 4)
+                *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < valid) p[i] = v[i];
+    }
+}
+
+template <int N, bool VEC>
+__device__ __forceinline__ void store_n(__nv_bfloat16 *p, const float *v, int valid = N)
+{
+    if constexpr (VEC && N == 8) {
+        if (valid > 0)
+            *reinterpret_cast<uint4 *>(p) = make_uint4(bf16x2_pack(v[0], v[1]), bf16x2_pack(v[2], v[3]),
+                                                       bf16x2_pack(v[4], v[5]), bf16x2_pack(v[6], v[7]));
+    } else if constexpr (VEC) {
+        static_assert(N == 4, "8- or 16-byte stores");
+        if (valid > 0)
+            *reinterpret_cast<uint2 *>(p) = make_uint2(bf16x2_pack(v[0], v[1]), bf16x2_pack(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < valid) p[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+// sigma(x) = 1 / (1 + e^-x); the quotient is 0 where e^-x overflows.
+__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1].  log(1 + e) = 2 atanh(s) with
+// s = e / (2 + e) <= 1/3, by the odd series of atanh to s^15: the first omitted term is below
+// 2^-29 of the sum, so a small step size keeps its relative accuracy (a logarithm of 1 + e
+// would lose it in rounding 1 + e).
+__device__ __forceinline__ float softplus_accurate(float x)
+{
+    const float e = __expf(-fabsf(x));
+    const float s = __fdividef(e, 2.f + e), q = s * s;
+    float p = 1.f / 15.f;
+    p = fmaf(p, q, 1.f / 13.f);
+    p = fmaf(p, q, 1.f / 11.f);
+    p = fmaf(p, q, 1.f / 9.f);
+    p = fmaf(p, q, 1.f / 7.f);
+    p = fmaf(p, q, 1.f / 5.f);
+    p = fmaf(p, q, 1.f / 3.f);
+    p = fmaf(p, q, 1.f);
+    // a NaN stays one through e; +-infinity gives e = 0
+    return fmaxf(x, 0.f) + 2.f * s * p;
+}
+
+// Sums across the lanes of mask M, M/2, ..., down to LO, of V values a lane, halving the
+// values as it goes: a lane whose bit is set in the current mask keeps the upper half.  After
+// it a lane holds max(1, V / steps') sums; where lanes outnumber values the rest of the steps
+// add whole values, so several lanes hold the same sum.
+template <int V, int M, int LO>
+__device__ __forceinline__ void reduce_halving(float *v, int lane)
+{
+    if constexpr (M >= LO) {
+        if constexpr (V > 1) {
+            const bool up = (lane & M) != 0;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const float keep = up ? v[V / 2 + i] : v[i], send = up ? v[i] : v[V / 2 + i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, M);
+            }
+            reduce_halving<V / 2, M / 2, LO>(v, lane);
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], M);
+            reduce_halving<1, M / 2, LO>(v, lane);
+        }
+    }
+}
+
+}  // namespace ldn

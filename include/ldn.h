@@ -28,6 +28,12 @@
  *   ldn_rla_fwd, ldn_rla_fwd_ws, ldn_rla_fwd_workspace_size
  *       Residual Linear Attention / Residual DeltaNet (the Residual Linear
  *       Attention notes, Sec. 2.2-2.4);
+ *   ldn_add_rmsnorm, _e4m3, _backward, _backward_workspace_size
+ *       the residual's addition and RMS norm before a block's projections;
+ *   ldn_short_conv, _step, _backward, _backward_workspace_size
+ *       the short causal convolution with a carried state;
+ *   ldn_ssm_scan, _scan_workspace_size, _step, _backward, _backward_workspace_size
+ *       the selective state space scan;
  *   ldn_get_device_status, ldn_status_string, ldn_version.
  *
  * Conventions shared by every entry point
@@ -461,6 +467,146 @@ int ldn_rla_fwd_ws(const void *q, const void *k, const void *v, const float *bet
 /* Bytes of workspace ldn_rla_fwd_ws uses for these sizes (0: none needed, or a
  * shape without the chunk form).  Pure host function. */
 size_t ldn_rla_fwd_workspace_size(int B, int T, int H, int dk, int dv, int delta, int dtype);
+
+/*
+ * ldn_add_rmsnorm -- the residual's addition and the RMS norm before a block's
+ * projections:
+ *   s = x + residual (stored in the residual's type; s = x when residual is NULL),
+ *   y = s / sqrt(mean_c s_c^2 + eps) * weight.
+ * The norm is taken of s as stored: with a bf16 residual the sum is rounded once
+ * and that value is what is normalised, what residual_out holds and what
+ * ldn_add_rmsnorm_backward reads.  Sums and statistics are fp32.
+ *   x, y         [rows][D] of `dtype`            weight [D] fp32
+ *   residual, residual_out [rows][D] of `residual_dtype` (LDN_F32, or `dtype`),
+ *                both given or both NULL; residual_out may be residual (in place)
+ *   rows >= 0, 1 <= D <= 32768 (any D; multiples of 8 with 16-byte aligned
+ *   pointers move in 16-byte vectors); eps >= 0.
+ * Pointers are aligned to their element.  One launch.
+ */
+int ldn_add_rmsnorm(const void *x, const void *residual, const float *weight, void *y, void *residual_out,
+                    long long rows, int D, int dtype, int residual_dtype, float eps, void *stream);
+
+/* ldn_add_rmsnorm with y in 8 bits (e4m3) and fp32 scales, y ~ q * scale:
+ *   scale = max(max |y| over the group, 2^-100) / 448,  q = e4m3(y / scale),
+ * to nearest even, saturating.  `group` is 0 (one scale per row, scale [rows]) or
+ * 128 (scale [rows][ceil(D / 128)], the last group of a row may be short).
+ *   q [rows][D] bytes.  A NaN in y is a NaN in q. */
+int ldn_add_rmsnorm_e4m3(const void *x, const void *residual, const float *weight, void *q, float *scale,
+                         void *residual_out, long long rows, int D, int group, int dtype, int residual_dtype,
+                         float eps, void *stream);
+
+/*
+ * ldn_add_rmsnorm_backward -- gradient of ldn_add_rmsnorm's y (and of s itself):
+ *   ds = dsum + rstd (weight dy - s rstd^2 mean_c(weight dy s)),  rstd from s,
+ *   dweight = sum over rows of dy s rstd.
+ *   dy [rows][D] of `dtype`; s (the forward's residual_out, or x) and dsum (the
+ *   gradient that reaches s from elsewhere, NULL: zero) of `residual_dtype`
+ *   dx [rows][D] of `dtype` and dresidual [rows][D] of `residual_dtype`: both are
+ *   ds; either may be NULL.  dweight [D] fp32.
+ *   workspace: ldn_add_rmsnorm_backward_workspace_size bytes, 16-byte aligned.
+ * The result is the same bit for bit on every call.  Two launches.
+ */
+int ldn_add_rmsnorm_backward(const void *dy, const void *s, const float *weight, const void *dsum, void *dx,
+                             void *dresidual, float *dweight, long long rows, int D, int dtype, int residual_dtype,
+                             float eps, void *workspace, size_t workspace_bytes, void *stream);
+size_t ldn_add_rmsnorm_backward_workspace_size(long long rows, int D);
+
+/*
+ * ldn_short_conv -- depthwise causal short convolution with a carried state, the
+ * form of ldn_prologue's convolution for serving and training:
+ *   p_t[c] = bias[c] + sum_j weight[c][j] x_{t-width+1+j}[c],  y = silu(p) or p.
+ *   x        [B][T][C] of `dtype`, rows ldx elements apart (ldx >= C), sequences T rows
+ *   weight   [C][width] fp32 (the last tap on the current token), bias [C] fp32 or NULL
+ *   state    [B][width-1][C] of `dtype`, the rows before the call, oldest first;
+ *            NULL: zeros.  state_out: the same shape, the last width - 1 rows at each
+ *            sequence's end, or NULL; it may be `state` (in place)
+ *   lens     [B] int32 on the device, or NULL: sequence b has min(max(lens[b], 0), T)
+ *            rows; rows past it are not read, and their y is zero
+ *   y        [B][T][C] of `dtype`, contiguous
+ *   activation 1: SiLU, 0: none.  width 1..8, any C; T = 0 copies the state.
+ * Arithmetic is fp32.  One launch.
+ */
+int ldn_short_conv(const void *x, long long ldx, const float *weight, const float *bias, const void *state,
+                   const int *lens, void *y, void *state_out, int B, int T, int C, int width, int activation,
+                   int dtype, void *stream);
+
+/* One token of ldn_short_conv for every sequence: x [B][C] with rows ldx apart,
+ * y [B][C]; state and state_out (may be the same) are needed for width > 1. */
+int ldn_short_conv_step(const void *x, long long ldx, const float *weight, const float *bias, const void *state,
+                        void *y, void *state_out, int B, int C, int width, int activation, int dtype, void *stream);
+
+/*
+ * ldn_short_conv_backward -- gradients of ldn_short_conv for y's gradient dy and the
+ * final state's dstate_out ([B][width-1][C] of `dtype`, NULL: zero).
+ *   dx [B][T][C] and dstate [B][width-1][C] (NULL: not wanted) of `dtype`, contiguous;
+ *   rows of dx past a sequence's end are zero.  dweight [C][width], dbias [C] (NULL: not
+ *   wanted) fp32.  workspace: ldn_short_conv_backward_workspace_size bytes, 16-byte
+ *   aligned.  The result is the same bit for bit on every call.  Two launches.
+ */
+int ldn_short_conv_backward(const void *x, long long ldx, const float *weight, const float *bias, const void *state,
+                            const int *lens, const void *dy, const void *dstate_out, void *dx, float *dweight,
+                            float *dbias, void *dstate, int B, int T, int C, int width, int activation, int dtype,
+                            void *workspace, size_t workspace_bytes, void *stream);
+size_t ldn_short_conv_backward_workspace_size(int B, int T, int C, int width);
+
+/*
+ * ldn_ssm_scan -- selective state space scan over whole sequences.  Channel d of
+ * group g = d / (D / G), state n:
+ *   dt = softplus(delta + delta_bias)  (delta_softplus = 0: delta + delta_bias),
+ *   h_t[d][n] = e^{dt A[d][n]} h_{t-1}[d][n] + dt u_t[d] B_t[g][n],
+ *   y_t[d] = (sum_n C_t[g][n] h_t[d][n] + Dskip[d] u_t[d]) silu(z_t[d]).
+ *   u, delta, z  [B][T][D] of `dtype`; z NULL: no output gate
+ *   Bm, Cm       [B][T][G][N] of `dtype`
+ *   Rows of these are ldu, ld_delta, ldz, ldb, ldc elements apart (slices of a
+ *   projection's output), sequences T rows.
+ *   A [D][N] fp32 (decay rates, <= 0 where nothing is to grow); Dskip, delta_bias [D]
+ *   fp32 or NULL; h0 [B][D][N] fp32 or NULL (zeros)
+ *   lens         [B] int32 on the device or NULL: sequence b has min(max(lens[b], 0), T)
+ *                rows; past them nothing is read, the state stays and y is zero
+ *   y            [B][T][D] of `dtype`, contiguous
+ *   h_final      [B][D][N] fp32 or NULL; it must not overlap h0
+ *   states       [B][ceil(T / 32)][D][N] fp32 or NULL: the state entering every 32
+ *                tokens, what ldn_ssm_backward starts from
+ *   N in {8, 16, 32, 64}; any D that G divides.  h0, h_final, states and workspace are
+ *   16-byte aligned.  T = 0 copies the state.
+ * Arithmetic and states are fp32.  With few channels and a workspace of
+ * ldn_ssm_scan_workspace_size bytes (0: none would be used) the tokens are cut into
+ * segments that run side by side, in two launches; without it one launch runs every
+ * sequence from end to end.  The two agree up to fp32 rounding.
+ */
+int ldn_ssm_scan(const void *u, long long ldu, const void *delta, long long ld_delta, const float *A, const void *Bm,
+                 long long ldb, const void *Cm, long long ldc, const float *Dskip, const void *z, long long ldz,
+                 const float *delta_bias, const float *h0, const int *lens, void *y, float *h_final, float *states,
+                 int B, int T, int D, int N, int G, int delta_softplus, int dtype, void *workspace,
+                 size_t workspace_bytes, void *stream);
+size_t ldn_ssm_scan_workspace_size(int B, int T, int D, int N, int G);
+
+/* One token of ldn_ssm_scan for every sequence: u, delta, z, y [B][D], Bm, Cm [B][G][N],
+ * h and h_out [B][D][N] fp32 16-byte aligned (may be the same: in place). */
+int ldn_ssm_step(const void *u, long long ldu, const void *delta, long long ld_delta, const float *A, const void *Bm,
+                 long long ldb, const void *Cm, long long ldc, const float *Dskip, const void *z, long long ldz,
+                 const float *delta_bias, const float *h, float *h_out, void *y, int B, int D, int N, int G,
+                 int delta_softplus, int dtype, void *stream);
+
+/*
+ * ldn_ssm_backward -- gradients of ldn_ssm_scan for y's gradient dy [B][T][D] of `dtype`
+ * and the final state's dh_final [B][D][N] fp32 (NULL: zero), from the forward's inputs
+ * and its `states`.
+ *   du, ddelta, dz [B][T][D] and dB, dC [B][T][G][N] of `dtype`, contiguous (dz given
+ *   exactly when z is); rows past a sequence's end are zero
+ *   dA [D][N], dD [D], ddelta_bias [D], dh0 [B][D][N] fp32; dD, ddelta_bias and dh0 may
+ *   be NULL (not wanted)
+ *   states, dh_final, dh0 and workspace (ldn_ssm_backward_workspace_size bytes) are
+ *   16-byte aligned.
+ * Arithmetic is fp32; the result is the same bit for bit on every call.
+ */
+int ldn_ssm_backward(const void *u, long long ldu, const void *delta, long long ld_delta, const float *A,
+                     const void *Bm, long long ldb, const void *Cm, long long ldc, const float *Dskip, const void *z,
+                     long long ldz, const float *delta_bias, const float *states, const int *lens, const void *dy,
+                     const float *dh_final, void *du, void *ddelta, float *dA, void *dB, void *dC, float *dD, void *dz,
+                     float *ddelta_bias, float *dh0, int B, int T, int D, int N, int G, int delta_softplus, int dtype,
+                     void *workspace, size_t workspace_bytes, void *stream);
+size_t ldn_ssm_backward_workspace_size(int B, int T, int D, int N, int G);
 
 /* Synchronises `stream`, then reads and clears the device status word on the
  * current device.  Returns LDN_OK, LDN_ERR_TIMEOUT (a kernel abandoned a
