@@ -47,6 +47,15 @@ __device__ __forceinline__ void load_n(const __nv_bfloat16 *p, float *v, int val
     }
 }
 
+// Two neighbouring elements at an even place.
+__device__ __forceinline__ float2 load_pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p)
+{
+    float v[2];
+    bf16x2_widen(*reinterpret_cast<const uint32_t *>(p), v);
+    return make_float2(v[0], v[1]);
+}
+
 __device__ __forceinline__ uint32_t bf16x2_pack(float a, float b)
 {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -90,24 +99,42 @@ __device__ __forceinline__ void store_n(__nv_bfloat16 *p, const float *v, int va
 // sigma(x) = 1 / (1 + e^-x); the quotient is 0 where e^-x overflows.
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
-// softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1].  log(1 + e) = 2 atanh(s) with
-// s = e / (2 + e) <= 1/3, by the odd series of atanh to s^15: the first omitted term is below
-// 2^-29 of the sum, so a small step size keeps its relative accuracy (a logarithm of 1 + e
-// would lose it in rounding 1 + e).
-__device__ __forceinline__ float softplus_accurate(float x)
+// softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1], of two values in packed
+// arithmetic.  log(1 + e) = 2 atanh(s) with s = e / (2 + e) <= 1/3; 2 atanh(s) / s is taken as
+// the Chebyshev interpolation of degree 4 in s^2 on [0, 1/9], within 8e-9 of it, so a small
+// step size keeps its relative accuracy (a logarithm of 1 + e would lose it in rounding 1 + e).
+// The exponent's rounding, worth |x| 2^-24 of e, is taken back to first order.
+__device__ __forceinline__ float2 softplus_accurate(float2 x)
 {
-    const float e = __expf(-fabsf(x));
-    const float s = __fdividef(e, 2.f + e), q = s * s;
-    float p = 1.f / 15.f;
-    p = fmaf(p, q, 1.f / 13.f);
-    p = fmaf(p, q, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
-    p = fmaf(p, q, 1.f);
-    // a NaN stays one through e; +-infinity gives e = 0
-    return fmaxf(x, 0.f) + 2.f * s * p;
+    // past 100 e is zero in fp32
+    const float2 ax = make_float2(fminf(fabsf(x.x), 100.f), fminf(fabsf(x.y), 100.f));
+    const float2 l2 = make_float2(-1.44269504f, -1.44269504f);
+    const float2 t = __fmul2_rn(ax, l2);
+    const float2 lost = __ffma2_rn(ax, l2, make_float2(-t.x, -t.y));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = __ffma2_rn(__fmul2_rn(e, lost), make_float2(0.69314718f, 0.69314718f), e);
+    const float2 d = __fadd2_rn(e, make_float2(2.f, 2.f));
+    const float2 s = make_float2(__fdividef(e.x, d.x), __fdividef(e.y, d.y));
+    const float2 q = __fmul2_rn(s, s);
+    float2 p = make_float2(0.281577796f, 0.281577796f);
+    p = __ffma2_rn(p, q, make_float2(0.279651582f, 0.279651582f));
+    p = __ffma2_rn(p, q, make_float2(0.400245965f, 0.400245965f));
+    p = __ffma2_rn(p, q, make_float2(0.666663229f, 0.666663229f));
+    p = __ffma2_rn(p, q, make_float2(2.f, 2.f));
+    float2 m;   // max(x, 0), where a NaN stays one
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m.x) : "f"(x.x));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m.y) : "f"(x.y));
+    return __ffma2_rn(s, p, m);
+}
+__device__ __forceinline__ float softplus_accurate(float x) { return softplus_accurate(make_float2(x, x)).x; }
+
+// x sigma(x) of two values.
+__device__ __forceinline__ float2 silu_fast(float2 x)
+{
+    const float2 d = __fadd2_rn(make_float2(__expf(-x.x), __expf(-x.y)), make_float2(1.f, 1.f));
+    return __fmul2_rn(x, make_float2(__fdividef(1.f, d.x), __fdividef(1.f, d.y)));
 }
 
 // Sums across the lanes of mask M, M/2, ..., down to LO, of V values a lane, halving the

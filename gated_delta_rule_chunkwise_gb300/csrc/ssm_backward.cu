@@ -131,10 +131,10 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
         if constexpr (STAGED) {
             const int rows = rows_of(t0);
             TIn(*raw)[TT * DB] = reinterpret_cast<TIn(*)[TT * DB]>(sm.raw);
-            if (PHASE == kMain) load_rows<TIn, DB, kThreads, true>(raw[0], u + (size_t)t0 * a.ldu, a.ldu, rows, cols);
-            load_rows<TIn, DB, kThreads, true>(raw[1], dl + (size_t)t0 * a.ldd, a.ldd, rows, cols);
-            load_rows<TIn, DB, kThreads, true>(raw[2], dy + (size_t)t0 * a.D, a.D, rows, cols);
-            if (z) load_rows<TIn, DB, kThreads, true>(raw[3], z + (size_t)t0 * a.ldz, a.ldz, rows, cols);
+            if (PHASE == kMain) load_rows<TIn, DB, DB, kThreads, true>(raw[0], u + (size_t)t0 * a.ldu, a.ldu, rows, cols);
+            load_rows<TIn, DB, DB, kThreads, true>(raw[1], dl + (size_t)t0 * a.ldd, a.ldd, rows, cols);
+            load_rows<TIn, DB, DB, kThreads, true>(raw[2], dy + (size_t)t0 * a.D, a.D, rows, cols);
+            if (z) load_rows<TIn, DB, DB, kThreads, true>(raw[3], z + (size_t)t0 * a.ldz, a.ldz, rows, cols);
             cp_async_commit();
         }
     };
@@ -148,10 +148,11 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
     float accD[2] = {0.f, 0.f}, accb[2] = {0.f, 0.f};
 
     RowRegs<TIn, N, kThreads> rB, rC;
+    const int vB = rB.alignment(Bm, a.ldb), vC = rC.alignment(Cm, a.ldc);
     const int last = tb + (te - 1 - tb) / TT * TT;   // the segment's last tile
     fetch(last);
-    if (PHASE == kMain) rB.load(Bm + (size_t)last * a.ldb, a.ldb, rows_of(last));
-    rC.load(Cm + (size_t)last * a.ldc, a.ldc, rows_of(last));
+    if (PHASE == kMain) rB.load(Bm + (size_t)last * a.ldb, a.ldb, rows_of(last), vB);
+    rC.load(Cm + (size_t)last * a.ldc, a.ldc, rows_of(last), vC);
     for (int t0 = last; t0 >= tb; t0 -= TT) {
         const int rows = rows_of(t0);
         float4 h0[KC];
@@ -166,8 +167,8 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
         }
         if constexpr (STAGED) cp_async_wait<0>();
         __syncthreads();   // this tile has arrived; the last tile's readers are done
-        if (PHASE == kMain) rB.store(sm.B);
-        rC.store(sm.C);
+        if (PHASE == kMain) rB.store(sm.B, Bm + (size_t)t0 * a.ldb, a.ldb, rows, vB);
+        rC.store(sm.C, Cm + (size_t)t0 * a.ldc, a.ldc, rows, vC);
         for (int i = tid; i < TT * PER; i += kThreads) {
             const int r = i / PER;
             const bool live = r < rows;
@@ -197,8 +198,8 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
         __syncthreads();
         if (t0 > tb) {
             fetch(t0 - TT);
-            if (PHASE == kMain) rB.load(Bm + (size_t)(t0 - TT) * a.ldb, a.ldb, rows_of(t0 - TT));
-            rC.load(Cm + (size_t)(t0 - TT) * a.ldc, a.ldc, rows_of(t0 - TT));
+            if (PHASE == kMain) rB.load(Bm + (size_t)(t0 - TT) * a.ldb, a.ldb, rows_of(t0 - TT), vB);
+            rC.load(Cm + (size_t)(t0 - TT) * a.ldc, a.ldc, rows_of(t0 - TT), vC);
         }
         auto row4 = [&](const float *m, int r, float2 *v) {
             const float4 q = *reinterpret_cast<const float4 *>(&m[r * N + l * S]);

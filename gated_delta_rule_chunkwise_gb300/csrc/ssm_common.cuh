@@ -22,47 +22,151 @@ __device__ __forceinline__ float ex2(float x)
 __device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
 __device__ __forceinline__ float2 dup(float x) { return make_float2(x, x); }
 
-// Rows t0 .. t0 + TT of DB channels to dst[TT][DB]; rows at and past `rows` and channels at
-// and past `cols` are zeros.  VEC: 16-byte copies, in flight until their group is waited for.
-template <typename T, int DB, int NT, bool VEC>
+// Copies BYTES (4, 8 or 16) from global to shared memory, or zeros where `ok` is false; in flight
+// until its group is waited for.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void *dst, const void *src, bool ok)
+{
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst), n = ok ? BYTES : 0;
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(d), "l"(src), "r"(n), "n"(BYTES)
+                     : "memory");
+}
+
+// Rows t0 .. t0 + TT of DB channels to dst, WC channels of all rows after one another:
+// dst[DB / WC][TT][WC].  Rows at and past `rows` and channels at and past `cols` are zeros.
+template <typename T, int DB, int WC, int NT, bool VEC>
 __device__ __forceinline__ void load_rows(T *dst, const T *src, long long ld, int rows, int cols)
 {
-    if constexpr (VEC) {
-        constexpr int E = 16 / sizeof(T), PER = DB / E;
-        for (int i = threadIdx.x; i < TT * PER; i += NT) {
-            const int r = i / PER, e = (i % PER) * E;
-            const bool ok = r < rows && e < cols;
-            cp_async16(dst + r * DB + e, ok ? src + r * ld + e : src, ok ? 16u : 0u);
-        }
-    } else {
-        for (int i = threadIdx.x; i < TT * DB; i += NT) {
-            const int r = i / DB, e = i % DB;
-            dst[i] = r < rows && e < cols ? src[r * ld + e] : T(0.f);
-        }
+    constexpr int E = VEC ? (WC * (int)sizeof(T) < 16 ? WC : 16 / (int)sizeof(T)) : 1, PER = DB / E;
+    for (int i = threadIdx.x; i < TT * PER; i += NT) {
+        const int r = i / PER, e = (i % PER) * E;
+        const bool ok = r < rows && e < cols;
+        T *to = dst + (e / WC * TT + r) * WC + e % WC;
+        if constexpr (VEC) cp_async<E * (int)sizeof(T)>(to, ok ? src + r * ld + e : src, ok);
+        else *to = ok ? src[r * ld + e] : T(0.f);
     }
 }
 
-// A run's B or C rows, widened, to dst[TT][N]; zeros at and past `rows`.  The rows are single
-// elements to the loads: a projection's slices start at any element.
+// A run's B or C rows, one tile ahead in registers, then widened to dst[TT][N] with zeros at
+// and past `rows`.  A thread takes K neighbouring elements.  They are kept as loaded (widening
+// them where they are loaded would wait for them there) in whole vectors or 4-byte words, as
+// the rows are aligned; a projection's slices may start at any element, and rows that are not
+// aligned to words are read where they are stored.
 template <typename T, int N, int NT>
 struct RowRegs {
-    static constexpr int K = (TT * N + NT - 1) / NT;
-    T v[K];
-    __device__ __forceinline__ void load(const T *src, long long ld, int rows)
+    static constexpr int MOST = 16 / (int)sizeof(T), PER = TT * N / NT;
+    static constexpr int K = PER < 4 ? 4 : PER < MOST ? PER : MOST;
+    static constexpr int TURNS = (TT * N + NT * K - 1) / (NT * K), WORDS = K * (int)sizeof(T) / 4;
+    enum { kSingles, kWords, kVectors };
+    uint32_t w[TURNS][WORDS];
+    static __device__ __forceinline__ int place(int k) { return (k * NT + (int)threadIdx.x) * K; }
+    __device__ __forceinline__ void load(const T *src, long long ld, int rows, int how)
     {
+        if (how == kSingles) return;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int i = k * NT + (int)threadIdx.x, r = i / N;
-            v[k] = r < rows && (TT * N % NT == 0 || i < TT * N) ? src[r * ld + i % N] : T(0.f);
+        for (int k = 0; k < TURNS; ++k) {
+            const int i = place(k), r = i / N;
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(src + r * ld + i % N);
+            if (how == kVectors && WORDS == 4) {
+                const uint4 q = r < rows ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+                w[k][0] = q.x; w[k][1] = q.y; w[k][2 % WORDS] = q.z; w[k][3 % WORDS] = q.w;
+            } else if (how == kVectors) {
+                const uint2 q = r < rows ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0, 0);
+                w[k][0] = q.x; w[k][1] = q.y;
+            } else {
+#pragma unroll
+                for (int c = 0; c < WORDS; ++c) w[k][c] = r < rows ? p[c] : 0u;
+            }
         }
     }
-    __device__ __forceinline__ void store(float *dst) const
+    __device__ __forceinline__ void store(float *dst, const T *src, long long ld, int rows, int how) const
     {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int i = k * NT + (int)threadIdx.x;
-            if (TT * N % NT == 0 || i < TT * N) dst[i] = (float)v[k];
+        for (int k = 0; k < TURNS; ++k) {
+            const int i = place(k), r = i / N;
+            if (TT * N % (NT * K) != 0 && i >= TT * N) continue;
+            float v[K];
+            if (how == kSingles) load_n<K, false>(src + r * ld + i % N, v, r < rows ? K : 0);
+            else if constexpr (sizeof(T) == 2)
+#pragma unroll
+                for (int c = 0; c < WORDS; ++c) bf16x2_widen(w[k][c], v + 2 * c);
+            else
+#pragma unroll
+                for (int c = 0; c < WORDS; ++c) v[c] = __uint_as_float(w[k][c]);
+#pragma unroll
+            for (int c = 0; c < K; c += 4)
+                *reinterpret_cast<float4 *>(dst + i + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
         }
+    }
+    static __device__ __forceinline__ int alignment(const T *p, long long ld)
+    {
+        const uintptr_t m = (uintptr_t)p | (uintptr_t)(ld * (long long)sizeof(T));
+        return m % (4 * WORDS) == 0 ? kVectors : m % 4 == 0 ? kWords : kSingles;
+    }
+};
+
+// The tile's rows of one warp's WC channels, to dst[TT][WC], by that warp; zeros outside.
+template <typename T, int WC, bool VEC>
+__device__ __forceinline__ void warp_rows(T *dst, const T *src, long long ld, int rows, int cols)
+{
+    constexpr int E = VEC ? (WC * (int)sizeof(T) < 16 ? WC : 16 / (int)sizeof(T)) : 1, PER = WC / E;
+#pragma unroll
+    for (int k = 0; k < TT * PER / 32; ++k) {
+        const int i = k * 32 + (int)(threadIdx.x & 31), r = i / PER, e = (i % PER) * E;
+        const bool ok = r < rows && e < cols;
+        if constexpr (VEC) cp_async<E * (int)sizeof(T)>(dst + i * E, ok ? src + r * ld + e : src, ok);
+        else dst[i] = ok ? src[r * ld + e] : T(0.f);
+    }
+}
+
+// A tile's B or C rows by NT threads: copied one tile ahead, then widened by the threads that
+// copied them to dst[TT][N], with zeros at and past `rows`.  A thread takes K neighbouring
+// elements, in whole vectors or 4-byte words as the rows are aligned; a projection's slices
+// may start at any element, and rows that are not aligned to words are read where they are
+// widened.
+template <typename T, int N, int NT>
+struct SharedRows {
+    static constexpr int MOST = 16 / (int)sizeof(T), PER = TT * N / NT;
+    static constexpr int K = PER < 4 ? 4 : PER < MOST ? PER : MOST;
+    static constexpr int TURNS = (TT * N + NT * K - 1) / (NT * K), BYTES = K * (int)sizeof(T);
+    enum { kSingles, kWords, kVectors };
+    static __device__ __forceinline__ void fetch(T *raw, const T *src, long long ld, int rows, int how, int tid)
+    {
+        if (how == kSingles) return;
+#pragma unroll
+        for (int k = 0; k < TURNS; ++k) {
+            const int i = (k * NT + tid) * K, r = i / N;
+            if (TT * N % (NT * K) != 0 && i >= TT * N) continue;
+            const bool ok = r < rows;
+            const T *p = ok ? src + r * ld + i % N : src;
+            if (how == kVectors) cp_async<BYTES>(raw + i, p, ok);
+            else
+#pragma unroll
+                for (int c = 0; c < K; c += 4 / (int)sizeof(T)) cp_async<4>(raw + i + c, ok ? p + c : p, ok);
+        }
+    }
+    static __device__ __forceinline__ void widen(float *dst, const T *raw, const T *src, long long ld, int rows,
+                                                 int how, int tid)
+    {
+#pragma unroll
+        for (int k = 0; k < TURNS; ++k) {
+            const int i = (k * NT + tid) * K, r = i / N;
+            if (TT * N % (NT * K) != 0 && i >= TT * N) continue;
+            float v[K];
+            if (how == kSingles) load_n<K, false>(src + r * ld + i % N, v, r < rows ? K : 0);
+            else load_n<K, true>(raw + i, v);
+#pragma unroll
+            for (int c = 0; c < K; c += 4)
+                *reinterpret_cast<float4 *>(dst + i + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+        }
+    }
+    static __device__ __forceinline__ int alignment(const T *p, long long ld)
+    {
+        const uintptr_t m = (uintptr_t)p | (uintptr_t)(ld * (long long)sizeof(T));
+        return m % BYTES == 0 ? kVectors : m % 4 == 0 ? kWords : kSingles;
     }
 };
 

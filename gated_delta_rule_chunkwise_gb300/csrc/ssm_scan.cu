@@ -21,6 +21,8 @@
 // composes what enters it, h <- e^{A sum dt} h + end, over the segments before it, and runs
 // with its outputs.  The exponentials are then taken twice, so it is done only where one wave
 // of unsplit blocks leaves the card under-occupied (ssm_segments).
+#include <type_traits>
+
 #include "ssm_common.cuh"
 
 namespace ldn {
@@ -29,24 +31,22 @@ using namespace ssm;
 
 enum { kWhole = 0, kEnds = 1, kFromEnds = 2 };
 
-template <int N> struct Shape;
-template <> struct Shape<8> { static constexpr int S = 4, KC = 1; };
-template <> struct Shape<16> { static constexpr int S = 4, KC = 1; };
-template <> struct Shape<32> { static constexpr int S = 8, KC = 1; };
-template <> struct Shape<64> { static constexpr int S = 8, KC = 1; };
+constexpr int kMain = 128, kThreads = 256;   // threads of the recurrence, of a block
 
-constexpr int kThreads = 128;
+// States of a lane, and the channels of a block.
+constexpr int lane_states(int N) { return N == 8 ? 4 : 8; }
+constexpr int block_channels(int N) { return kMain / (N / lane_states(N)); }
 
-// Channels per block.
-constexpr int block_channels(int N) { return N == 8 ? 64 : N <= 32 ? 32 : 16; }
-
-template <typename TIn, int DB, int N>
+// Tiles are kept by warp, [warp][token][channel of the warp]: only B and C are shared.
+template <typename TIn, int N>
 struct Smem {
-    TIn u[2][TT * DB], d[2][TT * DB], z[2][TT * DB];
-    float4 step[TT][DB];        // dt, dt, dt u, dt u
-    float B[TT * N], C[TT * N];
-    float y[TT][DB + 8];        // +8: the four token rows a warp stores differ in banks
-    float bias[DB], skip[DB];
+    static constexpr int WC = 32 / (N / lane_states(N)), WT = TT * WC;   // channels, elements of a warp
+    static constexpr int ROW = WC + 2;   // a row of step: two pairs more, so that rows differ in banks
+    TIn u[3][kMain / 32][WT], z[3][kMain / 32][WT], d[kMain / 32][WT];
+    TIn rawB[TT * N], rawC[TT * N];
+    // two rows more than a tile: the last tokens' loads run ahead into them, and go unused
+    float B[2][(TT + 2) * N], C[2][(TT + 2) * N];
+    float2 step[2][kMain / 32][(TT + 2) * ROW];   // dt, dt u; then a row's first WC floats the sums C h
 };
 
 struct Segs {
@@ -56,192 +56,237 @@ struct Segs {
 };
 
 template <typename TIn, int N, bool VEC, int PHASE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
 {
-    constexpr int S = Shape<N>::S, L = N / S, KC = Shape<N>::KC, SL = kThreads / L, DB = SL * KC;
-    static_assert(DB == block_channels(N), "host and device agree on a block's channels");
+    constexpr int S = lane_states(N), L = N / S, DB = block_channels(N);
+    constexpr int TG = 2 * L;   // tokens of a group: two for every lane of a channel
+    static_assert(TT % TG == 0, "whole groups");
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    Smem<TIn, DB, N> &sm = *reinterpret_cast<Smem<TIn, DB, N> *>(smem_raw);
+    using Sm = Smem<TIn, N>;
+    constexpr int WC = Sm::WC, ROW = Sm::ROW;
+    Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
     const int Dg = a.D / a.G;
     const unsigned cblocks = (unsigned)gblocks * a.G;
     const unsigned cb = blockIdx.x % cblocks, bs = blockIdx.x / cblocks;
     const int seg = (int)(bs % sg.n), b = (int)(bs / sg.n);
     const int grp = (int)(cb / gblocks), cg = (int)(cb % gblocks) * DB;
     const int c0 = grp * Dg + cg, cols = min(DB, Dg - cg);
-    const int tid = threadIdx.x, lane = tid & 31, l = tid % L, slot = tid / L;
+    const bool helper = threadIdx.x >= kMain;
+    const int tid = threadIdx.x % kMain, lane = tid & 31, warp = tid >> 5;
     const int len = seq_len(a.lens, b, a.T);
-    const int tb = seg * sg.len, te = min(tb + sg.len, a.T);
-    const size_t row0 = (size_t)b * a.T;
-    const TIn *u = (const TIn *)a.u + row0 * a.ldu + c0;
-    const TIn *dl = (const TIn *)a.delta + row0 * a.ldd + c0;
-    const TIn *z = a.z && PHASE != kEnds ? (const TIn *)a.z + row0 * a.ldz + c0 : nullptr;
-    const TIn *Bm = (const TIn *)a.Bm + row0 * a.ldb + (size_t)grp * N;
-    const TIn *Cm = (const TIn *)a.Cm + row0 * a.ldc + (size_t)grp * N;
+    const int tb = seg * sg.len, te = min(tb + sg.len, a.T), tiles = (te - tb + TT - 1) / TT;
+    const size_t row0 = (size_t)b * a.T + tb;   // the segment's first row
+    auto rows_of = [&](int it) { return min(max(min(len, te) - tb - it * TT, 0), TT); };
 
-    for (int i = tid; i < DB; i += kThreads) {
-        sm.bias[i] = a.bias && i < cols ? a.bias[c0 + i] : 0.f;
-        sm.skip[i] = a.Dskip && i < cols ? a.Dskip[c0 + i] : 0.f;
-    }
-    float2 A2[KC][S / 2], h[KC][S / 2];
-    float sumdt[KC];
-#pragma unroll
-    for (int k = 0; k < KC; ++k) {
-        const int ch = slot + k * SL;
-        const bool on = ch < cols;
-        const size_t at = (size_t)(c0 + ch) * N + l * S;
-        sumdt[k] = 0.f;
-#pragma unroll
-        for (int s = 0; s < S / 2; ++s) {
-            A2[k][s] = on ? make_float2(a.A[at + 2 * s] * kLog2e, a.A[at + 2 * s + 1] * kLog2e) : dup(0.f);
-            h[k][s] = dup(0.f);
-            if (PHASE != kEnds && on && a.h0) {
-                const float *p = a.h0 + (size_t)b * a.D * N + at + 2 * s;
-                h[k][s] = make_float2(p[0], p[1]);
-            }
-        }
-        if constexpr (PHASE == kFromEnds) {
-            if (on)
-                for (int j = 0; j < seg; ++j) {
-                    const size_t e = ((size_t)b * sg.n + j) * a.D + c0 + ch;
-                    const float sd = sg.sums[e];
-                    const float *p = sg.ends + e * N + l * S;
-#pragma unroll
-                    for (int s = 0; s < S / 2; ++s)
-                        h[k][s] = __ffma2_rn(ex2(__fmul2_rn(A2[k][s], dup(sd))), h[k][s],
-                                             make_float2(p[2 * s], p[2 * s + 1]));
-                }
-        }
-    }
+    if (helper) {
+        // Copies, the elementwise work before the recurrence (prepare: dt, dt u) and after it
+        // (finish: D u, the gate, the stores) for the channels of one recurrence warp, a tile
+        // ahead of it and a tile behind it.  Vectors of PV and FV channels of a row; a lane's
+        // channels stay the same.
+        constexpr int PV = 4, FV = WC < 8 ? WC : 8, PR = WC / PV, FR = WC / FV;
+        const int w0 = warp * WC, wcols = cols - w0;   // the warp's channels
+        const int pch = (lane % PR) * PV, fch = (lane % FR) * FV;
+        const TIn *u = (const TIn *)a.u + row0 * a.ldu + c0 + w0;
+        const TIn *dl = (const TIn *)a.delta + row0 * a.ldd + c0 + w0;
+        const bool gated = a.z && PHASE != kEnds;
+        const TIn *z = gated ? (const TIn *)a.z + row0 * a.ldz + c0 + w0 : nullptr;
+        const TIn *Bm = (const TIn *)a.Bm + row0 * a.ldb + (size_t)grp * N;
+        const TIn *Cm = (const TIn *)a.Cm + row0 * a.ldc + (size_t)grp * N;
+        using Rows = SharedRows<TIn, N, kMain>;
+        const int vB = Rows::alignment(Bm, a.ldb), vC = Rows::alignment(Cm, a.ldc);
+        float2 bias[PV / 2], skip[FV / 2];
+        load_n<PV, false>(a.bias + c0 + w0 + pch, reinterpret_cast<float *>(bias), a.bias ? wcols - pch : 0);
+        load_n<FV, false>(a.Dskip + c0 + w0 + fch, reinterpret_cast<float *>(skip), a.Dskip ? wcols - fch : 0);
 
-    auto rows_of = [&](int t0) { return min(max(min(len, te) - t0, 0), TT); };
-    auto fetch = [&](int t0, int st) {
-        const int rows = rows_of(t0);
-        load_rows<TIn, DB, kThreads, VEC>(sm.u[st], u + (size_t)t0 * a.ldu, a.ldu, rows, cols);
-        load_rows<TIn, DB, kThreads, VEC>(sm.d[st], dl + (size_t)t0 * a.ldd, a.ldd, rows, cols);
-        if (z) load_rows<TIn, DB, kThreads, VEC>(sm.z[st], z + (size_t)t0 * a.ldz, a.ldz, rows, cols);
-        cp_async_commit();
-    };
-    RowRegs<TIn, N, kThreads> rB, rC;
-    if (tb < te) {
-        fetch(tb, 0);
-        rB.load(Bm + (size_t)tb * a.ldb, a.ldb, rows_of(tb));
-        if (PHASE != kEnds) rC.load(Cm + (size_t)tb * a.ldc, a.ldc, rows_of(tb));
-    }
-    int st = 0;
-    for (int t0 = tb; t0 < te; t0 += TT, st ^= 1) {
-        const int rows = rows_of(t0);
-        cp_async_wait<0>();
-        __syncthreads();   // this tile has arrived; the last tile's readers are done
-        rB.store(sm.B);
-        if (PHASE != kEnds) rC.store(sm.C);
-        if (t0 + TT < te) {
-            fetch(t0 + TT, st ^ 1);
-            rB.load(Bm + (size_t)(t0 + TT) * a.ldb, a.ldb, rows_of(t0 + TT));
-            if (PHASE != kEnds) rC.load(Cm + (size_t)(t0 + TT) * a.ldc, a.ldc, rows_of(t0 + TT));
-        }
-        // (dt, dt u) of every channel and token; a row past the end steps by zero: a = 1, no input
-        for (int i = tid; i < TT * DB; i += kThreads) {
-            const int r = i / DB, c = i % DB;
-            float dt = (float)sm.d[st][i] + sm.bias[c];
-            if (a.softplus) dt = softplus_accurate(dt);
-            if (r >= rows) dt = 0.f;
-            const float du = r < rows ? dt * (float)sm.u[st][i] : 0.f;
-            sm.step[r][c] = make_float4(dt, dt, du, du);
-        }
-        if (PHASE != kEnds && a.states) {   // the state entering this tile
-            const size_t ck = (size_t)b * ((a.T + TT - 1) / TT) + t0 / TT;
+        auto fetch = [&](int it) {
+            const int rows = rows_of(it), t = it * TT;
+            warp_rows<TIn, WC, VEC>(sm.u[it % 3][warp], u + (size_t)t * a.ldu, a.ldu, rows, wcols);
+            warp_rows<TIn, WC, VEC>(sm.d[warp], dl + (size_t)t * a.ldd, a.ldd, rows, wcols);
+            if (gated) warp_rows<TIn, WC, VEC>(sm.z[it % 3][warp], z + (size_t)t * a.ldz, a.ldz, rows, wcols);
+            Rows::fetch(sm.rawB, Bm + (size_t)t * a.ldb, a.ldb, rows, vB, tid);
+            if (PHASE != kEnds) Rows::fetch(sm.rawC, Cm + (size_t)t * a.ldc, a.ldc, rows, vC, tid);
+            cp_async_commit();
+        };
+        auto prepare = [&](int it, auto soft) {
+            const int rows = rows_of(it);
+            const TIn *td = sm.d[warp], *tu = sm.u[it % 3][warp];
 #pragma unroll
-            for (int k = 0; k < KC; ++k) {
-                const int ch = slot + k * SL;
-                if (ch < cols) {
-                    float4 *p = reinterpret_cast<float4 *>(a.states + (ck * a.D + c0 + ch) * N + l * S);
+            for (int k = 0; k < TT * PR / 32; ++k) {
+                const int i = k * 32 + lane, r = i / PR;
+                float2 v[PV / 2], w[PV / 2];
+                load_n<PV, true>(td + i * PV, reinterpret_cast<float *>(v));
+                load_n<PV, true>(tu + i * PV, reinterpret_cast<float *>(w));
+                float4 *o = reinterpret_cast<float4 *>(sm.step[it & 1][warp] + r * ROW + pch);
 #pragma unroll
-                    for (int s = 0; s < S / 4; ++s)
-                        p[s] = make_float4(h[k][2 * s].x, h[k][2 * s].y, h[k][2 * s + 1].x, h[k][2 * s + 1].y);
+                for (int c = 0; c < PV / 2; ++c) {
+                    float2 dt = __fadd2_rn(v[c], bias[c]);
+                    if (soft) dt = softplus_accurate(dt);
+                    if (r >= rows) dt = dup(0.f);   // a row past the end steps by zero: a = 1, no input
+                    const float2 du = __fmul2_rn(dt, w[c]);
+                    o[c] = make_float4(dt.x, du.x, dt.y, du.y);
                 }
             }
+        };
+        auto ready = [&](int it) {   // tile `it` for the recurrence
+            cp_async_wait<0>();
+            const int rows = rows_of(it), t = it * TT;
+            Rows::widen(sm.B[it & 1], sm.rawB, Bm + (size_t)t * a.ldb, a.ldb, rows, vB, tid);
+            if (PHASE != kEnds) Rows::widen(sm.C[it & 1], sm.rawC, Cm + (size_t)t * a.ldc, a.ldc, rows, vC, tid);
+            __syncwarp();
+            if (a.softplus) prepare(it, std::true_type{});
+            else prepare(it, std::false_type{});
+            __syncwarp();
+        };
+        auto finish = [&](int it, auto gate) {
+            const int rows = rows_of(it), live = min(te - tb - it * TT, TT);
+            const TIn *tu = sm.u[it % 3][warp], *tz = sm.z[it % 3][warp];
+            const float *sums = reinterpret_cast<const float *>(sm.step[it & 1][warp]);
+            TIn *y = (TIn *)a.y + (row0 + it * TT) * a.D + c0 + w0 + fch;
+#pragma unroll
+            for (int k = 0; k < TT * FR / 32; ++k) {
+                const int i = k * 32 + lane, r = i / FR;
+                float2 uu[FV / 2], zz[FV / 2], v[FV / 2];
+                load_n<FV, true>(tu + i * FV, reinterpret_cast<float *>(uu));
+                if (gate) load_n<FV, true>(tz + i * FV, reinterpret_cast<float *>(zz));
+                load_n<FV, true>(sums + r * 2 * ROW + fch, reinterpret_cast<float *>(v));
+#pragma unroll
+                for (int c = 0; c < FV / 2; ++c) {
+                    v[c] = __ffma2_rn(skip[c], uu[c], v[c]);
+                    if (gate) v[c] = __fmul2_rn(v[c], silu_fast(zz[c]));
+                    if (r >= rows) v[c] = dup(0.f);   // a row past the sequence's end
+                }
+                if (r < live) store_n<FV, VEC>(y + (size_t)r * a.D, reinterpret_cast<float *>(v), wcols - fch);
+            }
+            __syncwarp();
+        };
+        auto finished = [&](int it) {
+            if constexpr (PHASE != kEnds) {
+                if (gated) finish(it, std::true_type{});
+                else finish(it, std::false_type{});
+            }
+        };
+        if (tiles > 0) {
+            fetch(0);
+            ready(0);
+            if (tiles > 1) fetch(1);
         }
         __syncthreads();
-#pragma unroll 1
-        for (int tq = 0; tq < TT; tq += 4) {
-            float yv[4 * KC];
+        for (int it = 0; it < tiles; ++it) {
+            if (it > 0) finished(it - 1);
+            if (it + 1 < tiles) ready(it + 1);
+            if (it + 2 < tiles) fetch(it + 2);
+            __syncthreads();
+        }
+        if (tiles > 0) finished(tiles - 1);
+        return;
+    }
+
+    // The recurrence: lane l of a channel's L has states l S .. l S + S - 1.
+    const int l = tid % L, slot = tid / L;
+    const bool on = slot < cols;
+    const size_t mine = (size_t)(c0 + slot) * N + l * S;
+    float A2[S], h[S], sumdt = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = tq + j;
-                float2 Bv[S / 2], Cv[S / 2];
+    for (int s = 0; s < S; ++s) {
+        A2[s] = on ? a.A[mine + s] * kLog2e : 0.f;
+        h[s] = PHASE != kEnds && on && a.h0 ? a.h0[(size_t)b * a.D * N + mine + s] : 0.f;
+    }
+    if (PHASE == kFromEnds && on)
+        for (int j = 0; j < seg; ++j) {
+            const size_t e = ((size_t)b * sg.n + j) * a.D + c0 + slot;
+            const float sd = sg.sums[e];
+            const float *p = sg.ends + e * N + l * S;
 #pragma unroll
-                for (int s = 0; s < S / 4; ++s) {
-                    const float4 q = *reinterpret_cast<const float4 *>(&sm.B[r * N + l * S + 4 * s]);
-                    Bv[2 * s] = make_float2(q.x, q.y);
-                    Bv[2 * s + 1] = make_float2(q.z, q.w);
+            for (int s = 0; s < S; ++s) h[s] = fmaf(ex2(A2[s] * sd), h[s], p[s]);
+        }
+    auto store_state = [&](float *p) {
+#pragma unroll
+        for (int s = 0; s < S; s += 4)
+            *reinterpret_cast<float4 *>(p + s) = make_float4(h[s], h[s + 1], h[s + 2], h[s + 3]);
+    };
+    __syncthreads();
+    for (int it = 0; it < tiles; ++it) {
+        if (PHASE != kEnds && a.states && on)   // the state entering this tile
+            store_state(a.states + ((size_t)b * ((a.T + TT - 1) / TT) + tb / TT + it) * a.D * N + mine);
+        // Operands are loaded two tokens ahead and decays formed one token ahead, in the
+        // source: a warp that loads and uses in one token waits for both latencies every token
+        // (17 against 9 cycles an update with one warp a scheduler).
+        float2 *step = sm.step[it & 1][warp];
+        const float2 *sp = step + slot % WC;
+        const float *Br = sm.B[it & 1] + l * S, *Cr = sm.C[it & 1] + l * S;
+        float2 q[3];
+        float bv[3][S], cv[3][S], e[2][S];
+        auto load = [&](int t, int i) {
+            q[i] = sp[t * ROW];
+#pragma unroll
+            for (int s = 0; s < S; s += 4) {
+                *reinterpret_cast<float4 *>(&bv[i][s]) = *reinterpret_cast<const float4 *>(Br + t * N + s);
+                if (PHASE != kEnds)
+                    *reinterpret_cast<float4 *>(&cv[i][s]) = *reinterpret_cast<const float4 *>(Cr + t * N + s);
+            }
+        };
+        auto decay = [&](int i, float *d) {
+#pragma unroll
+            for (int s = 0; s < S; s += 2) {
+                const float2 x = ex2(__fmul2_rn(make_float2(A2[s], A2[s + 1]), dup(q[i].x)));
+                d[s] = x.x;
+                d[s + 1] = x.y;
+            }
+        };
+        load(0, 0);
+        load(1, 1);
+        decay(0, e[0]);
+        constexpr int UG = TG >= 4 ? 1 : 4 / TG;   // groups in one body: at least four tokens
+#pragma unroll UG
+        for (int tq = 0; tq < TT; tq += TG) {
+            float yv[TG];
+#pragma unroll
+            for (int j = 0; j < TG; ++j) {
+                load(tq + j + 2, 2);
+                decay(1, e[1]);
+                if (PHASE == kEnds) sumdt += q[0].x;
+                float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+                for (int s = 0; s < S; s += 2) {
+                    const float2 in = __fmul2_rn(make_float2(bv[0][s], bv[0][s + 1]), dup(q[0].y));
+                    const float2 x = __ffma2_rn(make_float2(e[0][s], e[0][s + 1]), make_float2(h[s], h[s + 1]), in);
+                    h[s] = x.x;
+                    h[s + 1] = x.y;
                     if (PHASE != kEnds) {
-                        const float4 w = *reinterpret_cast<const float4 *>(&sm.C[r * N + l * S + 4 * s]);
-                        Cv[2 * s] = make_float2(w.x, w.y);
-                        Cv[2 * s + 1] = make_float2(w.z, w.w);
+                        y0 = fmaf(cv[0][s], x.x, y0);
+                        y1 = fmaf(cv[0][s + 1], x.y, y1);
                     }
                 }
+                yv[j] = y0 + y1;
+                q[0] = q[1];
+                q[1] = q[2];
 #pragma unroll
-                for (int k = 0; k < KC; ++k) {
-                    const float4 q = sm.step[r][slot + k * SL];
-                    const float2 dt = make_float2(q.x, q.y), du = make_float2(q.z, q.w);
-                    if (PHASE == kEnds) sumdt[k] += q.x;
-                    float2 acc = dup(0.f);
-#pragma unroll
-                    for (int s = 0; s < S / 2; ++s) {
-                        const float2 e = ex2(__fmul2_rn(A2[k][s], dt));
-                        h[k][s] = __ffma2_rn(e, h[k][s], __fmul2_rn(du, Bv[s]));
-                        if (PHASE != kEnds) acc = s ? __ffma2_rn(Cv[s], h[k][s], acc) : __fmul2_rn(Cv[s], h[k][s]);
-                    }
-                    yv[j * KC + k] = acc.x + acc.y;
+                for (int s = 0; s < S; ++s) {
+                    e[0][s] = e[1][s];
+                    bv[0][s] = bv[1][s]; bv[1][s] = bv[2][s];
+                    cv[0][s] = cv[1][s]; cv[1][s] = cv[2][s];
                 }
             }
             if constexpr (PHASE != kEnds) {
-                constexpr int V = 4 * KC;
-                reduce_halving<V, L / 2, 1>(yv, lane);
-                constexpr int HELD = V >= L ? V / L : 1, DUP = V >= L ? 1 : L / V;
-                if (l % DUP == 0)
-#pragma unroll
-                    for (int i = 0; i < HELD; ++i) {
-                        const int idx = (l / DUP) * HELD + i;
-                        sm.y[tq + idx / KC][slot + (idx % KC) * SL] = yv[i];
-                    }
+                // a lane gets the sums of two tokens, and writes them over steps that every lane
+                // of the warp has read
+                reduce_halving<TG, L / 2, 1>(yv, lane);
+                __syncwarp();
+                float *o = reinterpret_cast<float *>(step + (tq + 2 * l) * ROW) + slot % WC;
+                o[0] = yv[0];
+                o[2 * ROW] = yv[1];
             }
         }
-        if constexpr (PHASE != kEnds) {
-            __syncthreads();
-            constexpr int E = VEC ? 16 / (int)sizeof(TIn) : 1, PER = DB / E;
-            const int live = min(te - t0, TT);
-            TIn *y = (TIn *)a.y + (row0 + t0) * a.D + c0;
-            for (int i = tid; i < TT * PER; i += kThreads) {
-                const int r = i / PER, e = (i % PER) * E;
-                if (r >= live || e >= cols) continue;
-                float v[E], uu[E], zz[E];
-                load_n<E, VEC>(&sm.u[st][r * DB + e], uu);
-                if (z) load_n<E, VEC>(&sm.z[st][r * DB + e], zz);
-#pragma unroll
-                for (int k = 0; k < E; ++k) {
-                    v[k] = fmaf(sm.skip[e + k], uu[k], sm.y[r][e + k]);
-                    if (z) v[k] *= zz[k] * sigmoid_fast(zz[k]);
-                    if (r >= rows) v[k] = 0.f;   // a row past the sequence's end
-                }
-                store_n<E, VEC>(y + (size_t)r * a.D + e, v);
-            }
-        }
+        __syncthreads();
     }
-
-    if (PHASE == kEnds || (seg == sg.n - 1 && a.h_final)) {
-#pragma unroll
-        for (int k = 0; k < KC; ++k) {
-            const int ch = slot + k * SL;
-            if (ch >= cols) continue;
-            const size_t e = (PHASE == kEnds ? (size_t)b * sg.n + seg : (size_t)b) * a.D + c0 + ch;
-            float4 *p = reinterpret_cast<float4 *>((PHASE == kEnds ? sg.ends : a.h_final) + e * N + l * S);
-#pragma unroll
-            for (int s = 0; s < S / 4; ++s)
-                p[s] = make_float4(h[k][2 * s].x, h[k][2 * s].y, h[k][2 * s + 1].x, h[k][2 * s + 1].y);
-            if (PHASE == kEnds && l == 0) sg.sums[e] = sumdt[k];
-        }
+    if (!on) return;
+    if (PHASE == kEnds) {
+        const size_t e = ((size_t)b * sg.n + seg) * a.D + c0 + slot;
+        store_state(sg.ends + e * N + l * S);
+        if (l == 0) sg.sums[e] = sumdt;
+    } else if (seg == sg.n - 1 && a.h_final) {
+        store_state(a.h_final + (size_t)b * a.D * N + mine);
     }
 }
 
@@ -317,7 +362,7 @@ template <typename TIn, int N, bool VEC, int PHASE>
 cudaError_t scan_launch(const SsmArgs &a, const Segs &sg, cudaStream_t st)
 {
     constexpr int DB = block_channels(N);
-    constexpr int bytes = (int)sizeof(Smem<TIn, DB, N>);
+    constexpr int bytes = (int)sizeof(Smem<TIn, N>);
     auto *k = ssm_scan_kernel<TIn, N, VEC, PHASE>;
     if (bytes > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
