@@ -96,8 +96,26 @@ __device__ __forceinline__ void store_n(__nv_bfloat16 *p, const float *v, int va
     }
 }
 
-// sigma(x) = 1 / (1 + e^-x); the quotient is 0 where e^-x overflows.
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// 2^x and 1 / x to about one step, results below the normal numbers as zero.
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+__device__ __forceinline__ float2 rcp(float2 x) { return make_float2(rcp(x.x), rcp(x.y)); }
+__device__ __forceinline__ float2 dup(float x) { return make_float2(x, x); }
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// sigma(x) = 1 / (1 + e^-x): 0 where e^-x overflows.
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
 
 // softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1], of two values in packed
 // arithmetic.  log(1 + e) = 2 atanh(s) with s = e / (2 + e) <= 1/3; 2 atanh(s) / s is taken as
@@ -108,21 +126,18 @@ __device__ __forceinline__ float2 softplus_accurate(float2 x)
 {
     // past 100 e is zero in fp32
     const float2 ax = make_float2(fminf(fabsf(x.x), 100.f), fminf(fabsf(x.y), 100.f));
-    const float2 l2 = make_float2(-1.44269504f, -1.44269504f);
+    const float2 l2 = dup(-kLog2e);
     const float2 t = __fmul2_rn(ax, l2);
     const float2 lost = __ffma2_rn(ax, l2, make_float2(-t.x, -t.y));
-    float2 e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-    e = __ffma2_rn(__fmul2_rn(e, lost), make_float2(0.69314718f, 0.69314718f), e);
-    const float2 d = __fadd2_rn(e, make_float2(2.f, 2.f));
-    const float2 s = make_float2(__fdividef(e.x, d.x), __fdividef(e.y, d.y));
+    float2 e = ex2(t);
+    e = __ffma2_rn(__fmul2_rn(e, lost), dup(kLn2), e);
+    const float2 s = __fmul2_rn(e, rcp(__fadd2_rn(e, dup(2.f))));
     const float2 q = __fmul2_rn(s, s);
-    float2 p = make_float2(0.281577796f, 0.281577796f);
-    p = __ffma2_rn(p, q, make_float2(0.279651582f, 0.279651582f));
-    p = __ffma2_rn(p, q, make_float2(0.400245965f, 0.400245965f));
-    p = __ffma2_rn(p, q, make_float2(0.666663229f, 0.666663229f));
-    p = __ffma2_rn(p, q, make_float2(2.f, 2.f));
+    float2 p = dup(0.281577796f);
+    p = __ffma2_rn(p, q, dup(0.279651582f));
+    p = __ffma2_rn(p, q, dup(0.400245965f));
+    p = __ffma2_rn(p, q, dup(0.666663229f));
+    p = __ffma2_rn(p, q, dup(2.f));
     float2 m;   // max(x, 0), where a NaN stays one
     asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m.x) : "f"(x.x));
     asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m.y) : "f"(x.y));
@@ -133,8 +148,7 @@ __device__ __forceinline__ float softplus_accurate(float x) { return softplus_ac
 // x sigma(x) of two values.
 __device__ __forceinline__ float2 silu_fast(float2 x)
 {
-    const float2 d = __fadd2_rn(make_float2(__expf(-x.x), __expf(-x.y)), make_float2(1.f, 1.f));
-    return __fmul2_rn(x, make_float2(__fdividef(1.f, d.x), __fdividef(1.f, d.y)));
+    return __fmul2_rn(x, rcp(__fadd2_rn(ex2(__fmul2_rn(x, dup(-kLog2e))), dup(1.f))));
 }
 
 // Sums across the lanes of mask M, M/2, ..., down to LO, of V values a lane, halving the

@@ -11,17 +11,6 @@ using sm100::cp_async_commit;
 using sm100::cp_async_wait;
 
 constexpr int TT = kSsmChunk;   // tokens of a tile
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
-__device__ __forceinline__ float2 dup(float x) { return make_float2(x, x); }
-
 // Copies BYTES (4, 8 or 16) from global to shared memory, or zeros where `ok` is false; in flight
 // until its group is waited for.
 template <int BYTES>
@@ -109,14 +98,15 @@ struct RowRegs {
 };
 
 // The tile's rows of one warp's WC channels, to dst[TT][WC], by that warp; zeros outside.
-template <typename T, int WC, bool VEC>
+// FULL: nothing is outside.
+template <typename T, int WC, bool VEC, bool FULL>
 __device__ __forceinline__ void warp_rows(T *dst, const T *src, long long ld, int rows, int cols)
 {
     constexpr int E = VEC ? (WC * (int)sizeof(T) < 16 ? WC : 16 / (int)sizeof(T)) : 1, PER = WC / E;
 #pragma unroll
     for (int k = 0; k < TT * PER / 32; ++k) {
         const int i = k * 32 + (int)(threadIdx.x & 31), r = i / PER, e = (i % PER) * E;
-        const bool ok = r < rows && e < cols;
+        const bool ok = FULL || (r < rows && e < cols);
         if constexpr (VEC) cp_async<E * (int)sizeof(T)>(dst + i * E, ok ? src + r * ld + e : src, ok);
         else dst[i] = ok ? src[r * ld + e] : T(0.f);
     }

@@ -99,16 +99,24 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
         load_n<PV, false>(a.bias + c0 + w0 + pch, reinterpret_cast<float *>(bias), a.bias ? wcols - pch : 0);
         load_n<FV, false>(a.Dskip + c0 + w0 + fch, reinterpret_cast<float *>(skip), a.Dskip ? wcols - fch : 0);
 
+        // A tile whose rows and channels are all inside takes bodies without the tests.
+        auto whole = [&](int it) { return rows_of(it) == TT && wcols >= WC; };
+        auto copy = [&](int it, auto full) {
+            constexpr bool F = decltype(full)::value;
+            const int rows = rows_of(it), t = it * TT;
+            warp_rows<TIn, WC, VEC, F>(sm.u[it % 3][warp], u + (size_t)t * a.ldu, a.ldu, rows, wcols);
+            warp_rows<TIn, WC, VEC, F>(sm.d[warp], dl + (size_t)t * a.ldd, a.ldd, rows, wcols);
+            if (gated) warp_rows<TIn, WC, VEC, F>(sm.z[it % 3][warp], z + (size_t)t * a.ldz, a.ldz, rows, wcols);
+        };
         auto fetch = [&](int it) {
             const int rows = rows_of(it), t = it * TT;
-            warp_rows<TIn, WC, VEC>(sm.u[it % 3][warp], u + (size_t)t * a.ldu, a.ldu, rows, wcols);
-            warp_rows<TIn, WC, VEC>(sm.d[warp], dl + (size_t)t * a.ldd, a.ldd, rows, wcols);
-            if (gated) warp_rows<TIn, WC, VEC>(sm.z[it % 3][warp], z + (size_t)t * a.ldz, a.ldz, rows, wcols);
+            if (whole(it)) copy(it, std::true_type{});
+            else copy(it, std::false_type{});
             Rows::fetch(sm.rawB, Bm + (size_t)t * a.ldb, a.ldb, rows, vB, tid);
             if (PHASE != kEnds) Rows::fetch(sm.rawC, Cm + (size_t)t * a.ldc, a.ldc, rows, vC, tid);
             cp_async_commit();
         };
-        auto prepare = [&](int it, auto soft) {
+        auto prepare = [&](int it, auto soft, auto full) {
             const int rows = rows_of(it);
             const TIn *td = sm.d[warp], *tu = sm.u[it % 3][warp];
 #pragma unroll
@@ -122,7 +130,7 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
                 for (int c = 0; c < PV / 2; ++c) {
                     float2 dt = __fadd2_rn(v[c], bias[c]);
                     if (soft) dt = softplus_accurate(dt);
-                    if (r >= rows) dt = dup(0.f);   // a row past the end steps by zero: a = 1, no input
+                    if (!full && r >= rows) dt = dup(0.f);   // a row past the end steps by zero: a = 1, no input
                     const float2 du = __fmul2_rn(dt, w[c]);
                     o[c] = make_float4(dt.x, du.x, dt.y, du.y);
                 }
@@ -134,11 +142,12 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
             Rows::widen(sm.B[it & 1], sm.rawB, Bm + (size_t)t * a.ldb, a.ldb, rows, vB, tid);
             if (PHASE != kEnds) Rows::widen(sm.C[it & 1], sm.rawC, Cm + (size_t)t * a.ldc, a.ldc, rows, vC, tid);
             __syncwarp();
-            if (a.softplus) prepare(it, std::true_type{});
-            else prepare(it, std::false_type{});
+            if (!a.softplus) prepare(it, std::false_type{}, std::false_type{});
+            else if (whole(it)) prepare(it, std::true_type{}, std::true_type{});
+            else prepare(it, std::true_type{}, std::false_type{});
             __syncwarp();
         };
-        auto finish = [&](int it, auto gate) {
+        auto finish = [&](int it, auto gate, auto full) {
             const int rows = rows_of(it), live = min(te - tb - it * TT, TT);
             const TIn *tu = sm.u[it % 3][warp], *tz = sm.z[it % 3][warp];
             const float *sums = reinterpret_cast<const float *>(sm.step[it & 1][warp]);
@@ -154,16 +163,18 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
                 for (int c = 0; c < FV / 2; ++c) {
                     v[c] = __ffma2_rn(skip[c], uu[c], v[c]);
                     if (gate) v[c] = __fmul2_rn(v[c], silu_fast(zz[c]));
-                    if (r >= rows) v[c] = dup(0.f);   // a row past the sequence's end
+                    if (!full && r >= rows) v[c] = dup(0.f);   // a row past the sequence's end
                 }
-                if (r < live) store_n<FV, VEC>(y + (size_t)r * a.D, reinterpret_cast<float *>(v), wcols - fch);
+                if (full || r < live)
+                    store_n<FV, VEC>(y + (size_t)r * a.D, reinterpret_cast<float *>(v), full ? FV : wcols - fch);
             }
             __syncwarp();
         };
         auto finished = [&](int it) {
             if constexpr (PHASE != kEnds) {
-                if (gated) finish(it, std::true_type{});
-                else finish(it, std::false_type{});
+                if (!gated) finish(it, std::false_type{}, std::false_type{});
+                else if (whole(it)) finish(it, std::true_type{}, std::true_type{});
+                else finish(it, std::true_type{}, std::false_type{});
             }
         };
         if (tiles > 0) {
@@ -340,14 +351,14 @@ long long channel_blocks(int B, int D, int N, int G)
 
 struct Plan { int n, len; };
 
-// Segments per sequence.
+// Segments per sequence: as many as fill the SMs at two blocks each, from four on (a split
+// scan costs 1.6 times the work of a whole one, which up to one block an SM runs 1.5 times as
+// fast a token as two), of at least four tiles.
 Plan ssm_plan(int B, int T, int D, int N, int G)
 {
     const long long blocks = channel_blocks(B, D, N, G);
-    const long long want = kSms * 4;
-    int n = 1;
-    if (blocks * 2 <= kSms * 3) n = (int)std::min<long long>((want + blocks - 1) / blocks, std::min(T / 128, 64));
-    n = std::max(n, 1);
+    int n = (int)std::min<long long>(kSms * 2 / blocks, T / (4 * TT));
+    if (n < 4) n = 1;
     const int len = (int)((((long long)T + n - 1) / n + TT - 1) / TT) * TT;
     if (len <= 0) return {1, TT};
     return {std::max(1, (T + len - 1) / len), len};
