@@ -152,21 +152,30 @@ __device__ __forceinline__ float2 silu_fast(float2 x)
 }
 
 // Sums across the lanes of mask M, M/2, ..., down to LO, of V values a lane, halving the
-// values as it goes: a lane whose bit is set in the current mask keeps the upper half.  After
-// it a lane holds max(1, V / steps') sums; where lanes outnumber values the rest of the steps
-// add whole values, so several lanes hold the same sum.
+// values as it goes: a lane whose bit is set in the current mask keeps the upper half.  Where
+// lanes outnumber values the rest of the steps add whole values, so several lanes hold the
+// same sum.
 template <int V, int M, int LO>
 __device__ __forceinline__ void reduce_halving(float *v, int lane)
 {
     if constexpr (M >= LO) {
-        if constexpr (V > 1) {
+        if constexpr (V > 2) {
             const bool up = (lane & M) != 0;
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
-                const float keep = up ? v[V / 2 + i] : v[i], send = up ? v[i] : v[V / 2 + i];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, M);
+            for (int i = 0; i < V / 2; i += 2) {
+                const float2 keep = make_float2(up ? v[V / 2 + i] : v[i], up ? v[V / 2 + i + 1] : v[i + 1]);
+                const float2 got = make_float2(__shfl_xor_sync(0xffffffffu, up ? v[i] : v[V / 2 + i], M),
+                                               __shfl_xor_sync(0xffffffffu, up ? v[i + 1] : v[V / 2 + i + 1], M));
+                const float2 t = __fadd2_rn(keep, got);
+                v[i] = t.x;
+                v[i + 1] = t.y;
             }
             reduce_halving<V / 2, M / 2, LO>(v, lane);
+        } else if constexpr (V == 2) {
+            const bool up = (lane & M) != 0;
+            const float keep = up ? v[1] : v[0], send = up ? v[0] : v[1];
+            v[0] = keep + __shfl_xor_sync(0xffffffffu, send, M);
+            reduce_halving<1, M / 2, LO>(v, lane);
         } else {
             v[0] += __shfl_xor_sync(0xffffffffu, v[0], M);
             reduce_halving<1, M / 2, LO>(v, lane);

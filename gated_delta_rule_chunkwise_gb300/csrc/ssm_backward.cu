@@ -10,27 +10,37 @@
 // The forward saved the state entering every 32 tokens; a block takes those tiles in reverse
 // order.  Inside a tile it first runs the states forward, keeping every fourth in shared
 // memory, then takes four tokens at a time in reverse: their states and decays are formed
-// again into registers and the gradients follow.  A lane owns KC channels x 4 states, so the
+// again into registers and the gradients follow.  A lane owns two channels x 4 states, so the
 // channel sums of dB and dC start in registers; the rest goes by halving exchanges, over the
 // lanes of a channel for q, sum A w and sum C h (four tokens together), over the channels of a
 // warp for dB and dC.  About 16 fp32 operations and two exponentials for every state: the
-// kernel is bound by the fp32 pipe.
+// kernel is bound by instruction issue, and two blocks an SM have to hide its latencies.
+//
+// As in the forward a block is four warps of this recurrence and four helpers, which read the
+// rows, form dt, dt u and yb a tile ahead, and turn the sums into du, ddelta, dz and the
+// block's dB, dC a tile behind.  The recurrence needs most of the registers (states and decays
+// of four tokens), so the block's are split: 160 a thread for it, 96 for the helpers.
 //
 // Sums across blocks (dB, dC over the channel blocks of a group; dA, dD and the bias over
 // sequences and segments) go to the workspace and are added by a last launch in a fixed
 // order: no atomics, the same bits on every call.  Few channels: the tokens are cut into
 // segments; a first launch forms every segment's carry from zero (g alone, one exponential)
 // and a block composes what reaches its end from the later ones.
+#include <type_traits>
+
 #include "ssm_common.cuh"
 
 namespace ldn {
 namespace {
 using namespace ssm;
 
-constexpr int kThreads = 128, kWarps = 4, S = 4, KC = 2, SUB = 4;
+constexpr int kMain = 128, kThreads = 256, kWarps = 4, S = 4, KC = 2, SUB = 4;
+// Registers a thread: what the block is launched with, and what its halves hold after the split.
+constexpr int kRegs = 128, kRegsMain = 160, kRegsHelper = 96;
+static_assert(kRegsMain + kRegsHelper == 2 * kRegs, "the halves share what the block has");
 
-template <int N> constexpr int block_ch() { return kThreads / (N / S) * KC; }
-int block_channels(int N) { return kThreads / (N / S) * KC; }
+template <int N> constexpr int block_ch() { return kMain / (N / S) * KC; }
+int block_channels(int N) { return kMain / (N / S) * KC; }
 
 struct Plan {
     int n, len;      // segments per sequence, tokens of one (a multiple of TT)
@@ -45,63 +55,303 @@ struct Work {
     float *sums;     // [B * n][D]
 };
 
-template <typename TIn, int N>
+// Tiles are kept by warp, rows of the warp's WC channels.
+template <int N>
 struct Smem {
-    static constexpr int DB = block_ch<N>();
-    // copies of the next tile in flight (bf16 rows; fp32 rows are read where they are used)
-    __nv_bfloat16 raw[sizeof(TIn) == 2 ? 4 : 1][sizeof(TIn) == 2 ? TT * DB : 8];
-    float4 step[TT][DB];                     // dt, dt u, yb, -; then dt, q, sum C h, sum A2 w
-    float B[TT * N], C[TT * N];
-    float4 ckpt[TT / SUB][KC][kThreads];     // the state entering every SUB tokens
-    float red[kWarps][TT][2 * N];            // dB, dC summed over a warp's channels
-    float bias[DB], skip[DB];
+    static constexpr int WC = block_ch<N>() / kWarps, ROW = 2 * WC + 4;   // + 4: rows differ in banks
+    float step[2][kWarps][TT * ROW];        // dt, dt u of a channel; then dt, q
+    float yb[2][kWarps][TT * WC];           // yb; then sum C h
+    float ww[kWarps][TT * WC];              // sum A2 w
+    float B[2][TT * N], C[2][TT * N];
+    float4 ckpt[TT / SUB - 1][KC][kMain];   // the state entering every SUB tokens but the last
+    float red[kWarps][TT][2 * N];           // dB, dC summed over a warp's channels
 };
 
-// e^x parts of a channel and token
-struct Gate { float y, dy; };   // silu(z), silu'(z)
-__device__ __forceinline__ Gate gate_of(float z)
+struct Gate { float2 y, dy; };   // silu(z), silu'(z)
+__device__ __forceinline__ Gate gate_of(float2 z)
 {
-    const float s = sigmoid_fast(z);
-    return {z * s, s * fmaf(z, 1.f - s, 1.f)};
+    const float2 s = rcp(__fadd2_rn(ex2(__fmul2_rn(z, dup(-kLog2e))), dup(1.f)));
+    const float2 one_minus = __ffma2_rn(s, dup(-1.f), dup(1.f));
+    return {__fmul2_rn(z, s), __fmul2_rn(s, __ffma2_rn(z, one_minus, dup(1.f)))};
 }
 
-enum { kCarry = 0, kMain = 1 };
+template <int ID> __device__ __forceinline__ void bar_arrive()
+{
+    asm volatile("barrier.cta.arrive %0, %1;" ::"n"(ID), "n"(kThreads) : "memory");
+}
+template <int ID> __device__ __forceinline__ void bar_sync()
+{
+    asm volatile("barrier.cta.sync %0, %1;" ::"n"(ID), "n"(kThreads) : "memory");
+}
+constexpr int kTaken = 1;   // the last tile's red and ww have been read
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// Four neighbouring elements as loaded.
+template <typename T> struct Raw4;
+template <> struct Raw4<__nv_bfloat16> {
+    uint2 w;
+    __device__ __forceinline__ void widen(float2 *v) const
+    {
+        bf16x2_widen(w.x, reinterpret_cast<float *>(v));
+        bf16x2_widen(w.y, reinterpret_cast<float *>(v + 1));
+    }
+};
+template <> struct Raw4<float> {
+    float4 w;
+    __device__ __forceinline__ void widen(float2 *v) const
+    {
+        v[0] = make_float2(w.x, w.y);
+        v[1] = make_float2(w.z, w.w);
+    }
+};
+template <bool VEC, typename T>
+__device__ __forceinline__ Raw4<T> load_raw(const T *p, int valid)
+{
+    Raw4<T> q;
+    if constexpr (VEC) {
+        if (valid > 0) q.w = *reinterpret_cast<const decltype(q.w) *>(p);
+        else q.w = decltype(q.w){};
+    } else {
+        T *e = reinterpret_cast<T *>(&q.w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = i < valid ? p[i] : T(0.f);
+    }
+    return q;
+}
+
+// K neighbouring elements of a tile's B or C rows by each helper thread, widened to dst[TT][N].
+template <typename T, int N>
+__device__ __forceinline__ void rows_to_shared(float *dst, const T *src, long long ld, int rows, bool vec, int tid)
+{
+    constexpr int K = 4;
+#pragma unroll
+    for (int k = 0; k < (TT * N + kMain * K - 1) / (kMain * K); ++k) {
+        const int i = (k * kMain + tid) * K, r = i / N;
+        if (TT * N % (kMain * K) != 0 && i >= TT * N) continue;
+        float v[K];
+        const T *p = src + r * ld + i % N;
+        if (vec) load_n<K, true>(p, v, r < rows ? K : 0);
+        else load_n<K, false>(p, v, r < rows ? K : 0);
+        *reinterpret_cast<float4 *>(dst + i) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+enum { kCarry = 0, kFull = 1 };
 
 template <typename TIn, int N, bool VEC, int PHASE>
 __global__ void __launch_bounds__(kThreads, 2)
 ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
 {
-    constexpr int L = N / S, SL = kThreads / L, DB = SL * KC;
-    constexpr bool STAGED = VEC && sizeof(TIn) == 2;
+    constexpr int L = N / S, DB = block_ch<N>();
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    using Sm = Smem<TIn, N>;
+    using Sm = Smem<N>;
+    constexpr int WC = Sm::WC, ROW = Sm::ROW;
     Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
     const int Dg = a.D / a.G;
     const unsigned cblocks = (unsigned)pl.gblocks * a.G;
     const unsigned cb = blockIdx.x % cblocks, bs = blockIdx.x / cblocks;
-    const int seg = (int)(bs % pl.n), b = (int)(bs / pl.n);
+    // nothing takes the first segment's carry
+    const int segs = PHASE == kCarry ? pl.n - 1 : pl.n;
+    const int seg = (int)(bs % segs) + (PHASE == kCarry ? 1 : 0), b = (int)(bs / segs);
     const int grp = (int)(cb / pl.gblocks), gb = (int)(cb % pl.gblocks), cg = gb * DB;
     const int c0 = grp * Dg + cg, cols = min(DB, Dg - cg);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = tid % L, slot = tid / L;
+    const bool helper = threadIdx.x >= kMain;
+    const int tid = threadIdx.x % kMain, lane = tid & 31, warp = tid >> 5;
     const int len = seq_len(a.lens, b, a.T);
-    const int tb = seg * pl.len, te = min(tb + pl.len, a.T);
-    const size_t row0 = (size_t)b * a.T;
-    const TIn *u = (const TIn *)a.u + row0 * a.ldu + c0;
-    const TIn *dl = (const TIn *)a.delta + row0 * a.ldd + c0;
-    const TIn *z = a.z ? (const TIn *)a.z + row0 * a.ldz + c0 : nullptr;
-    const TIn *dy = (const TIn *)a.dy + row0 * a.D + c0;
-    const TIn *Bm = (const TIn *)a.Bm + row0 * a.ldb + (size_t)grp * N;
-    const TIn *Cm = (const TIn *)a.Cm + row0 * a.ldc + (size_t)grp * N;
+    const int tb = seg * pl.len, te = min(tb + pl.len, a.T), tiles = (te - tb + TT - 1) / TT;
+    const size_t row0 = (size_t)b * a.T + tb;   // the segment's first row
+    const size_t bseg = (size_t)b * pl.n + seg;
+    auto rows_of = [&](int it) { return min(max(min(len, te) - tb - it * TT, 0), TT); };
 
-    for (int i = tid; i < DB; i += kThreads) {
-        sm.bias[i] = a.bias && i < cols ? a.bias[c0 + i] : 0.f;
-        sm.skip[i] = a.Dskip && i < cols ? a.Dskip[c0 + i] : 0.f;
+    if (helper) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsHelper));
+        constexpr int V = WC < 4 ? WC : 4, PR = WC / V;   // channels of a vector, vectors of a row
+        static_assert(V == 4, "four channels a vector");
+        const int w0 = warp * WC, ch = (lane % PR) * V, valid = cols - w0 - ch;
+        const size_t cc = c0 + w0 + ch;
+        const TIn *u = (const TIn *)a.u + row0 * a.ldu + cc;
+        const TIn *dl = (const TIn *)a.delta + row0 * a.ldd + cc;
+        const TIn *z = a.z ? (const TIn *)a.z + row0 * a.ldz + cc : nullptr;
+        const TIn *dy = (const TIn *)a.dy + row0 * a.D + cc;
+        const TIn *Bm = (const TIn *)a.Bm + row0 * a.ldb + (size_t)grp * N;
+        const TIn *Cm = (const TIn *)a.Cm + row0 * a.ldc + (size_t)grp * N;
+        auto whole = [](const TIn *p, long long ld) {
+            return (((uintptr_t)p | (uintptr_t)(ld * (long long)sizeof(TIn))) & (4 * sizeof(TIn) - 1)) == 0;
+        };
+        const bool vB = whole(Bm, a.ldb), vC = whole(Cm, a.ldc);
+        float2 bias[2], skip[2], accD[2] = {dup(0.f), dup(0.f)}, accb[2] = {dup(0.f), dup(0.f)};
+        load_n<V, false>(a.bias + cc, reinterpret_cast<float *>(bias), a.bias ? valid : 0);
+        load_n<V, false>(a.Dskip + cc, reinterpret_cast<float *>(skip), a.Dskip ? valid : 0);
+
+        // A batch of rows is loaded before any of it is used: one latency for the batch.
+        constexpr int ITEMS = TT * PR / 32, BATCH = ITEMS < 2 ? ITEMS : 2;
+        using Raw = Raw4<TIn>;
+        auto load_batch = [&](int t, int rows, int k0, Raw *ru, Raw *rd, Raw *ry, Raw *rz) {
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int row = ((k0 + k) * 32 + lane) / PR, n = row < rows ? valid : 0;
+                const size_t at = t + row;
+                if (PHASE == kFull) ru[k] = load_raw<VEC>(u + at * a.ldu, n);
+                rd[k] = load_raw<VEC>(dl + at * a.ldd, n);
+                ry[k] = load_raw<VEC>(dy + at * a.D, n);
+                if (z) rz[k] = load_raw<VEC>(z + at * a.ldz, n);
+            }
+        };
+        // A tile's lines to L2, one iteration before they are loaded: a thread a row of a tensor,
+        // and of the entering states.
+        auto announce = [&](int it) {
+            const int rows = rows_of(it), row = tid % TT, which = tid / TT;
+            if (row < rows) {
+                const TIn *p = which == 0 ? dl : which == 1 ? dy : which == 2 ? z : u;
+                const long long ld = which == 0 ? a.ldd : which == 1 ? a.D : which == 2 ? a.ldz : a.ldu;
+                const int first = w0 + ch;   // p is this lane's place in the row
+                if (p && (which < 3 || PHASE == kFull))
+                    for (int c = 0; c < cols; c += 128 / (int)sizeof(TIn))
+                        prefetch_l2(p - first + (size_t)(it * TT + row) * ld + c);
+            }
+            if (PHASE == kFull) {
+                const size_t ck = (size_t)b * ((a.T + TT - 1) / TT) + tb / TT + it;
+                for (int i = tid * 32; i < cols * N; i += kMain * 32) prefetch_l2(a.states + (ck * a.D + c0) * N + i);
+            }
+        };
+        auto ready = [&](int it) {
+            const int rows = rows_of(it), t = it * TT;
+#pragma unroll 1
+            for (int k0 = 0; k0 < ITEMS; k0 += BATCH) {
+                Raw ru[BATCH], rd[BATCH], ry[BATCH], rz[BATCH];
+                load_batch(t, rows, k0, ru, rd, ry, rz);
+                if (k0 == 0) {
+                    if (PHASE == kFull)
+                        rows_to_shared<TIn, N>(sm.B[it & 1], Bm + (size_t)t * a.ldb, a.ldb, rows, vB, tid);
+                    rows_to_shared<TIn, N>(sm.C[it & 1], Cm + (size_t)t * a.ldc, a.ldc, rows, vC, tid);
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int row = ((k0 + k) * 32 + lane) / PR;
+                    float2 vu[2] = {dup(0.f), dup(0.f)}, vd[2], vy[2], vz[2];
+                    if (PHASE == kFull) ru[k].widen(vu);
+                    rd[k].widen(vd);
+                    ry[k].widen(vy);
+                    if (z) rz[k].widen(vz);
+                    float4 *o = reinterpret_cast<float4 *>(sm.step[it & 1][warp] + row * ROW + 2 * ch);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float2 dt = __fadd2_rn(vd[c], bias[c]);
+                        if (a.softplus) dt = softplus_accurate(dt);
+                        if (row >= rows) dt = dup(0.f);   // a row past the end steps by zero: g stays
+                        const float2 du = __fmul2_rn(dt, vu[c]);
+                        o[c] = make_float4(dt.x, du.x, dt.y, du.y);
+                        if (z) vy[c] = __fmul2_rn(vy[c], silu_fast(vz[c]));
+                    }
+                    *reinterpret_cast<float4 *>(sm.yb[it & 1][warp] + row * WC + ch) =
+                        make_float4(vy[0].x, vy[0].y, vy[1].x, vy[1].y);
+                }
+            }
+            __syncwarp();
+        };
+        auto finished = [&](int it) {
+            const int rows = rows_of(it), t = it * TT, live = min(te - tb - t, TT);
+            float *bc = wk.bc + (((size_t)gb * a.B * a.T + row0 + t) * a.G + grp) * (2 * N);
+            TIn *du = (TIn *)a.du + (row0 + t) * a.D + cc, *dd = (TIn *)a.ddelta + (row0 + t) * a.D + cc;
+            TIn *dz = z ? (TIn *)a.dz + (row0 + t) * a.D + cc : nullptr;
+#pragma unroll 1
+            for (int k0 = 0; k0 < ITEMS; k0 += BATCH) {
+                Raw ru[BATCH], rd[BATCH], ry[BATCH], rz[BATCH];
+                load_batch(t, rows, k0, ru, rd, ry, rz);
+                if (k0 == 0)   // dB, dC of the block's channels, while the rows arrive
+                    for (int i = tid; i < live * (2 * N / 4); i += kMain) {
+                        const int row = i / (2 * N / 4), n = i % (2 * N / 4) * 4;
+                        float4 s = *reinterpret_cast<const float4 *>(&sm.red[0][row][n]);
+#pragma unroll
+                        for (int k = 1; k < kWarps; ++k) {
+                            const float4 q = *reinterpret_cast<const float4 *>(&sm.red[k][row][n]);
+                            s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
+                        }
+                        *reinterpret_cast<float4 *>(bc + (size_t)row * a.G * (2 * N) + n) = s;
+                    }
+                // the rows' du, ddelta, dz
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int row = ((k0 + k) * 32 + lane) / PR;
+                    float2 vu[2], vd[2], vy[2], vz[2], pre[2], ww[2], oz[2], ou[2], od[2];
+                    ru[k].widen(vu);
+                    rd[k].widen(vd);
+                    ry[k].widen(vy);
+                    if (z) rz[k].widen(vz);
+                    load_n<V, true>(sm.yb[it & 1][warp] + row * WC + ch, reinterpret_cast<float *>(pre));
+                    load_n<V, true>(sm.ww[warp] + row * WC + ch, reinterpret_cast<float *>(ww));
+                    const float4 *o = reinterpret_cast<const float4 *>(sm.step[it & 1][warp] + row * ROW + 2 * ch);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float4 s = o[c];
+                        const float2 dt = make_float2(s.x, s.z), q = make_float2(s.y, s.w);
+                        float2 yb = vy[c];
+                        if (z) {
+                            const Gate gt = gate_of(vz[c]);
+                            oz[c] = __fmul2_rn(__fmul2_rn(vy[c], gt.dy), __ffma2_rn(skip[c], vu[c], pre[c]));
+                            yb = __fmul2_rn(vy[c], gt.y);
+                        }
+                        ou[c] = __ffma2_rn(dt, q, __fmul2_rn(skip[c], yb));
+                        od[c] = __ffma2_rn(ww[c], dup(kLn2), __fmul2_rn(vu[c], q));
+                        if (a.softplus) {
+                            const float2 x = __fadd2_rn(vd[c], bias[c]);
+                            od[c] = __fmul2_rn(od[c], rcp(__fadd2_rn(ex2(__fmul2_rn(x, dup(-kLog2e))), dup(1.f))));
+                        }
+                        if (row >= rows) ou[c] = od[c] = oz[c] = yb = dup(0.f);
+                        accD[c] = __ffma2_rn(yb, vu[c], accD[c]);
+                        accb[c] = __fadd2_rn(accb[c], od[c]);
+                    }
+                    if (row < live) {
+                        store_n<V, VEC>(du + (size_t)row * a.D, reinterpret_cast<float *>(ou), valid);
+                        store_n<V, VEC>(dd + (size_t)row * a.D, reinterpret_cast<float *>(od), valid);
+                        if (z) store_n<V, VEC>(dz + (size_t)row * a.D, reinterpret_cast<float *>(oz), valid);
+                    }
+                }
+            }
+            __syncwarp();
+        };
+        ready(tiles - 1);
+        if (tiles > 1) announce(tiles - 2);
+        __syncthreads();
+        for (int it = tiles - 1; it >= 0; --it) {
+            if (PHASE == kFull) {
+                if (it + 1 < tiles) finished(it + 1);
+                bar_arrive<kTaken>();
+            }
+            if (it > 1) announce(it - 2);
+            if (it > 0) ready(it - 1);
+            __syncthreads();
+        }
+        if (PHASE == kFull) {
+            finished(0);
+            // dD and the bias over the lanes that share a vector's channels
+#pragma unroll
+            for (int o = 16; o >= PR; o >>= 1)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    accD[c].x += __shfl_xor_sync(0xffffffffu, accD[c].x, o);
+                    accD[c].y += __shfl_xor_sync(0xffffffffu, accD[c].y, o);
+                    accb[c].x += __shfl_xor_sync(0xffffffffu, accb[c].x, o);
+                    accb[c].y += __shfl_xor_sync(0xffffffffu, accb[c].y, o);
+                }
+            if (lane < PR) {
+                store_n<V, false>(wk.D + bseg * a.D + cc, reinterpret_cast<float *>(accD), valid);
+                store_n<V, false>(wk.bias + bseg * a.D + cc, reinterpret_cast<float *>(accb), valid);
+            }
+        }
+        return;
     }
+
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMain));
+    // The recurrence: lane l of a channel pair's L has states l S .. l S + S - 1 of channels
+    // 2 slot and 2 slot + 1.
+    const int l = tid % L, slot = tid / L, wch = 2 * slot - warp * WC;   // the pair's place in the warp
     float2 A2[KC][2], g[KC][2], dA[KC][2];
     float sumdt[KC];
 #pragma unroll
     for (int k = 0; k < KC; ++k) {
-        const int ch = slot + k * SL;
+        const int ch = KC * slot + k;
         const bool on = ch < cols;
         const size_t at = (size_t)(c0 + ch) * N + l * S;
         sumdt[k] = 0.f;
@@ -109,12 +359,12 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
         for (int s = 0; s < 2; ++s) {
             A2[k][s] = on ? make_float2(a.A[at + 2 * s] * kLog2e, a.A[at + 2 * s + 1] * kLog2e) : dup(0.f);
             g[k][s] = dA[k][s] = dup(0.f);
-            if (PHASE == kMain && on && a.dh_final) {
+            if (PHASE == kFull && on && a.dh_final) {
                 const float *p = a.dh_final + (size_t)b * a.D * N + at + 2 * s;
                 g[k][s] = make_float2(p[0], p[1]);
             }
         }
-        if (PHASE == kMain && on)
+        if (PHASE == kFull && on)
             for (int j = pl.n - 1; j > seg; --j) {   // through the later segments
                 const size_t e = ((size_t)b * pl.n + j) * a.D + c0 + ch;
                 const float sd = wk.sums[e];
@@ -125,176 +375,117 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
                                          make_float2(p[2 * s], p[2 * s + 1]));
             }
     }
-
-    auto rows_of = [&](int t0) { return min(max(min(len, te) - t0, 0), TT); };
-    auto fetch = [&](int t0) {
-        if constexpr (STAGED) {
-            const int rows = rows_of(t0);
-            TIn(*raw)[TT * DB] = reinterpret_cast<TIn(*)[TT * DB]>(sm.raw);
-            if (PHASE == kMain) load_rows<TIn, DB, DB, kThreads, true>(raw[0], u + (size_t)t0 * a.ldu, a.ldu, rows, cols);
-            load_rows<TIn, DB, DB, kThreads, true>(raw[1], dl + (size_t)t0 * a.ldd, a.ldd, rows, cols);
-            load_rows<TIn, DB, DB, kThreads, true>(raw[2], dy + (size_t)t0 * a.D, a.D, rows, cols);
-            if (z) load_rows<TIn, DB, DB, kThreads, true>(raw[3], z + (size_t)t0 * a.ldz, a.ldz, rows, cols);
-            cp_async_commit();
-        }
-    };
-    // two neighbouring channels of a row, zeros outside
-    auto pair = [&](const TIn *p, long long ld, int t0, int r, int c, bool live, float *v) {
-        load_n<2, false>(p + (size_t)(t0 + r) * ld + c, v, live ? cols - c : 0);
-    };
-    constexpr int PER = DB / 2;
-    static_assert(kThreads % PER == 0, "a thread keeps its channels in every pass over a tile");
-    const int pc = (tid % PER) * 2;
-    float accD[2] = {0.f, 0.f}, accb[2] = {0.f, 0.f};
-
-    RowRegs<TIn, N, kThreads> rB, rC;
-    const int vB = rB.alignment(Bm, a.ldb), vC = rC.alignment(Cm, a.ldc);
-    const int last = tb + (te - 1 - tb) / TT * TT;   // the segment's last tile
-    fetch(last);
-    if (PHASE == kMain) rB.load(Bm + (size_t)last * a.ldb, a.ldb, rows_of(last), vB);
-    rC.load(Cm + (size_t)last * a.ldc, a.ldc, rows_of(last), vC);
-    for (int t0 = last; t0 >= tb; t0 -= TT) {
-        const int rows = rows_of(t0);
-        float4 h0[KC];
-        if (PHASE == kMain) {
-            const size_t ck = (size_t)b * ((a.T + TT - 1) / TT) + t0 / TT;
-#pragma unroll
-            for (int k = 0; k < KC; ++k) {
-                const int ch = slot + k * SL;
-                h0[k] = ch < cols ? *reinterpret_cast<const float4 *>(a.states + (ck * a.D + c0 + ch) * N + l * S)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-        }
-        if constexpr (STAGED) cp_async_wait<0>();
-        __syncthreads();   // this tile has arrived; the last tile's readers are done
-        if (PHASE == kMain) rB.store(sm.B, Bm + (size_t)t0 * a.ldb, a.ldb, rows, vB);
-        rC.store(sm.C, Cm + (size_t)t0 * a.ldc, a.ldc, rows, vC);
-        for (int i = tid; i < TT * PER; i += kThreads) {
-            const int r = i / PER;
-            const bool live = r < rows;
-            float vu[2] = {0.f, 0.f}, vd[2], vy[2], vz[2];
-            if constexpr (STAGED) {
-                const TIn(*raw)[TT * DB] = reinterpret_cast<const TIn(*)[TT * DB]>(sm.raw);
-                const int o = r * DB + pc;
-                if (PHASE == kMain) load_n<2, false>(&raw[0][o], vu);
-                load_n<2, false>(&raw[1][o], vd);
-                load_n<2, false>(&raw[2][o], vy);
-                if (z) load_n<2, false>(&raw[3][o], vz);
-            } else {
-                if (PHASE == kMain) pair(u, a.ldu, t0, r, pc, live, vu);
-                pair(dl, a.ldd, t0, r, pc, live, vd);
-                pair(dy, a.D, t0, r, pc, live, vy);
-                if (z) pair(z, a.ldz, t0, r, pc, live, vz);
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float dt = vd[k] + sm.bias[pc + k];
-                if (a.softplus) dt = softplus_accurate(dt);
-                if (!live) dt = 0.f;
-                const float yb = z ? vy[k] * gate_of(vz[k]).y : vy[k];
-                sm.step[r][pc + k] = make_float4(dt, live ? dt * vu[k] : 0.f, live ? yb : 0.f, 0.f);
-            }
-        }
-        __syncthreads();
-        if (t0 > tb) {
-            fetch(t0 - TT);
-            if (PHASE == kMain) rB.load(Bm + (size_t)(t0 - TT) * a.ldb, a.ldb, rows_of(t0 - TT), vB);
-            rC.load(Cm + (size_t)(t0 - TT) * a.ldc, a.ldc, rows_of(t0 - TT), vC);
-        }
-        auto row4 = [&](const float *m, int r, float2 *v) {
-            const float4 q = *reinterpret_cast<const float4 *>(&m[r * N + l * S]);
-            v[0] = make_float2(q.x, q.y);
-            v[1] = make_float2(q.z, q.w);
-        };
+    __syncthreads();
+    for (int it = tiles - 1; it >= 0; --it) {
+        float *step = sm.step[it & 1][warp] + 2 * wch, *yb = sm.yb[it & 1][warp] + wch;
+        const float *Br = sm.B[it & 1] + l * S, *Cr = sm.C[it & 1] + l * S;
         if constexpr (PHASE == kCarry) {
-#pragma unroll 4
+#pragma unroll 8
             for (int r = TT - 1; r >= 0; --r) {
-                float2 Cv[2];
-                row4(sm.C, r, Cv);
+                const float4 q = *reinterpret_cast<const float4 *>(step + r * ROW);
+                const float2 y = *reinterpret_cast<const float2 *>(yb + r * WC);
+                const float4 c = *reinterpret_cast<const float4 *>(Cr + r * N);
+                const float2 Cv[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
+                sumdt[0] += q.x;
+                sumdt[1] += q.z;
 #pragma unroll
-                for (int k = 0; k < KC; ++k) {
-                    const float4 q = sm.step[r][slot + k * SL];
-                    sumdt[k] += q.x;
+                for (int k = 0; k < KC; ++k)
 #pragma unroll
                     for (int s = 0; s < 2; ++s)
-                        g[k][s] = __fmul2_rn(ex2(__fmul2_rn(A2[k][s], dup(q.x))), __ffma2_rn(Cv[s], dup(q.z), g[k][s]));
-                }
+                        g[k][s] = __fmul2_rn(ex2(__fmul2_rn(A2[k][s], dup(k ? q.z : q.x))),
+                                             __ffma2_rn(Cv[s], dup(k ? y.y : y.x), g[k][s]));
             }
         } else {
             float2 h[KC][2];
+            const size_t ck = (size_t)b * ((a.T + TT - 1) / TT) + tb / TT + it;
 #pragma unroll
             for (int k = 0; k < KC; ++k) {
-                h[k][0] = make_float2(h0[k].x, h0[k].y);
-                h[k][1] = make_float2(h0[k].z, h0[k].w);
+                const int ch = KC * slot + k;
+                const float4 q = ch < cols
+                    ? *reinterpret_cast<const float4 *>(a.states + (ck * a.D + c0 + ch) * N + l * S)
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                h[k][0] = make_float2(q.x, q.y);
+                h[k][1] = make_float2(q.z, q.w);
             }
-#pragma unroll 1
-            for (int sub = 0; sub < TT / SUB; ++sub) {
+            // one token of the states: h = a h + dt u B, given its row of step and of B
+            auto advance = [&](const float4 &q, const float4 &c, float2 (*av)[2], const float2 (*hi)[2],
+                               float2 (*ho)[2]) {
+                const float2 Bv[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
+#pragma unroll
+                for (int k = 0; k < KC; ++k)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        av[k][s] = ex2(__fmul2_rn(A2[k][s], dup(k ? q.z : q.x)));
+                        ho[k][s] = __ffma2_rn(av[k][s], hi[k][s], __fmul2_rn(dup(k ? q.w : q.y), Bv[s]));
+                    }
+            };
+#pragma unroll
+            for (int sub = 0; sub < TT / SUB - 1; ++sub) {
+                float4 q[SUB], c[SUB];
+#pragma unroll
+                for (int j = 0; j < SUB; ++j) {
+                    q[j] = *reinterpret_cast<const float4 *>(step + (sub * SUB + j) * ROW);
+                    c[j] = *reinterpret_cast<const float4 *>(Br + (sub * SUB + j) * N);
+                }
 #pragma unroll
                 for (int k = 0; k < KC; ++k)
                     sm.ckpt[sub][k][tid] = make_float4(h[k][0].x, h[k][0].y, h[k][1].x, h[k][1].y);
-                if (sub == TT / SUB - 1) break;
+#pragma unroll
+                for (int j = 0; j < SUB; ++j) {
+                    float2 av[KC][2];
+                    advance(q[j], c[j], av, h, h);
+                }
+            }
+            bar_sync<kTaken>();
+#pragma unroll 1
+            for (int sub = TT / SUB - 1; sub >= 0; --sub) {
+                float4 q[SUB], bq[SUB], cq[SUB];
+                float2 y[SUB];
 #pragma unroll
                 for (int j = 0; j < SUB; ++j) {
                     const int r = sub * SUB + j;
-                    float2 Bv[2];
-                    row4(sm.B, r, Bv);
-#pragma unroll
-                    for (int k = 0; k < KC; ++k) {
-                        const float4 q = sm.step[r][slot + k * SL];
-#pragma unroll
-                        for (int s = 0; s < 2; ++s)
-                            h[k][s] = __ffma2_rn(ex2(__fmul2_rn(A2[k][s], dup(q.x))), h[k][s],
-                                                 __fmul2_rn(dup(q.y), Bv[s]));
-                    }
+                    q[j] = *reinterpret_cast<const float4 *>(step + r * ROW);
+                    bq[j] = *reinterpret_cast<const float4 *>(Br + r * N);
+                    cq[j] = *reinterpret_cast<const float4 *>(Cr + r * N);
+                    y[j] = *reinterpret_cast<const float2 *>(yb + r * WC);
                 }
-            }
-#pragma unroll 1
-            for (int sub = TT / SUB - 1; sub >= 0; --sub) {
                 float2 hh[SUB + 1][KC][2], av[SUB][KC][2];   // states before each token, decays
 #pragma unroll
                 for (int k = 0; k < KC; ++k) {
-                    const float4 q = sm.ckpt[sub][k][tid];
-                    hh[0][k][0] = make_float2(q.x, q.y);
-                    hh[0][k][1] = make_float2(q.z, q.w);
-                }
-#pragma unroll
-                for (int j = 0; j < SUB; ++j) {
-                    const int r = sub * SUB + j;
-                    float2 Bv[2];
-                    row4(sm.B, r, Bv);
-#pragma unroll
-                    for (int k = 0; k < KC; ++k) {
-                        const float4 q = sm.step[r][slot + k * SL];
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            av[j][k][s] = ex2(__fmul2_rn(A2[k][s], dup(q.x)));
-                            hh[j + 1][k][s] = __ffma2_rn(av[j][k][s], hh[j][k][s], __fmul2_rn(dup(q.y), Bv[s]));
-                        }
+                    if (sub < TT / SUB - 1) {
+                        const float4 v = sm.ckpt[sub][k][tid];
+                        h[k][0] = make_float2(v.x, v.y);
+                        h[k][1] = make_float2(v.z, v.w);
                     }
+                    hh[0][k][0] = h[k][0];
+                    hh[0][k][1] = h[k][1];
                 }
+#pragma unroll
+                for (int j = 0; j < SUB; ++j) advance(q[j], bq[j], av[j], hh[j], hh[j + 1]);
                 float qs[SUB * KC], ws[SUB * KC], ps[SUB * KC];
 #pragma unroll
                 for (int j = SUB - 1; j >= 0; --j) {
                     const int r = sub * SUB + j;
-                    float2 Bv[2], Cv[2], dB[2], dC[2];
-                    row4(sm.B, r, Bv);
-                    row4(sm.C, r, Cv);
+                    const float2 Bv[2] = {make_float2(bq[j].x, bq[j].y), make_float2(bq[j].z, bq[j].w)};
+                    const float2 Cv[2] = {make_float2(cq[j].x, cq[j].y), make_float2(cq[j].z, cq[j].w)};
+                    float2 dB[2], dC[2];
 #pragma unroll
                     for (int k = 0; k < KC; ++k) {
-                        const float4 q = sm.step[r][slot + k * SL];
+                        const float2 dt = dup(k ? q[j].z : q[j].x), du = dup(k ? q[j].w : q[j].y);
+                        const float2 ybk = dup(k ? y[j].y : y[j].x);
                         float2 aq, aw, ap;
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
                             const float2 ht = hh[j + 1][k][s];
-                            g[k][s] = __ffma2_rn(Cv[s], dup(q.z), g[k][s]);
-                            dB[s] = k ? __ffma2_rn(g[k][s], dup(q.y), dB[s]) : __fmul2_rn(g[k][s], dup(q.y));
-                            dC[s] = k ? __ffma2_rn(ht, dup(q.z), dC[s]) : __fmul2_rn(ht, dup(q.z));
+                            g[k][s] = __ffma2_rn(Cv[s], ybk, g[k][s]);
+                            dB[s] = k ? __ffma2_rn(g[k][s], du, dB[s]) : __fmul2_rn(g[k][s], du);
+                            dC[s] = k ? __ffma2_rn(ht, ybk, dC[s]) : __fmul2_rn(ht, ybk);
                             aq = s ? __ffma2_rn(g[k][s], Bv[s], aq) : __fmul2_rn(g[k][s], Bv[s]);
                             ap = s ? __ffma2_rn(ht, Cv[s], ap) : __fmul2_rn(ht, Cv[s]);
                             g[k][s] = __fmul2_rn(g[k][s], av[j][k][s]);
                             const float2 w = __fmul2_rn(g[k][s], hh[j][k][s]);
                             aw = s ? __ffma2_rn(A2[k][s], w, aw) : __fmul2_rn(A2[k][s], w);
-                            dA[k][s] = __ffma2_rn(w, dup(q.x), dA[k][s]);
+                            dA[k][s] = __ffma2_rn(w, dt, dA[k][s]);
                         }
                         qs[j * KC + k] = aq.x + aq.y;
                         ws[j * KC + k] = aw.x + aw.y;
@@ -321,63 +512,18 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
                 if (l % DUP == 0)
 #pragma unroll
                     for (int i = 0; i < HELD; ++i) {
-                        const int idx = (l / DUP) * HELD + i;
-                        float4 &o = sm.step[sub * SUB + idx / KC][slot + (idx % KC) * SL];
-                        o.y = qs[i];
-                        o.z = ps[i];
-                        o.w = ws[i];
+                        const int idx = (l / DUP) * HELD + i, r = sub * SUB + idx / KC, c = idx % KC;
+                        step[r * ROW + 2 * c + 1] = qs[i];
+                        yb[r * WC + c] = ps[i];
+                        sm.ww[warp][r * WC + wch + c] = ws[i];
                     }
-            }
-            __syncthreads();
-            // the tile's rows: du, ddelta, dz
-            const int live_rows = min(te - t0, TT);
-            TIn *du = (TIn *)a.du + (row0 + t0) * a.D + c0, *dd = (TIn *)a.ddelta + (row0 + t0) * a.D + c0;
-            TIn *dz = a.dz ? (TIn *)a.dz + (row0 + t0) * a.D + c0 : nullptr;
-            for (int i = tid; i < TT * PER; i += kThreads) {
-                const int r = i / PER;
-                if (r >= live_rows || pc >= cols) continue;
-                const bool live = r < rows;
-                float vu[2], vd[2], vy[2], vz[2], ou[2], od[2], oz[2];
-                pair(u, a.ldu, t0, r, pc, live, vu);
-                pair(dl, a.ldd, t0, r, pc, live, vd);
-                pair(dy, a.D, t0, r, pc, live, vy);
-                if (z) pair(z, a.ldz, t0, r, pc, live, vz);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float4 q = sm.step[r][pc + k];
-                    float yb = vy[k];
-                    oz[k] = 0.f;
-                    if (z) {
-                        const Gate gt = gate_of(vz[k]);
-                        oz[k] = vy[k] * gt.dy * fmaf(sm.skip[pc + k], vu[k], q.z);
-                        yb = vy[k] * gt.y;
-                    }
-                    ou[k] = fmaf(q.x, q.y, sm.skip[pc + k] * yb);
-                    od[k] = fmaf(kLn2, q.w, vu[k] * q.y);
-                    if (a.softplus) od[k] *= sigmoid_fast(vd[k] + sm.bias[pc + k]);
-                    if (!live) ou[k] = od[k] = oz[k] = yb = 0.f;
-                    accD[k] = fmaf(yb, vu[k], accD[k]);
-                    accb[k] += od[k];
-                }
-                store_n<2, false>(du + (size_t)r * a.D + pc, ou, cols - pc);
-                store_n<2, false>(dd + (size_t)r * a.D + pc, od, cols - pc);
-                if (z) store_n<2, false>(dz + (size_t)r * a.D + pc, oz, cols - pc);
-            }
-            float *bc = wk.bc + (((size_t)gb * a.B * a.T + row0 + t0) * a.G + grp) * (2 * N);
-            for (int i = tid; i < live_rows * 2 * N; i += kThreads) {
-                const int r = i / (2 * N), n = i % (2 * N);
-                float t = sm.red[0][r][n];
-#pragma unroll
-                for (int k = 1; k < kWarps; ++k) t += sm.red[k][r][n];
-                bc[(size_t)r * a.G * (2 * N) + n] = t;
             }
         }
+        __syncthreads();
     }
-
-    const size_t bseg = (size_t)b * pl.n + seg;
 #pragma unroll
     for (int k = 0; k < KC; ++k) {
-        const int ch = slot + k * SL;
+        const int ch = KC * slot + k;
         if (ch >= cols) continue;
         const size_t e = bseg * a.D + c0 + ch;
         const float4 gv = make_float4(g[k][0].x, g[k][0].y, g[k][1].x, g[k][1].y);
@@ -389,23 +535,6 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
                 make_float4(dA[k][0].x, dA[k][0].y, dA[k][1].x, dA[k][1].y);
             if (seg == 0 && a.dh0)
                 *reinterpret_cast<float4 *>(a.dh0 + ((size_t)b * a.D + c0 + ch) * N + l * S) = gv;
-        }
-    }
-    if constexpr (PHASE == kMain) {   // dD and the bias: over the threads that share a channel pair
-        __syncthreads();
-        float4 *t4 = reinterpret_cast<float4 *>(sm.red);
-        t4[tid] = make_float4(accD[0], accD[1], accb[0], accb[1]);
-        __syncthreads();
-        if (tid < PER) {
-            float4 t = t4[tid];
-#pragma unroll
-            for (int i = 1; i < kThreads / PER; ++i) {
-                const float4 q = t4[tid + i * PER];
-                t.x += q.x; t.y += q.y; t.z += q.z; t.w += q.w;
-            }
-            const size_t e = bseg * a.D + c0 + pc;
-            if (pc < cols) { wk.D[e] = t.x; wk.bias[e] = t.z; }
-            if (pc + 1 < cols) { wk.D[e + 1] = t.y; wk.bias[e + 1] = t.w; }
         }
     }
 }
@@ -448,12 +577,12 @@ ssm_sum_kernel(const SsmBwdArgs a, const Work wk, int gblocks, int np, unsigned 
 
 constexpr int kSms = 152;
 
+// Segments per sequence: enough to fill the SMs at two blocks each, of at least four tiles.
 Plan bwd_plan(int B, int T, int D, int N, int G)
 {
     const int db = block_channels(N), gblocks = (D / G + db - 1) / db;
-    const long long blocks = (long long)B * G * gblocks, want = kSms * 2 * 3;   // two blocks an SM, three waves
-    int n = (int)std::min<long long>((want + blocks - 1) / blocks, std::max(1, T / 64));
-    n = std::max(1, std::min(n, 64));
+    const long long blocks = (long long)B * G * gblocks;
+    const int n = (int)std::max(1LL, std::min<long long>(kSms * 2 / blocks, T / (4 * TT)));
     const int len = std::max(TT, (int)((((long long)T + n - 1) / n + TT - 1) / TT) * TT);
     return {std::max(1, (T + len - 1) / len), len, gblocks};
 }
@@ -478,11 +607,17 @@ size_t lay_out(const Plan &p, int B, int T, int D, int N, int G, float *base, Wo
 template <typename TIn, int N, bool VEC, int PHASE>
 cudaError_t bwd_launch(const SsmBwdArgs &a, const Plan &p, const Work &w, cudaStream_t st)
 {
-    constexpr int bytes = (int)sizeof(Smem<TIn, N>);
+    constexpr int bytes = (int)sizeof(Smem<N>);
     auto *k = ssm_backward_kernel<TIn, N, VEC, PHASE>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)((long long)p.gblocks * a.G * a.B * p.n), kThreads, bytes, st>>>(a, p, w);
+    // the split of the registers waits for what the launch has to hold
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, k);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < kRegs) return cudaErrorInvalidConfiguration;
+    const long long segs = PHASE == kCarry ? p.n - 1 : p.n;
+    k<<<(unsigned)(p.gblocks * segs * a.G * a.B), kThreads, bytes, st>>>(a, p, w);
     return cudaGetLastError();
 }
 
@@ -496,7 +631,7 @@ cudaError_t bwd_run(const SsmBwdArgs &a, cudaStream_t st)
         const cudaError_t e = bwd_launch<TIn, N, VEC, kCarry>(a, p, w, st);
         if (e != cudaSuccess) return e;
     }
-    const cudaError_t e = bwd_launch<TIn, N, VEC, kMain>(a, p, w, st);
+    const cudaError_t e = bwd_launch<TIn, N, VEC, kFull>(a, p, w, st);
     if (e != cudaSuccess) return e;
     const unsigned bcb = (unsigned)(((size_t)a.B * a.T * a.G * 2 * N / 4 + 255) / 256);
     const unsigned pb = (unsigned)(((size_t)a.D * (N + 2) + 255) / 256);

@@ -69,7 +69,8 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
     const int Dg = a.D / a.G;
     const unsigned cblocks = (unsigned)gblocks * a.G;
     const unsigned cb = blockIdx.x % cblocks, bs = blockIdx.x / cblocks;
-    const int seg = (int)(bs % sg.n), b = (int)(bs / sg.n);
+    const int segs = PHASE == kEnds ? sg.n - 1 : sg.n;   // nothing takes the last segment's end
+    const int seg = (int)(bs % segs), b = (int)(bs / segs);
     const int grp = (int)(cb / gblocks), cg = (int)(cb % gblocks) * DB;
     const int c0 = grp * Dg + cg, cols = min(DB, Dg - cg);
     const bool helper = threadIdx.x >= kMain;
@@ -380,7 +381,8 @@ cudaError_t scan_launch(const SsmArgs &a, const Segs &sg, cudaStream_t st)
         if (e != cudaSuccess) return e;
     }
     const int gblocks = (a.D / a.G + DB - 1) / DB;
-    k<<<(unsigned)((long long)gblocks * a.G * a.B * sg.n), kThreads, bytes, st>>>(a, sg, gblocks);
+    const long long segs = PHASE == kEnds ? sg.n - 1 : sg.n;
+    k<<<(unsigned)(gblocks * segs * a.G * a.B), kThreads, bytes, st>>>(a, sg, gblocks);
     return cudaGetLastError();
 }
 
