@@ -19,6 +19,7 @@ namespace ldn {
 namespace {
 
 constexpr int kE = 8;   // channels per thread and vector
+constexpr int kMostThreads = 512;
 constexpr float kE4m3Max = 448.f;
 
 template <int NV>
@@ -85,7 +86,7 @@ __device__ __forceinline__ float as_stored(float x, const __nv_bfloat16 *)
 
 // EIGHT: 0 = y in TIn, 1 = e4m3 with a scale per row, 2 = per 128 channels.
 template <typename TIn, typename TRes, int EIGHT, int VPT, bool VEC>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(kMostThreads)
 add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__restrict__ w, void *__restrict__ y,
                    float *__restrict__ scale, TRes *r_out, int D, float eps)
 {
@@ -93,11 +94,13 @@ add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__rest
     const size_t row = blockIdx.x;
     const int nt = blockDim.x, nwarps = nt >> 5;
     const TIn *xr = x + row * D;
-    float v[VPT][kE], ss = 0.f;
+    constexpr bool AHEAD = VPT <= 4;   // the weights come with the row: not after the sum
+    float v[VPT][kE], g[AHEAD ? VPT : 1][kE], ss = 0.f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int c = (k * nt + (int)threadIdx.x) * kE, valid = D - c;
         load_n<kE, VEC>(xr + c, v[k], valid);
+        if constexpr (AHEAD) load_n<kE, VEC>(w + c, g[k], valid);
         if (r) {
             float q[kE];
             load_n<kE, VEC>(r + row * D + c, q, valid);
@@ -118,10 +121,9 @@ add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__rest
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int c = (k * nt + (int)threadIdx.x) * kE, valid = D - c;
-        float g[kE];
-        load_n<kE, false>(w + c, g, valid);
+        if constexpr (!AHEAD) load_n<kE, VEC>(w + c, g[0], valid);
 #pragma unroll
-        for (int i = 0; i < kE; ++i) v[k][i] *= rstd * g[i];
+        for (int i = 0; i < kE; ++i) v[k][i] *= rstd * g[AHEAD ? k : 0][i];
         if constexpr (EIGHT == 0) {
             store_n<kE, VEC>((TIn *)y + row * D + c, v[k], valid);
         } else {
@@ -158,10 +160,11 @@ add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__rest
     }
 }
 
-// A block walks rows blockIdx.x, + gridDim.x, ...; the columns' share of dw stays in
-// registers over all of them and goes to `part` [gridDim.x][D] once.
+// A block walks rows blockIdx.x, + gridDim.x, ...; the next row is on its way while one is
+// summed.  The columns' share of dw stays in registers over all rows and goes to `part`
+// [gridDim.x][D] once.
 template <typename TIn, typename TRes, int VPT, bool VEC>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(kMostThreads)
 add_rmsnorm_bwd_kernel(const TIn *__restrict__ dy, const TRes *__restrict__ s, const float *__restrict__ w,
                        const TRes *__restrict__ dsum, TIn *__restrict__ dx, TRes *__restrict__ dres,
                        float *__restrict__ part, long long rows, int D, float eps)
@@ -172,50 +175,56 @@ add_rmsnorm_bwd_kernel(const TIn *__restrict__ dy, const TRes *__restrict__ s, c
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int c = (k * nt + (int)threadIdx.x) * kE;
-        load_n<kE, false>(w + c, g[k], D - c);
+        load_n<kE, VEC>(w + c, g[k], D - c);
 #pragma unroll
         for (int i = 0; i < kE; ++i) acc[k][i] = 0.f;
     }
-    int turn = 0;
-    for (long long row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
-        float sv[VPT][kE], gy[VPT][kE], sums[2] = {0.f, 0.f};
+    Raw<TRes, kE> rs[VPT], rd[VPT];
+    Raw<TIn, kE> ry[VPT];
+    auto fetch = [&](long long row) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int c = (k * nt + (int)threadIdx.x) * kE, valid = D - c;
-            load_n<kE, VEC>(s + row * D + c, sv[k], valid);
-            load_n<kE, VEC>(dy + row * D + c, gy[k], valid);
+            const int c = (k * nt + (int)threadIdx.x) * kE, valid = row < rows ? D - c : 0;
+            rs[k].template load<VEC>(s + row * D + c, valid);
+            ry[k].template load<VEC>(dy + row * D + c, valid);
+            rd[k].template load<VEC>(dsum + row * D + c, dsum ? valid : 0);
         }
+    };
+    fetch(blockIdx.x);
+    int turn = 0;
+    for (long long row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
+        float sv[VPT][kE], gy[VPT][kE], d[VPT][kE], sums[2] = {0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < VPT; ++k)
+        for (int k = 0; k < VPT; ++k) {
+            rs[k].widen(sv[k]);
+            ry[k].widen(gy[k]);
+            rd[k].widen(d[k]);
 #pragma unroll
             for (int i = 0; i < kE; ++i) {
                 sums[0] = fmaf(sv[k][i], sv[k][i], sums[0]);
                 sums[1] = fmaf(g[k][i] * gy[k][i], sv[k][i], sums[1]);
             }
+        }
+        fetch(row + gridDim.x);
         block_sum<2>(sums, sm[turn], nwarps);   // two buffers: the next row's sums pass no reader of these
         const float rstd = rsqrtf(sums[0] / (float)D + eps);
         const float m = rstd * rstd * (sums[1] / (float)D);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = (k * nt + (int)threadIdx.x) * kE, valid = D - c;
-            float d[kE];
-            if (dsum) load_n<kE, VEC>(dsum + row * D + c, d, valid);
-            else
-#pragma unroll
-                for (int i = 0; i < kE; ++i) d[i] = 0.f;
 #pragma unroll
             for (int i = 0; i < kE; ++i) {
                 acc[k][i] = fmaf(gy[k][i], sv[k][i] * rstd, acc[k][i]);
-                d[i] = fmaf(rstd, g[k][i] * gy[k][i] - sv[k][i] * m, d[i]);
+                d[k][i] = fmaf(rstd, g[k][i] * gy[k][i] - sv[k][i] * m, d[k][i]);
             }
-            if (dx) store_n<kE, VEC>(dx + row * D + c, d, valid);
-            if (dres) store_n<kE, VEC>(dres + row * D + c, d, valid);
+            if (dx) store_n<kE, VEC>(dx + row * D + c, d[k], valid);
+            if (dres) store_n<kE, VEC>(dres + row * D + c, d[k], valid);
         }
     }
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int c = (k * nt + (int)threadIdx.x) * kE;
-        store_n<kE, false>(part + (size_t)blockIdx.x * D + c, acc[k], D - c);
+        store_n<kE, VEC>(part + (size_t)blockIdx.x * D + c, acc[k], D - c);
     }
 }
 
@@ -237,11 +246,62 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float *__restrict
     }
 }
 
-// Threads for D channels at VPT vectors of 8 each, in whole warps.
-int norm_threads(int D, int vpt) { return std::min(1024, (((D + kE * vpt - 1) / (kE * vpt) + 31) / 32) * 32); }
+// Rows too wide for registers: s and dy are read again (from L2) after the sums, and the
+// columns' share of dw stays in shared memory, each column its thread's own.
+template <typename TIn, typename TRes, bool VEC>
+__global__ void __launch_bounds__(kMostThreads)
+add_rmsnorm_bwd_wide_kernel(const TIn *__restrict__ dy, const TRes *__restrict__ s, const float *__restrict__ w,
+                            const TRes *__restrict__ dsum, TIn *__restrict__ dx, TRes *__restrict__ dres,
+                            float *__restrict__ part, long long rows, int D, float eps)
+{
+    extern __shared__ float acc[];
+    __shared__ float sm[2][64];
+    const int nt = blockDim.x, step = nt * kE, first = (int)threadIdx.x * kE;
+    for (int c = first; c < D; c += step)
+#pragma unroll
+        for (int i = 0; i < kE; ++i)
+            if (c + i < D) acc[c + i] = 0.f;
+    int turn = 0;
+    for (long long row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
+        float sums[2] = {0.f, 0.f}, sv[kE], gy[kE], g[kE], d[kE];
+        for (int c = first; c < D; c += step) {
+            load_n<kE, VEC>(s + row * D + c, sv, D - c);
+            load_n<kE, VEC>(dy + row * D + c, gy, D - c);
+            load_n<kE, VEC>(w + c, g, D - c);
+#pragma unroll
+            for (int i = 0; i < kE; ++i) {
+                sums[0] = fmaf(sv[i], sv[i], sums[0]);
+                sums[1] = fmaf(g[i] * gy[i], sv[i], sums[1]);
+            }
+        }
+        block_sum<2>(sums, sm[turn], nt >> 5);
+        const float rstd = rsqrtf(sums[0] / (float)D + eps);
+        const float m = rstd * rstd * (sums[1] / (float)D);
+        for (int c = first; c < D; c += step) {
+            load_n<kE, VEC>(s + row * D + c, sv, D - c);
+            load_n<kE, VEC>(dy + row * D + c, gy, D - c);
+            load_n<kE, VEC>(w + c, g, D - c);
+            load_n<kE, VEC>(dsum + row * D + c, d, dsum ? D - c : 0);
+#pragma unroll
+            for (int i = 0; i < kE; ++i) {
+                if (c + i < D) acc[c + i] = fmaf(gy[i], sv[i] * rstd, acc[c + i]);
+                d[i] = fmaf(rstd, g[i] * gy[i] - sv[i] * m, d[i]);
+            }
+            if (dx) store_n<kE, VEC>(dx + row * D + c, d, D - c);
+            if (dres) store_n<kE, VEC>(dres + row * D + c, d, D - c);
+        }
+    }
+    for (int c = first; c < D; c += step)
+#pragma unroll
+        for (int i = 0; i < kE; ++i)
+            if (c + i < D) part[(size_t)blockIdx.x * D + c + i] = acc[c + i];
+}
 
-// Vectors per thread: the fewest that fit 1024 threads, but two from 4096 channels on.
-int norm_vpt(int D) { return D < 4096 ? 1 : D <= 16384 ? 2 : 4; }
+// Vectors per thread: the fewest that fit 512 threads, but two from 4096 channels on.
+int norm_vpt(int D) { return D < 4096 ? 1 : D <= 8192 ? 2 : D <= 16384 ? 4 : 8; }
+constexpr int kWide = 8192;   // the gradient's rows past this are wide
+// Threads for D channels at vpt vectors of 8 each, in whole warps.
+int norm_threads(int D, int vpt) { return std::min(kMostThreads, (((D + kE * vpt - 1) / (kE * vpt) + 31) / 32) * 32); }
 
 template <typename TIn, typename TRes, int EIGHT, int VPT>
 void norm_run(const AddNormArgs &a, bool vec, cudaStream_t st)
@@ -261,9 +321,9 @@ void norm_pick(const AddNormArgs &a, bool vec, cudaStream_t st)
     const int v = norm_vpt(a.D);
     const int e = !a.scale ? 0 : a.group ? 2 : 1;
 #define LDN_NORM(E, V) norm_run<TIn, TRes, E, V>(a, vec, st)
-    if (e == 0) v == 1 ? LDN_NORM(0, 1) : v == 2 ? LDN_NORM(0, 2) : LDN_NORM(0, 4);
-    if (e == 1) v == 1 ? LDN_NORM(1, 1) : v == 2 ? LDN_NORM(1, 2) : LDN_NORM(1, 4);
-    if (e == 2) v == 1 ? LDN_NORM(2, 1) : v == 2 ? LDN_NORM(2, 2) : LDN_NORM(2, 4);
+    if (e == 0) v == 1 ? LDN_NORM(0, 1) : v == 2 ? LDN_NORM(0, 2) : v == 4 ? LDN_NORM(0, 4) : LDN_NORM(0, 8);
+    if (e == 1) v == 1 ? LDN_NORM(1, 1) : v == 2 ? LDN_NORM(1, 2) : v == 4 ? LDN_NORM(1, 4) : LDN_NORM(1, 8);
+    if (e == 2) v == 1 ? LDN_NORM(2, 1) : v == 2 ? LDN_NORM(2, 2) : v == 4 ? LDN_NORM(2, 4) : LDN_NORM(2, 8);
 #undef LDN_NORM
 }
 
@@ -283,43 +343,56 @@ void norm_bwd_run(const AddNormBwdArgs &a, int grid, bool vec, cudaStream_t st)
             a.part, a.rows, a.D, a.eps);
 }
 
-template <typename TIn, typename TRes>
-void norm_bwd_pick(const AddNormBwdArgs &a, int grid, bool vec, cudaStream_t st)
+template <typename TIn, typename TRes, bool VEC>
+cudaError_t norm_bwd_wide(const AddNormBwdArgs &a, int grid, cudaStream_t st)
 {
-    const int v = norm_vpt(a.D);
-    v == 1   ? norm_bwd_run<TIn, TRes, 1>(a, grid, vec, st)
-    : v == 2 ? norm_bwd_run<TIn, TRes, 2>(a, grid, vec, st)
-             : norm_bwd_run<TIn, TRes, 4>(a, grid, vec, st);
+    auto *k = add_rmsnorm_bwd_wide_kernel<TIn, TRes, VEC>;
+    const int bytes = a.D * (int)sizeof(float);
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    k<<<grid, kMostThreads, bytes, st>>>((const TIn *)a.dy, (const TRes *)a.s, a.weight, (const TRes *)a.dsum,
+                                         (TIn *)a.dx, (TRes *)a.dres, a.part, a.rows, a.D, a.eps);
+    return cudaGetLastError();
+}
+
+template <typename TIn, typename TRes>
+cudaError_t norm_bwd_pick(const AddNormBwdArgs &a, int grid, bool vec, cudaStream_t st)
+{
+    if (a.D > kWide) return vec ? norm_bwd_wide<TIn, TRes, true>(a, grid, st) : norm_bwd_wide<TIn, TRes, false>(a, grid, st);
+    if (norm_vpt(a.D) == 1) norm_bwd_run<TIn, TRes, 1>(a, grid, vec, st);
+    else norm_bwd_run<TIn, TRes, 2>(a, grid, vec, st);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_add_rmsnorm(const AddNormArgs &a, cudaStream_t st)
 {
-    const bool vec = a.D % kE == 0 && vec16(a.x) && vec16(a.residual) && vec16(a.residual_out) && vec16(a.y);
+    const bool vec = a.D % kE == 0 && vec16(a.x) && vec16(a.residual) && vec16(a.residual_out) &&
+                     vec16(a.weight) && (a.scale ? ((uintptr_t)a.y & 7u) == 0 : vec16(a.y));
     if (a.dtype == LDN_F32) norm_pick<float, float>(a, vec, st);
     else if (a.res_dtype == LDN_F32) norm_pick<__nv_bfloat16, float>(a, vec, st);
     else norm_pick<__nv_bfloat16, __nv_bfloat16>(a, vec, st);
     return cudaGetLastError();
 }
 
-// Blocks of the gradient's row walk: enough to fill the SMs (2048 threads each), no more than
-// rows.  A fixed 152 SMs, so that the workspace's size needs no device.
+// Blocks of the gradient's row walk: enough to fill the SMs (1024 threads each, one block of
+// wide rows), no more than rows.  A fixed 152 SMs, so that the workspace's size needs no device.
 int add_rmsnorm_bwd_blocks(long long rows, int D)
 {
-    const int per = std::max(1, 1024 / norm_threads(D, norm_vpt(D)));
+    const int per = D > kWide ? 1 : std::max(1, 1024 / norm_threads(D, norm_vpt(D)));
     return (int)std::min<long long>(rows, 152LL * per);
 }
 
 cudaError_t launch_add_rmsnorm_bwd(const AddNormBwdArgs &a, cudaStream_t st)
 {
-    const bool vec = a.D % kE == 0 && vec16(a.dy) && vec16(a.s) && vec16(a.dsum) && vec16(a.dx) && vec16(a.dres);
+    const bool vec = a.D % kE == 0 && vec16(a.dy) && vec16(a.s) && vec16(a.dsum) && vec16(a.dx) && vec16(a.dres) &&
+                     vec16(a.weight);
     const int grid = add_rmsnorm_bwd_blocks(a.rows, a.D);
     if (grid > 0) {
-        if (a.dtype == LDN_F32) norm_bwd_pick<float, float>(a, grid, vec, st);
-        else if (a.res_dtype == LDN_F32) norm_bwd_pick<__nv_bfloat16, float>(a, grid, vec, st);
-        else norm_bwd_pick<__nv_bfloat16, __nv_bfloat16>(a, grid, vec, st);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = a.dtype == LDN_F32       ? norm_bwd_pick<float, float>(a, grid, vec, st)
+                              : a.res_dtype == LDN_F32 ? norm_bwd_pick<__nv_bfloat16, float>(a, grid, vec, st)
+                                                       : norm_bwd_pick<__nv_bfloat16, __nv_bfloat16>(a, grid, vec, st);
         if (e != cudaSuccess) return e;
     }
     column_sum_kernel<<<(a.D + 31) / 32, dim3(32, 8), 0, st>>>(a.part, a.dweight, grid, a.D);

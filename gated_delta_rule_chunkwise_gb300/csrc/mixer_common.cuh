@@ -145,6 +145,47 @@ __device__ __forceinline__ float2 softplus_accurate(float2 x)
 }
 __device__ __forceinline__ float softplus_accurate(float x) { return softplus_accurate(make_float2(x, x)).x; }
 
+// N consecutive elements as loaded (16 bytes at a time where VEC): what is prefetched is kept
+// so, since widening it would wait for it.
+template <typename T, int N>
+struct Raw {
+    static constexpr int WORDS = N * (int)sizeof(T) / 4 < 1 ? 1 : N * (int)sizeof(T) / 4;
+    uint32_t w[WORDS];
+    template <bool VEC>
+    __device__ __forceinline__ void load(const T *p, int valid)
+    {
+        if constexpr (VEC && WORDS >= 4) {
+#pragma unroll
+            for (int i = 0; i < WORDS; i += 4) {
+                const uint4 q = valid > 0 ? reinterpret_cast<const uint4 *>(p)[i / 4] : make_uint4(0, 0, 0, 0);
+                w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
+            }
+        } else if constexpr (VEC) {
+            static_assert(WORDS == 2, "8- or 16-byte loads");
+            const uint2 q = valid > 0 ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0, 0);
+            w[0] = q.x; w[1] = q.y;
+        } else {
+            T *e = reinterpret_cast<T *>(w);
+#pragma unroll
+            for (int i = 0; i < N; ++i) e[i] = i < valid ? p[i] : T(0.f);
+        }
+    }
+    __device__ __forceinline__ void widen(float *v) const
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = __uint_as_float(w[i]);
+        } else if constexpr (N % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) bf16x2_widen(w[i / 2], v + i);
+        } else {
+            const T *e = reinterpret_cast<const T *>(w);
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = (float)e[i];
+        }
+    }
+};
+
 // x sigma(x) of two values.
 __device__ __forceinline__ float2 silu_fast(float2 x)
 {

@@ -19,6 +19,7 @@ namespace ldn {
 namespace {
 
 constexpr int kWarps = 4;   // runs per block, one warp each; all warps take the same channels
+constexpr int kBatch = 4;   // rows on their way at a time
 
 __device__ __forceinline__ int seq_len(const int *lens, int b, int T)
 {
@@ -71,25 +72,51 @@ short_conv_kernel(const ConvArgs a, int run, int runs, int cblocks)
             load_n<E, VEC>(x + (size_t)t * a.ldx, v, t < len ? valid : 0);
         }
     };
-    float win[W][E];
+    // win: the W - 1 rows before a batch, then the batch; the next batch is on its way as loaded
+    float win[W - 1 + kBatch][E];
+    Raw<TIn, E> next[kBatch];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            next[k].template load<VEC>(x + (size_t)(t + k) * a.ldx, t + k < min(len, t1) ? valid : 0);
+    };
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) row(t0 - (W - 1) + j, win[j]);
-    for (int t = t0; t < t1; ++t) {
-        row(t, win[W - 1]);
-        float p[E];
+    fetch(t0);
+    for (int t = t0; t < t1; t += kBatch) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            p[i] = bias[i];
+        for (int k = 0; k < kBatch; ++k) next[k].widen(win[W - 1 + k]);
+        fetch(t + kBatch);
 #pragma unroll
-            for (int j = 0; j < W; ++j) p[i] = fmaf(wt[j][i], win[j][i], p[i]);
-            if (a.act) p[i] *= sigmoid_fast(p[i]);
-            if (t >= len) p[i] = 0.f;
+        for (int k = 0; k < kBatch; ++k) {
+            float p[E];
+            if constexpr (E % 2 == 0) {
+#pragma unroll
+                for (int i = 0; i < E; i += 2) {
+                    float2 q = make_float2(bias[i], bias[i + 1]);
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        q = __ffma2_rn(make_float2(wt[j][i], wt[j][i + 1]),
+                                       make_float2(win[k + j][i], win[k + j][i + 1]), q);
+                    if (a.act) q = silu_fast(q);
+                    p[i] = q.x;
+                    p[i + 1] = q.y;
+                }
+            } else {
+                p[0] = bias[0];
+#pragma unroll
+                for (int j = 0; j < W; ++j) p[0] = fmaf(wt[j][0], win[k + j][0], p[0]);
+                if (a.act) p[0] *= sigmoid_fast(p[0]);
+            }
+            if (t + k >= len)
+#pragma unroll
+                for (int i = 0; i < E; ++i) p[i] = 0.f;
+            if (t + k < t1) store_n<E, VEC>(y + (size_t)(t + k) * a.C, p, valid);
         }
-        store_n<E, VEC>(y + (size_t)t * a.C, p, valid);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-            for (int i = 0; i < E; ++i) win[j][i] = win[j + 1][i];
+            for (int i = 0; i < E; ++i) win[j][i] = win[j + kBatch][i];
     }
     // The first run alone reads state rows (a run is at least W - 1 tokens), so its lanes may
     // write state_out over them once they have read the last rows.
@@ -181,53 +208,87 @@ short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
                 load_n<E, VEC>(x + (size_t)t * a.ldx, v, t < len ? valid : 0);
             }
         };
-        float win[W][E], dp[W][E];   // rows t-W+1 .. t of x, and of dp
+        // rows t-W+1 .. of x and of dp, a batch at a time; the next batch is on its way as loaded
+        float win[W - 1 + kBatch][E], dp[W - 1 + kBatch][E];
+        Raw<TIn, E> nx[kBatch], ny[kBatch];
+        auto fetch = [&](int t) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int n = t + k < min(len, t1 + W - 1) ? valid : 0;
+                nx[k].template load<VEC>(x + (size_t)(t + k) * a.ldx, n);
+                ny[k].template load<VEC>(dy + (size_t)(t + k) * a.C, n);
+            }
+        };
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             row(t0 - (W - 1) + j, win[j]);
 #pragma unroll
             for (int i = 0; i < E; ++i) dp[j][i] = 0.f;
         }
-        for (int t = t0; t < t1 + W - 1; ++t) {
-            row(t, win[W - 1]);
-            load_n<E, VEC>(dy + (size_t)t * a.C, dp[W - 1], t < len ? valid : 0);
+        fetch(t0);
+        for (int t = t0; t < t1 + W - 1; t += kBatch) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                if (a.act) {
-                    float p = bias[i];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) p = fmaf(wt[j][i], win[j][i], p);
-                    const float g = sigmoid_fast(p);
-                    // nothing flows from past the end, whatever p is there
-                    dp[W - 1][i] = t < len ? dp[W - 1][i] * (g * fmaf(p, 1.f - g, 1.f)) : 0.f;
-                }
-                if (t < t1) {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j][i] = fmaf(dp[W - 1][i], win[j][i], dw[j][i]);
-                    dw[W][i] += dp[W - 1][i];
-                }
+            for (int k = 0; k < kBatch; ++k) {
+                nx[k].widen(win[W - 1 + k]);
+                ny[k].widen(dp[W - 1 + k]);
             }
-            const int r = t - (W - 1);
-            if (r >= t0 || (ri == 0 && dst)) {
-                float d[E];
-                const int j0 = r - (len - (W - 1));   // this row's place in state_out
-                if (dso && j0 >= 0 && j0 < W - 1) load_n<E, VEC>(dso + (size_t)j0 * a.C, d, valid);
-                else
+            fetch(t + kBatch);
 #pragma unroll
-                    for (int i = 0; i < E; ++i) d[i] = 0.f;
+            for (int k = 0; k < kBatch; ++k) {
+                float *now = dp[W - 1 + k];
+                if constexpr (E % 2 == 0) {
 #pragma unroll
-                for (int i = 0; i < E; ++i)
+                    for (int i = 0; i < E; i += 2) {
+                        float2 d = make_float2(now[i], now[i + 1]);
+                        if (a.act) {
+                            float2 p = make_float2(bias[i], bias[i + 1]);
 #pragma unroll
-                    for (int j = 0; j < W; ++j) d[i] = fmaf(wt[W - 1 - j][i], dp[j][i], d[i]);
-                if (r >= 0) store_n<E, VEC>(dx + (size_t)r * a.C, d, valid);
-                else store_n<E, VEC>(dst + (size_t)(r + W - 1) * a.C, d, valid);
+                            for (int j = 0; j < W; ++j)
+                                p = __ffma2_rn(make_float2(wt[j][i], wt[j][i + 1]),
+                                               make_float2(win[k + j][i], win[k + j][i + 1]), p);
+                            const float2 g = rcp(__fadd2_rn(ex2(__fmul2_rn(p, dup(-kLog2e))), dup(1.f)));
+                            const float2 rest = __ffma2_rn(g, dup(-1.f), dup(1.f));
+                            d = __fmul2_rn(d, __fmul2_rn(g, __ffma2_rn(p, rest, dup(1.f))));
+                        }
+                        now[i] = d.x;
+                        now[i + 1] = d.y;
+                    }
+                } else if (a.act) {
+                    float p = bias[0];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) p = fmaf(wt[j][0], win[k + j][0], p);
+                    const float g = sigmoid_fast(p);
+                    now[0] *= g * fmaf(p, 1.f - g, 1.f);
+                }
+                if (t + k >= len)   // nothing flows from past the end, whatever p is there
+#pragma unroll
+                    for (int i = 0; i < E; ++i) now[i] = 0.f;
+                if (t + k < t1)
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+#pragma unroll
+                        for (int j = 0; j < W; ++j) dw[j][i] = fmaf(now[i], win[k + j][i], dw[j][i]);
+                        dw[W][i] += now[i];
+                    }
+                const int r = t + k - (W - 1);
+                if (r < t1 && (r >= t0 || (ri == 0 && dst))) {
+                    float d[E];
+                    const int j0 = r - (len - (W - 1));   // this row's place in state_out
+                    load_n<E, VEC>(dso + (dso ? (long long)j0 * a.C : 0), d, dso && j0 >= 0 && j0 < W - 1 ? valid : 0);
+#pragma unroll
+                    for (int i = 0; i < E; ++i)
+#pragma unroll
+                        for (int j = 0; j < W; ++j) d[i] = fmaf(wt[W - 1 - j][i], dp[k + j][i], d[i]);
+                    if (r >= 0) store_n<E, VEC>(dx + (size_t)r * a.C, d, valid);
+                    else store_n<E, VEC>(dst + (size_t)(r + W - 1) * a.C, d, valid);
+                }
             }
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    win[j][i] = win[j + 1][i];
-                    dp[j][i] = dp[j + 1][i];
+                    win[j][i] = win[j + kBatch][i];
+                    dp[j][i] = dp[j + kBatch][i];
                 }
         }
     }

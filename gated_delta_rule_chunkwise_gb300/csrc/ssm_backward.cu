@@ -87,39 +87,6 @@ constexpr int kTaken = 1;   // the last tile's red and ww have been read
 
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// Four neighbouring elements as loaded.
-template <typename T> struct Raw4;
-template <> struct Raw4<__nv_bfloat16> {
-    uint2 w;
-    __device__ __forceinline__ void widen(float2 *v) const
-    {
-        bf16x2_widen(w.x, reinterpret_cast<float *>(v));
-        bf16x2_widen(w.y, reinterpret_cast<float *>(v + 1));
-    }
-};
-template <> struct Raw4<float> {
-    float4 w;
-    __device__ __forceinline__ void widen(float2 *v) const
-    {
-        v[0] = make_float2(w.x, w.y);
-        v[1] = make_float2(w.z, w.w);
-    }
-};
-template <bool VEC, typename T>
-__device__ __forceinline__ Raw4<T> load_raw(const T *p, int valid)
-{
-    Raw4<T> q;
-    if constexpr (VEC) {
-        if (valid > 0) q.w = *reinterpret_cast<const decltype(q.w) *>(p);
-        else q.w = decltype(q.w){};
-    } else {
-        T *e = reinterpret_cast<T *>(&q.w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = i < valid ? p[i] : T(0.f);
-    }
-    return q;
-}
-
 // K neighbouring elements of a tile's B or C rows by each helper thread, widened to dst[TT][N].
 template <typename T, int N>
 __device__ __forceinline__ void rows_to_shared(float *dst, const T *src, long long ld, int rows, bool vec, int tid)
@@ -186,16 +153,16 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
 
         // A batch of rows is loaded before any of it is used: one latency for the batch.
         constexpr int ITEMS = TT * PR / 32, BATCH = ITEMS < 2 ? ITEMS : 2;
-        using Raw = Raw4<TIn>;
-        auto load_batch = [&](int t, int rows, int k0, Raw *ru, Raw *rd, Raw *ry, Raw *rz) {
+        using R4 = Raw<TIn, 4>;
+        auto load_batch = [&](int t, int rows, int k0, R4 *ru, R4 *rd, R4 *ry, R4 *rz) {
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
                 const int row = ((k0 + k) * 32 + lane) / PR, n = row < rows ? valid : 0;
                 const size_t at = t + row;
-                if (PHASE == kFull) ru[k] = load_raw<VEC>(u + at * a.ldu, n);
-                rd[k] = load_raw<VEC>(dl + at * a.ldd, n);
-                ry[k] = load_raw<VEC>(dy + at * a.D, n);
-                if (z) rz[k] = load_raw<VEC>(z + at * a.ldz, n);
+                if (PHASE == kFull) ru[k].template load<VEC>(u + at * a.ldu, n);
+                rd[k].template load<VEC>(dl + at * a.ldd, n);
+                ry[k].template load<VEC>(dy + at * a.D, n);
+                if (z) rz[k].template load<VEC>(z + at * a.ldz, n);
             }
         };
         // A tile's lines to L2, one iteration before they are loaded: a thread a row of a tensor,
@@ -219,7 +186,7 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
             const int rows = rows_of(it), t = it * TT;
 #pragma unroll 1
             for (int k0 = 0; k0 < ITEMS; k0 += BATCH) {
-                Raw ru[BATCH], rd[BATCH], ry[BATCH], rz[BATCH];
+                R4 ru[BATCH], rd[BATCH], ry[BATCH], rz[BATCH];
                 load_batch(t, rows, k0, ru, rd, ry, rz);
                 if (k0 == 0) {
                     if (PHASE == kFull)
@@ -230,10 +197,10 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
                 for (int k = 0; k < BATCH; ++k) {
                     const int row = ((k0 + k) * 32 + lane) / PR;
                     float2 vu[2] = {dup(0.f), dup(0.f)}, vd[2], vy[2], vz[2];
-                    if (PHASE == kFull) ru[k].widen(vu);
-                    rd[k].widen(vd);
-                    ry[k].widen(vy);
-                    if (z) rz[k].widen(vz);
+                    if (PHASE == kFull) ru[k].widen(reinterpret_cast<float *>(vu));
+                    rd[k].widen(reinterpret_cast<float *>(vd));
+                    ry[k].widen(reinterpret_cast<float *>(vy));
+                    if (z) rz[k].widen(reinterpret_cast<float *>(vz));
                     float4 *o = reinterpret_cast<float4 *>(sm.step[it & 1][warp] + row * ROW + 2 * ch);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
@@ -257,7 +224,7 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
             TIn *dz = z ? (TIn *)a.dz + (row0 + t) * a.D + cc : nullptr;
 #pragma unroll 1
             for (int k0 = 0; k0 < ITEMS; k0 += BATCH) {
-                Raw ru[BATCH], rd[BATCH], ry[BATCH], rz[BATCH];
+                R4 ru[BATCH], rd[BATCH], ry[BATCH], rz[BATCH];
                 load_batch(t, rows, k0, ru, rd, ry, rz);
                 if (k0 == 0)   // dB, dC of the block's channels, while the rows arrive
                     for (int i = tid; i < live * (2 * N / 4); i += kMain) {
@@ -275,10 +242,10 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
                 for (int k = 0; k < BATCH; ++k) {
                     const int row = ((k0 + k) * 32 + lane) / PR;
                     float2 vu[2], vd[2], vy[2], vz[2], pre[2], ww[2], oz[2], ou[2], od[2];
-                    ru[k].widen(vu);
-                    rd[k].widen(vd);
-                    ry[k].widen(vy);
-                    if (z) rz[k].widen(vz);
+                    ru[k].widen(reinterpret_cast<float *>(vu));
+                    rd[k].widen(reinterpret_cast<float *>(vd));
+                    ry[k].widen(reinterpret_cast<float *>(vy));
+                    if (z) rz[k].widen(reinterpret_cast<float *>(vz));
                     load_n<V, true>(sm.yb[it & 1][warp] + row * WC + ch, reinterpret_cast<float *>(pre));
                     load_n<V, true>(sm.ww[warp] + row * WC + ch, reinterpret_cast<float *>(ww));
                     const float4 *o = reinterpret_cast<const float4 *>(sm.step[it & 1][warp] + row * ROW + 2 * ch);
