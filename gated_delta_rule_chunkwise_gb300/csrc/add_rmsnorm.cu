@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kE = 8;   // channels per thread and vector
 constexpr int kMostThreads = 512;
+constexpr int kNormThreads = 768;   // an SM's threads in the row walk
 constexpr float kE4m3Max = 448.f;
 
 template <int NV>
@@ -84,79 +85,96 @@ __device__ __forceinline__ float as_stored(float x, const __nv_bfloat16 *)
     return __bfloat162float(__float2bfloat16_rn(x));
 }
 
-// EIGHT: 0 = y in TIn, 1 = e4m3 with a scale per row, 2 = per 128 channels.
+// EIGHT: 0 = y in TIn, 1 = e4m3 with a scale per row, 2 = per 128 channels.  A block walks rows
+// blockIdx.x, + gridDim.x, ...; the next row is on its way while one is summed and stored.
 template <typename TIn, typename TRes, int EIGHT, int VPT, bool VEC>
 __global__ void __launch_bounds__(kMostThreads)
 add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__restrict__ w, void *__restrict__ y,
-                   float *__restrict__ scale, TRes *r_out, int D, float eps)
+                   float *__restrict__ scale, TRes *r_out, long long rows, int D, float eps)
 {
-    __shared__ float sm[64];
-    const size_t row = blockIdx.x;
+    __shared__ float sm[2][64];
     const int nt = blockDim.x, nwarps = nt >> 5;
-    const TIn *xr = x + row * D;
-    constexpr bool AHEAD = VPT <= 4;   // the weights come with the row: not after the sum
-    float v[VPT][kE], g[AHEAD ? VPT : 1][kE], ss = 0.f;
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const int c = (k * nt + (int)threadIdx.x) * kE, valid = D - c;
-        load_n<kE, VEC>(xr + c, v[k], valid);
-        if constexpr (AHEAD) load_n<kE, VEC>(w + c, g[k], valid);
-        if (r) {
-            float q[kE];
-            load_n<kE, VEC>(r + row * D + c, q, valid);
-#pragma unroll
-            for (int i = 0; i < kE; ++i) v[k][i] = as_stored(v[k][i] + q[i], r);
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const int c = (k * nt + (int)threadIdx.x) * kE;
-        if (r) store_n<kE, VEC>(r_out + row * D + c, v[k], D - c);
-#pragma unroll
-        for (int i = 0; i < kE; ++i) ss = fmaf(v[k][i], v[k][i], ss);
-    }
-    block_sum<1>(&ss, sm, nwarps);
-    const float rstd = rsqrtf(ss / (float)D + eps);
-    float top = 0.f;
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const int c = (k * nt + (int)threadIdx.x) * kE, valid = D - c;
-        if constexpr (!AHEAD) load_n<kE, VEC>(w + c, g[0], valid);
-#pragma unroll
-        for (int i = 0; i < kE; ++i) v[k][i] *= rstd * g[AHEAD ? k : 0][i];
-        if constexpr (EIGHT == 0) {
-            store_n<kE, VEC>((TIn *)y + row * D + c, v[k], valid);
-        } else {
-            float m = 0.f;
-#pragma unroll
-            for (int i = 0; i < kE; ++i) m = fmaxf(m, fabsf(v[k][i]));
-            if constexpr (EIGHT == 2) {
-                // 128 channels are the 8-channel vectors of 16 neighbouring lanes
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                m = fmaxf(m, 0x1p-100f);
-                const float up = kE4m3Max / m;
-#pragma unroll
-                for (int i = 0; i < kE; ++i) v[k][i] *= up;
-                store_e4m3<kE, VEC>((uint8_t *)y + row * D + c, v[k], valid);
-                if ((threadIdx.x & 15) == 0 && valid > 0)
-                    scale[row * (size_t)((D + 127) / 128) + c / 128] = m / kE4m3Max;
-            } else {
-                top = fmaxf(top, m);
-            }
-        }
-    }
-    if constexpr (EIGHT == 1) {
-        top = fmaxf(block_max(top, sm + 32, nwarps), 0x1p-100f);
-        const float up = kE4m3Max / top;
+    constexpr bool KEEP = VPT <= 2;   // the weights stay in registers, the next row comes ahead
+    float g[KEEP ? VPT : 1][kE];
+    if constexpr (KEEP)
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = (k * nt + (int)threadIdx.x) * kE;
-#pragma unroll
-            for (int i = 0; i < kE; ++i) v[k][i] *= up;
-            store_e4m3<kE, VEC>((uint8_t *)y + row * D + c, v[k], D - c);
+            load_n<kE, VEC>(w + c, g[k], D - c);
         }
-        if (threadIdx.x == 0) scale[row] = top / kE4m3Max;
+    Raw<TIn, kE> rx[VPT];
+    Raw<TRes, kE> rr[VPT];
+    auto fetch = [&](long long row) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * nt + (int)threadIdx.x) * kE, valid = row < rows ? D - c : 0;
+            rx[k].template load<VEC>(x + row * D + c, valid);
+            rr[k].template load<VEC>(r + (r ? row * D + c : 0), r ? valid : 0);
+        }
+    };
+    fetch(blockIdx.x);
+    int turn = 0;
+    for (long long row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
+        float v[VPT][kE], ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * nt + (int)threadIdx.x) * kE;
+            rx[k].widen(v[k]);
+            if (r) {
+                float q[kE];
+                rr[k].widen(q);
+#pragma unroll
+                for (int i = 0; i < kE; ++i) v[k][i] = as_stored(v[k][i] + q[i], r);
+                store_n<kE, VEC>(r_out + row * D + c, v[k], D - c);
+            }
+#pragma unroll
+            for (int i = 0; i < kE; ++i) ss = fmaf(v[k][i], v[k][i], ss);
+        }
+        if constexpr (KEEP) fetch(row + gridDim.x);
+        block_sum<1>(&ss, sm[turn], nwarps);   // two buffers: the next row's sums pass no reader of these
+        const float rstd = rsqrtf(ss / (float)D + eps);
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = (k * nt + (int)threadIdx.x) * kE, valid = D - c;
+            if constexpr (!KEEP) load_n<kE, VEC>(w + c, g[0], valid);
+#pragma unroll
+            for (int i = 0; i < kE; ++i) v[k][i] *= rstd * g[KEEP ? k : 0][i];
+            if constexpr (EIGHT == 0) {
+                store_n<kE, VEC>((TIn *)y + row * D + c, v[k], valid);
+            } else {
+                float m = 0.f;
+#pragma unroll
+                for (int i = 0; i < kE; ++i) m = fmaxf(m, fabsf(v[k][i]));
+                if constexpr (EIGHT == 2) {
+                    // 128 channels are the 8-channel vectors of 16 neighbouring lanes
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    m = fmaxf(m, 0x1p-100f);
+                    const float up = kE4m3Max / m;
+#pragma unroll
+                    for (int i = 0; i < kE; ++i) v[k][i] *= up;
+                    store_e4m3<kE, VEC>((uint8_t *)y + row * D + c, v[k], valid);
+                    if ((threadIdx.x & 15) == 0 && valid > 0)
+                        scale[row * (long long)((D + 127) / 128) + c / 128] = m / kE4m3Max;
+                } else {
+                    top = fmaxf(top, m);
+                }
+            }
+        }
+        if constexpr (EIGHT == 1) {
+            top = fmaxf(block_max(top, sm[turn] + 32, nwarps), 0x1p-100f);
+            const float up = kE4m3Max / top;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int c = (k * nt + (int)threadIdx.x) * kE;
+#pragma unroll
+                for (int i = 0; i < kE; ++i) v[k][i] *= up;
+                store_e4m3<kE, VEC>((uint8_t *)y + row * D + c, v[k], D - c);
+            }
+            if (threadIdx.x == 0) scale[row] = top / kE4m3Max;
+        }
+        if constexpr (!KEEP) fetch(row + gridDim.x);
     }
 }
 
@@ -306,13 +324,16 @@ int norm_threads(int D, int vpt) { return std::min(kMostThreads, (((D + kE * vpt
 template <typename TIn, typename TRes, int EIGHT, int VPT>
 void norm_run(const AddNormArgs &a, bool vec, cudaStream_t st)
 {
-    const dim3 grid((unsigned)a.rows), block(norm_threads(a.D, VPT));
+    const int nt = norm_threads(a.D, VPT);
+    const dim3 grid((unsigned)std::min<long long>(a.rows, 152LL * std::max(1, kNormThreads / nt))), block(nt);
     if (vec)
         add_rmsnorm_kernel<TIn, TRes, EIGHT, VPT, true><<<grid, block, 0, st>>>(
-            (const TIn *)a.x, (const TRes *)a.residual, a.weight, a.y, a.scale, (TRes *)a.residual_out, a.D, a.eps);
+            (const TIn *)a.x, (const TRes *)a.residual, a.weight, a.y, a.scale, (TRes *)a.residual_out, a.rows, a.D,
+            a.eps);
     else
         add_rmsnorm_kernel<TIn, TRes, EIGHT, VPT, false><<<grid, block, 0, st>>>(
-            (const TIn *)a.x, (const TRes *)a.residual, a.weight, a.y, a.scale, (TRes *)a.residual_out, a.D, a.eps);
+            (const TIn *)a.x, (const TRes *)a.residual, a.weight, a.y, a.scale, (TRes *)a.residual_out, a.rows, a.D,
+            a.eps);
 }
 
 template <typename TIn, typename TRes>

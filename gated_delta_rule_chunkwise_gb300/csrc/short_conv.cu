@@ -138,20 +138,18 @@ __global__ void __launch_bounds__(128) short_conv_step_kernel(const ConvArgs a)
     const long long id = (long long)blockIdx.x * 128 + threadIdx.x;
     if (id >= (long long)a.B * per) return;
     const int b = (int)(id / per), c = (int)(id % per) * E, valid = a.C - c;
-    float rows[W][E], p[E];
+    float rows[W][E], p[E], wt[E * W];
+    load_n<E * W, VEC>(a.w + (size_t)c * W, wt, valid * W);   // taps of one channel after another
     const TIn *st = (const TIn *)a.state + (size_t)b * (W - 1) * a.C + c;
     TIn *so = (TIn *)a.state_out + (size_t)b * (W - 1) * a.C + c;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) load_n<E, VEC>(st + (size_t)j * a.C, rows[j], valid);
     load_n<E, VEC>((const TIn *)a.x + (size_t)b * a.ldx + c, rows[W - 1], valid);
+    load_n<E, VEC>(a.bias + (a.bias ? c : 0), p, a.bias ? valid : 0);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-        p[i] = 0.f;
-        if (i < valid) {
-            if (a.bias) p[i] = __ldg(a.bias + c + i);
 #pragma unroll
-            for (int j = 0; j < W; ++j) p[i] = fmaf(__ldg(a.w + (size_t)(c + i) * W + j), rows[j][i], p[i]);
-        }
+        for (int j = 0; j < W; ++j) p[i] = fmaf(wt[i * W + j], rows[j][i], p[i]);
         if (a.act) p[i] *= sigmoid_fast(p[i]);
     }
     store_n<E, VEC>((TIn *)a.y + (size_t)b * a.C + c, p, valid);
@@ -327,12 +325,12 @@ conv_param_sum_kernel(const float *__restrict__ part, float *__restrict__ dw, fl
 }
 
 // Tokens of a run: long enough that the W - 1 rows read twice cost little, short enough that
-// every SM has warps.
+// every SM has the 24 warps whose rows on their way (2 KB a warp) keep HBM busy.
 int conv_run(int B, int T, int C, int e)
 {
     const long long lanes = (long long)B * ((C + 32 * e - 1) / (32 * e));   // warps per token run
     int run = 64;
-    while (run > 8 && lanes * ((T + run - 1) / run) < 152 * 16) run /= 2;
+    while (run > 8 && lanes * ((T + run - 1) / run) < 152 * 24) run /= 2;
     return run;
 }
 
@@ -355,9 +353,10 @@ cudaError_t conv_fwd(const ConvArgs &a, cudaStream_t st)
 template <typename TIn, int W>
 cudaError_t conv_step(const ConvArgs &a, cudaStream_t st)
 {
-    constexpr int E = 16 / sizeof(TIn);
-    const bool vec = a.C % E == 0 && a.ldx % E == 0 && aligned_to(a.x, 16) && aligned_to(a.y, 16) &&
-                     aligned_to(a.state, 16) && aligned_to(a.state_out, 16);
+    constexpr int E = 4, A = E * (int)sizeof(TIn);   // a token's work is latency: many small threads
+    const bool vec = a.C % E == 0 && a.ldx % E == 0 && aligned_to(a.x, A) && aligned_to(a.y, A) &&
+                     aligned_to(a.state, A) && aligned_to(a.state_out, A) && aligned_to(a.w, 16) &&
+                     aligned_to(a.bias, 16);
     const long long n = (long long)a.B * ((a.C + (vec ? E : 1) - 1) / (vec ? E : 1));
     const unsigned blocks = (unsigned)((n + 127) / 128);
     if (vec) short_conv_step_kernel<TIn, W, E, true><<<blocks, 128, 0, st>>>(a);

@@ -303,41 +303,55 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
 }
 
 // One token for every sequence: a lane takes four states of one channel, the channel's lanes
-// sum; h is read and written once, which is nearly all of the traffic.
-template <typename TIn, int N>
+// sum; h is read and written once, which is nearly all of the traffic.  A lane goes through
+// kStepB sequences at once: their loads are in flight together, and A is read once for them.
+constexpr int kStepB = 2;
+
+template <typename TIn, int N, bool VEC>
 __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmArgs a)
 {
     constexpr int L = N / 4;
-    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-    const long long unit = id / L;
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x, unit = id / L;
     const int l = (int)(id % L);
-    const bool on = unit < (long long)a.B * a.D;
-    const int b = on ? (int)(unit / a.D) : 0, d = on ? (int)(unit % a.D) : 0, g = d / (a.D / a.G);
-    const TIn *Bm = (const TIn *)a.Bm + (size_t)b * a.ldb + g * N + l * 4;
-    const TIn *Cm = (const TIn *)a.Cm + (size_t)b * a.ldc + g * N + l * 4;
-    const size_t at = ((size_t)b * a.D + d) * N + l * 4;
-    const float4 hv = *reinterpret_cast<const float4 *>(a.h0 + at);
-    float h[4] = {hv.x, hv.y, hv.z, hv.w}, Av[4], y = 0.f;
-    load_n<4, false>(a.A + (size_t)d * N + l * 4, Av);
-    const float u = load_in((const TIn *)a.u, (size_t)b * a.ldu + d);
-    float dt = load_in((const TIn *)a.delta, (size_t)b * a.ldd + d) + (a.bias ? a.bias[d] : 0.f);
-    if (a.softplus) dt = softplus_accurate(dt);
-    const float du = dt * u;
+    const long long groups = (a.B + kStepB - 1) / kStepB;
+    const bool on = unit < groups * a.D;
+    const int d = on ? (int)(unit % a.D) : 0, g = d / (a.D / a.G), b0 = on ? (int)(unit / a.D) * kStepB : 0;
+    float Av[4], h[kStepB][4], Bv[kStepB][4], Cv[kStepB][4], u[kStepB], dt[kStepB], z[kStepB], y[kStepB];
+    load_n<4, VEC>(a.A + (size_t)d * N + l * 4, Av);
+    const float bias = a.bias ? a.bias[d] : 0.f, skip = a.Dskip ? a.Dskip[d] : 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i] = fmaf(ex2(dt * (Av[i] * kLog2e)), h[i], du * load_in(Bm, i));
-        y = fmaf(load_in(Cm, i), h[i], y);
+    for (int k = 0; k < kStepB; ++k) {
+        const int b = min(b0 + k, a.B - 1);   // past the last: that one again, not stored
+        load_n<4, true>(a.h0 + ((size_t)b * a.D + d) * N + l * 4, h[k]);
+        load_n<4, VEC>((const TIn *)a.Bm + (size_t)b * a.ldb + g * N + l * 4, Bv[k]);
+        load_n<4, VEC>((const TIn *)a.Cm + (size_t)b * a.ldc + g * N + l * 4, Cv[k]);
+        u[k] = load_in((const TIn *)a.u, (size_t)b * a.ldu + d);
+        dt[k] = load_in((const TIn *)a.delta, (size_t)b * a.ldd + d) + bias;
+        z[k] = a.z ? load_in((const TIn *)a.z, (size_t)b * a.ldz + d) : 0.f;
     }
-    if (on) *reinterpret_cast<float4 *>(a.h_final + at) = make_float4(h[0], h[1], h[2], h[3]);
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (on && l == 0) {
-        if (a.Dskip) y = fmaf(a.Dskip[d], u, y);
-        if (a.z) {
-            const float z = load_in((const TIn *)a.z, (size_t)b * a.ldz + d);
-            y *= z * sigmoid_fast(z);
+    for (int k = 0; k < kStepB; ++k) {
+        if (a.softplus) dt[k] = softplus_accurate(dt[k]);
+        const float du = dt[k] * u[k];
+        y[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[k][i] = fmaf(ex2(dt[k] * (Av[i] * kLog2e)), h[k][i], du * Bv[k][i]);
+            y[k] = fmaf(Cv[k][i], h[k][i], y[k]);
         }
-        store_out((TIn *)a.y, (size_t)b * a.D + d, y);
+    }
+#pragma unroll
+    for (int k = 0; k < kStepB; ++k) {
+        const bool mine = on && b0 + k < a.B;
+        const size_t row = (size_t)(b0 + k) * a.D + d;
+        if (mine) store_n<4, true>(a.h_final + row * N + l * 4, h[k]);
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) y[k] += __shfl_xor_sync(0xffffffffu, y[k], o);
+        if (mine && l == 0) {
+            float v = fmaf(skip, u[k], y[k]);
+            if (a.z) v *= z[k] * sigmoid_fast(z[k]);
+            store_out((TIn *)a.y, row, v);
+        }
     }
 }
 
@@ -412,8 +426,15 @@ cudaError_t scan_pick(const SsmArgs &a, cudaStream_t st)
 template <typename TIn, int N>
 cudaError_t step_run(const SsmArgs &a, cudaStream_t st)
 {
-    const long long n = (long long)a.B * a.D * (N / 4);
-    ssm_step_kernel<TIn, N><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
+    constexpr int A = 4 * (int)sizeof(TIn);
+    auto ok = [](const void *p, long long ld) {
+        return (((uintptr_t)p | (uintptr_t)(ld * (long long)sizeof(TIn))) & (A - 1)) == 0;
+    };
+    const bool vec = ok(a.Bm, a.ldb) && ok(a.Cm, a.ldc) && ((uintptr_t)a.A & 15u) == 0;
+    const long long n = (long long)((a.B + kStepB - 1) / kStepB) * a.D * (N / 4);
+    const unsigned blocks = (unsigned)((n + 255) / 256);
+    if (vec) ssm_step_kernel<TIn, N, true><<<blocks, 256, 0, st>>>(a);
+    else ssm_step_kernel<TIn, N, false><<<blocks, 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 
