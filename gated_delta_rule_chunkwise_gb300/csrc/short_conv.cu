@@ -9,50 +9,58 @@
 //   dp_t = dy_t silu'(p_t),   dx_t = sum_j w[j] dp_{t+W-1-j} (+ dstate_out's row),
 //   dw[j] = sum_t dp_t x_{t-W+1+j},   db = sum_t dp_t.
 //
-// Every direction streams its rows once and is bound by HBM.  A lane owns 16 bytes of a row
-// (8 bf16 / 4 fp32 channels; the gradient 4 channels) and walks a run of tokens with the last
-// W rows in registers, so nothing goes through shared memory but the weights; a warp covers
-// 512 contiguous bytes of every row.
+// Every direction streams its rows once and is bound by HBM.  A lane owns four channels and
+// walks a run of tokens with the last W rows in registers, so nothing goes through shared
+// memory but the weights; rows are loaded a batch ahead and kept as loaded until used.
+#include <type_traits>
+
 #include "mixer_common.cuh"
 
 namespace ldn {
 namespace {
 
 constexpr int kWarps = 4;   // runs per block, one warp each; all warps take the same channels
-constexpr int kBatch = 4;   // rows on their way at a time
+// Rows on their way at a time, and the registers a thread that leaves (blocks an SM): what
+// measured fastest of 2, 3, 4 rows and 4 to 10 blocks at 4 x 2048 x 4096 (forward: 31 us, 33 at
+// two rows, 42 with 16-byte loads and twice the registers; gradient at half the channels 39 us).
+constexpr int kBatch = 4, kBwdBatch = 3;
+constexpr int fwd_blocks(int W) { return W <= 4 ? 7 : 4; }
+constexpr int bwd_blocks(int W) { return W <= 4 ? 4 : 2; }
+constexpr int kE = 4;   // channels a lane
 
 __device__ __forceinline__ int seq_len(const int *lens, int b, int T)
 {
     return lens ? min(max(lens[b], 0), T) : T;
 }
 
-// The block's weights to shared memory, tap by tap: wsm[j][32 * E].
-template <int W, int E>
+// The weights of CH channels from c0 to shared memory, tap by tap: wsm[j][CH].
+template <int W, int CH>
 __device__ __forceinline__ void load_taps(float *wsm, const float *w, int c0, int C)
 {
-    for (int i = threadIdx.x; i < 32 * E * W; i += blockDim.x) {
+    for (int i = threadIdx.x; i < CH * W; i += blockDim.x) {
         const int c = i / W, j = i % W;
-        wsm[j * 32 * E + c] = c0 + c < C ? __ldg(w + (size_t)(c0 + c) * W + j) : 0.f;
+        wsm[j * CH + c] = c0 + c < C ? __ldg(w + (size_t)(c0 + c) * W + j) : 0.f;
     }
     __syncthreads();
 }
 
+// A block is one run of tokens; its warps take neighbouring channels, so that it reads and
+// writes 1 KB (bf16) of every row.
 template <typename TIn, int W, int E, bool VEC>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, fwd_blocks(W))
 short_conv_kernel(const ConvArgs a, int run, int runs, int cblocks)
 {
-    __shared__ __align__(16) float wsm[W * 32 * E];
+    constexpr int CH = 32 * kWarps * E;
+    __shared__ __align__(16) float wsm[W * CH];
     const int cb = blockIdx.x % cblocks;
     const unsigned rb = blockIdx.x / cblocks;
-    const int rblocks = (runs + kWarps - 1) / kWarps;
-    const int b = (int)(rb / rblocks), ri = (int)(rb % rblocks) * kWarps + (threadIdx.x >> 5);
-    const int c0 = cb * 32 * E, lane = threadIdx.x & 31;
-    load_taps<W, E>(wsm, a.w, c0, a.C);
-    const int c = c0 + lane * E, valid = a.C - c;
-    if (ri >= runs || valid <= 0) return;
+    const int b = (int)(rb / runs), ri = (int)(rb % runs);
+    load_taps<W, CH>(wsm, a.w, cb * CH, a.C);
+    const int at = (int)threadIdx.x * E, c = cb * CH + at, valid = a.C - c;
+    if (valid <= 0) return;
     float wt[W][E], bias[E];
 #pragma unroll
-    for (int j = 0; j < W; ++j) load_n<E, (E % 4 == 0)>(&wsm[j * 32 * E + lane * E], wt[j]);
+    for (int j = 0; j < W; ++j) load_n<E, (E % 4 == 0)>(&wsm[j * CH + at], wt[j]);
     if (a.bias) load_n<E, false>(a.bias + c, bias, valid);
     else
 #pragma unroll
@@ -75,18 +83,18 @@ short_conv_kernel(const ConvArgs a, int run, int runs, int cblocks)
     // win: the W - 1 rows before a batch, then the batch; the next batch is on its way as loaded
     float win[W - 1 + kBatch][E];
     Raw<TIn, E> next[kBatch];
-    auto fetch = [&](int t) {
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            next[k].template load<VEC>(x + (size_t)(t + k) * a.ldx, t + k < min(len, t1) ? valid : 0);
-    };
+    const int stop = min(len, t1);   // rows past it are not read
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) row(t0 - (W - 1) + j, win[j]);
-    fetch(t0);
-    for (int t = t0; t < t1; t += kBatch) {
+    // EDGE: some of the batch's rows or of the next one's may be outside
+    auto batch = [&](int t, auto edge) {
+        constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) next[k].widen(win[W - 1 + k]);
-        fetch(t + kBatch);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            next[k].template load<VEC>(x + (size_t)(t + kBatch + k) * a.ldx,
+                                       !EDGE || t + kBatch + k < stop ? valid : 0);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             float p[E];
@@ -108,15 +116,22 @@ short_conv_kernel(const ConvArgs a, int run, int runs, int cblocks)
                 for (int j = 0; j < W; ++j) p[0] = fmaf(wt[j][0], win[k + j][0], p[0]);
                 if (a.act) p[0] *= sigmoid_fast(p[0]);
             }
-            if (t + k >= len)
+            if (EDGE && t + k >= len)
 #pragma unroll
                 for (int i = 0; i < E; ++i) p[i] = 0.f;
-            if (t + k < t1) store_n<E, VEC>(y + (size_t)(t + k) * a.C, p, valid);
+            if (!EDGE || t + k < t1) store_n<E, VEC>(y + (size_t)(t + k) * a.C, p, valid);
         }
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
 #pragma unroll
             for (int i = 0; i < E; ++i) win[j][i] = win[j + kBatch][i];
+    };
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+        next[k].template load<VEC>(x + (size_t)(t0 + k) * a.ldx, t0 + k < stop ? valid : 0);
+    for (int t = t0; t < t1; t += kBatch) {
+        if (t + 2 * kBatch <= stop) batch(t, std::false_type{});
+        else batch(t, std::true_type{});
     }
     // The first run alone reads state rows (a run is at least W - 1 tokens), so its lanes may
     // write state_out over them once they have read the last rows.
@@ -162,7 +177,7 @@ __global__ void __launch_bounds__(128) short_conv_step_kernel(const ConvArgs a)
 // rows (t < 0).  dw and db over the run's own tokens, summed over the block's warps, go to
 // part [rblocks * B][W + 1][C].
 template <typename TIn, int W, int E, bool VEC>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, bwd_blocks(W))
 short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
 {
     __shared__ __align__(16) float wsm[W * 32 * E];
@@ -173,7 +188,7 @@ short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = (int)(rb / rblocks), ri = (int)(rb % rblocks) * kWarps + warp;
     const int c0 = cb * 32 * E;
-    load_taps<W, E>(wsm, a.w, c0, a.C);
+    load_taps<W, 32 * E>(wsm, a.w, c0, a.C);
     const int c = c0 + lane * E, valid = a.C - c;
     float dw[W + 1][E];
 #pragma unroll
@@ -207,12 +222,13 @@ short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
             }
         };
         // rows t-W+1 .. of x and of dp, a batch at a time; the next batch is on its way as loaded
-        float win[W - 1 + kBatch][E], dp[W - 1 + kBatch][E];
-        Raw<TIn, E> nx[kBatch], ny[kBatch];
-        auto fetch = [&](int t) {
+        float win[W - 1 + kBwdBatch][E], dp[W - 1 + kBwdBatch][E];
+        Raw<TIn, E> nx[kBwdBatch], ny[kBwdBatch];
+        const int end = t1 + W - 1, stop = min(len, end);   // dp_t to end; rows past stop are not read
+        auto fetch = [&](int t, auto edge) {
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int n = t + k < min(len, t1 + W - 1) ? valid : 0;
+            for (int k = 0; k < kBwdBatch; ++k) {
+                const int n = !decltype(edge)::value || t + k < stop ? valid : 0;
                 nx[k].template load<VEC>(x + (size_t)(t + k) * a.ldx, n);
                 ny[k].template load<VEC>(dy + (size_t)(t + k) * a.C, n);
             }
@@ -223,16 +239,17 @@ short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
 #pragma unroll
             for (int i = 0; i < E; ++i) dp[j][i] = 0.f;
         }
-        fetch(t0);
-        for (int t = t0; t < t1 + W - 1; t += kBatch) {
+        // EDGE: some of the batch's rows, of those it finishes or of the next ones may be outside
+        auto batch = [&](int t, auto edge) {
+            constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
+            for (int k = 0; k < kBwdBatch; ++k) {
                 nx[k].widen(win[W - 1 + k]);
                 ny[k].widen(dp[W - 1 + k]);
             }
-            fetch(t + kBatch);
+            fetch(t + kBwdBatch, edge);
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
+            for (int k = 0; k < kBwdBatch; ++k) {
                 float *now = dp[W - 1 + k];
                 if constexpr (E % 2 == 0) {
 #pragma unroll
@@ -248,36 +265,61 @@ short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
                             const float2 rest = __ffma2_rn(g, dup(-1.f), dup(1.f));
                             d = __fmul2_rn(d, __fmul2_rn(g, __ffma2_rn(p, rest, dup(1.f))));
                         }
+                        if (EDGE && t + k >= len) d = dup(0.f);   // nothing flows from past the end, whatever p is
                         now[i] = d.x;
                         now[i + 1] = d.y;
-                    }
-                } else if (a.act) {
-                    float p = bias[0];
+                        if (!EDGE || t + k < t1) {
 #pragma unroll
-                    for (int j = 0; j < W; ++j) p = fmaf(wt[j][0], win[k + j][0], p);
-                    const float g = sigmoid_fast(p);
-                    now[0] *= g * fmaf(p, 1.f - g, 1.f);
+                            for (int j = 0; j < W; ++j) {
+                                const float2 q = __ffma2_rn(d, make_float2(win[k + j][i], win[k + j][i + 1]),
+                                                            make_float2(dw[j][i], dw[j][i + 1]));
+                                dw[j][i] = q.x;
+                                dw[j][i + 1] = q.y;
+                            }
+                            const float2 q = __fadd2_rn(d, make_float2(dw[W][i], dw[W][i + 1]));
+                            dw[W][i] = q.x;
+                            dw[W][i + 1] = q.y;
+                        }
+                    }
+                } else {
+                    if (a.act) {
+                        float p = bias[0];
+#pragma unroll
+                        for (int j = 0; j < W; ++j) p = fmaf(wt[j][0], win[k + j][0], p);
+                        const float g = sigmoid_fast(p);
+                        now[0] *= g * fmaf(p, 1.f - g, 1.f);
+                    }
+                    if (EDGE && t + k >= len) now[0] = 0.f;
+                    if (!EDGE || t + k < t1) {
+#pragma unroll
+                        for (int j = 0; j < W; ++j) dw[j][0] = fmaf(now[0], win[k + j][0], dw[j][0]);
+                        dw[W][0] += now[0];
+                    }
                 }
-                if (t + k >= len)   // nothing flows from past the end, whatever p is there
-#pragma unroll
-                    for (int i = 0; i < E; ++i) now[i] = 0.f;
-                if (t + k < t1)
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][i] = fmaf(now[i], win[k + j][i], dw[j][i]);
-                        dw[W][i] += now[i];
-                    }
-                const int r = t + k - (W - 1);
-                if (r < t1 && (r >= t0 || (ri == 0 && dst))) {
+                const int r = t + k - (W - 1);   // the row that dp_{t + k} completes
+                if (!EDGE || (r < t1 && (r >= t0 || (ri == 0 && dst)))) {
                     float d[E];
-                    const int j0 = r - (len - (W - 1));   // this row's place in state_out
-                    load_n<E, VEC>(dso + (dso ? (long long)j0 * a.C : 0), d, dso && j0 >= 0 && j0 < W - 1 ? valid : 0);
+                    const int j0 = r - (len - (W - 1));   // its place in state_out
+                    if (EDGE && dso && j0 >= 0 && j0 < W - 1) load_n<E, VEC>(dso + (size_t)j0 * a.C, d, valid);
+                    else
 #pragma unroll
-                    for (int i = 0; i < E; ++i)
+                        for (int i = 0; i < E; ++i) d[i] = 0.f;
+                    if constexpr (E % 2 == 0) {
 #pragma unroll
-                        for (int j = 0; j < W; ++j) d[i] = fmaf(wt[W - 1 - j][i], dp[k + j][i], d[i]);
-                    if (r >= 0) store_n<E, VEC>(dx + (size_t)r * a.C, d, valid);
+                        for (int i = 0; i < E; i += 2) {
+                            float2 q = make_float2(d[i], d[i + 1]);
+#pragma unroll
+                            for (int j = 0; j < W; ++j)
+                                q = __ffma2_rn(make_float2(wt[W - 1 - j][i], wt[W - 1 - j][i + 1]),
+                                               make_float2(dp[k + j][i], dp[k + j][i + 1]), q);
+                            d[i] = q.x;
+                            d[i + 1] = q.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < W; ++j) d[0] = fmaf(wt[W - 1 - j][0], dp[k + j][0], d[0]);
+                    }
+                    if (!EDGE || r >= 0) store_n<E, VEC>(dx + (long long)r * a.C, d, valid);
                     else store_n<E, VEC>(dst + (size_t)(r + W - 1) * a.C, d, valid);
                 }
             }
@@ -285,9 +327,14 @@ short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
             for (int j = 0; j < W - 1; ++j)
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    win[j][i] = win[j + kBatch][i];
-                    dp[j][i] = dp[j + kBatch][i];
+                    win[j][i] = win[j + kBwdBatch][i];
+                    dp[j][i] = dp[j + kBwdBatch][i];
                 }
+        };
+        fetch(t0, std::true_type{});
+        for (int t = t0; t < end; t += kBwdBatch) {
+            if (t >= t0 + W - 1 && t + kBwdBatch <= t1 && t + 2 * kBwdBatch <= stop) batch(t, std::false_type{});
+            else batch(t, std::true_type{});
         }
     }
 #pragma unroll
@@ -339,12 +386,12 @@ bool aligned_to(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0;
 template <typename TIn, int W>
 cudaError_t conv_fwd(const ConvArgs &a, cudaStream_t st)
 {
-    constexpr int E = 16 / sizeof(TIn);
-    const bool vec = a.C % E == 0 && a.ldx % E == 0 && aligned_to(a.x, 16) && aligned_to(a.y, 16) &&
-                     aligned_to(a.state, 16) && aligned_to(a.state_out, 16);
+    constexpr int E = kE, A = E * (int)sizeof(TIn);
+    const bool vec = a.C % E == 0 && a.ldx % E == 0 && aligned_to(a.x, A) && aligned_to(a.y, A) &&
+                     aligned_to(a.state, A) && aligned_to(a.state_out, A);
     const int run = conv_run(a.B, a.T, a.C, vec ? E : 1), runs = std::max(1, (a.T + run - 1) / run);
-    const int cblocks = (a.C + 32 * (vec ? E : 1) - 1) / (32 * (vec ? E : 1));
-    const long long blocks = (long long)cblocks * a.B * ((runs + kWarps - 1) / kWarps);
+    const int per = 32 * kWarps * (vec ? E : 1), cblocks = (a.C + per - 1) / per;
+    const long long blocks = (long long)cblocks * a.B * runs;
     if (vec) short_conv_kernel<TIn, W, E, true><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
     else short_conv_kernel<TIn, W, 1, false><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
     return cudaGetLastError();
@@ -353,7 +400,7 @@ cudaError_t conv_fwd(const ConvArgs &a, cudaStream_t st)
 template <typename TIn, int W>
 cudaError_t conv_step(const ConvArgs &a, cudaStream_t st)
 {
-    constexpr int E = 4, A = E * (int)sizeof(TIn);   // a token's work is latency: many small threads
+    constexpr int E = kE, A = E * (int)sizeof(TIn);
     const bool vec = a.C % E == 0 && a.ldx % E == 0 && aligned_to(a.x, A) && aligned_to(a.y, A) &&
                      aligned_to(a.state, A) && aligned_to(a.state_out, A) && aligned_to(a.w, 16) &&
                      aligned_to(a.bias, 16);
@@ -364,20 +411,19 @@ cudaError_t conv_step(const ConvArgs &a, cudaStream_t st)
     return cudaGetLastError();
 }
 
-constexpr int kBwdE = 4;
 
 template <typename TIn, int W>
 cudaError_t conv_bwd(const ConvBwdArgs &a, cudaStream_t st)
 {
-    constexpr int A = kBwdE * sizeof(TIn);
-    const bool vec = a.C % kBwdE == 0 && a.ldx % kBwdE == 0 && aligned_to(a.x, A) && aligned_to(a.dy, A) &&
+    constexpr int A = kE * sizeof(TIn);
+    const bool vec = a.C % kE == 0 && a.ldx % kE == 0 && aligned_to(a.x, A) && aligned_to(a.dy, A) &&
                      aligned_to(a.dx, A) && aligned_to(a.state, A) && aligned_to(a.dstate, A) &&
                      aligned_to(a.dstate_out, A);
     // the run goes by 4 channels a lane whatever the alignment: the workspace's size follows it
-    const int run = conv_run(a.B, a.T, a.C, kBwdE), runs = std::max(1, (a.T + run - 1) / run);
-    const int per = 32 * (vec ? kBwdE : 1), cblocks = (a.C + per - 1) / per;
+    const int run = conv_run(a.B, a.T, a.C, kE), runs = std::max(1, (a.T + run - 1) / run);
+    const int per = 32 * (vec ? kE : 1), cblocks = (a.C + per - 1) / per;
     const long long blocks = (long long)cblocks * a.B * ((runs + kWarps - 1) / kWarps);
-    if (vec) short_conv_bwd_kernel<TIn, W, kBwdE, true><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
+    if (vec) short_conv_bwd_kernel<TIn, W, kE, true><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
     else short_conv_bwd_kernel<TIn, W, 1, false><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -407,7 +453,7 @@ cudaError_t launch_short_conv_bwd(const ConvBwdArgs &a, cudaStream_t st) { LDN_B
 
 size_t short_conv_bwd_workspace_bytes(int B, int T, int C, int W)
 {
-    const int run = conv_run(B, T, C, kBwdE), runs = std::max(1, (T + run - 1) / run);
+    const int run = conv_run(B, T, C, kE), runs = std::max(1, (T + run - 1) / run);
     return (size_t)B * ((runs + kWarps - 1) / kWarps) * (W + 1) * C * sizeof(float);
 }
 
