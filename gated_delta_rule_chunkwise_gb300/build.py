@@ -3,7 +3,9 @@
 Each .cu file directly under csrc/ is compiled by its own nvcc process (in
 parallel), then the objects are linked into lib/libldn.so inside the package.
 The diagnostic kernels (csrc/diag/, include/ldn_diag.h) are linked into a
-library of their own, lib/libldn_diag.so, which only the tests load.  The CUDA
+library of their own, lib/libldn_diag.so, which only the tests load.  The native
+half of mixer.py (csrc/torch/) is a host-only extension module, lib/_ldn_torch.so,
+compiled against the installed torch and linked to libldn.so beside it.  The CUDA
 runtime is linked statically, so the libraries need only the driver at run
 time.  Nothing here runs at import time; __graft_entry__.build() and the
 tests call build().
@@ -15,6 +17,7 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -24,6 +27,9 @@ LIB_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libldn.so")
 DIAG_DIR = os.path.join(CSRC, "diag")
 DIAG_LIB_PATH = os.path.join(LIB_DIR, "libldn_diag.so")
+
+TORCH_SRC = os.path.join(CSRC, "torch", "mixer_binding.cpp")
+TORCH_LIB_PATH = os.path.join(LIB_DIR, "_ldn_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -52,10 +58,12 @@ def _headers():
 
 
 def _stamp() -> str:
+    import torch
     h = hashlib.sha256()
-    for p in _sources() + _diag_sources() + _headers():
+    for p in _sources() + _diag_sources() + _headers() + [TORCH_SRC]:
         with open(p, "rb") as f:
             h.update(p.encode() + f.read())
+    h.update(torch.__version__.encode())
     h.update(" ".join(ARCH + NVCC_FLAGS).encode())
     return h.hexdigest()
 
@@ -72,6 +80,34 @@ def _compile(nvcc, src, log_dir):
     return obj
 
 
+def _compile_torch(log_dir):
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(OBJ_DIR, "mixer_binding.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-I", INCLUDE, "-isystem", root, "-isystem",
+           os.path.join(root, "torch", "csrc", "api", "include"), "-isystem", cuda, "-isystem",
+           sysconfig.get_paths()["include"], "-c", TORCH_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    with open(os.path.join(log_dir, "mixer_binding.cpp.log"), "w") as f:
+        f.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {TORCH_SRC}:\n{r.stderr[-6000:]}")
+    return obj
+
+
+def _link_torch(obj):
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = TORCH_LIB_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", LIB_DIR, "-l:libldn.so", "-Wl,-rpath,$ORIGIN", "-L", libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _ldn_torch.so failed:\n{r.stderr[-6000:]}")
+    os.replace(tmp, TORCH_LIB_PATH)
+
+
 def _link(nvcc, objs, path):
     tmp = path + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
@@ -82,22 +118,24 @@ def _link(nvcc, objs, path):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libldn.so and libldn_diag.so if any source changed;
-    return the path of libldn.so."""
+    """Compile and link libldn.so, libldn_diag.so and _ldn_torch.so if any source
+    changed; return the path of libldn.so."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
     stamp_file = os.path.join(OBJ_DIR, "stamp")
     stamp = _stamp()
     if (not force and os.path.exists(LIB_PATH) and os.path.exists(DIAG_LIB_PATH) and
-            os.path.exists(stamp_file)):
+            os.path.exists(TORCH_LIB_PATH) and os.path.exists(stamp_file)):
         with open(stamp_file) as f:
             if f.read() == stamp:
                 return LIB_PATH
     nvcc = _nvcc()
     srcs, dsrcs = _sources(), _diag_sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + len(dsrcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, 1 + len(srcs) + len(dsrcs))) as ex:
+        torch_obj = ex.submit(_compile_torch, OBJ_DIR)
         objs = list(ex.map(lambda s: _compile(nvcc, s, OBJ_DIR), srcs + dsrcs))
     _link(nvcc, objs[:len(srcs)], LIB_PATH)
+    _link_torch(torch_obj.result())
     _link(nvcc, objs[len(srcs):], DIAG_LIB_PATH)
     with open(stamp_file, "w") as f:
         f.write(stamp)
