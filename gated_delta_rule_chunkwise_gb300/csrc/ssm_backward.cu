@@ -126,7 +126,9 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
     const bool helper = threadIdx.x >= kMain;
     const int tid = threadIdx.x % kMain, lane = tid & 31, warp = tid >> 5;
     const int len = seq_len(a.lens, b, a.T);
-    const int tb = seg * pl.len, te = min(tb + pl.len, a.T), tiles = (te - tb + TT - 1) / TT;
+    const int tb = seg * pl.len, te = min(tb + pl.len, a.T);
+    // tiles with rows of the sequence; through those behind its end g passes unchanged
+    const int tiles = (max(min(len, te) - tb, 0) + TT - 1) / TT;
     const size_t row0 = (size_t)b * a.T + tb;   // the segment's first row
     const size_t bseg = (size_t)b * pl.n + seg;
     auto rows_of = [&](int it) { return min(max(min(len, te) - tb - it * TT, 0), TT); };
@@ -278,7 +280,7 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
             }
             __syncwarp();
         };
-        ready(tiles - 1);
+        if (tiles > 0) ready(tiles - 1);
         if (tiles > 1) announce(tiles - 2);
         __syncthreads();
         for (int it = tiles - 1; it >= 0; --it) {
@@ -291,7 +293,18 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
             __syncthreads();
         }
         if (PHASE == kFull) {
-            finished(0);
+            if (tiles > 0) finished(0);
+            // behind the end: no gradient
+            const float zeros[V] = {};
+            for (int i = tiles * TT * PR + lane; i < (te - tb) * PR; i += 32) {
+                const size_t at = (row0 + i / PR) * a.D + cc;
+                store_n<V, VEC>((TIn *)a.du + at, zeros, valid);
+                store_n<V, VEC>((TIn *)a.ddelta + at, zeros, valid);
+                if (z) store_n<V, VEC>((TIn *)a.dz + at, zeros, valid);
+            }
+            for (int i = tid + tiles * TT * (2 * N / 4); i < (te - tb) * (2 * N / 4); i += kMain)
+                *reinterpret_cast<float4 *>(wk.bc + (((size_t)gb * a.B * a.T + row0 + i / (2 * N / 4)) * a.G + grp) * (2 * N) +
+                                            i % (2 * N / 4) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
             // dD and the bias over the lanes that share a vector's channels
 #pragma unroll
             for (int o = 16; o >= PR; o >>= 1)

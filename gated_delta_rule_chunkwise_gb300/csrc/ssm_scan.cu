@@ -76,7 +76,9 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
     const bool helper = threadIdx.x >= kMain;
     const int tid = threadIdx.x % kMain, lane = tid & 31, warp = tid >> 5;
     const int len = seq_len(a.lens, b, a.T);
-    const int tb = seg * sg.len, te = min(tb + sg.len, a.T), tiles = (te - tb + TT - 1) / TT;
+    const int tb = seg * sg.len, te = min(tb + sg.len, a.T);
+    // tiles with rows of the sequence, and all of the segment's: behind the end the state stays
+    const int tiles = (max(min(len, te) - tb, 0) + TT - 1) / TT, all = (te - tb + TT - 1) / TT;
     const size_t row0 = (size_t)b * a.T + tb;   // the segment's first row
     auto rows_of = [&](int it) { return min(max(min(len, te) - tb - it * TT, 0), TT); };
 
@@ -84,8 +86,10 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
         // Copies, the elementwise work before the recurrence (prepare: dt, dt u) and after it
         // (finish: D u, the gate, the stores) for the channels of one recurrence warp, a tile
         // ahead of it and a tile behind it.  Vectors of PV and FV channels of a row; a lane's
-        // channels stay the same.
-        constexpr int PV = 4, FV = WC < 8 ? WC : 8, PR = WC / PV, FR = WC / FV;
+        // channels stay the same.  FV channels are at most 16 bytes: VEC has groups of whole
+        // 16-byte vectors, so that such a vector is inside its group or outside.
+        constexpr int MOST = 16 / (int)sizeof(TIn);
+        constexpr int PV = 4, FV = WC < MOST ? WC : MOST, PR = WC / PV, FR = WC / FV;
         const int w0 = warp * WC, wcols = cols - w0;   // the warp's channels
         const int pch = (lane % PR) * PV, fch = (lane % FR) * FV;
         const TIn *u = (const TIn *)a.u + row0 * a.ldu + c0 + w0;
@@ -191,6 +195,11 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
             __syncthreads();
         }
         if (tiles > 0) finished(tiles - 1);
+        if constexpr (PHASE != kEnds) {   // rows of the tiles behind the end
+            const float zeros[FV] = {};
+            for (int i = tiles * TT * FR + lane; i < (te - tb) * FR; i += 32)
+                store_n<FV, VEC>((TIn *)a.y + (row0 + i / FR) * a.D + c0 + w0 + fch, zeros, wcols - fch);
+        }
         return;
     }
 
@@ -293,6 +302,9 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
         __syncthreads();
     }
     if (!on) return;
+    if (PHASE != kEnds && a.states)
+        for (int it = tiles; it < all; ++it)
+            store_state(a.states + ((size_t)b * ((a.T + TT - 1) / TT) + tb / TT + it) * a.D * N + mine);
     if (PHASE == kEnds) {
         const size_t e = ((size_t)b * sg.n + seg) * a.D + c0 + slot;
         store_state(sg.ends + e * N + l * S);

@@ -316,6 +316,11 @@ SCAN_CASES = [  # B, T, D, N, G, dtype, options, lens, pad, off
     (2, 40, 130, 8, 1, "f32", dict(z=False, skip=False, bias=False, h0=False), [500, -1], 0, 0),
     (1, 290, 20, 16, 1, "bf16", {}, None, 0, 0),                # segments
     (2, 420, 6, 32, 2, "f32", {}, [420, 200], 0, 0),            # segments, one sequence ends early
+    (3, 37, 40, 16, 2, "f32", {}, [37, 0, 5], 0, 0),            # groups of an odd number of 16-byte vectors
+    (3, 70, 24, 32, 2, "f32", {}, [1, 70, 33], 0, 0),
+    (2, 34, 12, 64, 3, "f32", {}, [34, 2], 0, 0),
+    (2, 300, 56, 8, 7, "bf16", {}, [2, 300], 0, 0),
+    (2, 300, 40, 16, 5, "bf16", {}, [130, 300], 0, 0),
 ]
 
 
