@@ -19,7 +19,7 @@
 // As in the forward a block is four warps of this recurrence and four helpers, which read the
 // rows, form dt, dt u and yb a tile ahead, and turn the sums into du, ddelta, dz and the
 // block's dB, dC a tile behind.  The recurrence needs most of the registers (states and decays
-// of four tokens), so the block's are split: 160 a thread for it, 96 for the helpers.
+// of four tokens), so the block's are split: 152 a thread for it, 104 for the helpers.
 //
 // Sums across blocks (dB, dC over the channel blocks of a group; dA, dD and the bias over
 // sequences and segments) go to the workspace and are added by a last launch in a fixed
@@ -36,7 +36,7 @@ using namespace ssm;
 
 constexpr int kMain = 128, kThreads = 256, kWarps = 4, S = 4, KC = 2, SUB = 4;
 // Registers a thread: what the block is launched with, and what its halves hold after the split.
-constexpr int kRegs = 128, kRegsMain = 160, kRegsHelper = 96;
+constexpr int kRegs = 128, kRegsMain = 152, kRegsHelper = 104;
 static_assert(kRegsMain + kRegsHelper == 2 * kRegs, "the halves share what the block has");
 
 template <int N> constexpr int block_ch() { return kMain / (N / S) * KC; }
@@ -327,7 +327,9 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
     // The recurrence: lane l of a channel pair's L has states l S .. l S + S - 1 of channels
     // 2 slot and 2 slot + 1.
     const int l = tid % L, slot = tid / L, wch = 2 * slot - warp * WC;   // the pair's place in the warp
-    float2 A2[KC][2], g[KC][2], dA[KC][2];
+    // dA is summed tile by tile: 32 additions and then one a tile keep the sum of thousands of
+    // tokens to a few roundings
+    float2 A2[KC][2], g[KC][2], dA[KC][2], dAsum[KC][2];
     float sumdt[KC];
 #pragma unroll
     for (int k = 0; k < KC; ++k) {
@@ -338,7 +340,7 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             A2[k][s] = on ? make_float2(a.A[at + 2 * s] * kLog2e, a.A[at + 2 * s + 1] * kLog2e) : dup(0.f);
-            g[k][s] = dA[k][s] = dup(0.f);
+            g[k][s] = dA[k][s] = dAsum[k][s] = dup(0.f);
             if (PHASE == kFull && on && a.dh_final) {
                 const float *p = a.dh_final + (size_t)b * a.D * N + at + 2 * s;
                 g[k][s] = make_float2(p[0], p[1]);
@@ -498,6 +500,13 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
                         sm.ww[warp][r * WC + wch + c] = ws[i];
                     }
             }
+#pragma unroll
+            for (int k = 0; k < KC; ++k)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    dAsum[k][s] = __fadd2_rn(dAsum[k][s], dA[k][s]);
+                    dA[k][s] = dup(0.f);
+                }
         }
         __syncthreads();
     }
@@ -512,7 +521,7 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
             if (l == 0) wk.sums[e] = sumdt[k];
         } else {
             *reinterpret_cast<float4 *>(wk.A + e * N + l * S) =
-                make_float4(dA[k][0].x, dA[k][0].y, dA[k][1].x, dA[k][1].y);
+                make_float4(dAsum[k][0].x, dAsum[k][0].y, dAsum[k][1].x, dAsum[k][1].y);
             if (seg == 0 && a.dh0)
                 *reinterpret_cast<float4 *>(a.dh0 + ((size_t)b * a.D + c0 + ch) * N + l * S) = gv;
         }
