@@ -351,21 +351,23 @@ short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
     }
 }
 
-// dw [C][W] and db [C] from part [n][W + 1][C]: 32 columns a block, 8 rows in flight.
-__global__ void __launch_bounds__(256)
+// dw [C][W] and db [C] from part [n][W + 1][C]: 32 columns a block, kSumRows rows at a time.
+constexpr int kSumRows = 16;
+__global__ void __launch_bounds__(32 * kSumRows)
 conv_param_sum_kernel(const float *__restrict__ part, float *__restrict__ dw, float *__restrict__ db, int n, int W,
                       int C)
 {
-    __shared__ float sm[8][33];
+    __shared__ float sm[kSumRows][33];
     const int c = blockIdx.x * 32 + threadIdx.x, j = blockIdx.y, y = threadIdx.y;
     float t = 0.f;
     if (c < C)
-        for (int i = y; i < n; i += 8) t += part[((size_t)i * (W + 1) + j) * C + c];
+#pragma unroll 8
+        for (int i = y; i < n; i += kSumRows) t += part[((size_t)i * (W + 1) + j) * C + c];
     sm[y][threadIdx.x] = t;
     __syncthreads();
     if (y == 0 && c < C) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) t += sm[i][threadIdx.x];
+        for (int i = 1; i < kSumRows; ++i) t += sm[i][threadIdx.x];
         if (j < W) dw[(size_t)c * W + j] = t;
         else if (db) db[c] = t;
     }
@@ -428,7 +430,7 @@ cudaError_t conv_bwd(const ConvBwdArgs &a, cudaStream_t st)
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int n = a.B * ((runs + kWarps - 1) / kWarps);
-    conv_param_sum_kernel<<<dim3((a.C + 31) / 32, W + 1), dim3(32, 8), 0, st>>>(a.part, a.dw, a.db, n, W, a.C);
+    conv_param_sum_kernel<<<dim3((a.C + 31) / 32, W + 1), dim3(32, kSumRows), 0, st>>>(a.part, a.dw, a.db, n, W, a.C);
     return cudaGetLastError();
 }
 

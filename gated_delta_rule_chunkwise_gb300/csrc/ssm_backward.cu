@@ -339,7 +339,7 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
         sumdt[k] = 0.f;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            A2[k][s] = on ? make_float2(a.A[at + 2 * s] * kLog2e, a.A[at + 2 * s + 1] * kLog2e) : dup(0.f);
+            A2[k][s] = on ? make_float2(rate(a.A[at + 2 * s]), rate(a.A[at + 2 * s + 1])) : dup(0.f);
             g[k][s] = dA[k][s] = dAsum[k][s] = dup(0.f);
             if (PHASE == kFull && on && a.dh_final) {
                 const float *p = a.dh_final + (size_t)b * a.D * N + at + 2 * s;
@@ -347,6 +347,7 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
             }
         }
         if (PHASE == kFull && on)
+#pragma unroll 4
             for (int j = pl.n - 1; j > seg; --j) {   // through the later segments
                 const size_t e = ((size_t)b * pl.n + j) * a.D + c0 + ch;
                 const float sd = wk.sums[e];
@@ -565,13 +566,14 @@ ssm_sum_kernel(const SsmBwdArgs a, const Work wk, int gblocks, int np, unsigned 
 }
 
 constexpr int kSms = 152;
+constexpr long long kMostSegs = 64;   // the first one composes all others, one after another
 
 // Segments per sequence: enough to fill the SMs at two blocks each, of at least four tiles.
 Plan bwd_plan(int B, int T, int D, int N, int G)
 {
     const int db = block_channels(N), gblocks = (D / G + db - 1) / db;
     const long long blocks = (long long)B * G * gblocks;
-    const int n = (int)std::max(1LL, std::min<long long>(kSms * 2 / blocks, T / (4 * TT)));
+    const int n = (int)std::max(1LL, std::min<long long>({kSms * 2 / blocks, T / (4 * TT), kMostSegs}));
     const int len = std::max(TT, (int)((((long long)T + n - 1) / n + TT - 1) / TT) * TT);
     return {std::max(1, (T + len - 1) / len), len, gblocks};
 }

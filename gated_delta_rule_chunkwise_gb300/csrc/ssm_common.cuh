@@ -1,16 +1,16 @@
-// Pieces of the selective scan shared by its directions: the tile of a token run in shared
-// memory and the packed arithmetic.
+// Pieces of the selective scan shared by its directions: a tile's rows on their way to shared
+// memory, and the decay rates.
 #pragma once
 #include "mixer_common.cuh"
 #include "sm100_ptx.cuh"
 
 namespace ldn {
 namespace ssm {
-using sm100::cp_async16;
 using sm100::cp_async_commit;
 using sm100::cp_async_wait;
 
 constexpr int TT = kSsmChunk;   // tokens of a tile
+
 // Copies BYTES (4, 8 or 16) from global to shared memory, or zeros where `ok` is false; in flight
 // until its group is waited for.
 template <int BYTES>
@@ -23,79 +23,6 @@ __device__ __forceinline__ void cp_async(void *dst, const void *src, bool ok)
         asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(d), "l"(src), "r"(n), "n"(BYTES)
                      : "memory");
 }
-
-// Rows t0 .. t0 + TT of DB channels to dst, WC channels of all rows after one another:
-// dst[DB / WC][TT][WC].  Rows at and past `rows` and channels at and past `cols` are zeros.
-template <typename T, int DB, int WC, int NT, bool VEC>
-__device__ __forceinline__ void load_rows(T *dst, const T *src, long long ld, int rows, int cols)
-{
-    constexpr int E = VEC ? (WC * (int)sizeof(T) < 16 ? WC : 16 / (int)sizeof(T)) : 1, PER = DB / E;
-    for (int i = threadIdx.x; i < TT * PER; i += NT) {
-        const int r = i / PER, e = (i % PER) * E;
-        const bool ok = r < rows && e < cols;
-        T *to = dst + (e / WC * TT + r) * WC + e % WC;
-        if constexpr (VEC) cp_async<E * (int)sizeof(T)>(to, ok ? src + r * ld + e : src, ok);
-        else *to = ok ? src[r * ld + e] : T(0.f);
-    }
-}
-
-// A run's B or C rows, one tile ahead in registers, then widened to dst[TT][N] with zeros at
-// and past `rows`.  A thread takes K neighbouring elements.  They are kept as loaded (widening
-// them where they are loaded would wait for them there) in whole vectors or 4-byte words, as
-// the rows are aligned; a projection's slices may start at any element, and rows that are not
-// aligned to words are read where they are stored.
-template <typename T, int N, int NT>
-struct RowRegs {
-    static constexpr int MOST = 16 / (int)sizeof(T), PER = TT * N / NT;
-    static constexpr int K = PER < 4 ? 4 : PER < MOST ? PER : MOST;
-    static constexpr int TURNS = (TT * N + NT * K - 1) / (NT * K), WORDS = K * (int)sizeof(T) / 4;
-    enum { kSingles, kWords, kVectors };
-    uint32_t w[TURNS][WORDS];
-    static __device__ __forceinline__ int place(int k) { return (k * NT + (int)threadIdx.x) * K; }
-    __device__ __forceinline__ void load(const T *src, long long ld, int rows, int how)
-    {
-        if (how == kSingles) return;
-#pragma unroll
-        for (int k = 0; k < TURNS; ++k) {
-            const int i = place(k), r = i / N;
-            const uint32_t *p = reinterpret_cast<const uint32_t *>(src + r * ld + i % N);
-            if (how == kVectors && WORDS == 4) {
-                const uint4 q = r < rows ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
-                w[k][0] = q.x; w[k][1] = q.y; w[k][2 % WORDS] = q.z; w[k][3 % WORDS] = q.w;
-            } else if (how == kVectors) {
-                const uint2 q = r < rows ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0, 0);
-                w[k][0] = q.x; w[k][1] = q.y;
-            } else {
-#pragma unroll
-                for (int c = 0; c < WORDS; ++c) w[k][c] = r < rows ? p[c] : 0u;
-            }
-        }
-    }
-    __device__ __forceinline__ void store(float *dst, const T *src, long long ld, int rows, int how) const
-    {
-#pragma unroll
-        for (int k = 0; k < TURNS; ++k) {
-            const int i = place(k), r = i / N;
-            if (TT * N % (NT * K) != 0 && i >= TT * N) continue;
-            float v[K];
-            if (how == kSingles) load_n<K, false>(src + r * ld + i % N, v, r < rows ? K : 0);
-            else if constexpr (sizeof(T) == 2)
-#pragma unroll
-                for (int c = 0; c < WORDS; ++c) bf16x2_widen(w[k][c], v + 2 * c);
-            else
-#pragma unroll
-                for (int c = 0; c < WORDS; ++c) v[c] = __uint_as_float(w[k][c]);
-#pragma unroll
-            for (int c = 0; c < K; c += 4)
-                *reinterpret_cast<float4 *>(dst + i + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
-        }
-    }
-    static __device__ __forceinline__ int alignment(const T *p, long long ld)
-    {
-        const uintptr_t m = (uintptr_t)p | (uintptr_t)(ld * (long long)sizeof(T));
-        return m % (4 * WORDS) == 0 ? kVectors : m % 4 == 0 ? kWords : kSingles;
-    }
-};
 
 // The tile's rows of one warp's WC channels, to dst[TT][WC], by that warp; zeros outside.
 // FULL: nothing is outside.
@@ -159,6 +86,15 @@ struct SharedRows {
         return m % BYTES == 0 ? kVectors : m % 4 == 0 ? kWords : kSingles;
     }
 };
+
+// A log2 e, finite: -infinity forgets whatever the step, but a row behind a sequence's end steps
+// by zero and keeps the state.
+__device__ __forceinline__ float rate(float A)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, 0fff7fffff;" : "=f"(r) : "f"(A * kLog2e));
+    return r;
+}
 
 __device__ __forceinline__ int seq_len(const int *lens, int b, int T)
 {

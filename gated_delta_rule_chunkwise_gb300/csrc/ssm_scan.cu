@@ -6,21 +6,29 @@
 //
 // One update costs four fp32 operations (dt A, dt u B, a h + ., C h + .) and one exponential
 // for every state of every channel and token: at N = 16 that outweighs the eight bytes a
-// channel and token of traffic, so the kernel is bound by the fp32 and exponential pipes, and
-// what the layout minimises is everything else per update.  L = N / S neighbouring lanes own
-// one channel, S states each, in registers over the whole run; exponentials take e^x = 2^{x
-// log2 e} with log2 e folded into A.  A block walks tiles of 32 tokens: u, delta and z arrive
-// by 16-byte asynchronous copies one tile ahead; a first step widens them and forms (dt, dt u)
-// once per channel and token, doubled so that packed fp32x2 operands are one load; the scan
-// step reads those and the B, C rows (shared by all channels) from shared memory; the sum
-// over a channel's lanes is taken for four tokens together (a halving exchange); a last step
-// adds D u, applies the output gate and stores whole rows.
+// channel and token of traffic.  Per SM and cycle the GPU makes 128 fp32 results and 32
+// exponentials (measured), so 32 updates: 58 us for 4 x 2048 tokens of 4096 x 16, against 40 us
+// for their bytes.  What stands above that is everything else an update needs in registers --
+// each register written, by arithmetic or by a load, takes its turn at the register file, and
+// at five results an update the operands' loads add two -- and the elementwise work.
+//
+// L = N / S neighbouring lanes own one channel, S states each, in registers over the whole run;
+// exponentials take e^x = 2^{x log2 e} with log2 e folded into A; products are packed pairs.
+// A block is four warps of this recurrence and four helpers, a tile of 32 tokens the step: the
+// helpers copy rows two tiles ahead (16-byte asynchronous copies), form dt and dt u a tile ahead,
+// and add D u, apply the output gate and store a tile behind, while the recurrence reads its
+// steps and the B, C rows (shared by all channels) from shared memory.  Each of the two has too
+// few warps to cover its own latencies (one to two a scheduler at 4 x 4096 channels), so they
+// cover each other's: 184 us, against 330 us for the same work one after another in one kind of
+// warp.  One barrier a tile.  The sum over a channel's lanes is taken for 2 L tokens together (a
+// halving exchange).
 //
 // Few channels for the card: the tokens are cut into segments that run side by side.  A first
 // launch forms each segment's end state from zero and its sum of dt; in the second a segment
 // composes what enters it, h <- e^{A sum dt} h + end, over the segments before it, and runs
-// with its outputs.  The exponentials are then taken twice, so it is done only where one wave
-// of unsplit blocks leaves the card under-occupied (ssm_segments).
+// with its outputs.  The exponentials are then taken twice, so it is done only where whole
+// sequences leave the card under-occupied (ssm_plan: 32768 tokens of 2048 x 16 in 556 us, 1737
+// unsplit at the rate of 8192).
 #include <type_traits>
 
 #include "ssm_common.cuh"
@@ -210,10 +218,11 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
     float A2[S], h[S], sumdt = 0.f;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        A2[s] = on ? a.A[mine + s] * kLog2e : 0.f;
+        A2[s] = on ? rate(a.A[mine + s]) : 0.f;
         h[s] = PHASE != kEnds && on && a.h0 ? a.h0[(size_t)b * a.D * N + mine + s] : 0.f;
     }
     if (PHASE == kFromEnds && on)
+#pragma unroll 4
         for (int j = 0; j < seg; ++j) {
             const size_t e = ((size_t)b * sg.n + j) * a.D + c0 + slot;
             const float sd = sg.sums[e];
@@ -316,7 +325,8 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
 
 // One token for every sequence: a lane takes four states of one channel, the channel's lanes
 // sum; h is read and written once, which is nearly all of the traffic.  A lane goes through
-// kStepB sequences at once: their loads are in flight together, and A is read once for them.
+// kStepB sequences at once: their loads are in flight together, and A is read once for them
+// (64 x 4096 x 16: 10.2 us; one sequence a lane 12.5, four 11.4, eight 14.7).
 constexpr int kStepB = 2;
 
 template <typename TIn, int N, bool VEC>
@@ -348,7 +358,7 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmArgs a)
         y[k] = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            h[k][i] = fmaf(ex2(dt[k] * (Av[i] * kLog2e)), h[k][i], du * Bv[k][i]);
+            h[k][i] = fmaf(ex2(dt[k] * rate(Av[i])), h[k][i], du * Bv[k][i]);
             y[k] = fmaf(Cv[k][i], h[k][i], y[k]);
         }
     }
@@ -377,14 +387,17 @@ long long channel_blocks(int B, int D, int N, int G)
 }
 
 struct Plan { int n, len; };
+constexpr long long kMostSegs = 64;   // the last one composes all others, one after another
 
-// Segments per sequence: as many as fill the SMs at two blocks each, from four on (a split
-// scan costs 1.6 times the work of a whole one, which up to one block an SM runs 1.5 times as
-// fast a token as two), of at least four tiles.
+// Segments per sequence: as many as fill the SMs at two blocks each, from four on, of at least
+// four tiles.  A split scan costs 1.6 times the work of a whole one, and whole sequences of one
+// block an SM run 1.6 times as fast a token as of two.  2048 tokens of one sequence, whole and
+// split: 64 channels 110 and 23 us, 2048 channels 111 and 50, 4096 channels (four segments) 111
+// and 84, 6144 channels (three) 111 and 114.
 Plan ssm_plan(int B, int T, int D, int N, int G)
 {
     const long long blocks = channel_blocks(B, D, N, G);
-    int n = (int)std::min<long long>(kSms * 2 / blocks, T / (4 * TT));
+    int n = (int)std::min<long long>({kSms * 2 / blocks, T / (4 * TT), kMostSegs});
     if (n < 4) n = 1;
     const int len = (int)((((long long)T + n - 1) / n + TT - 1) / TT) * TT;
     if (len <= 0) return {1, TT};

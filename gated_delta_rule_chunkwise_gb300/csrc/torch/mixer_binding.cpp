@@ -16,6 +16,8 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
 
+#include <algorithm>
+#include <climits>
 #include <cstdarg>
 #include <cstdio>
 #include <initializer_list>
@@ -57,6 +59,10 @@ struct Refusal {
     catch (const Refusal &e)                            \
     {                                                   \
         PyErr_SetString(e.type, e.what.c_str());        \
+        return nullptr;                                 \
+    }                                                   \
+    catch (const PythonError &)                         \
+    {                                                   \
         return nullptr;                                 \
     }                                                   \
     END_HANDLE_TH_ERRORS
@@ -218,16 +224,39 @@ T *output(const Call &c, PyObject *&o, const char *name, Shape shape, at::Scalar
     return (T *)t.data_ptr();
 }
 
-int as_int(PyObject *o) { return (int)PyLong_AsLong(o); }
-int truth(PyObject *o) { return PyObject_IsTrue(o) ? 1 : 0; }
+struct PythonError {};   // one is set
+
+int as_int(PyObject *o)
+{
+    const int v = PyLong_Check(o) ? (int)std::max(-1L, std::min(PyLong_AsLong(o), (long)INT_MAX)) : -1;
+    if (!PyLong_Check(o)) refuse(PyExc_TypeError, "an int is wanted, got %s", Py_TYPE(o)->tp_name);
+    if (PyErr_Occurred()) throw PythonError{};
+    return v;
+}
+int truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw PythonError{};
+    return v;
+}
+float as_float(PyObject *o)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw PythonError{};
+    return (float)v;
+}
+// A size as the C entry points take it.
+int size(int64_t n)
+{
+    if (n > INT_MAX) refuse(PyExc_ValueError, "a dimension of %lld is too large", (long long)n);
+    return (int)n;
+}
 
 #define NEEDS(n)                                                                      \
     if (nargs != (n)) {                                                               \
         PyErr_SetString(PyExc_TypeError, "wrong number of arguments");                \
         return nullptr;                                                               \
     }
-#define MUST_CHECK_ERR() \
-    if (PyErr_Occurred()) return nullptr
 
 // ---- RMS norm with the residual's addition ----
 // (x, residual, weight, eps, out, residual_out) -> (y, s); with (group, scale) appended
@@ -241,8 +270,7 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     if (!here(x, "x")) Py_RETURN_NONE;
     if (x.dim() < 1) refuse(PyExc_ValueError, "x must have at least one dimension");
     const Call c(x);
-    const float eps = (float)PyFloat_AsDouble(a[3]);
-    MUST_CHECK_ERR();
+    const float eps = as_float(a[3]);
     const Shape shape = x.sizes();
     const int64_t D = shape.back(), n = D ? x.numel() / D : 0, wshape[] = {D};
     const int cx = code(x, "x");
@@ -260,7 +288,6 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     std::vector<int64_t> sshape;
     if (eight) {
         group = as_int(a[6]);
-        MUST_CHECK_ERR();
         sshape.assign(shape.begin(), shape.end() - 1);
         if (group) sshape.push_back((D + 127) / 128);
     }
@@ -279,9 +306,9 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     if (eight) {
         float *ps = output<float>(c, scale, "scale", sshape, at::kFloat);
         hold_scale = scale;
-        st = ldn_add_rmsnorm_e4m3(px, pr, pw, py, ps, po, n, (int)D, group, cx, cr, eps, c.stream());
+        st = ldn_add_rmsnorm_e4m3(px, pr, pw, py, ps, po, n, size(D), group, cx, cr, eps, c.stream());
     } else {
-        st = ldn_add_rmsnorm(px, pr, pw, py, po, n, (int)D, cx, cr, eps, c.stream());
+        st = ldn_add_rmsnorm(px, pr, pw, py, po, n, size(D), cx, cr, eps, c.stream());
     }
     if (!done(st, eight ? "ldn_add_rmsnorm_e4m3" : "ldn_add_rmsnorm")) return nullptr;
     if (eight) return tuple({hold_y.release(), hold_scale.release(), hold_s.release()});
@@ -299,20 +326,19 @@ PyObject *add_rmsnorm_backward(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     if (!here(dy, "dy")) Py_RETURN_NONE;
     if (dy.dim() < 1) refuse(PyExc_ValueError, "dy must have at least one dimension");
     const Call c(dy);
-    const float eps = (float)PyFloat_AsDouble(a[4]);
-    MUST_CHECK_ERR();
+    const float eps = as_float(a[4]);
     const Shape shape = dy.sizes();
     const int64_t D = shape.back(), n = D ? dy.numel() / D : 0, wshape[] = {D};
     const int cx = code(dy, "dy"), cr = code(must(s, "s"), "s");
     void *pdy = address(&dy, "dy", shape, dy.scalar_type(), c.dev), *ps = address(s, "s", shape, s->scalar_type(), c.dev);
     float *pw = address<float>(&must(w, "weight"), "weight", Shape(wshape, 1), at::kFloat, c.dev);
     void *pd = address(dsum, "dsum", shape, s->scalar_type(), c.dev);
-    const size_t need = ldn_add_rmsnorm_backward_workspace_size(n, (int)D);
+    const size_t need = ldn_add_rmsnorm_backward_workspace_size(n, size(D));
     const int64_t ws_n[] = {(int64_t)need};
     const Tensor dx = c.make(shape, dy.scalar_type()), dres = cx == cr ? dx : c.make(shape, s->scalar_type()),
                  dw = c.make(Shape(wshape, 1), at::kFloat), ws = c.make(Shape(ws_n, 1), at::kByte);
     if (!done(ldn_add_rmsnorm_backward(pdy, ps, pw, pd, dx.data_ptr(), cx == cr ? nullptr : dres.data_ptr(),
-                                       (float *)dw.data_ptr(), n, (int)D, cx, cr, eps, need ? ws.data_ptr() : nullptr,
+                                       (float *)dw.data_ptr(), n, size(D), cx, cr, eps, need ? ws.data_ptr() : nullptr,
                                        need, c.stream()), "ldn_add_rmsnorm_backward"))
         return nullptr;
     PyObject *d = dict({{"dx", &dx}, {"dweight", &dw}});
@@ -367,7 +393,7 @@ PyObject *short_conv(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     hold_y = y;
     void *ps = output(c, so, "state_out", Shape(ss, 3), t);
     hold_s = so;
-    if (!done(ldn_short_conv(in.x.p, in.x.ld, in.w, in.b, pst, pl, py, ps, (int)B, (int)T, (int)in.C, (int)in.W,
+    if (!done(ldn_short_conv(in.x.p, in.x.ld, in.w, in.b, pst, pl, py, ps, size(B), size(T), size(in.C), size(in.W),
                              truth(a[5]), in.code, c.stream()), "ldn_short_conv"))
         return nullptr;
     return tuple({hold_y.release(), hold_s.release()});
@@ -390,7 +416,7 @@ PyObject *short_conv_step(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     PyObject *y = a[5];
     void *py = output(c, y, "out", Shape(ys, 2), t);
     THPObjectPtr hold_y(y);
-    if (!done(ldn_short_conv_step(in.x.p, in.x.ld, in.w, in.b, pst, py, ps, (int)B, (int)in.C, (int)in.W, truth(a[4]),
+    if (!done(ldn_short_conv_step(in.x.p, in.x.ld, in.w, in.b, pst, py, ps, size(B), size(in.C), size(in.W), truth(a[4]),
                                   in.code, c.stream()), "ldn_short_conv_step"))
         return nullptr;
     return hold_y.release();
@@ -414,7 +440,7 @@ PyObject *short_conv_backward(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     void *pds = address(tensor(a[5], "dstate_out"), "dstate_out", Shape(ss, 3), t, c.dev);
     void *pdy = address(&must(dy, "dy"), "dy", Shape(ys, 3), t, c.dev);
     int *pl = address<int>(tensor(a[6], "lens"), "lens", Shape(ls, 1), at::kInt, c.dev);
-    const size_t need = ldn_short_conv_backward_workspace_size((int)B, (int)T, (int)in.C, (int)in.W);
+    const size_t need = ldn_short_conv_backward_workspace_size(size(B), size(T), size(in.C), size(in.W));
     const int64_t nws[] = {(int64_t)(need ? need : 16)};
     Tensor dx = c.make(Shape(ys, 3), t), dw = c.make(Shape(ws_, 2), at::kFloat), ws = c.make(Shape(nws, 1), at::kByte), db,
            dst;
@@ -422,7 +448,7 @@ PyObject *short_conv_backward(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     if (state) dst = c.make(Shape(ss, 3), t);
     if (!done(ldn_short_conv_backward(in.x.p, in.x.ld, in.w, in.b, pst, pl, pdy, pds, dx.data_ptr(),
                                       (float *)dw.data_ptr(), bias ? (float *)db.data_ptr() : nullptr,
-                                      state ? dst.data_ptr() : nullptr, (int)B, (int)T, (int)in.C, (int)in.W,
+                                      state ? dst.data_ptr() : nullptr, size(B), size(T), size(in.C), size(in.W),
                                       truth(a[7]), in.code, ws.data_ptr(), need, c.stream()),
               "ldn_short_conv_backward"))
         return nullptr;
@@ -496,14 +522,14 @@ PyObject *selective_scan(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     if (given) {
         pws = address(given, "workspace", given->sizes(), at::kByte, c.dev);
         nws = (size_t)given->numel();
-    } else if ((nws = ldn_ssm_scan_workspace_size((int)nb, (int)T, (int)in.Dm, (int)in.N, (int)in.G)) != 0) {
+    } else if ((nws = ldn_ssm_scan_workspace_size(size(nb), size(T), size(in.Dm), size(in.N), size(in.G))) != 0) {
         const int64_t n[] = {(int64_t)nws};
         ws = c.make(Shape(n, 1), at::kByte);
         pws = ws.data_ptr();
     }
     if (!done(ldn_ssm_scan(in.u.p, in.u.ld, in.d.p, in.d.ld, in.A, in.B.p, in.B.ld, in.C.p, in.C.ld, in.D, in.z.p,
-                           in.z.ld, in.bias, ph, pl, py, pf, save ? (float *)states.data_ptr() : nullptr, (int)nb,
-                           (int)T, (int)in.Dm, (int)in.N, (int)in.G, truth(a[9]), in.code, nws ? pws : nullptr, nws,
+                           in.z.ld, in.bias, ph, pl, py, pf, save ? (float *)states.data_ptr() : nullptr, size(nb),
+                           size(T), size(in.Dm), size(in.N), size(in.G), truth(a[9]), in.code, nws ? pws : nullptr, nws,
                            c.stream()), "ldn_ssm_scan"))
         return nullptr;
     if (save) return tuple({hold_y.release(), hold_h.release(), wrap(states)});
@@ -527,7 +553,7 @@ PyObject *selective_scan_step(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     void *py = output(c, y, "out", u.sizes(), u.scalar_type());
     THPObjectPtr hold_y(y);
     if (!done(ldn_ssm_step(in.u.p, in.u.ld, in.d.p, in.d.ld, in.A, in.B.p, in.B.ld, in.C.p, in.C.ld, in.D, in.z.p,
-                           in.z.ld, in.bias, ph, po, py, (int)nb, (int)in.Dm, (int)in.N, (int)in.G, truth(a[9]),
+                           in.z.ld, in.bias, ph, po, py, size(nb), size(in.Dm), size(in.N), size(in.G), truth(a[9]),
                            in.code, c.stream()), "ldn_ssm_step"))
         return nullptr;
     return hold_y.release();
@@ -556,13 +582,13 @@ PyObject *selective_scan_backward(PyObject *, PyObject *const *a, Py_ssize_t nar
     if (a[6] != Py_None) dz = c.make(u.sizes(), t);
     if (in.bias) db = c.make(Shape(as, 1), at::kFloat);
     auto p = [](const Tensor &x) { return x.defined() ? x.data_ptr() : nullptr; };
-    const size_t need = ldn_ssm_backward_workspace_size((int)nb, (int)T, (int)in.Dm, (int)in.N, (int)in.G);
+    const size_t need = ldn_ssm_backward_workspace_size(size(nb), size(T), size(in.Dm), size(in.N), size(in.G));
     const int64_t nws[] = {(int64_t)(need ? need : 16)};
     const Tensor ws = c.make(Shape(nws, 1), at::kByte);
     if (!done(ldn_ssm_backward(in.u.p, in.u.ld, in.d.p, in.d.ld, in.A, in.B.p, in.B.ld, in.C.p, in.C.ld, in.D, in.z.p,
                                in.z.ld, in.bias, ps, pl, pdy, pdh, p(du), p(dd), (float *)p(dA), p(dB), p(dC),
-                               (float *)p(dD), p(dz), (float *)p(db), (float *)p(dh0), (int)nb, (int)T, (int)in.Dm,
-                               (int)in.N, (int)in.G, truth(a[11]), in.code, ws.data_ptr(), need, c.stream()),
+                               (float *)p(dD), p(dz), (float *)p(db), (float *)p(dh0), size(nb), size(T), size(in.Dm),
+                               size(in.N), size(in.G), truth(a[11]), in.code, ws.data_ptr(), need, c.stream()),
               "ldn_ssm_backward"))
         return nullptr;
     return dict({{"du", &du}, {"ddelta", &dd}, {"dA", &dA}, {"dB", &dB}, {"dC", &dC}, {"dD", &dD}, {"dz", &dz},
