@@ -154,7 +154,8 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
         load_n<V, false>(a.Dskip + cc, reinterpret_cast<float *>(skip), a.Dskip ? valid : 0);
 
         // A batch of rows is loaded before any of it is used: one latency for the batch.
-        constexpr int ITEMS = TT * PR / 32, BATCH = ITEMS < 2 ? ITEMS : 2;
+        constexpr int ITEMS = TT * PR / 32, MOST = PHASE == kCarry && sizeof(TIn) == 2 ? 4 : 2,
+                      BATCH = ITEMS < MOST ? ITEMS : MOST;
         using R4 = Raw<TIn, 4>;
         auto load_batch = [&](int t, int rows, int k0, R4 *ru, R4 *rd, R4 *ry, R4 *rz) {
 #pragma unroll
@@ -529,19 +530,32 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
     }
 }
 
-// The sums across blocks, each by one thread in order: dB, dC over the channel blocks of a
-// group; dA, dD and the bias over sequences and segments (np of them).
+// The sums across blocks in a fixed order: dB, dC over the channel blocks of a group, four
+// values a thread and kSlices threads a value (few rows are few threads, and one thread alone
+// would wait for every block's load in turn); dA, dD and the bias over sequences and segments
+// (np of them), a thread each.
+constexpr int kSlices = 8, kSums = 32;   // 32 x 8 threads
 template <typename TIn>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kSums * kSlices)
 ssm_sum_kernel(const SsmBwdArgs a, const Work wk, int gblocks, int np, unsigned bc_blocks)
 {
-    const int N = a.N;
+    __shared__ float4 sm[kSlices][kSums];
+    const int N = a.N, x = threadIdx.x % kSums, y = threadIdx.x / kSums;
     if (blockIdx.x < bc_blocks) {
-        const size_t n = (size_t)a.B * a.T * a.G * 2 * N, i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
-        if (i >= n) return;
-        float4 t = *reinterpret_cast<const float4 *>(wk.bc + i);
-        for (int k = 1; k < gblocks; ++k) {
-            const float4 q = *reinterpret_cast<const float4 *>(wk.bc + (size_t)k * n + i);
+        const size_t n = (size_t)a.B * a.T * a.G * 2 * N, i = ((size_t)blockIdx.x * kSums + x) * 4;
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n)
+#pragma unroll 4
+            for (int k = y; k < gblocks; k += kSlices) {
+                const float4 q = *reinterpret_cast<const float4 *>(wk.bc + (size_t)k * n + i);
+                t.x += q.x; t.y += q.y; t.z += q.z; t.w += q.w;
+            }
+        sm[y][x] = t;
+        __syncthreads();
+        if (y != 0 || i >= n) return;
+#pragma unroll
+        for (int k = 1; k < kSlices; ++k) {
+            const float4 q = sm[k][x];
             t.x += q.x; t.y += q.y; t.z += q.z; t.w += q.w;
         }
         const size_t row = i / (2 * N);
@@ -551,7 +565,7 @@ ssm_sum_kernel(const SsmBwdArgs a, const Work wk, int gblocks, int np, unsigned 
         store_n<4, false>(o, v);
         return;
     }
-    const size_t i = (size_t)(blockIdx.x - bc_blocks) * 256 + threadIdx.x, nA = (size_t)a.D * N;
+    const size_t i = (size_t)(blockIdx.x - bc_blocks) * (kSums * kSlices) + threadIdx.x, nA = (size_t)a.D * N;
     const float *src;
     float *dst;
     size_t per, o;
@@ -561,6 +575,7 @@ ssm_sum_kernel(const SsmBwdArgs a, const Work wk, int gblocks, int np, unsigned 
     else return;
     if (!dst) return;
     float t = 0.f;
+#pragma unroll 4
     for (int k = 0; k < np; ++k) t += src[k * per + o];
     dst[o] = t;
 }
@@ -624,9 +639,9 @@ cudaError_t bwd_run(const SsmBwdArgs &a, cudaStream_t st)
     }
     const cudaError_t e = bwd_launch<TIn, N, VEC, kFull>(a, p, w, st);
     if (e != cudaSuccess) return e;
-    const unsigned bcb = (unsigned)(((size_t)a.B * a.T * a.G * 2 * N / 4 + 255) / 256);
-    const unsigned pb = (unsigned)(((size_t)a.D * (N + 2) + 255) / 256);
-    ssm_sum_kernel<TIn><<<bcb + pb, 256, 0, st>>>(a, w, p.gblocks, a.B * p.n, bcb);
+    const unsigned bcb = (unsigned)(((size_t)a.B * a.T * a.G * 2 * N / 4 + kSums - 1) / kSums);
+    const unsigned pb = (unsigned)(((size_t)a.D * (N + 2) + kSums * kSlices - 1) / (kSums * kSlices));
+    ssm_sum_kernel<TIn><<<bcb + pb, kSums * kSlices, 0, st>>>(a, w, p.gblocks, a.B * p.n, bcb);
     return cudaGetLastError();
 }
 
