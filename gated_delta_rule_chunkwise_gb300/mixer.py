@@ -51,8 +51,8 @@ def _call(f, stream, x, *args):
             return r
         with torch.cuda.device(x.device):
             return f(x, *args)
-    if not isinstance(x, torch.Tensor) or stream.device != x.device:
-        raise ValueError(f"{f.__name__}: stream is of {stream.device}, the first tensor is not")
+    if not isinstance(stream, torch.cuda.Stream) or not isinstance(x, torch.Tensor) or stream.device != x.device:
+        raise ValueError(f"{f.__name__}: stream must be a torch.cuda.Stream of the first tensor's device")
     with torch.cuda.stream(stream):
         return f(x, *args)
 

@@ -415,6 +415,35 @@ def test_selective_scan_steps_of_all_magnitudes():
     within(h, wh[:, -1], bound["h"], "h")
 
 
+def test_selective_scan_forgets_and_keeps_at_infinity():
+    """A rate of -infinity leaves only the last token's input, whatever rows lie behind the
+    sequence's end; a step of -infinity (a masked token) leaves the state; NaN stays in its
+    channel."""
+    import torch
+    p = scan_inputs(2, 40, 8, 16, 1, "f32", z=False)
+    p["A"][3] = -np.inf
+    p["A"][5] = -3.4e38
+    p["delta"][:, 7:9, 1] = -np.inf
+    p["u"][0, 2, 6] = np.nan
+    n = [40, 35]
+    t = scan_tensors(p, n, "f32")
+    gl, h0 = dev(np.array(n)), dev(p["h0"])
+    for ws in (None, torch.empty(0, dtype=torch.uint8, device="cuda")):
+        y, h = ldn.selective_scan(*t, h0, lens=gl, workspace=ws)
+        dt = ref.softplus(p["delta"] + p["bias"])
+        for i in range(2):
+            for c in (3, 5):
+                last = dt[i, n[i] - 1, c] * p["u"][i, n[i] - 1, c] * p["B"][i, n[i] - 1, 0]
+                within(h[i, c], last, np.abs(last) * 64 * U + 1e-30, "only the last input")
+        assert torch.isnan(h[0, 6]).all() and torch.isnan(y[0, 2:, 6]).all() and torch.isfinite(y[0, :2]).all()
+        keep = [c for c in range(8) if c != 6]
+        assert torch.isfinite(h[:, keep]).all() and torch.isfinite(y[1]).all() and torch.isfinite(y[0][:, keep]).all()
+    # up to the masked tokens and over them, the state is the same
+    cut = lambda k: [m[:, :k].contiguous() if m is not None and m.dim() > 2 else m for m in t]  # noqa: E731
+    before, over = ldn.selective_scan(*cut(7), h0)[1], ldn.selective_scan(*cut(9), h0)[1]
+    assert torch.equal(before[:, 1], over[:, 1]) and not torch.equal(before[:, 0], over[:, 0])
+
+
 # ---- streams, graphs, several calls ----
 def mixer_calls():
     """One call of each operator with fixed inputs: name -> (call, outputs)."""
@@ -522,6 +551,18 @@ def test_torch_layer_refuses():
     B = torch.zeros(1, 4, 1, 16, device="cuda")
     with pytest.raises(ldn.LdnError):
         ldn.selective_scan(x[None], x[None], torch.zeros(64, 16, device="cuda"), B, B, h0=h, h_final=h)
+    with pytest.raises(TypeError):
+        ldn.add_rmsnorm_e4m3(x, None, w, group=128.0)
+    with pytest.raises(TypeError):
+        ldn.add_rmsnorm(x, None, w, eps="small")
+    with pytest.raises(RuntimeError):
+        ldn.short_conv(x[None], torch.ones(64, 4, device="cuda"), activation=torch.ones(2))
+    with pytest.raises(ValueError):
+        ldn.add_rmsnorm(x, None, w, stream=3)
+    with pytest.raises(ValueError):     # B of one row for x's four
+        ldn.selective_scan_step(x, x, torch.zeros(64, 16, device="cuda"), B[:, 0], None, None, None, None, h)
+    with pytest.raises(ldn.LdnError):
+        ldn.add_rmsnorm(x.half().float(), None, w, eps=float("nan"))
 
 
 # ---- the operators together ----
