@@ -9,9 +9,12 @@
 //   dp_t = dy_t silu'(p_t),   dx_t = sum_j w[j] dp_{t+W-1-j} (+ dstate_out's row),
 //   dw[j] = sum_t dp_t x_{t-W+1+j},   db = sum_t dp_t.
 //
-// Every direction streams its rows once and is bound by HBM.  A lane owns four channels and
+// Every direction streams its rows once: HBM is the floor (bf16, W = 4: 20 us for 4 x 2048 x
+// 4096 forward, 15 us for the gradient at half the channels).  A lane owns four channels and
 // walks a run of tokens with the last W rows in registers, so nothing goes through shared
-// memory but the weights; rows are loaded a batch ahead and kept as loaded until used.
+// memory but the weights; rows are loaded a batch ahead and kept as loaded until used.  That
+// takes 30 and 33 us: half the issue slots are used, and the rest is waiting for rows (loads
+// in flight are bound by the registers that hold them) and for the taps' chains.
 #include <type_traits>
 
 #include "mixer_common.cuh"
@@ -21,8 +24,8 @@ namespace {
 
 constexpr int kWarps = 4;   // runs per block, one warp each; all warps take the same channels
 // Rows on their way at a time, and the registers a thread that leaves (blocks an SM): what
-// measured fastest of 2, 3, 4 rows and 4 to 10 blocks at 4 x 2048 x 4096 (forward: 31 us, 33 at
-// two rows, 42 with 16-byte loads and twice the registers; gradient at half the channels 39 us).
+// measured fastest of 2, 3, 4 rows and 4 to 10 blocks at 4 x 2048 x 4096 (forward: 30 us, 33 at
+// two rows, 42 with 16-byte loads and twice the registers).
 constexpr int kBatch = 4, kBwdBatch = 3;
 constexpr int fwd_blocks(int W) { return W <= 4 ? 7 : 4; }
 constexpr int bwd_blocks(int W) { return W <= 4 ? 4 : 2; }
@@ -373,14 +376,32 @@ conv_param_sum_kernel(const float *__restrict__ part, float *__restrict__ dw, fl
     }
 }
 
-// Tokens of a run: long enough that the W - 1 rows read twice cost little, short enough that
-// every SM has the 24 warps whose rows on their way (2 KB a warp) keep HBM busy.
-int conv_run(int B, int T, int C, int e)
+// Tokens of a run, of which a block has `per`; `units` blocks take a run of every sequence and
+// channel.  Blocks come in waves of those that fit on the card, and a part wave takes as long
+// as a whole one: of the runs that just fill one to four waves the one whose waves are shortest,
+// a block's start and end counted as kStart tokens.  Against runs of 64, 32, 16 or 8 tokens,
+// halved until there were 24 warps an SM: gradient of 4 x 2048 x 2048 33.2 us for 35.9, 3 x 3000
+// x 2560 41 for 51, 7 x 777 x 1028 (fp32, W = 3) 16.6 for 24.5 and forward 9.4 for 11.4; where
+// those runs happened to fill their waves the two are the same.
+constexpr int kStart = 8;
+int conv_run(long long units, int T, int W, int per, int blocks_sm)
 {
-    const long long lanes = (long long)B * ((C + 32 * e - 1) / (32 * e));   // warps per token run
-    int run = 64;
-    while (run > 8 && lanes * ((T + run - 1) / run) < 152 * 24) run /= 2;
-    return run;
+    const long long fit = 152ll * blocks_sm;
+    int best = 8;
+    long long least = 0;
+    for (int w = 1; w <= 4; ++w) {
+        const long long rb = std::max(1ll, w * fit / std::max(1ll, units)), most = rb * per;
+        const int run = (int)std::max(8ll, (T + most - 1) / most), runs = (T + run - 1) / run;
+        const long long waves = (units * ((runs + per - 1) / per) + fit - 1) / fit, cost = waves * (run + W - 1 + kStart);
+        if (w == 1 || cost < least) best = run, least = cost;
+    }
+    return best;
+}
+
+// Runs of the gradient go by 4 channels a lane whatever the alignment: the workspace's size follows.
+int conv_bwd_run(int B, int T, int C, int W)
+{
+    return conv_run((long long)B * ((C + 32 * kE - 1) / (32 * kE)), T, W, kWarps, bwd_blocks(W));
 }
 
 bool aligned_to(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -391,8 +412,8 @@ cudaError_t conv_fwd(const ConvArgs &a, cudaStream_t st)
     constexpr int E = kE, A = E * (int)sizeof(TIn);
     const bool vec = a.C % E == 0 && a.ldx % E == 0 && aligned_to(a.x, A) && aligned_to(a.y, A) &&
                      aligned_to(a.state, A) && aligned_to(a.state_out, A);
-    const int run = conv_run(a.B, a.T, a.C, vec ? E : 1), runs = std::max(1, (a.T + run - 1) / run);
     const int per = 32 * kWarps * (vec ? E : 1), cblocks = (a.C + per - 1) / per;
+    const int run = conv_run((long long)a.B * cblocks, a.T, W, 1, fwd_blocks(W)), runs = std::max(1, (a.T + run - 1) / run);
     const long long blocks = (long long)cblocks * a.B * runs;
     if (vec) short_conv_kernel<TIn, W, E, true><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
     else short_conv_kernel<TIn, W, 1, false><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
@@ -421,8 +442,7 @@ cudaError_t conv_bwd(const ConvBwdArgs &a, cudaStream_t st)
     const bool vec = a.C % kE == 0 && a.ldx % kE == 0 && aligned_to(a.x, A) && aligned_to(a.dy, A) &&
                      aligned_to(a.dx, A) && aligned_to(a.state, A) && aligned_to(a.dstate, A) &&
                      aligned_to(a.dstate_out, A);
-    // the run goes by 4 channels a lane whatever the alignment: the workspace's size follows it
-    const int run = conv_run(a.B, a.T, a.C, kE), runs = std::max(1, (a.T + run - 1) / run);
+    const int run = conv_bwd_run(a.B, a.T, a.C, W), runs = std::max(1, (a.T + run - 1) / run);
     const int per = 32 * (vec ? kE : 1), cblocks = (a.C + per - 1) / per;
     const long long blocks = (long long)cblocks * a.B * ((runs + kWarps - 1) / kWarps);
     if (vec) short_conv_bwd_kernel<TIn, W, kE, true><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
@@ -455,7 +475,7 @@ cudaError_t launch_short_conv_bwd(const ConvBwdArgs &a, cudaStream_t st) { LDN_B
 
 size_t short_conv_bwd_workspace_bytes(int B, int T, int C, int W)
 {
-    const int run = conv_run(B, T, C, kE), runs = std::max(1, (T + run - 1) / run);
+    const int run = conv_bwd_run(B, T, C, W), runs = std::max(1, (T + run - 1) / run);
     return (size_t)B * ((runs + kWarps - 1) / kWarps) * (W + 1) * C * sizeof(float);
 }
 

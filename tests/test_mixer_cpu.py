@@ -268,3 +268,12 @@ def test_e4m3_reference():
     # what lies past the largest value saturates in the kernel; torch's own cast gives NaN there
     got = torch.from_numpy(np.clip(v, -448, 448)).float().to(torch.float8_e4m3fn).double().numpy()
     assert np.array_equal(ref.e4m3(np.clip(v, -448, 448).astype(np.float32).astype(np.float64)), got)
+
+
+def test_sequences_near_the_largest_int_are_refused():
+    """Runs and segments of tokens may end a little past the sequence, so a length within
+    2^16 of the largest int is refused."""
+    most = (1 << 31) - 1 - (1 << 16)
+    for T, st in ((most, True), (most + 1, False), ((1 << 31) - 1, False)):
+        assert (ldn.ldn_short_conv_backward_workspace_size(1, T, 1, 4) > 0) == st
+        assert (ldn.ldn_ssm_backward_workspace_size(1, T, 16, 8, 1) > 0) == st
