@@ -13,8 +13,11 @@
 // again into registers and the gradients follow.  A lane owns two channels x 4 states, so the
 // channel sums of dB and dC start in registers; the rest goes by halving exchanges, over the
 // lanes of a channel for q, sum A w and sum C h (four tokens together), over the channels of a
-// warp for dB and dC.  About 16 fp32 operations and two exponentials for every state: the
-// kernel is bound by instruction issue, and two blocks an SM have to hide its latencies.
+// warp for dB and dC.  An update costs 15 fp32 operations and two exponentials (108 us for
+// 2 x 2048 tokens of 4096 x 16 on the fp32 pipes alone) and takes 24 instructions, packed pairs
+// counted once: the sums' shuffles, selections and additions are a quarter of them, broadcasts
+// into pairs, loads and the elementwise work another.  350 us: two warps a scheduler run the
+// recurrence and issue 53 % of the time.
 //
 // As in the forward a block is four warps of this recurrence and four helpers, which read the
 // rows, form dt, dt u and yb a tile ahead, and turn the sums into du, ddelta, dz and the
@@ -24,7 +27,8 @@
 // Sums across blocks (dB, dC over the channel blocks of a group; dA, dD and the bias over
 // sequences and segments) go to the workspace and are added by a last launch in a fixed
 // order: no atomics, the same bits on every call.  Few channels: the tokens are cut into
-// segments; a first launch forms every segment's carry from zero (g alone, one exponential)
+// segments; a first launch forms every segment's carry from zero (g alone, one exponential;
+// in two parts where that launch would fill half the card: 46 us for 56 at the size above)
 // and a block composes what reaches its end from the later ones.
 #include <type_traits>
 
@@ -45,14 +49,16 @@ int block_channels(int N) { return kMain / (N / S) * KC; }
 struct Plan {
     int n, len;      // segments per sequence, tokens of one (a multiple of TT)
     int gblocks;     // channel blocks per group
+    int parts;       // parts of a segment whose carries are formed side by side
+    __host__ __device__ int part_len() const { return ((len + parts - 1) / parts + TT - 1) / TT * TT; }
 };
 
 struct Work {
     float *bc;       // [gblocks][B * T][G][2][N]
     float *A;        // [B * n][D][N]
     float *D, *bias; // [B * n][D]
-    float *carry;    // [B * n][D][N]
-    float *sums;     // [B * n][D]
+    float *carry;    // [B * n * parts][D][N]
+    float *sums;     // [B * n * parts][D]
 };
 
 // Tiles are kept by warp, rows of the warp's WC channels.
@@ -118,19 +124,22 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
     const int Dg = a.D / a.G;
     const unsigned cblocks = (unsigned)pl.gblocks * a.G;
     const unsigned cb = blockIdx.x % cblocks, bs = blockIdx.x / cblocks;
-    // nothing takes the first segment's carry
-    const int segs = PHASE == kCarry ? pl.n - 1 : pl.n;
-    const int seg = (int)(bs % segs) + (PHASE == kCarry ? 1 : 0), b = (int)(bs / segs);
+    // kCarry: the parts of all segments but the first, whose carry nothing takes
+    const int segs = PHASE == kCarry ? (pl.n - 1) * pl.parts : pl.n, b = (int)(bs / segs);
+    const int part = PHASE == kCarry ? (int)(bs % segs) + pl.parts : 0;
+    const int seg = PHASE == kCarry ? part / pl.parts : (int)(bs % segs);
     const int grp = (int)(cb / pl.gblocks), gb = (int)(cb % pl.gblocks), cg = gb * DB;
     const int c0 = grp * Dg + cg, cols = min(DB, Dg - cg);
     const bool helper = threadIdx.x >= kMain;
     const int tid = threadIdx.x % kMain, lane = tid & 31, warp = tid >> 5;
     const int len = seq_len(a.lens, b, a.T);
-    const int tb = seg * pl.len, te = min(tb + pl.len, a.T);
+    const int plen = PHASE == kCarry ? pl.part_len() : pl.len;
+    const int tb = seg * pl.len + (PHASE == kCarry ? part % pl.parts * plen : 0);
+    const int te = min(min(tb + plen, (seg + 1) * pl.len), a.T);   // before tb: an empty part
     // tiles with rows of the sequence; through those behind its end g passes unchanged
     const int tiles = (max(min(len, te) - tb, 0) + TT - 1) / TT;
     const size_t row0 = (size_t)b * a.T + tb;   // the segment's first row
-    const size_t bseg = (size_t)b * pl.n + seg;
+    const size_t bseg = PHASE == kCarry ? (size_t)b * pl.n * pl.parts + part : (size_t)b * pl.n + seg;
     auto rows_of = [&](int it) { return min(max(min(len, te) - tb - it * TT, 0), TT); };
 
     if (helper) {
@@ -349,8 +358,8 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
         }
         if (PHASE == kFull && on)
 #pragma unroll 4
-            for (int j = pl.n - 1; j > seg; --j) {   // through the later segments
-                const size_t e = ((size_t)b * pl.n + j) * a.D + c0 + ch;
+            for (int j = pl.n * pl.parts - 1; j >= (seg + 1) * pl.parts; --j) {   // through the later segments
+                const size_t e = ((size_t)b * pl.n * pl.parts + j) * a.D + c0 + ch;
                 const float sd = wk.sums[e];
                 const float *p = wk.carry + e * N + l * S;
 #pragma unroll
@@ -590,7 +599,10 @@ Plan bwd_plan(int B, int T, int D, int N, int G)
     const long long blocks = (long long)B * G * gblocks;
     const int n = (int)std::max(1LL, std::min<long long>({kSms * 2 / blocks, T / (4 * TT), kMostSegs}));
     const int len = std::max(TT, (int)((((long long)T + n - 1) / n + TT - 1) / TT) * TT);
-    return {std::max(1, (T + len - 1) / len), len, gblocks};
+    const int segs = std::max(1, (T + len - 1) / len);
+    // the carries' launch leaves half the card empty where it has one of two segments
+    const int parts = segs > 1 && 2 * (segs - 1) * blocks <= kSms * 2 ? 2 : 1;
+    return {segs, len, gblocks, parts};
 }
 
 size_t up4(size_t n) { return (n + 3) / 4 * 4; }
@@ -605,8 +617,8 @@ size_t lay_out(const Plan &p, int B, int T, int D, int N, int G, float *base, Wo
     w->A = take(np * D * N);
     w->D = take(np * D);
     w->bias = take(np * D);
-    w->carry = take(p.n > 1 ? np * D * N : 0);
-    w->sums = take(p.n > 1 ? np * D : 0);
+    w->carry = take(p.n > 1 ? np * p.parts * D * N : 0);
+    w->sums = take(p.n > 1 ? np * p.parts * D : 0);
     return at;
 }
 
@@ -622,7 +634,7 @@ cudaError_t bwd_launch(const SsmBwdArgs &a, const Plan &p, const Work &w, cudaSt
     e = cudaFuncGetAttributes(&fa, k);
     if (e != cudaSuccess) return e;
     if (fa.numRegs < kRegs) return cudaErrorInvalidConfiguration;
-    const long long segs = PHASE == kCarry ? p.n - 1 : p.n;
+    const long long segs = PHASE == kCarry ? (p.n - 1) * p.parts : p.n;
     k<<<(unsigned)(p.gblocks * segs * a.G * a.B), kThreads, bytes, st>>>(a, p, w);
     return cudaGetLastError();
 }
