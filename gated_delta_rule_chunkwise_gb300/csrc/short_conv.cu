@@ -13,7 +13,7 @@
 // 4096 forward, 15 us for the gradient at half the channels).  A lane owns four channels and
 // walks a run of tokens with the last W rows in registers, so nothing goes through shared
 // memory but the weights; rows are loaded a batch ahead and kept as loaded until used.  That
-// takes 30 and 33 us: half the issue slots are used, and the rest is waiting for rows (loads
+// takes 28 and 33 us: half the issue slots are used, and the rest is waiting for rows (loads
 // in flight are bound by the registers that hold them) and for the taps' chains.
 #include <type_traits>
 
@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kWarps = 4;   // runs per block, one warp each; all warps take the same channels
 // Rows on their way at a time, and the registers a thread that leaves (blocks an SM): what
-// measured fastest of 2, 3, 4 rows and 4 to 10 blocks at 4 x 2048 x 4096 (forward: 30 us, 33 at
+// measured fastest of 2, 3, 4 rows and 4 to 10 blocks at 4 x 2048 x 4096 (forward: 28 us, 33 at
 // two rows, 42 with 16-byte loads and twice the registers).
 constexpr int kBatch = 4, kBwdBatch = 3;
 constexpr int fwd_blocks(int W) { return W <= 4 ? 7 : 4; }
@@ -132,9 +132,19 @@ short_conv_kernel(const ConvArgs a, int run, int runs, int cblocks)
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
         next[k].template load<VEC>(x + (size_t)(t0 + k) * a.ldx, t0 + k < stop ? valid : 0);
+    // Two batches in one body leave half the window's moves from register to register: 28.3 us
+    // for 29.7 at 4 x 2048 x 4096 in bf16; fp32 rows (22.9 us for 21.6 at half the channels) and
+    // more than four taps (44 for 37 at W = 8) have no registers left for it.
+    constexpr bool TWO = W <= 4 && sizeof(TIn) == 2;
     for (int t = t0; t < t1; t += kBatch) {
-        if (t + 2 * kBatch <= stop) batch(t, std::false_type{});
-        else batch(t, std::true_type{});
+        if (TWO && t + 3 * kBatch <= stop) {
+            batch(t, std::false_type{});
+            batch(t += kBatch, std::false_type{});
+        } else if (!TWO && t + 2 * kBatch <= stop) {
+            batch(t, std::false_type{});
+        } else {
+            batch(t, std::true_type{});
+        }
     }
     // The first run alone reads state rows (a run is at least W - 1 tokens), so its lanes may
     // write state_out over them once they have read the last rows.
@@ -392,7 +402,8 @@ int conv_run(long long units, int T, int W, int per, int blocks_sm)
     for (int w = 1; w <= 4; ++w) {
         const long long rb = std::max(1ll, w * fit / std::max(1ll, units)), most = rb * per;
         const int run = (int)std::max(8ll, (T + most - 1) / most), runs = (T + run - 1) / run;
-        const long long waves = (units * ((runs + per - 1) / per) + fit - 1) / fit, cost = waves * (run + W - 1 + kStart);
+        const long long waves = (units * ((runs + per - 1) / per) + fit - 1) / fit;
+        const long long cost = waves * (run + W - 1 + kStart);
         if (w == 1 || cost < least) best = run, least = cost;
     }
     return best;
@@ -413,7 +424,8 @@ cudaError_t conv_fwd(const ConvArgs &a, cudaStream_t st)
     const bool vec = a.C % E == 0 && a.ldx % E == 0 && aligned_to(a.x, A) && aligned_to(a.y, A) &&
                      aligned_to(a.state, A) && aligned_to(a.state_out, A);
     const int per = 32 * kWarps * (vec ? E : 1), cblocks = (a.C + per - 1) / per;
-    const int run = conv_run((long long)a.B * cblocks, a.T, W, 1, fwd_blocks(W)), runs = std::max(1, (a.T + run - 1) / run);
+    const int run = conv_run((long long)a.B * cblocks, a.T, W, 1, fwd_blocks(W));
+    const int runs = std::max(1, (a.T + run - 1) / run);
     const long long blocks = (long long)cblocks * a.B * runs;
     if (vec) short_conv_kernel<TIn, W, E, true><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
     else short_conv_kernel<TIn, W, 1, false><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);

@@ -313,8 +313,9 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
                 if (z) store_n<V, VEC>((TIn *)a.dz + at, zeros, valid);
             }
             for (int i = tid + tiles * TT * (2 * N / 4); i < (te - tb) * (2 * N / 4); i += kMain)
-                *reinterpret_cast<float4 *>(wk.bc + (((size_t)gb * a.B * a.T + row0 + i / (2 * N / 4)) * a.G + grp) * (2 * N) +
-                                            i % (2 * N / 4) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4 *>(
+                    wk.bc + (((size_t)gb * a.B * a.T + row0 + i / (2 * N / 4)) * a.G + grp) * (2 * N) +
+                    i % (2 * N / 4) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
             // dD and the bias over the lanes that share a vector's channels
 #pragma unroll
             for (int o = 16; o >= PR; o >>= 1)
@@ -691,7 +692,8 @@ size_t ssm_backward_workspace_bytes(int B, int T, int D, int N, int G)
 cudaError_t launch_ssm_backward(const SsmBwdArgs &a, cudaStream_t st)
 {
     if (a.T == 0) {
-        ssm_backward_empty_kernel<<<(unsigned)std::min<size_t>(((size_t)a.B * a.D * a.N + 255) / 256, 1024), 256, 0, st>>>(a);
+        const size_t blocks = std::min<size_t>(((size_t)a.B * a.D * a.N + 255) / 256, 1024);
+        ssm_backward_empty_kernel<<<(unsigned)blocks, 256, 0, st>>>(a);
         return cudaGetLastError();
     }
     switch (a.N) {
