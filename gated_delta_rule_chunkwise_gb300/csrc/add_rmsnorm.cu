@@ -200,33 +200,32 @@ add_rmsnorm_bwd_kernel(const TIn *__restrict__ dy, const TRes *__restrict__ s, c
 #pragma unroll
         for (int i = 0; i < kE; ++i) acc[k][i] = 0.f;
     }
-    Raw<TRes, kE> rs[VPT], rd[VPT];
-    Raw<TIn, kE> ry[VPT];
-    auto fetch = [&](long long row) {
+    constexpr int AHEAD = VPT == 1 ? 2 : 1;   // rows on their way
+    Raw<TRes, kE> rs[AHEAD][VPT], rd[AHEAD][VPT];
+    Raw<TIn, kE> ry[AHEAD][VPT];
+    auto fetch = [&](int h, long long row) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = (k * nt + (int)threadIdx.x) * kE, valid = row < rows ? D - c : 0;
-            rs[k].template load<VEC>(s + row * D + c, valid);
-            ry[k].template load<VEC>(dy + row * D + c, valid);
-            rd[k].template load<VEC>(dsum + row * D + c, dsum ? valid : 0);
+            rs[h][k].template load<VEC>(s + row * D + c, valid);
+            ry[h][k].template load<VEC>(dy + row * D + c, valid);
+            rd[h][k].template load<VEC>(dsum + row * D + c, dsum ? valid : 0);
         }
     };
-    fetch(blockIdx.x);
-    int turn = 0;
-    for (long long row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
+    auto one = [&](int h, int turn, long long row) {
         float sv[VPT][kE], gy[VPT][kE], d[VPT][kE], sums[2] = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            rs[k].widen(sv[k]);
-            ry[k].widen(gy[k]);
-            rd[k].widen(d[k]);
+            rs[h][k].widen(sv[k]);
+            ry[h][k].widen(gy[k]);
+            rd[h][k].widen(d[k]);
 #pragma unroll
             for (int i = 0; i < kE; ++i) {
                 sums[0] = fmaf(sv[k][i], sv[k][i], sums[0]);
                 sums[1] = fmaf(g[k][i] * gy[k][i], sv[k][i], sums[1]);
             }
         }
-        fetch(row + gridDim.x);
+        fetch(h, row + (long long)AHEAD * gridDim.x);
         block_sum<2>(sums, sm[turn], nwarps);   // two buffers: the next row's sums pass no reader of these
         const float rstd = rsqrtf(sums[0] / (float)D + eps);
         const float m = rstd * rstd * (sums[1] / (float)D);
@@ -241,6 +240,12 @@ add_rmsnorm_bwd_kernel(const TIn *__restrict__ dy, const TRes *__restrict__ s, c
             if (dx) store_n<kE, VEC>(dx + row * D + c, d[k], valid);
             if (dres) store_n<kE, VEC>(dres + row * D + c, d[k], valid);
         }
+    };
+    fetch(0, blockIdx.x);
+    if constexpr (AHEAD == 2) fetch(1, blockIdx.x + (long long)gridDim.x);
+    for (long long row = blockIdx.x; row < rows; row += 2ll * gridDim.x) {
+        one(0, 0, row);
+        if (row + gridDim.x < rows) one(AHEAD - 1, 1, row + gridDim.x);
     }
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
