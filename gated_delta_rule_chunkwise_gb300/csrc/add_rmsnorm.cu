@@ -10,7 +10,9 @@
 //   ds = dsum + rstd (w dy - s rstd^2 mean_c(w dy s)),  dw = sum over rows of dy s rstd.
 //
 // Both directions move every byte once and are bound by HBM: a row lives in registers (8
-// consecutive channels a thread and vector), two block sums a row.  Arithmetic is fp32.
+// channels a thread and vector), two block sums a row.  Arithmetic is fp32.  16384 x 4096 in
+// bf16 to e4m3 by rows takes 72 us (6,480 GB/s), 8192 x 2048 with an fp32 residual stream 31.7
+// and the gradient 43.7 (5,300 and 6,200 GB/s).
 #include <cuda_fp8.h>
 
 #include "mixer_common.cuh"
@@ -60,7 +62,7 @@ __device__ __forceinline__ float block_max(float v, float *sm, int nwarps)
     return t;
 }
 
-template <int N, bool VEC>
+template <int N, bool VEC, int STEP>
 __device__ __forceinline__ void store_e4m3(uint8_t *p, const float *v, int valid)
 {
     static_assert(N == 8, "two words");
@@ -77,8 +79,19 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float *v, int valid
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (i < valid) p[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+            if (i * STEP < valid) p[i * STEP] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
     }
+}
+
+// A thread's place in a vector of the block's, and the distance of its 8 channels: consecutive
+// where rows are whole 16-byte vectors; otherwise 32 apart, so that a warp takes the same 256
+// channels and its single elements are neighbours (5000 x 777 in bf16: 9.8 us for 22.5 with
+// consecutive ones, gradient 13.4 for 18.2).
+template <bool VEC> constexpr int kStep = VEC ? 1 : 32;
+template <bool VEC> __device__ __forceinline__ int place(int k)
+{
+    const int t = (int)threadIdx.x;
+    return k * (int)blockDim.x * kE + (VEC ? t * kE : (t & ~31) * kE + (t & 31));
 }
 
 // Rounds to the stored type and back.
@@ -102,17 +115,17 @@ add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__rest
     if constexpr (KEEP)
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int c = (k * nt + (int)threadIdx.x) * kE;
-            load_n<kE, VEC>(w + c, g[k], D - c);
+            const int c = place<VEC>(k);
+            load_n<kE, VEC, kStep<VEC>>(w + c, g[k], D - c);
         }
-    Raw<TIn, kE> rx[VPT];
-    Raw<TRes, kE> rr[VPT];
+    Raw<TIn, kE, VEC> rx[VPT];
+    Raw<TRes, kE, VEC> rr[VPT];
     auto fetch = [&](long long row) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int c = (k * nt + (int)threadIdx.x) * kE, valid = row < rows ? D - c : 0;
-            rx[k].template load<VEC>(x + row * D + c, valid);
-            rr[k].template load<VEC>(r + (r ? row * D + c : 0), r ? valid : 0);
+            const int c = place<VEC>(k), valid = row < rows ? D - c : 0;
+            rx[k].template load<VEC, kStep<VEC>>(x + row * D + c, valid);
+            rr[k].template load<VEC, kStep<VEC>>(r + (r ? row * D + c : 0), r ? valid : 0);
         }
     };
     fetch(blockIdx.x);
@@ -121,14 +134,14 @@ add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__rest
         float v[VPT][kE], ss = 0.f;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int c = (k * nt + (int)threadIdx.x) * kE;
+            const int c = place<VEC>(k);
             rx[k].widen(v[k]);
             if (r) {
                 float q[kE];
                 rr[k].widen(q);
 #pragma unroll
                 for (int i = 0; i < kE; ++i) v[k][i] = as_stored(v[k][i] + q[i], r);
-                store_n<kE, VEC>(r_out + row * D + c, v[k], D - c);
+                store_n<kE, VEC, kStep<VEC>>(r_out + row * D + c, v[k], D - c);
             }
 #pragma unroll
             for (int i = 0; i < kE; ++i) ss = fmaf(v[k][i], v[k][i], ss);
@@ -139,17 +152,34 @@ add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__rest
         float top = 0.f;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int c = (k * nt + (int)threadIdx.x) * kE, valid = D - c;
-            if constexpr (!KEEP) load_n<kE, VEC>(w + c, g[0], valid);
+            const int c = place<VEC>(k), valid = D - c;
+            if constexpr (!KEEP) load_n<kE, VEC, kStep<VEC>>(w + c, g[0], valid);
 #pragma unroll
             for (int i = 0; i < kE; ++i) v[k][i] *= rstd * g[KEEP ? k : 0][i];
             if constexpr (EIGHT == 0) {
-                store_n<kE, VEC>((TIn *)y + row * D + c, v[k], valid);
+                store_n<kE, VEC, kStep<VEC>>((TIn *)y + row * D + c, v[k], valid);
             } else {
                 float m = 0.f;
+                if constexpr (EIGHT == 1 || VEC)
 #pragma unroll
-                for (int i = 0; i < kE; ++i) m = fmaxf(m, fabsf(v[k][i]));
-                if constexpr (EIGHT == 2) {
+                    for (int i = 0; i < kE; ++i) m = fmaxf(m, fabsf(v[k][i]));
+                if constexpr (EIGHT == 2 && !VEC) {
+                    // 128 channels are four of every lane's
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        m = 0x1p-100f;
+#pragma unroll
+                        for (int i = 4 * h; i < 4 * h + 4; ++i) m = fmaxf(m, fabsf(v[k][i]));
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        const float up = kE4m3Max / m;
+#pragma unroll
+                        for (int i = 4 * h; i < 4 * h + 4; ++i) v[k][i] *= up;
+                        if ((threadIdx.x & 31) == 0 && valid > 128 * h)
+                            scale[row * (long long)((D + 127) / 128) + c / 128 + h] = m / kE4m3Max;
+                    }
+                    store_e4m3<kE, VEC, kStep<VEC>>((uint8_t *)y + row * D + c, v[k], valid);
+                } else if constexpr (EIGHT == 2) {
                     // 128 channels are the 8-channel vectors of 16 neighbouring lanes
 #pragma unroll
                     for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -157,7 +187,7 @@ add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__rest
                     const float up = kE4m3Max / m;
 #pragma unroll
                     for (int i = 0; i < kE; ++i) v[k][i] *= up;
-                    store_e4m3<kE, VEC>((uint8_t *)y + row * D + c, v[k], valid);
+                    store_e4m3<kE, VEC, kStep<VEC>>((uint8_t *)y + row * D + c, v[k], valid);
                     if ((threadIdx.x & 15) == 0 && valid > 0)
                         scale[row * (long long)((D + 127) / 128) + c / 128] = m / kE4m3Max;
                 } else {
@@ -170,10 +200,10 @@ add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__rest
             const float up = kE4m3Max / top;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int c = (k * nt + (int)threadIdx.x) * kE;
+                const int c = place<VEC>(k);
 #pragma unroll
                 for (int i = 0; i < kE; ++i) v[k][i] *= up;
-                store_e4m3<kE, VEC>((uint8_t *)y + row * D + c, v[k], D - c);
+                store_e4m3<kE, VEC, kStep<VEC>>((uint8_t *)y + row * D + c, v[k], D - c);
             }
             if (threadIdx.x == 0) scale[row] = top / kE4m3Max;
         }
@@ -195,21 +225,21 @@ add_rmsnorm_bwd_kernel(const TIn *__restrict__ dy, const TRes *__restrict__ s, c
     float acc[VPT][kE], g[VPT][kE];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int c = (k * nt + (int)threadIdx.x) * kE;
-        load_n<kE, VEC>(w + c, g[k], D - c);
+        const int c = place<VEC>(k);
+        load_n<kE, VEC, kStep<VEC>>(w + c, g[k], D - c);
 #pragma unroll
         for (int i = 0; i < kE; ++i) acc[k][i] = 0.f;
     }
-    constexpr int AHEAD = VPT == 1 ? 2 : 1;   // rows on their way
-    Raw<TRes, kE> rs[AHEAD][VPT], rd[AHEAD][VPT];
-    Raw<TIn, kE> ry[AHEAD][VPT];
+    constexpr int AHEAD = VPT == 1 ? 2 : 1;   // rows on their way: as many as there are registers for
+    Raw<TRes, kE, VEC> rs[AHEAD][VPT], rd[AHEAD][VPT];
+    Raw<TIn, kE, VEC> ry[AHEAD][VPT];
     auto fetch = [&](int h, long long row) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int c = (k * nt + (int)threadIdx.x) * kE, valid = row < rows ? D - c : 0;
-            rs[h][k].template load<VEC>(s + row * D + c, valid);
-            ry[h][k].template load<VEC>(dy + row * D + c, valid);
-            rd[h][k].template load<VEC>(dsum + row * D + c, dsum ? valid : 0);
+            const int c = place<VEC>(k), valid = row < rows ? D - c : 0;
+            rs[h][k].template load<VEC, kStep<VEC>>(s + row * D + c, valid);
+            ry[h][k].template load<VEC, kStep<VEC>>(dy + row * D + c, valid);
+            rd[h][k].template load<VEC, kStep<VEC>>(dsum + row * D + c, dsum ? valid : 0);
         }
     };
     auto one = [&](int h, int turn, long long row) {
@@ -231,14 +261,14 @@ add_rmsnorm_bwd_kernel(const TIn *__restrict__ dy, const TRes *__restrict__ s, c
         const float m = rstd * rstd * (sums[1] / (float)D);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int c = (k * nt + (int)threadIdx.x) * kE, valid = D - c;
+            const int c = place<VEC>(k), valid = D - c;
 #pragma unroll
             for (int i = 0; i < kE; ++i) {
                 acc[k][i] = fmaf(gy[k][i], sv[k][i] * rstd, acc[k][i]);
                 d[k][i] = fmaf(rstd, g[k][i] * gy[k][i] - sv[k][i] * m, d[k][i]);
             }
-            if (dx) store_n<kE, VEC>(dx + row * D + c, d[k], valid);
-            if (dres) store_n<kE, VEC>(dres + row * D + c, d[k], valid);
+            if (dx) store_n<kE, VEC, kStep<VEC>>(dx + row * D + c, d[k], valid);
+            if (dres) store_n<kE, VEC, kStep<VEC>>(dres + row * D + c, d[k], valid);
         }
     };
     fetch(0, blockIdx.x);
@@ -249,8 +279,8 @@ add_rmsnorm_bwd_kernel(const TIn *__restrict__ dy, const TRes *__restrict__ s, c
     }
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int c = (k * nt + (int)threadIdx.x) * kE;
-        store_n<kE, VEC>(part + (size_t)blockIdx.x * D + c, acc[k], D - c);
+        const int c = place<VEC>(k);
+        store_n<kE, VEC, kStep<VEC>>(part + (size_t)blockIdx.x * D + c, acc[k], D - c);
     }
 }
 
@@ -284,18 +314,19 @@ add_rmsnorm_bwd_wide_kernel(const TIn *__restrict__ dy, const TRes *__restrict__
 {
     extern __shared__ float acc[];
     __shared__ float sm[2][64];
-    const int nt = blockDim.x, step = nt * kE, first = (int)threadIdx.x * kE;
+    const int nt = blockDim.x, step = nt * kE, first = place<VEC>(0);
+    constexpr int E = kStep<VEC>;   // a thread's channels are c + i E
     for (int c = first; c < D; c += step)
 #pragma unroll
         for (int i = 0; i < kE; ++i)
-            if (c + i < D) acc[c + i] = 0.f;
+            if (c + i * E < D) acc[c + i * E] = 0.f;
     int turn = 0;
     for (long long row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
         float sums[2] = {0.f, 0.f}, sv[kE], gy[kE], g[kE], d[kE];
         for (int c = first; c < D; c += step) {
-            load_n<kE, VEC>(s + row * D + c, sv, D - c);
-            load_n<kE, VEC>(dy + row * D + c, gy, D - c);
-            load_n<kE, VEC>(w + c, g, D - c);
+            load_n<kE, VEC, kStep<VEC>>(s + row * D + c, sv, D - c);
+            load_n<kE, VEC, kStep<VEC>>(dy + row * D + c, gy, D - c);
+            load_n<kE, VEC, kStep<VEC>>(w + c, g, D - c);
 #pragma unroll
             for (int i = 0; i < kE; ++i) {
                 sums[0] = fmaf(sv[i], sv[i], sums[0]);
@@ -306,23 +337,23 @@ add_rmsnorm_bwd_wide_kernel(const TIn *__restrict__ dy, const TRes *__restrict__
         const float rstd = rsqrtf(sums[0] / (float)D + eps);
         const float m = rstd * rstd * (sums[1] / (float)D);
         for (int c = first; c < D; c += step) {
-            load_n<kE, VEC>(s + row * D + c, sv, D - c);
-            load_n<kE, VEC>(dy + row * D + c, gy, D - c);
-            load_n<kE, VEC>(w + c, g, D - c);
-            load_n<kE, VEC>(dsum + row * D + c, d, dsum ? D - c : 0);
+            load_n<kE, VEC, kStep<VEC>>(s + row * D + c, sv, D - c);
+            load_n<kE, VEC, kStep<VEC>>(dy + row * D + c, gy, D - c);
+            load_n<kE, VEC, kStep<VEC>>(w + c, g, D - c);
+            load_n<kE, VEC, kStep<VEC>>(dsum + row * D + c, d, dsum ? D - c : 0);
 #pragma unroll
             for (int i = 0; i < kE; ++i) {
-                if (c + i < D) acc[c + i] = fmaf(gy[i], sv[i] * rstd, acc[c + i]);
+                if (c + i * E < D) acc[c + i * E] = fmaf(gy[i], sv[i] * rstd, acc[c + i * E]);
                 d[i] = fmaf(rstd, g[i] * gy[i] - sv[i] * m, d[i]);
             }
-            if (dx) store_n<kE, VEC>(dx + row * D + c, d, D - c);
-            if (dres) store_n<kE, VEC>(dres + row * D + c, d, D - c);
+            if (dx) store_n<kE, VEC, kStep<VEC>>(dx + row * D + c, d, D - c);
+            if (dres) store_n<kE, VEC, kStep<VEC>>(dres + row * D + c, d, D - c);
         }
     }
     for (int c = first; c < D; c += step)
 #pragma unroll
         for (int i = 0; i < kE; ++i)
-            if (c + i < D) part[(size_t)blockIdx.x * D + c + i] = acc[c + i];
+            if (c + i * E < D) part[(size_t)blockIdx.x * D + c + i * E] = acc[c + i * E];
 }
 
 // Vectors per thread: the fewest that fit 512 threads, but two from 4096 channels on.
@@ -389,7 +420,8 @@ cudaError_t norm_bwd_wide(const AddNormBwdArgs &a, int grid, cudaStream_t st)
 template <typename TIn, typename TRes>
 cudaError_t norm_bwd_pick(const AddNormBwdArgs &a, int grid, bool vec, cudaStream_t st)
 {
-    if (a.D > kWide) return vec ? norm_bwd_wide<TIn, TRes, true>(a, grid, st) : norm_bwd_wide<TIn, TRes, false>(a, grid, st);
+    if (a.D > kWide)
+        return vec ? norm_bwd_wide<TIn, TRes, true>(a, grid, st) : norm_bwd_wide<TIn, TRes, false>(a, grid, st);
     if (norm_vpt(a.D) == 1) norm_bwd_run<TIn, TRes, 1>(a, grid, vec, st);
     else norm_bwd_run<TIn, TRes, 2>(a, grid, vec, st);
     return cudaGetLastError();
@@ -409,8 +441,8 @@ cudaError_t launch_add_rmsnorm(const AddNormArgs &a, cudaStream_t st)
 
 // Blocks of the gradient's row walk: 512 threads an SM (one block of wide rows), no more than
 // rows: two 256-thread blocks an SM with the next row on its way keep HBM busy, and each block
-// more is a row more for the column sum (8192 x 2048: 54 us at 512 threads, 57 at 1024, 64 at
-// 2048, 81 at 256).  A fixed 152 SMs, so that the workspace's size needs no device.
+// more is a row more for the column sum (8192 x 2048, with one row on its way: 54 us at 512
+// threads, 57 at 1024, 64 at 2048, 81 at 256; two rows on their way take 2 us off).  A fixed 152 SMs, so that the workspace's size needs no device.
 int add_rmsnorm_bwd_blocks(long long rows, int D)
 {
     const int per = D > kWide ? 1 : std::max(1, 512 / norm_threads(D, norm_vpt(D)));

@@ -2,14 +2,16 @@
 // residual's addition (add_rmsnorm.cu), the short convolution (short_conv.cu) and the
 // selective scan (ssm_scan.cu, ssm_backward.cu).
 #pragma once
+#include <type_traits>
+
 #include "ldn_internal.cuh"
 
 namespace ldn {
 
 // N consecutive elements, widened to fp32.  Vectors of 8 / 16 bytes when VEC (the address is
-// then a multiple of the vector), single elements otherwise; elements at and past `valid`
-// read as zero (VEC vectors are wholly inside or wholly outside).
-template <int N, bool VEC>
+// then a multiple of the vector), single elements otherwise, STEP apart; places at and past
+// `valid` read as zero (VEC vectors are wholly inside or wholly outside).
+template <int N, bool VEC, int STEP = 1>
 __device__ __forceinline__ void load_n(const float *p, float *v, int valid = N)
 {
     if constexpr (VEC) {
@@ -21,7 +23,7 @@ __device__ __forceinline__ void load_n(const float *p, float *v, int valid = N)
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = i < valid ? p[i] : 0.f;
+        for (int i = 0; i < N; ++i) v[i] = i * STEP < valid ? p[i * STEP] : 0.f;
     }
 }
 
@@ -31,7 +33,7 @@ __device__ __forceinline__ void bf16x2_widen(uint32_t u, float *v)
     v[1] = __uint_as_float(u & 0xffff0000u);
 }
 
-template <int N, bool VEC>
+template <int N, bool VEC, int STEP = 1>
 __device__ __forceinline__ void load_n(const __nv_bfloat16 *p, float *v, int valid = N)
 {
     if constexpr (VEC && N == 8) {
@@ -43,7 +45,7 @@ __device__ __forceinline__ void load_n(const __nv_bfloat16 *p, float *v, int val
         bf16x2_widen(u.x, v); bf16x2_widen(u.y, v + 2);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = i < valid ? __bfloat162float(p[i]) : 0.f;
+        for (int i = 0; i < N; ++i) v[i] = i * STEP < valid ? __bfloat162float(p[i * STEP]) : 0.f;
     }
 }
 
@@ -63,7 +65,7 @@ __device__ __forceinline__ uint32_t bf16x2_pack(float a, float b)
 }
 
 // N consecutive results, each rounded once to the element type; nothing at and past `valid`.
-template <int N, bool VEC>
+template <int N, bool VEC, int STEP = 1>
 __device__ __forceinline__ void store_n(float *p, const float *v, int valid = N)
 {
     if constexpr (VEC) {
@@ -74,11 +76,11 @@ __device__ __forceinline__ void store_n(float *p, const float *v, int valid = N)
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (i < valid) p[i] = v[i];
+            if (i * STEP < valid) p[i * STEP] = v[i];
     }
 }
 
-template <int N, bool VEC>
+template <int N, bool VEC, int STEP = 1>
 __device__ __forceinline__ void store_n(__nv_bfloat16 *p, const float *v, int valid = N)
 {
     if constexpr (VEC && N == 8) {
@@ -92,7 +94,7 @@ __device__ __forceinline__ void store_n(__nv_bfloat16 *p, const float *v, int va
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (i < valid) p[i] = __float2bfloat16_rn(v[i]);
+            if (i * STEP < valid) p[i * STEP] = __float2bfloat16_rn(v[i]);
     }
 }
 
@@ -145,16 +147,21 @@ __device__ __forceinline__ float2 softplus_accurate(float2 x)
 }
 __device__ __forceinline__ float softplus_accurate(float x) { return softplus_accurate(make_float2(x, x)).x; }
 
-// N consecutive elements as loaded (16 bytes at a time where VEC): what is prefetched is kept
-// so, since widening it would wait for it.
-template <typename T, int N>
+// N elements as loaded (16 bytes at a time where VEC): what is prefetched is kept so, since
+// widening it would wait for it.  Not PACKED: single elements, a word each, for the same reason.
+template <typename T, int N, bool PACKED = true>
 struct Raw {
-    static constexpr int WORDS = N * (int)sizeof(T) / 4 < 1 ? 1 : N * (int)sizeof(T) / 4;
+    static constexpr int WORDS = !PACKED ? N : N * (int)sizeof(T) / 4 < 1 ? 1 : N * (int)sizeof(T) / 4;
     uint32_t w[WORDS];
-    template <bool VEC>
+    template <bool VEC, int STEP = 1>
     __device__ __forceinline__ void load(const T *p, int valid)
     {
-        if constexpr (VEC && WORDS >= 4) {
+        if constexpr (!PACKED) {
+            using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                w[i] = i * STEP < valid ? *reinterpret_cast<const Bits *>(p + i * STEP) : 0u;
+        } else if constexpr (VEC && WORDS >= 4) {
 #pragma unroll
             for (int i = 0; i < WORDS; i += 4) {
                 const uint4 q = valid > 0 ? reinterpret_cast<const uint4 *>(p)[i / 4] : make_uint4(0, 0, 0, 0);
@@ -175,6 +182,9 @@ struct Raw {
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] = __uint_as_float(w[i]);
+        } else if constexpr (!PACKED) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = __uint_as_float(w[i] << 16);
         } else if constexpr (N % 2 == 0) {
 #pragma unroll
             for (int i = 0; i < N; i += 2) bf16x2_widen(w[i / 2], v + i);
