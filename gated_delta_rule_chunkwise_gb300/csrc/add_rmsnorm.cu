@@ -442,7 +442,8 @@ cudaError_t launch_add_rmsnorm(const AddNormArgs &a, cudaStream_t st)
 // Blocks of the gradient's row walk: 512 threads an SM (one block of wide rows), no more than
 // rows: two 256-thread blocks an SM with the next row on its way keep HBM busy, and each block
 // more is a row more for the column sum (8192 x 2048, with one row on its way: 54 us at 512
-// threads, 57 at 1024, 64 at 2048, 81 at 256; two rows on their way take 2 us off).  A fixed 152 SMs, so that the workspace's size needs no device.
+// threads, 57 at 1024, 64 at 2048, 81 at 256; two rows on their way take 2 us off).  A fixed
+// 152 SMs, so that the workspace's size needs no device.
 int add_rmsnorm_bwd_blocks(long long rows, int D)
 {
     const int per = D > kWide ? 1 : std::max(1, 512 / norm_threads(D, norm_vpt(D)));

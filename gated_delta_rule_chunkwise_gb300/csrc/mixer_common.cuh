@@ -12,7 +12,7 @@ namespace ldn {
 // then a multiple of the vector), single elements otherwise, STEP apart; places at and past
 // `valid` read as zero (VEC vectors are wholly inside or wholly outside).
 template <int N, bool VEC, int STEP = 1>
-__device__ __forceinline__ void load_n(const float *p, float *v, int valid = N)
+__device__ __forceinline__ void load_n(const float *p, float *v, int valid = N * STEP)
 {
     if constexpr (VEC) {
         static_assert(N % 4 == 0, "float4 loads");
@@ -34,7 +34,7 @@ __device__ __forceinline__ void bf16x2_widen(uint32_t u, float *v)
 }
 
 template <int N, bool VEC, int STEP = 1>
-__device__ __forceinline__ void load_n(const __nv_bfloat16 *p, float *v, int valid = N)
+__device__ __forceinline__ void load_n(const __nv_bfloat16 *p, float *v, int valid = N * STEP)
 {
     if constexpr (VEC && N == 8) {
         const uint4 u = valid > 0 ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t bf16x2_pack(float a, float b)
 
 // N consecutive results, each rounded once to the element type; nothing at and past `valid`.
 template <int N, bool VEC, int STEP = 1>
-__device__ __forceinline__ void store_n(float *p, const float *v, int valid = N)
+__device__ __forceinline__ void store_n(float *p, const float *v, int valid = N * STEP)
 {
     if constexpr (VEC) {
         if (valid > 0)
@@ -81,7 +81,7 @@ __device__ __forceinline__ void store_n(float *p, const float *v, int valid = N)
 }
 
 template <int N, bool VEC, int STEP = 1>
-__device__ __forceinline__ void store_n(__nv_bfloat16 *p, const float *v, int valid = N)
+__device__ __forceinline__ void store_n(__nv_bfloat16 *p, const float *v, int valid = N * STEP)
 {
     if constexpr (VEC && N == 8) {
         if (valid > 0)

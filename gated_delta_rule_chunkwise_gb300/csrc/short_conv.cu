@@ -27,44 +27,61 @@ constexpr int kWarps = 4;   // runs per block, one warp each; all warps take the
 // measured fastest of 2, 3, 4 rows and 4 to 10 blocks at 4 x 2048 x 4096 (forward: 28 us, 33 at
 // two rows, 42 with 16-byte loads and twice the registers).
 constexpr int kBatch = 4, kBwdBatch = 3;
-constexpr int fwd_blocks(int W) { return W <= 4 ? 7 : 4; }
-constexpr int bwd_blocks(int W) { return W <= 4 ? 4 : 2; }
-constexpr int kE = 4;   // channels a lane
+// Single elements (a word each on their way) leave room for fewer blocks.
+constexpr int fwd_blocks(int W, bool vec) { return W > 4 ? 4 : vec ? 7 : 5; }
+constexpr int bwd_blocks(int W, bool vec) { return W > 4 ? 2 : vec ? 4 : 3; }
+
+// A lane owns 4 channels: consecutive ones where rows are whole vectors of 4, otherwise 32
+// apart, so that a warp's single elements are neighbours (against one channel a lane: 4 x 2048
+// x 1001 bf16 12.6 us for 14.2, gradient 29.7 for 31.9; 8 x 700 x 5003 30 for 41, gradient 87
+// for 81; 2 x 100 x 301, which has too few lanes then, 4.5 for 3.1).
+constexpr int kE = 4;
+constexpr int step_of(bool vec) { return vec ? 1 : 32; }
+__device__ __forceinline__ int place(bool vec, int t) { return vec ? t * kE : (t & ~31) * kE + (t & 31); }
 
 __device__ __forceinline__ int seq_len(const int *lens, int b, int T)
 {
     return lens ? min(max(lens[b], 0), T) : T;
 }
 
-// The weights of CH channels from c0 to shared memory, tap by tap: wsm[j][CH].
+// The weights of CH channels from c0 to shared memory, tap by tap: wsm[j][CH].  (Loaded one
+// after another they cost a block 1 us: 300 x 512 3.6 us for 4.3, 4 x 2048 x 4096 27.5 for 28.4.)
 template <int W, int CH>
 __device__ __forceinline__ void load_taps(float *wsm, const float *w, int c0, int C)
 {
-    for (int i = threadIdx.x; i < CH * W; i += blockDim.x) {
-        const int c = i / W, j = i % W;
-        wsm[j * CH + c] = c0 + c < C ? __ldg(w + (size_t)(c0 + c) * W + j) : 0.f;
+    constexpr int EACH = CH * W / (32 * kWarps);
+    float v[EACH];   // all on their way at once
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        const int i = k * 32 * kWarps + (int)threadIdx.x;
+        v[k] = c0 + i / W < C ? __ldg(w + (size_t)c0 * W + i) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        const int i = k * 32 * kWarps + (int)threadIdx.x;
+        wsm[i % W * CH + i / W] = v[k];
     }
     __syncthreads();
 }
 
 // A block is one run of tokens; its warps take neighbouring channels, so that it reads and
 // writes 1 KB (bf16) of every row.
-template <typename TIn, int W, int E, bool VEC>
-__global__ void __launch_bounds__(32 * kWarps, fwd_blocks(W))
+template <typename TIn, int W, bool VEC>
+__global__ void __launch_bounds__(32 * kWarps, fwd_blocks(W, VEC))
 short_conv_kernel(const ConvArgs a, int run, int runs, int cblocks)
 {
-    constexpr int CH = 32 * kWarps * E;
+    constexpr int E = kE, STEP = step_of(VEC), CH = 32 * kWarps * E;
     __shared__ __align__(16) float wsm[W * CH];
     const int cb = blockIdx.x % cblocks;
     const unsigned rb = blockIdx.x / cblocks;
     const int b = (int)(rb / runs), ri = (int)(rb % runs);
     load_taps<W, CH>(wsm, a.w, cb * CH, a.C);
-    const int at = (int)threadIdx.x * E, c = cb * CH + at, valid = a.C - c;
+    const int at = place(VEC, threadIdx.x), c = cb * CH + at, valid = a.C - c;
     if (valid <= 0) return;
     float wt[W][E], bias[E];
 #pragma unroll
-    for (int j = 0; j < W; ++j) load_n<E, (E % 4 == 0)>(&wsm[j * CH + at], wt[j]);
-    if (a.bias) load_n<E, false>(a.bias + c, bias, valid);
+    for (int j = 0; j < W; ++j) load_n<E, VEC, STEP>(&wsm[j * CH + at], wt[j]);
+    if (a.bias) load_n<E, false, STEP>(a.bias + c, bias, valid);
     else
 #pragma unroll
         for (int i = 0; i < E; ++i) bias[i] = 0.f;
@@ -75,17 +92,17 @@ short_conv_kernel(const ConvArgs a, int run, int runs, int cblocks)
     // row t of the sequence: the state's for t < 0, zeros at and past the end
     auto row = [&](int t, float *v) {
         if (t < 0) {
-            if (st) load_n<E, VEC>(st + (size_t)(t + W - 1) * a.C, v, valid);
+            if (st) load_n<E, VEC, STEP>(st + (size_t)(t + W - 1) * a.C, v, valid);
             else
 #pragma unroll
                 for (int i = 0; i < E; ++i) v[i] = 0.f;
         } else {
-            load_n<E, VEC>(x + (size_t)t * a.ldx, v, t < len ? valid : 0);
+            load_n<E, VEC, STEP>(x + (size_t)t * a.ldx, v, t < len ? valid : 0);
         }
     };
     // win: the W - 1 rows before a batch, then the batch; the next batch is on its way as loaded
     float win[W - 1 + kBatch][E];
-    Raw<TIn, E> next[kBatch];
+    Raw<TIn, E, VEC> next[kBatch];
     const int stop = min(len, t1);   // rows past it are not read
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) row(t0 - (W - 1) + j, win[j]);
@@ -96,33 +113,26 @@ short_conv_kernel(const ConvArgs a, int run, int runs, int cblocks)
         for (int k = 0; k < kBatch; ++k) next[k].widen(win[W - 1 + k]);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-            next[k].template load<VEC>(x + (size_t)(t + kBatch + k) * a.ldx,
+            next[k].template load<VEC, STEP>(x + (size_t)(t + kBatch + k) * a.ldx,
                                        !EDGE || t + kBatch + k < stop ? valid : 0);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             float p[E];
-            if constexpr (E % 2 == 0) {
 #pragma unroll
-                for (int i = 0; i < E; i += 2) {
-                    float2 q = make_float2(bias[i], bias[i + 1]);
+            for (int i = 0; i < E; i += 2) {
+                float2 q = make_float2(bias[i], bias[i + 1]);
 #pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        q = __ffma2_rn(make_float2(wt[j][i], wt[j][i + 1]),
-                                       make_float2(win[k + j][i], win[k + j][i + 1]), q);
-                    if (a.act) q = silu_fast(q);
-                    p[i] = q.x;
-                    p[i + 1] = q.y;
-                }
-            } else {
-                p[0] = bias[0];
-#pragma unroll
-                for (int j = 0; j < W; ++j) p[0] = fmaf(wt[j][0], win[k + j][0], p[0]);
-                if (a.act) p[0] *= sigmoid_fast(p[0]);
+                for (int j = 0; j < W; ++j)
+                    q = __ffma2_rn(make_float2(wt[j][i], wt[j][i + 1]),
+                                   make_float2(win[k + j][i], win[k + j][i + 1]), q);
+                if (a.act) q = silu_fast(q);
+                p[i] = q.x;
+                p[i + 1] = q.y;
             }
             if (EDGE && t + k >= len)
 #pragma unroll
                 for (int i = 0; i < E; ++i) p[i] = 0.f;
-            if (!EDGE || t + k < t1) store_n<E, VEC>(y + (size_t)(t + k) * a.C, p, valid);
+            if (!EDGE || t + k < t1) store_n<E, VEC, STEP>(y + (size_t)(t + k) * a.C, p, valid);
         }
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
@@ -131,7 +141,7 @@ short_conv_kernel(const ConvArgs a, int run, int runs, int cblocks)
     };
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
-        next[k].template load<VEC>(x + (size_t)(t0 + k) * a.ldx, t0 + k < stop ? valid : 0);
+        next[k].template load<VEC, STEP>(x + (size_t)(t0 + k) * a.ldx, t0 + k < stop ? valid : 0);
     // Two batches in one body leave half the window's moves from register to register: 28.3 us
     // for 29.7 at 4 x 2048 x 4096 in bf16; fp32 rows (22.9 us for 21.6 at half the channels) and
     // more than four taps (44 for 37 at W = 8) have no registers left for it.
@@ -154,7 +164,7 @@ short_conv_kernel(const ConvArgs a, int run, int runs, int cblocks)
         for (int j = 0; j < W - 1; ++j) row(len - (W - 1) + j, last[j]);
         TIn *so = (TIn *)a.state_out + (size_t)b * (W - 1) * a.C + c;
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) store_n<E, VEC>(so + (size_t)j * a.C, last[j], valid);
+        for (int j = 0; j < W - 1; ++j) store_n<E, VEC, STEP>(so + (size_t)j * a.C, last[j], valid);
     }
 }
 
@@ -189,20 +199,21 @@ __global__ void __launch_bounds__(128) short_conv_step_kernel(const ConvArgs a)
 // then row t - (W - 1) of dx, whose last term dp_t is.  The first run also emits the state's
 // rows (t < 0).  dw and db over the run's own tokens, summed over the block's warps, go to
 // part [rblocks * B][W + 1][C].
-template <typename TIn, int W, int E, bool VEC>
-__global__ void __launch_bounds__(32 * kWarps, bwd_blocks(W))
+template <typename TIn, int W, bool VEC>
+__global__ void __launch_bounds__(32 * kWarps, bwd_blocks(W, VEC))
 short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
 {
+    constexpr int E = kE, STEP = step_of(VEC);
     __shared__ __align__(16) float wsm[W * 32 * E];
     __shared__ float sums[kWarps][W + 1][32 * E];
     const int cb = blockIdx.x % cblocks;
     const unsigned rb = blockIdx.x / cblocks;
     const int rblocks = (runs + kWarps - 1) / kWarps;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, at = place(VEC, threadIdx.x & 31);
     const int b = (int)(rb / rblocks), ri = (int)(rb % rblocks) * kWarps + warp;
     const int c0 = cb * 32 * E;
     load_taps<W, 32 * E>(wsm, a.w, c0, a.C);
-    const int c = c0 + lane * E, valid = a.C - c;
+    const int c = c0 + at, valid = a.C - c;
     float dw[W + 1][E];
 #pragma unroll
     for (int j = 0; j <= W; ++j)
@@ -211,8 +222,8 @@ short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
     if (ri < runs && valid > 0) {
         float wt[W][E], bias[E];
 #pragma unroll
-        for (int j = 0; j < W; ++j) load_n<E, (E % 4 == 0)>(&wsm[j * 32 * E + lane * E], wt[j]);
-        if (a.bias) load_n<E, false>(a.bias + c, bias, valid);
+        for (int j = 0; j < W; ++j) load_n<E, VEC, STEP>(&wsm[j * 32 * E + at], wt[j]);
+        if (a.bias) load_n<E, false, STEP>(a.bias + c, bias, valid);
         else
 #pragma unroll
             for (int i = 0; i < E; ++i) bias[i] = 0.f;
@@ -226,24 +237,24 @@ short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
         TIn *dst = a.dstate ? (TIn *)a.dstate + so : nullptr;
         auto row = [&](int t, float *v) {
             if (t < 0) {
-                if (st) load_n<E, VEC>(st + (size_t)(t + W - 1) * a.C, v, valid);
+                if (st) load_n<E, VEC, STEP>(st + (size_t)(t + W - 1) * a.C, v, valid);
                 else
 #pragma unroll
                     for (int i = 0; i < E; ++i) v[i] = 0.f;
             } else {
-                load_n<E, VEC>(x + (size_t)t * a.ldx, v, t < len ? valid : 0);
+                load_n<E, VEC, STEP>(x + (size_t)t * a.ldx, v, t < len ? valid : 0);
             }
         };
         // rows t-W+1 .. of x and of dp, a batch at a time; the next batch is on its way as loaded
         float win[W - 1 + kBwdBatch][E], dp[W - 1 + kBwdBatch][E];
-        Raw<TIn, E> nx[kBwdBatch], ny[kBwdBatch];
+        Raw<TIn, E, VEC> nx[kBwdBatch], ny[kBwdBatch];
         const int end = t1 + W - 1, stop = min(len, end);   // dp_t to end; rows past stop are not read
         auto fetch = [&](int t, auto edge) {
 #pragma unroll
             for (int k = 0; k < kBwdBatch; ++k) {
                 const int n = !decltype(edge)::value || t + k < stop ? valid : 0;
-                nx[k].template load<VEC>(x + (size_t)(t + k) * a.ldx, n);
-                ny[k].template load<VEC>(dy + (size_t)(t + k) * a.C, n);
+                nx[k].template load<VEC, STEP>(x + (size_t)(t + k) * a.ldx, n);
+                ny[k].template load<VEC, STEP>(dy + (size_t)(t + k) * a.C, n);
             }
         };
 #pragma unroll
@@ -264,76 +275,55 @@ short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
 #pragma unroll
             for (int k = 0; k < kBwdBatch; ++k) {
                 float *now = dp[W - 1 + k];
-                if constexpr (E % 2 == 0) {
 #pragma unroll
-                    for (int i = 0; i < E; i += 2) {
-                        float2 d = make_float2(now[i], now[i + 1]);
-                        if (a.act) {
-                            float2 p = make_float2(bias[i], bias[i + 1]);
-#pragma unroll
-                            for (int j = 0; j < W; ++j)
-                                p = __ffma2_rn(make_float2(wt[j][i], wt[j][i + 1]),
-                                               make_float2(win[k + j][i], win[k + j][i + 1]), p);
-                            const float2 g = rcp(__fadd2_rn(ex2(__fmul2_rn(p, dup(-kLog2e))), dup(1.f)));
-                            const float2 rest = __ffma2_rn(g, dup(-1.f), dup(1.f));
-                            d = __fmul2_rn(d, __fmul2_rn(g, __ffma2_rn(p, rest, dup(1.f))));
-                        }
-                        if (EDGE && t + k >= len) d = dup(0.f);   // nothing flows from past the end, whatever p is
-                        now[i] = d.x;
-                        now[i + 1] = d.y;
-                        if (!EDGE || t + k < t1) {
-#pragma unroll
-                            for (int j = 0; j < W; ++j) {
-                                const float2 q = __ffma2_rn(d, make_float2(win[k + j][i], win[k + j][i + 1]),
-                                                            make_float2(dw[j][i], dw[j][i + 1]));
-                                dw[j][i] = q.x;
-                                dw[j][i + 1] = q.y;
-                            }
-                            const float2 q = __fadd2_rn(d, make_float2(dw[W][i], dw[W][i + 1]));
-                            dw[W][i] = q.x;
-                            dw[W][i + 1] = q.y;
-                        }
-                    }
-                } else {
+                for (int i = 0; i < E; i += 2) {
+                    float2 d = make_float2(now[i], now[i + 1]);
                     if (a.act) {
-                        float p = bias[0];
+                        float2 p = make_float2(bias[i], bias[i + 1]);
 #pragma unroll
-                        for (int j = 0; j < W; ++j) p = fmaf(wt[j][0], win[k + j][0], p);
-                        const float g = sigmoid_fast(p);
-                        now[0] *= g * fmaf(p, 1.f - g, 1.f);
+                        for (int j = 0; j < W; ++j)
+                            p = __ffma2_rn(make_float2(wt[j][i], wt[j][i + 1]),
+                                           make_float2(win[k + j][i], win[k + j][i + 1]), p);
+                        const float2 g = rcp(__fadd2_rn(ex2(__fmul2_rn(p, dup(-kLog2e))), dup(1.f)));
+                        const float2 rest = __ffma2_rn(g, dup(-1.f), dup(1.f));
+                        d = __fmul2_rn(d, __fmul2_rn(g, __ffma2_rn(p, rest, dup(1.f))));
                     }
-                    if (EDGE && t + k >= len) now[0] = 0.f;
+                    if (EDGE && t + k >= len) d = dup(0.f);   // nothing flows from past the end, whatever p is
+                    now[i] = d.x;
+                    now[i + 1] = d.y;
                     if (!EDGE || t + k < t1) {
 #pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][0] = fmaf(now[0], win[k + j][0], dw[j][0]);
-                        dw[W][0] += now[0];
+                        for (int j = 0; j < W; ++j) {
+                            const float2 q = __ffma2_rn(d, make_float2(win[k + j][i], win[k + j][i + 1]),
+                                                        make_float2(dw[j][i], dw[j][i + 1]));
+                            dw[j][i] = q.x;
+                            dw[j][i + 1] = q.y;
+                        }
+                        const float2 q = __fadd2_rn(d, make_float2(dw[W][i], dw[W][i + 1]));
+                        dw[W][i] = q.x;
+                        dw[W][i + 1] = q.y;
                     }
                 }
                 const int r = t + k - (W - 1);   // the row that dp_{t + k} completes
                 if (!EDGE || (r < t1 && (r >= t0 || (ri == 0 && dst)))) {
                     float d[E];
                     const int j0 = r - (len - (W - 1));   // its place in state_out
-                    if (EDGE && dso && j0 >= 0 && j0 < W - 1) load_n<E, VEC>(dso + (size_t)j0 * a.C, d, valid);
+                    if (EDGE && dso && j0 >= 0 && j0 < W - 1) load_n<E, VEC, STEP>(dso + (size_t)j0 * a.C, d, valid);
                     else
 #pragma unroll
                         for (int i = 0; i < E; ++i) d[i] = 0.f;
-                    if constexpr (E % 2 == 0) {
 #pragma unroll
-                        for (int i = 0; i < E; i += 2) {
-                            float2 q = make_float2(d[i], d[i + 1]);
+                    for (int i = 0; i < E; i += 2) {
+                        float2 q = make_float2(d[i], d[i + 1]);
 #pragma unroll
-                            for (int j = 0; j < W; ++j)
-                                q = __ffma2_rn(make_float2(wt[W - 1 - j][i], wt[W - 1 - j][i + 1]),
-                                               make_float2(dp[k + j][i], dp[k + j][i + 1]), q);
-                            d[i] = q.x;
-                            d[i + 1] = q.y;
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < W; ++j) d[0] = fmaf(wt[W - 1 - j][0], dp[k + j][0], d[0]);
+                        for (int j = 0; j < W; ++j)
+                            q = __ffma2_rn(make_float2(wt[W - 1 - j][i], wt[W - 1 - j][i + 1]),
+                                           make_float2(dp[k + j][i], dp[k + j][i + 1]), q);
+                        d[i] = q.x;
+                        d[i + 1] = q.y;
                     }
-                    if (!EDGE || r >= 0) store_n<E, VEC>(dx + (long long)r * a.C, d, valid);
-                    else store_n<E, VEC>(dst + (size_t)(r + W - 1) * a.C, d, valid);
+                    if (!EDGE || r >= 0) store_n<E, VEC, STEP>(dx + (long long)r * a.C, d, valid);
+                    else store_n<E, VEC, STEP>(dst + (size_t)(r + W - 1) * a.C, d, valid);
                 }
             }
 #pragma unroll
@@ -353,7 +343,7 @@ short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
 #pragma unroll
     for (int j = 0; j <= W; ++j)
 #pragma unroll
-        for (int i = 0; i < E; ++i) sums[warp][j][lane * E + i] = dw[j][i];
+        for (int i = 0; i < E; ++i) sums[warp][j][at + i * STEP] = dw[j][i];
     __syncthreads();
     for (int i = threadIdx.x; i < (W + 1) * 32 * E; i += 32 * kWarps) {
         const int j = i / (32 * E), cc = i % (32 * E);
@@ -409,10 +399,10 @@ int conv_run(long long units, int T, int W, int per, int blocks_sm)
     return best;
 }
 
-// Runs of the gradient go by 4 channels a lane whatever the alignment: the workspace's size follows.
+// Runs of the gradient do not go by the alignment: the workspace's size follows them.
 int conv_bwd_run(int B, int T, int C, int W)
 {
-    return conv_run((long long)B * ((C + 32 * kE - 1) / (32 * kE)), T, W, kWarps, bwd_blocks(W));
+    return conv_run((long long)B * ((C + 32 * kE - 1) / (32 * kE)), T, W, kWarps, bwd_blocks(W, true));
 }
 
 bool aligned_to(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -423,12 +413,13 @@ cudaError_t conv_fwd(const ConvArgs &a, cudaStream_t st)
     constexpr int E = kE, A = E * (int)sizeof(TIn);
     const bool vec = a.C % E == 0 && a.ldx % E == 0 && aligned_to(a.x, A) && aligned_to(a.y, A) &&
                      aligned_to(a.state, A) && aligned_to(a.state_out, A);
-    const int per = 32 * kWarps * (vec ? E : 1), cblocks = (a.C + per - 1) / per;
-    const int run = conv_run((long long)a.B * cblocks, a.T, W, 1, fwd_blocks(W));
+    constexpr int per = 32 * kWarps * E;
+    const int cblocks = (a.C + per - 1) / per;
+    const int run = conv_run((long long)a.B * cblocks, a.T, W, 1, fwd_blocks(W, vec));
     const int runs = std::max(1, (a.T + run - 1) / run);
     const long long blocks = (long long)cblocks * a.B * runs;
-    if (vec) short_conv_kernel<TIn, W, E, true><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
-    else short_conv_kernel<TIn, W, 1, false><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
+    if (vec) short_conv_kernel<TIn, W, true><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
+    else short_conv_kernel<TIn, W, false><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
     return cudaGetLastError();
 }
 
@@ -455,10 +446,10 @@ cudaError_t conv_bwd(const ConvBwdArgs &a, cudaStream_t st)
                      aligned_to(a.dx, A) && aligned_to(a.state, A) && aligned_to(a.dstate, A) &&
                      aligned_to(a.dstate_out, A);
     const int run = conv_bwd_run(a.B, a.T, a.C, W), runs = std::max(1, (a.T + run - 1) / run);
-    const int per = 32 * (vec ? kE : 1), cblocks = (a.C + per - 1) / per;
+    const int cblocks = (a.C + 32 * kE - 1) / (32 * kE);
     const long long blocks = (long long)cblocks * a.B * ((runs + kWarps - 1) / kWarps);
-    if (vec) short_conv_bwd_kernel<TIn, W, kE, true><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
-    else short_conv_bwd_kernel<TIn, W, 1, false><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
+    if (vec) short_conv_bwd_kernel<TIn, W, true><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
+    else short_conv_bwd_kernel<TIn, W, false><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(a, run, runs, cblocks);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int n = a.B * ((runs + kWarps - 1) / kWarps);
