@@ -365,7 +365,7 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
                 const float *p = wk.carry + e * N + l * S;
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
-                    g[k][s] = __ffma2_rn(ex2(__fmul2_rn(A2[k][s], dup(sd))), g[k][s],
+                    g[k][s] = __ffma2_rn(decay(A2[k][s], sd), g[k][s],
                                          make_float2(p[2 * s], p[2 * s + 1]));
             }
     }
@@ -386,7 +386,7 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
                 for (int k = 0; k < KC; ++k)
 #pragma unroll
                     for (int s = 0; s < 2; ++s)
-                        g[k][s] = __fmul2_rn(ex2(__fmul2_rn(A2[k][s], dup(k ? q.z : q.x))),
+                        g[k][s] = __fmul2_rn(decay(A2[k][s], k ? q.z : q.x),
                                              __ffma2_rn(Cv[s], dup(k ? y.y : y.x), g[k][s]));
             }
         } else {
@@ -409,7 +409,7 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
                 for (int k = 0; k < KC; ++k)
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        av[k][s] = ex2(__fmul2_rn(A2[k][s], dup(k ? q.z : q.x)));
+                        av[k][s] = decay(A2[k][s], k ? q.z : q.x);
                         ho[k][s] = __ffma2_rn(av[k][s], hi[k][s], __fmul2_rn(dup(k ? q.w : q.y), Bv[s]));
                     }
             };

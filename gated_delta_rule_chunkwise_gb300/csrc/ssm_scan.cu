@@ -228,7 +228,7 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
             const float sd = sg.sums[e];
             const float *p = sg.ends + e * N + l * S;
 #pragma unroll
-            for (int s = 0; s < S; ++s) h[s] = fmaf(ex2(A2[s] * sd), h[s], p[s]);
+            for (int s = 0; s < S; ++s) h[s] = fmaf(decay(A2[s], sd), h[s], p[s]);
         }
     auto store_state = [&](float *p) {
 #pragma unroll
@@ -256,17 +256,17 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
                     *reinterpret_cast<float4 *>(&cv[i][s]) = *reinterpret_cast<const float4 *>(Cr + t * N + s);
             }
         };
-        auto decay = [&](int i, float *d) {
+        auto decays = [&](int i, float *d) {
 #pragma unroll
             for (int s = 0; s < S; s += 2) {
-                const float2 x = ex2(__fmul2_rn(make_float2(A2[s], A2[s + 1]), dup(q[i].x)));
+                const float2 x = decay(make_float2(A2[s], A2[s + 1]), q[i].x);
                 d[s] = x.x;
                 d[s + 1] = x.y;
             }
         };
         load(0, 0);
         load(1, 1);
-        decay(0, e[0]);
+        decays(0, e[0]);
         constexpr int UG = TG >= 4 ? 1 : 4 / TG;   // groups in one body: at least four tokens
 #pragma unroll UG
         for (int tq = 0; tq < TT; tq += TG) {
@@ -274,7 +274,7 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
 #pragma unroll
             for (int j = 0; j < TG; ++j) {
                 load(tq + j + 2, 2);
-                decay(1, e[1]);
+                decays(1, e[1]);
                 if (PHASE == kEnds) sumdt += q[0].x;
                 float y0 = 0.f, y1 = 0.f;
 #pragma unroll
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmArgs a)
         y[k] = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            h[k][i] = fmaf(ex2(dt[k] * rate(Av[i])), h[k][i], du * Bv[k][i]);
+            h[k][i] = fmaf(decay(rate(Av[i]), dt[k]), h[k][i], du * Bv[k][i]);
             y[k] = fmaf(Cv[k][i], h[k][i], y[k]);
         }
     }
