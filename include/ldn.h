@@ -523,7 +523,8 @@ size_t ldn_add_rmsnorm_backward_workspace_size(long long rows, int D);
  *   lens     [B] int32 on the device, or NULL: sequence b has min(max(lens[b], 0), T)
  *            rows; rows past it are not read, and their y is zero
  *   y        [B][T][C] of `dtype`, contiguous
- *   activation 1: SiLU, 0: none.  width 1..8, any C; T = 0 copies the state.
+ *   activation 1: SiLU, 0: none.  width 1..8, any C, T up to 2^31 - 2^16 - 1; T = 0
+ *   copies the state.
  * Arithmetic is fp32.  One launch.
  */
 int ldn_short_conv(const void *x, long long ldx, const float *weight, const float *bias, const void *state,
@@ -567,8 +568,8 @@ size_t ldn_short_conv_backward_workspace_size(int B, int T, int C, int width);
  *   h_final      [B][D][N] fp32 or NULL; it must not overlap h0
  *   states       [B][ceil(T / 32)][D][N] fp32 or NULL: the state entering every 32
  *                tokens, what ldn_ssm_backward starts from
- *   N in {8, 16, 32, 64}; any D that G divides.  h0, h_final, states and workspace are
- *   16-byte aligned.  T = 0 copies the state.
+ *   N in {8, 16, 32, 64}; any D that G divides; T up to 2^31 - 2^16 - 1.  h0, h_final,
+ *   states and workspace are 16-byte aligned.  T = 0 copies the state.
  * Arithmetic and states are fp32.  With few channels and a workspace of
  * ldn_ssm_scan_workspace_size bytes (0: none would be used) the tokens are cut into
  * segments that run side by side, in two launches; without it one launch runs every
@@ -598,7 +599,8 @@ int ldn_ssm_step(const void *u, long long ldu, const void *delta, long long ld_d
  *   be NULL (not wanted)
  *   states, dh_final, dh0 and workspace (ldn_ssm_backward_workspace_size bytes) are
  *   16-byte aligned.
- * Arithmetic is fp32; the result is the same bit for bit on every call.
+ * Arithmetic is fp32; the result is the same bit for bit on every call.  Two launches, three
+ * where few channels have the tokens cut into segments.
  */
 int ldn_ssm_backward(const void *u, long long ldu, const void *delta, long long ld_delta, const float *A,
                      const void *Bm, long long ldb, const void *Cm, long long ldc, const float *Dskip, const void *z,
