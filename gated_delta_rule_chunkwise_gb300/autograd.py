@@ -7,7 +7,8 @@ marshalling only: both directions run in the CUDA kernels of libldn.so.
 Capturing a backward pass into a CUDA graph follows torch's rules for leaves: no
 eager graph of the same leaves may be alive, since their gradient accumulators are
 tied to the stream that made them.  The ``*_backward`` calls of ``mixer`` have no
-such state and are captured freely.
+such state and are captured freely.  The gradients of add_rmsnorm, short_conv and
+selective_scan have no gradients of their own: asking for them raises.
 
 The gradients of q, k and v are returned in their dtype (the kernel computes
 them in fp32); beta, gate and S0 are fp32 throughout.  The output's gradient
@@ -19,6 +20,7 @@ layout contiguous.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _native, mixer
 
@@ -58,6 +60,7 @@ class _AddRmsNorm(torch.autograd.Function):
         return (y, s) if residual is not None else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, ds=None):
         s, weight = ctx.saved_tensors
         if dy is None:      # only the sum was used
@@ -84,6 +87,7 @@ class _ShortConv(torch.autograd.Function):
         return mixer.short_conv(x, weight, bias, state, lens=lens, activation=activation)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dlast):
         x, weight, bias, state, lens = ctx.saved_tensors
         dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
@@ -108,6 +112,7 @@ class _SelectiveScan(torch.autograd.Function):
         return y, h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh):
         u, delta, A, B, C, D, z, delta_bias, lens, states = ctx.saved_tensors
         dy = torch.zeros(u.shape, dtype=u.dtype, device=u.device) if dy is None else dy.contiguous()

@@ -75,6 +75,19 @@ def test_selective_scan_gradients(whole):
             assert torch.equal(m.grad, g[k]), k
 
 
+def test_gradients_of_gradients_are_refused():
+    import torch
+    from gated_delta_rule_chunkwise_gb300 import autograd as ag
+    x = torch.randn(2, 9, 16, device="cuda", requires_grad=True)
+    w, taps = torch.ones(16, device="cuda"), torch.ones(16, 4, device="cuda")
+    A, Bm = -torch.ones(16, 8, device="cuda"), torch.randn(2, 9, 1, 8, device="cuda")
+    for f in (lambda: ag.add_rmsnorm(x, x.detach(), w)[0], lambda: ag.short_conv(x, taps)[0],
+              lambda: ag.selective_scan(x, x, A, Bm, Bm)[0]):
+        g, = torch.autograd.grad((f() ** 2).sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            g.sum().backward()
+
+
 def test_a_block_trains():
     """Gradients of every parameter of norm -> convolution -> scan in fp32 against torch's
     differentiation of the same formulas in 64 bits."""
