@@ -3,7 +3,8 @@
 //   s = x + r (stored in the residual's type),  rstd = 1 / sqrt(mean_c s_c^2 + eps),
 //   y = s rstd w,   as the element type or in e4m3 with scales:
 //   scale = max(max_group |y|, 2^-100) / 448,  q = e4m3(y / scale), saturating;
-//   a group is 128 consecutive channels or the whole row.
+//   a group is 128 consecutive channels or the whole row.  y and scale are fp32: one result in
+//   1.5 million lies so near a border of e4m3 that 64 bits would round it to the other side.
 // The norm is taken of s AS STORED: a bf16 residual stream rounds the sum once, and that
 // value is what the next block adds to and what the gradient reads back.
 //
