@@ -663,8 +663,9 @@ cudaError_t bwd_pick(const SsmBwdArgs &a, cudaStream_t st)
 {
     constexpr int E = 16 / sizeof(TIn);
     auto ok = [](const void *p) { return ((uintptr_t)p & 15u) == 0; };
+    // every row that is loaded or stored in vectors: inputs and outputs
     const bool vec = (a.D / a.G) % E == 0 && a.ldu % E == 0 && a.ldd % E == 0 && ok(a.u) && ok(a.delta) && ok(a.dy) &&
-                     (!a.z || (a.ldz % E == 0 && ok(a.z)));
+                     ok(a.du) && ok(a.ddelta) && (!a.z || (a.ldz % E == 0 && ok(a.z) && ok(a.dz)));
     return vec ? bwd_run<TIn, N, true>(a, st) : bwd_run<TIn, N, false>(a, st);
 }
 

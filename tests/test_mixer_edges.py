@@ -1,0 +1,67 @@
+"""Calls of the operators around a token mixer that their documentation allows and that are easy
+to miss: outputs at any element's address, sequences and channel counts near the largest int,
+several threads, streams and saved tensors, sizes at which a block walks many rows or tokens."""
+import numpy as np
+import pytest
+
+import gated_delta_rule_chunkwise_gb300 as ldn
+from tests import _mixer_ref as ref
+from tests.test_mixer_parity import _t, dev, host, rounded, scan_inputs, scan_tensors, within  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+U = ref.U
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gated_delta_rule_chunkwise_gb300 import build
+    build.build()
+    ldn.load()
+
+
+def ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+# ---- outputs of the scan's gradient at any element's address ----
+def backward_into(t, states, dy, dh, g, dtype, softplus=True):
+    """ldn_ssm_backward into the given tensors."""
+    import torch
+    u, dl, A, Bm, Cm, Ds, z, bias = t
+    B, T, D = u.shape
+    G, N = Bm.shape[2:]
+    need = ldn.ldn_ssm_backward_workspace_size(B, T, D, N, G)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    ld = lambda m, w: w if m is None else m.stride(1)  # noqa: E731
+    st = ldn.ldn_ssm_backward(ptr(u), ld(u, D), ptr(dl), ld(dl, D), ptr(A), ptr(Bm), ld(Bm, G * N), ptr(Cm),
+                              ld(Cm, G * N), ptr(Ds), ptr(z), ld(z, D), ptr(bias), ptr(states), None, ptr(dy), ptr(dh),
+                              ptr(g["du"]), ptr(g["ddelta"]), ptr(g["dA"]), ptr(g["dB"]), ptr(g["dC"]), ptr(g["dD"]),
+                              ptr(g["dz"]), ptr(g["ddelta_bias"]), ptr(g["dh0"]), B, T, D, N, G, int(softplus),
+                              ldn.LDN_F32 if dtype == "f32" else ldn.LDN_BF16, ptr(ws), need,
+                              torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    return st
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shifted", ["du", "ddelta", "dz", "dB", "dC", "dA", "dD", "ddelta_bias"])
+def test_scan_gradients_at_any_address(dtype, shifted):
+    """Aligned inputs, one output a slice that starts at an odd element: the same values bit for
+    bit, and nothing written around the slice."""
+    import torch
+    p = scan_inputs(2, 70, 32, 16, 2, dtype)
+    t = scan_tensors(p, [70, 70], dtype)
+    h0 = dev(p["h0"])
+    states = ldn.selective_scan(*t, h0, save_states=True)[2]
+    r = np.random.default_rng(8)
+    dy, dh = dev(r.normal(size=(2, 70, 32)), dtype), dev(r.normal(size=(2, 32, 16)))
+    want = ldn.selective_scan_backward(*t, states, dy, dh)
+    got, edges = {}, {}
+    for k, w in want.items():
+        off = 1 if k == shifted else 0
+        flat = torch.full((w.numel() + 16,), 7.0, dtype=w.dtype, device="cuda")
+        got[k], edges[k] = flat[off:off + w.numel()].view(w.shape), (flat[:off], flat[off + w.numel():])
+    assert backward_into(t, states, dy, dh, got, dtype) == ldn.LDN_OK
+    for k, w in want.items():
+        assert torch.equal(got[k], w), k
+        assert all((e == 7.0).all() for e in edges[k]), k
