@@ -304,15 +304,16 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
         }
         if (PHASE == kFull) {
             if (tiles > 0) finished(0);
-            // behind the end: no gradient
+            // behind the end: no gradient (64 bits: a segment's vectors may outnumber an int)
             const float zeros[V] = {};
-            for (int i = tiles * TT * PR + lane; i < (te - tb) * PR; i += 32) {
+            for (long long i = (long long)tiles * TT * PR + lane; i < (long long)(te - tb) * PR; i += 32) {
                 const size_t at = (row0 + i / PR) * a.D + cc;
                 store_n<V, VEC>((TIn *)a.du + at, zeros, valid);
                 store_n<V, VEC>((TIn *)a.ddelta + at, zeros, valid);
                 if (z) store_n<V, VEC>((TIn *)a.dz + at, zeros, valid);
             }
-            for (int i = tid + tiles * TT * (2 * N / 4); i < (te - tb) * (2 * N / 4); i += kMain)
+            for (long long i = tid + (long long)tiles * TT * (2 * N / 4); i < (long long)(te - tb) * (2 * N / 4);
+                 i += kMain)
                 *reinterpret_cast<float4 *>(
                     wk.bc + (((size_t)gb * a.B * a.T + row0 + i / (2 * N / 4)) * a.G + grp) * (2 * N) +
                     i % (2 * N / 4) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);

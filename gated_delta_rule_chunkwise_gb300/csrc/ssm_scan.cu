@@ -204,8 +204,9 @@ ssm_scan_kernel(const SsmArgs a, const Segs sg, int gblocks)
         }
         if (tiles > 0) finished(tiles - 1);
         if constexpr (PHASE != kEnds) {   // rows of the tiles behind the end
+            // (64 bits: vectors of an unsplit sequence may outnumber an int)
             const float zeros[FV] = {};
-            for (int i = tiles * TT * FR + lane; i < (te - tb) * FR; i += 32)
+            for (long long i = (long long)tiles * TT * FR + lane; i < (long long)(te - tb) * FR; i += 32)
                 store_n<FV, VEC>((TIn *)a.y + (row0 + i / FR) * a.D + c0 + w0 + fch, zeros, wcols - fch);
         }
         return;

@@ -65,3 +65,37 @@ def test_scan_gradients_at_any_address(dtype, shifted):
     for k, w in want.items():
         assert torch.equal(got[k], w), k
         assert all((e == 7.0).all() for e in edges[k]), k
+
+
+# ---- sizes near the largest int ----
+def room(gb):
+    """Skips where the GPU has not that many GB free."""
+    import torch
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gb * 1e9:
+        pytest.skip(f"needs {gb} GB of free GPU memory")
+
+
+@pytest.mark.parametrize("dtype,T", [("f32", 1 << 29), ("bf16", 1 << 30)])
+def test_rows_behind_the_end_of_a_very_long_sequence(dtype, T):
+    """One channel, unsplit, five rows of 2^29 or 2^30: the vectors of the rows behind them, four
+    or two a row, are more than an int counts, and all are zeroed."""
+    import torch
+    room(30)
+    try:
+        x = torch.empty(1, T, 1, dtype=_t(dtype), device="cuda")
+        x[:, :5] = 0.5
+        m = torch.empty(1, T, 1, 8, dtype=_t(dtype), device="cuda")
+        m[:, :5] = 0.25
+        y = torch.full((1, T, 1), 7.0, dtype=_t(dtype), device="cuda")
+        A = -torch.ones(1, 8, device="cuda")
+        none = torch.empty(0, dtype=torch.uint8, device="cuda")
+        lens = torch.tensor([5], dtype=torch.int32, device="cuda")
+        _, h = ldn.selective_scan(x, x, A, m, m, lens=lens, out=y, workspace=none)
+        cut = lambda v: v[:, :5].contiguous()  # noqa: E731
+        y5, h5 = ldn.selective_scan(cut(x), cut(x), A, cut(m), cut(m), workspace=none)
+        assert torch.equal(y[:, :5], y5) and torch.equal(h, h5)
+        assert torch.count_nonzero(y[:, 5:]).item() == 0
+    finally:
+        x = m = y = None
+        torch.cuda.empty_cache()
