@@ -360,6 +360,7 @@ add_rmsnorm_bwd_wide_kernel(const TIn *__restrict__ dy, const TRes *__restrict__
 // Vectors per thread: the fewest that fit 512 threads, but two from 4096 channels on.
 int norm_vpt(int D) { return D < 4096 ? 1 : D <= 8192 ? 2 : D <= 16384 ? 4 : 8; }
 constexpr int kWide = 8192;   // the gradient's rows past this are wide
+constexpr int kWidest = 32768;   // channels that the entry points accept
 // Threads for D channels at vpt vectors of 8 each, in whole warps.
 int norm_threads(int D, int vpt) { return std::min(kMostThreads, (((D + kE * vpt - 1) / (kE * vpt) + 31) / 32) * 32); }
 
@@ -410,11 +411,14 @@ template <typename TIn, typename TRes, bool VEC>
 cudaError_t norm_bwd_wide(const AddNormBwdArgs &a, int grid, cudaStream_t st)
 {
     auto *k = add_rmsnorm_bwd_wide_kernel<TIn, TRes, VEC>;
-    const int bytes = a.D * (int)sizeof(float);
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // the attribute is the kernel's, shared by all host threads: always the widest row's, so that a
+    // call between another's two lines changes nothing
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kWidest * (int)sizeof(float));
     if (e != cudaSuccess) return e;
-    k<<<grid, kMostThreads, bytes, st>>>((const TIn *)a.dy, (const TRes *)a.s, a.weight, (const TRes *)a.dsum,
-                                         (TIn *)a.dx, (TRes *)a.dres, a.part, a.rows, a.D, a.eps);
+    k<<<grid, kMostThreads, a.D * sizeof(float), st>>>((const TIn *)a.dy, (const TRes *)a.s, a.weight,
+                                                       (const TRes *)a.dsum, (TIn *)a.dx, (TRes *)a.dres, a.part,
+                                                       a.rows, a.D, a.eps);
     return cudaGetLastError();
 }
 

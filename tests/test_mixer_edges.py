@@ -99,3 +99,43 @@ def test_rows_behind_the_end_of_a_very_long_sequence(dtype, T):
     finally:
         x = m = y = None
         torch.cuda.empty_cache()
+
+
+# ---- several host threads ----
+def test_wide_norm_gradients_from_several_threads():
+    """The C entry points are re-entrant: threads that call the gradient of rows of different
+    widths at once (ctypes gives up the interpreter's lock) all get what a call alone gives."""
+    import threading
+
+    import torch
+    rows = 3
+    calls = []
+    for D in (32768, 8200, 20000, 9001):
+        g = torch.Generator(device="cuda").manual_seed(D)
+        f = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+        dy, s, w, s_ = f(rows, D), f(rows, D), f(D), torch.cuda.Stream()
+        need = ldn.ldn_add_rmsnorm_backward_workspace_size(rows, D)
+        dx, dw, ws = torch.empty_like(dy), torch.empty_like(w), torch.empty(need, dtype=torch.uint8, device="cuda")
+        want = ldn.add_rmsnorm_backward(dy, s, w)
+        calls.append((want, dx, dw, (ptr(dy), ptr(s), ptr(w), None, ptr(dx), None, ptr(dw), rows, D, ldn.LDN_F32,
+                                     ldn.LDN_F32, 1e-6, ptr(ws), need, s_.cuda_stream), (dy, s, w, s_, ws)))
+    torch.cuda.synchronize()
+    start, failed = threading.Barrier(len(calls)), []
+
+    def work(args):
+        start.wait()
+        for _ in range(1500):
+            st = ldn.ldn_add_rmsnorm_backward(*args)
+            if st != ldn.LDN_OK:
+                failed.append((args[8], st))
+                return
+
+    threads = [threading.Thread(target=work, args=(c[3],)) for c in calls]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for want, dx, dw, _, _ in calls:
+        assert torch.equal(dx, want["dx"]) and torch.equal(dw, want["dweight"])
