@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(128) short_conv_step_kernel(const ConvArgs a)
     if (id >= (long long)a.B * per) return;
     const int b = (int)(id / per), c = (int)(id % per) * E, valid = a.C - c;
     float rows[W][E], p[E], wt[E * W];
-    load_n<E * W, VEC>(a.w + (size_t)c * W, wt, valid * W);   // taps of one channel after another
+    load_n<E * W, VEC>(a.w + (size_t)c * W, wt, min(valid, E) * W);   // taps of one channel after another
     const TIn *st = (const TIn *)a.state + (size_t)b * (W - 1) * a.C + c;
     TIn *so = (TIn *)a.state_out + (size_t)b * (W - 1) * a.C + c;
 #pragma unroll

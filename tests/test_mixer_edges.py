@@ -101,6 +101,27 @@ def test_rows_behind_the_end_of_a_very_long_sequence(dtype, T):
         torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("more", [8, 9])
+def test_conv_step_of_very_many_channels(more):
+    """8 x (2^28 + 8 or 9) taps are more than an int counts: the first and the last channels against
+    the formula."""
+    import torch
+    room(30)
+    C, W = (1 << 28) + more, 8
+    try:
+        f = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_()  # noqa: E731
+        x, state, w = f(1, C), f(1, W - 1, C), torch.empty(C, W, device="cuda").normal_()
+        y = ldn.short_conv_step(x, w, None, state, activation=False, state_out=torch.empty_like(state))
+        for part in (slice(0, 64), slice(C - 64, C)):
+            seq = np.concatenate([host(state[0, :, part]), host(x[:, part])])
+            terms = seq.T * host(w[part])
+            want = terms.sum(1)
+            within(y[0, part], want, np.abs(want) * ref.HALF["bf16"] + np.abs(terms).sum(1) * W * U, "y")
+    finally:
+        x = state = w = y = None
+        torch.cuda.empty_cache()
+
+
 # ---- several host threads ----
 def test_wide_norm_gradients_from_several_threads():
     """The C entry points are re-entrant: threads that call the gradient of rows of different
