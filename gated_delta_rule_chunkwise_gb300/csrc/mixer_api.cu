@@ -127,12 +127,13 @@ extern "C" int ldn_add_rmsnorm_backward(const void *dy, const void *s, const flo
 
 // ---- Short causal convolution with a carried state ----
 
-constexpr int kMostTokens = 0x7fffffff - (1 << 16);   // of a sequence: runs and segments may end a little past it
+// Tokens of a sequence, and channels: runs, segments and blocks of channels may end a little past them.
+constexpr int kMostInt = 0x7fffffff - (1 << 16);
 
 static int check_conv(int B, int T, int C, int W, int dtype, long long ldx)
 {
     if (!known(dtype) || B < 1 || T < 0 || C < 1 || W < 1 || ldx < C) return LDN_ERR_INVALID_ARG;
-    if (W > 8 || T > kMostTokens) return LDN_ERR_UNSUPPORTED;
+    if (W > 8 || T > kMostInt || C > kMostInt) return LDN_ERR_UNSUPPORTED;
     // elements from the first row to the last, and blocks of one launch (eight tokens of 32 channels each at least)
     if (ldx > kMostElements || (long long)B * std::max(T, W) > kMostElements / ldx) return LDN_ERR_UNSUPPORTED;
     if ((long long)B * ((T + 7LL) / 8) * ((C + 31) / 32) > 0x7fffffffLL) return LDN_ERR_UNSUPPORTED;
@@ -218,7 +219,7 @@ extern "C" int ldn_short_conv_backward(const void *x, long long ldx, const float
 static int check_ssm(int B, int T, int D, int N, int G, int dtype)
 {
     if (!known(dtype) || B < 1 || T < 0 || D < 1 || N < 1 || G < 1 || D % G != 0) return LDN_ERR_INVALID_ARG;
-    if (!ssm_supported_n(N) || T > kMostTokens) return LDN_ERR_UNSUPPORTED;
+    if (!ssm_supported_n(N) || T > kMostInt || D > kMostInt) return LDN_ERR_UNSUPPORTED;
     // elements of [B][T][D], of [B][D][N], and blocks of one launch (32 tokens of 16 channels at least)
     if ((long long)B * std::max(T, N) > kMostElements / D) return LDN_ERR_UNSUPPORTED;
     if ((long long)B * ((T + 31LL) / 32 + 1) > 0x7fffffffLL / ((long long)G * (D / G / 16 + 1))) return LDN_ERR_UNSUPPORTED;

@@ -523,7 +523,7 @@ size_t ldn_add_rmsnorm_backward_workspace_size(long long rows, int D);
  *   lens     [B] int32 on the device, or NULL: sequence b has min(max(lens[b], 0), T)
  *            rows; rows past it are not read, and their y is zero
  *   y        [B][T][C] of `dtype`, contiguous
- *   activation 1: SiLU, 0: none.  width 1..8, any C, T up to 2^31 - 2^16 - 1; T = 0
+ *   activation 1: SiLU, 0: none.  width 1..8, C and T up to 2^31 - 2^16 - 1; T = 0
  *   copies the state.
  * Arithmetic is fp32.  One launch.
  */
@@ -568,7 +568,7 @@ size_t ldn_short_conv_backward_workspace_size(int B, int T, int C, int width);
  *   h_final      [B][D][N] fp32 or NULL; it must not overlap h0
  *   states       [B][ceil(T / 32)][D][N] fp32 or NULL: the state entering every 32
  *                tokens, what ldn_ssm_backward starts from
- *   N in {8, 16, 32, 64}; any D that G divides; T up to 2^31 - 2^16 - 1.  h0, h_final,
+ *   N in {8, 16, 32, 64}; any D that G divides; D and T up to 2^31 - 2^16 - 1.  h0, h_final,
  *   states and workspace are 16-byte aligned.  T = 0 copies the state.
  * Arithmetic and states are fp32.  With few channels and a workspace of
  * ldn_ssm_scan_workspace_size bytes (0: none would be used) the tokens are cut into
