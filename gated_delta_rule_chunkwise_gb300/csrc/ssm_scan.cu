@@ -346,8 +346,8 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmArgs a)
     for (int k = 0; k < kStepB; ++k) {
         const int b = min(b0 + k, a.B - 1);   // past the last: that one again, not stored
         load_n<4, true>(a.h0 + ((size_t)b * a.D + d) * N + l * 4, h[k]);
-        load_n<4, VEC>((const TIn *)a.Bm + (size_t)b * a.ldb + g * N + l * 4, Bv[k]);
-        load_n<4, VEC>((const TIn *)a.Cm + (size_t)b * a.ldc + g * N + l * 4, Cv[k]);
+        load_n<4, VEC>((const TIn *)a.Bm + (size_t)b * a.ldb + (size_t)g * N + l * 4, Bv[k]);
+        load_n<4, VEC>((const TIn *)a.Cm + (size_t)b * a.ldc + (size_t)g * N + l * 4, Cv[k]);
         u[k] = load_in((const TIn *)a.u, (size_t)b * a.ldu + d);
         dt[k] = load_in((const TIn *)a.delta, (size_t)b * a.ldd + d) + bias;
         z[k] = a.z ? load_in((const TIn *)a.z, (size_t)b * a.ldz + d) : 0.f;

@@ -122,6 +122,29 @@ def test_conv_step_of_very_many_channels(more):
         torch.cuda.empty_cache()
 
 
+def test_scan_step_of_very_many_groups():
+    """2^28 + 4 groups of one channel and eight states: a group's place in a row of B or C is past
+    an int in the last ones."""
+    import torch
+    room(60)
+    D, N = (1 << 28) + 4, 8
+    try:
+        u = torch.empty(1, D, dtype=torch.bfloat16, device="cuda").uniform_(0.5, 1)
+        m = torch.empty(1, D, N, dtype=torch.bfloat16, device="cuda").uniform_(0.5, 1)
+        h = torch.zeros(1, D, N, device="cuda")
+        A = torch.zeros(D, N, device="cuda")     # nothing decays: h = dt u B, y = sum C h, all terms positive
+        y = ldn.selective_scan_step(u, u, A, m, m, None, None, None, h, delta_softplus=False)
+        for part in (slice(0, 64), slice(D - 64, D)):
+            uu, mm = host(u[0, part]), host(m[0, part])
+            hh = (uu * uu)[:, None] * mm
+            within(h[0, part], hh, hh * 4 * U, "h")
+            want = (hh * mm).sum(1)
+            within(y[0, part], want, want * (ref.HALF["bf16"] + (N + 8) * U), "y")
+    finally:
+        u = m = h = A = y = None
+        torch.cuda.empty_cache()
+
+
 # ---- several host threads ----
 def test_wide_norm_gradients_from_several_threads():
     """The C entry points are re-entrant: threads that call the gradient of rows of different
