@@ -262,9 +262,11 @@ extern "C" int ldn_ssm_scan(const void *u, long long ldu, const void *delta, lon
                        {A, (size_t)D * N * 4}, rows_span(Bm, rows, ldb, gn, dtype),
                        rows_span(Cm, rows, ldc, gn, dtype), {Dskip, (size_t)D * 4}, rows_span(z, rows, ldz, D, dtype),
                        {delta_bias, (size_t)D * 4}, {h0, nh}, {lens, (size_t)B * 4}};
+    // a workspace that is too small stays unused: the scan runs unsplit
+    const size_t need = ldn_ssm_scan_workspace_size(B, T, D, N, G);
+    if (workspace_bytes < need) workspace = nullptr;
     const Span out[] = {{y, (size_t)rows * D * es}, {h_final, nh},
-                        {states, nh * (size_t)((T + kSsmChunk - 1) / kSsmChunk)},
-                        {workspace, workspace ? ldn_ssm_scan_workspace_size(B, T, D, N, G) : 0}};
+                        {states, nh * (size_t)((T + kSsmChunk - 1) / kSsmChunk)}, {workspace, need}};
     if (overlapping(in, out)) return LDN_ERR_INVALID_ARG;
     const SsmArgs a{u, delta, Bm, Cm, z, ldu, ld_delta, ldb, ldc, ldz, A, Dskip, delta_bias, h0, lens, y, h_final,
                     states, (float *)workspace, workspace ? workspace_bytes : 0, B, T, D, N, G, delta_softplus,

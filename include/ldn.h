@@ -572,8 +572,9 @@ size_t ldn_short_conv_backward_workspace_size(int B, int T, int C, int width);
  *   states and workspace are 16-byte aligned.  T = 0 copies the state.
  * Arithmetic and states are fp32.  With few channels and a workspace of
  * ldn_ssm_scan_workspace_size bytes (0: none would be used) the tokens are cut into
- * segments that run side by side, in two launches; without it one launch runs every
- * sequence from end to end.  The two agree up to fp32 rounding.
+ * segments that run side by side, in two launches; without it (NULL, or fewer bytes: it
+ * is then not touched) one launch runs every sequence from end to end.  The two agree up
+ * to fp32 rounding.
  */
 int ldn_ssm_scan(const void *u, long long ldu, const void *delta, long long ld_delta, const float *A, const void *Bm,
                  long long ldb, const void *Cm, long long ldc, const float *Dskip, const void *z, long long ldz,

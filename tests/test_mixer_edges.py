@@ -145,6 +145,28 @@ def test_scan_step_of_very_many_groups():
         torch.cuda.empty_cache()
 
 
+# ---- a workspace that is too small ----
+def test_scan_with_a_small_workspace_beside_its_outputs():
+    """A workspace smaller than the segments need is not used, so what lies behind it may be an
+    output: results as without one, the workspace untouched."""
+    import torch
+    p = scan_inputs(1, 600, 20, 16, 1, "f32")
+    t = scan_tensors(p, [600], "f32")
+    h0 = dev(p["h0"])
+    need = ldn.ldn_ssm_scan_workspace_size(1, 600, 20, 16, 1)
+    assert need > 256
+    n, nh = 600 * 20, 20 * 16
+    arena = torch.full((64 + n + nh,), 7.0, device="cuda")
+    small, y, h = arena[:64].view(torch.uint8), arena[64:64 + n].view(1, 600, 20), arena[64 + n:].view(1, 20, 16)
+    assert small.numel() < need
+    ldn.selective_scan(*t, h0, out=y, h_final=h, workspace=small)
+    want = ldn.selective_scan(*t, h0, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(y, want[0]) and torch.equal(h, want[1]) and (arena[:64] == 7.0).all()
+    # one that is large enough is used, and may not be shared with an output
+    with pytest.raises(ldn.LdnError):
+        ldn.selective_scan(*t, h0, out=y, h_final=h, workspace=arena.view(torch.uint8))
+
+
 # ---- several host threads ----
 def test_wide_norm_gradients_from_several_threads():
     """The C entry points are re-entrant: threads that call the gradient of rows of different
