@@ -22,7 +22,13 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _native, mixer
+from . import _native
+
+
+def _mixer():
+    # delta_rule needs no native torch layer: it is loaded where an operator of it is called
+    from . import mixer
+    return mixer
 
 
 class _DeltaRule(torch.autograd.Function):
@@ -52,7 +58,7 @@ def delta_rule(q, k, v, beta, gate=None, S0=None, *, mode):
 class _AddRmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, eps):
-        y, s = mixer.add_rmsnorm(x, residual, weight, eps=eps)
+        y, s = _mixer().add_rmsnorm(x, residual, weight, eps=eps)
         ctx.set_materialize_grads(False)
         ctx.eps = eps
         ctx.save_for_backward(s, weight)
@@ -65,8 +71,8 @@ class _AddRmsNorm(torch.autograd.Function):
         s, weight = ctx.saved_tensors
         if dy is None:      # only the sum was used
             return (None if ds is None else ds.to(ctx.dtype)), ds, None, None
-        g = mixer.add_rmsnorm_backward(dy.contiguous(), s, weight, None if ds is None else ds.contiguous(),
-                                       eps=ctx.eps)
+        g = _mixer().add_rmsnorm_backward(dy.contiguous(), s, weight, None if ds is None else ds.contiguous(),
+                                          eps=ctx.eps)
         return g["dx"], g["dresidual"] if ctx.added else None, g["dweight"], None
 
 
@@ -84,15 +90,15 @@ class _ShortConv(torch.autograd.Function):
         ctx.set_materialize_grads(False)
         ctx.activation = activation
         ctx.save_for_backward(x, weight, bias, state, lens)
-        return mixer.short_conv(x, weight, bias, state, lens=lens, activation=activation)
+        return _mixer().short_conv(x, weight, bias, state, lens=lens, activation=activation)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dlast):
         x, weight, bias, state, lens = ctx.saved_tensors
         dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
-        g = mixer.short_conv_backward(x, weight, bias, dy, state, None if dlast is None else dlast.contiguous(),
-                                      lens=lens, activation=ctx.activation)
+        g = _mixer().short_conv_backward(x, weight, bias, dy, state, None if dlast is None else dlast.contiguous(),
+                                         lens=lens, activation=ctx.activation)
         return g["dx"], g["dweight"], g["dbias"], g["dstate"], None, None
 
 
@@ -106,8 +112,8 @@ class _SelectiveScan(torch.autograd.Function):
     def forward(ctx, u, delta, A, B, C, D, z, delta_bias, h0, lens, delta_softplus):
         ctx.set_materialize_grads(False)
         ctx.delta_softplus = delta_softplus
-        y, h, states = mixer.selective_scan(u, delta, A, B, C, D, z, delta_bias, h0, lens=lens,
-                                            delta_softplus=delta_softplus, save_states=True)
+        y, h, states = _mixer().selective_scan(u, delta, A, B, C, D, z, delta_bias, h0, lens=lens,
+                                               delta_softplus=delta_softplus, save_states=True)
         ctx.save_for_backward(u, delta, A, B, C, D, z, delta_bias, lens, states)
         return y, h
 
@@ -116,9 +122,9 @@ class _SelectiveScan(torch.autograd.Function):
     def backward(ctx, dy, dh):
         u, delta, A, B, C, D, z, delta_bias, lens, states = ctx.saved_tensors
         dy = torch.zeros(u.shape, dtype=u.dtype, device=u.device) if dy is None else dy.contiguous()
-        g = mixer.selective_scan_backward(u, delta, A, B, C, D, z, delta_bias, states, dy,
-                                          None if dh is None else dh.contiguous(), lens=lens,
-                                          delta_softplus=ctx.delta_softplus)
+        g = _mixer().selective_scan_backward(u, delta, A, B, C, D, z, delta_bias, states, dy,
+                                             None if dh is None else dh.contiguous(), lens=lens,
+                                             delta_softplus=ctx.delta_softplus)
         return (g["du"], g["ddelta"], g["dA"], g["dB"], g["dC"], g["dD"], g["dz"], g["ddelta_bias"],
                 g["dh0"] if ctx.needs_input_grad[8] else None, None, None)
 

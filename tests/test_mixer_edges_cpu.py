@@ -30,3 +30,30 @@ def test_channels_near_the_largest_int_are_refused():
     assert ldn.ldn_ssm_scan(*(SCAN | far | dict(T=1)).values()) == UNSUP
     assert ldn.ldn_ssm_step(*(STEP | far).values()) == UNSUP
     assert ldn.ldn_ssm_backward(*(SBWD | far | dict(T=1)).values()) == UNSUP
+
+
+# ---- what needs no native torch layer ----
+def in_a_process(code):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_delta_rule_needs_no_native_torch_layer():
+    """autograd.delta_rule runs on libldn.so alone; the operators of the native torch layer say
+    what is missing where they are called."""
+    in_a_process("""
+import sys
+sys.modules["gated_delta_rule_chunkwise_gb300.mixer"] = None    # as if its library could not be loaded
+from gated_delta_rule_chunkwise_gb300 import autograd
+assert callable(autograd.delta_rule)
+try:
+    autograd.short_conv(None, None)
+except ImportError:
+    pass
+else:
+    raise SystemExit("no ImportError")
+""")
