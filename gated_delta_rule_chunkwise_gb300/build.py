@@ -5,8 +5,9 @@ parallel), then the objects are linked into lib/libldn.so inside the package.
 The diagnostic kernels (csrc/diag/, include/ldn_diag.h) are linked into a
 library of their own, lib/libldn_diag.so, which only the tests load.  The native
 half of mixer.py (csrc/torch/) is a host-only extension module, lib/_ldn_torch.so,
-compiled against the installed torch and linked to libldn.so beside it.  The CUDA
-runtime is linked statically, so the libraries need only the driver at run
+compiled against the installed torch and linked to libldn.so beside it; without a
+torch it is left out, and where it fails libldn.so is in place before that is raised.
+The CUDA runtime is linked statically, so the libraries need only the driver at run
 time.  Nothing here runs at import time; __graft_entry__.build() and the
 tests call build().
 """
@@ -57,15 +58,39 @@ def _headers():
     return sorted(hs)
 
 
-def _stamp() -> str:
-    import torch
+def _digest(paths, *words) -> str:
     h = hashlib.sha256()
-    for p in _sources() + _diag_sources() + _headers() + [TORCH_SRC]:
+    for p in paths:
         with open(p, "rb") as f:
             h.update(p.encode() + f.read())
-    h.update(torch.__version__.encode())
-    h.update(" ".join(ARCH + NVCC_FLAGS).encode())
+    h.update(" ".join(words).encode())
     return h.hexdigest()
+
+
+def _stamp() -> str:
+    return _digest(_sources() + _diag_sources() + _headers(), *ARCH, *NVCC_FLAGS)
+
+
+def _torch_stamp():
+    """None where there is no torch: the C library is wanted alone."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return _digest([TORCH_SRC, os.path.join(INCLUDE, "ldn.h")], torch.__version__)
+
+
+def _fresh(stamp, name, *libs) -> bool:
+    at = os.path.join(OBJ_DIR, name)
+    if not all(os.path.exists(p) for p in (*libs, at)):
+        return False
+    with open(at) as f:
+        return f.read() == stamp
+
+
+def _set_stamp(stamp, name):
+    with open(os.path.join(OBJ_DIR, name), "w") as f:
+        f.write(stamp)
 
 
 def _compile(nvcc, src, log_dir):
@@ -118,27 +143,27 @@ def _link(nvcc, objs, path):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libldn.so, libldn_diag.so and _ldn_torch.so if any source
-    changed; return the path of libldn.so."""
+    """Compile and link libldn.so and libldn_diag.so, and where torch is installed
+    _ldn_torch.so, each if its sources changed; return the path of libldn.so."""
     os.makedirs(OBJ_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
-    stamp_file = os.path.join(OBJ_DIR, "stamp")
-    stamp = _stamp()
-    if (not force and os.path.exists(LIB_PATH) and os.path.exists(DIAG_LIB_PATH) and
-            os.path.exists(TORCH_LIB_PATH) and os.path.exists(stamp_file)):
-        with open(stamp_file) as f:
-            if f.read() == stamp:
-                return LIB_PATH
-    nvcc = _nvcc()
+    stamp, torch_stamp = _stamp(), _torch_stamp()
+    stale = force or not _fresh(stamp, "stamp", LIB_PATH, DIAG_LIB_PATH)
+    torch_stale = torch_stamp is not None and (force or not _fresh(torch_stamp, "stamp_torch", TORCH_LIB_PATH))
+    if not stale and not torch_stale:
+        return LIB_PATH
     srcs, dsrcs = _sources(), _diag_sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, 1 + len(srcs) + len(dsrcs))) as ex:
-        torch_obj = ex.submit(_compile_torch, OBJ_DIR)
-        objs = list(ex.map(lambda s: _compile(nvcc, s, OBJ_DIR), srcs + dsrcs))
-    _link(nvcc, objs[:len(srcs)], LIB_PATH)
-    _link_torch(torch_obj.result())
-    _link(nvcc, objs[len(srcs):], DIAG_LIB_PATH)
-    with open(stamp_file, "w") as f:
-        f.write(stamp)
+        torch_obj = ex.submit(_compile_torch, OBJ_DIR) if torch_stale else None
+        if stale:
+            nvcc = _nvcc()
+            objs = list(ex.map(lambda s: _compile(nvcc, s, OBJ_DIR), srcs + dsrcs))
+            _link(nvcc, objs[:len(srcs)], LIB_PATH)
+            _link(nvcc, objs[len(srcs):], DIAG_LIB_PATH)
+            _set_stamp(stamp, "stamp")
+    if torch_stale:
+        _link_torch(torch_obj.result())
+        _set_stamp(torch_stamp, "stamp_torch")
     if verbose:
         for s in srcs + dsrcs:
             with open(os.path.join(OBJ_DIR, os.path.basename(s) + ".log")) as f:

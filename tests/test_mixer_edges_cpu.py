@@ -57,3 +57,52 @@ except ImportError:
 else:
     raise SystemExit("no ImportError")
 """)
+
+
+@pytest.fixture
+def made(monkeypatch, tmp_path):
+    """build() into an empty folder with its compilers replaced: the list of what they made."""
+    import os
+    done = []
+
+    def make(path):
+        with open(path, "w"):
+            pass
+        done.append(os.path.basename(path))
+        return path
+
+    for k in ("OBJ_DIR", "LIB_DIR"):
+        monkeypatch.setattr(ldn_build, k, str(tmp_path))
+    for k in ("LIB_PATH", "DIAG_LIB_PATH", "TORCH_LIB_PATH"):
+        monkeypatch.setattr(ldn_build, k, str(tmp_path / os.path.basename(getattr(ldn_build, k))))
+    monkeypatch.setattr(ldn_build, "_compile", lambda nvcc, src, log: src)
+    monkeypatch.setattr(ldn_build, "_link", lambda nvcc, objs, path: make(path))
+    monkeypatch.setattr(ldn_build, "_compile_torch", lambda log: "binding.o")
+    monkeypatch.setattr(ldn_build, "_link_torch", lambda obj: make(ldn_build.TORCH_LIB_PATH))
+    return done
+
+
+def test_the_c_library_builds_without_torch(made, monkeypatch):
+    import sys
+    monkeypatch.setitem(sys.modules, "torch", None)     # importing it raises ImportError
+    assert ldn_build.build() == ldn_build.LIB_PATH
+    assert made == ["libldn.so", "libldn_diag.so"]
+    ldn_build.build()
+    assert len(made) == 2
+
+
+def test_the_c_library_is_in_place_where_the_torch_layer_fails(made, monkeypatch):
+    import os
+
+    def fails(log):
+        raise RuntimeError("no headers")
+    with monkeypatch.context() as m:
+        m.setattr(ldn_build, "_compile_torch", fails)
+        for _ in range(2):
+            with pytest.raises(RuntimeError, match="no headers"):
+                ldn_build.build()
+    assert made == ["libldn.so", "libldn_diag.so"] and os.path.exists(ldn_build.LIB_PATH)
+    ldn_build.build()
+    assert made == ["libldn.so", "libldn_diag.so", "_ldn_torch.so"]
+    ldn_build.build()
+    assert len(made) == 3
