@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -226,6 +227,24 @@ T *output(const Call &c, PyObject *&o, const char *name, Shape shape, at::Scalar
 
 struct PythonError {};   // one is set
 
+// These calls record no gradients.  Where a graph is being recorded and an argument wants one,
+// the caller most likely meant autograd's form, and would otherwise see only that a gradient is
+// missing.  The warning is the caller's of mixer.py's function.
+void warn_without_gradient(PyObject *const *a, Py_ssize_t n, const char *name, bool recorded = true)
+{
+    if (!c10::GradMode::is_enabled()) return;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        if (!THPVariable_Check(a[i]) || !THPVariable_Unpack(a[i]).requires_grad()) continue;
+        const int failed = recorded
+            ? PyErr_WarnFormat(PyExc_UserWarning, 3, "%s: an argument requires a gradient and this call records none: "
+                               "call autograd.%s, or this one under torch.no_grad()", name, name)
+            : PyErr_WarnFormat(PyExc_UserWarning, 3, "%s: an argument requires a gradient and this call has none",
+                               name);
+        if (failed) throw PythonError{};
+        return;
+    }
+}
+
 int as_int(PyObject *o)
 {
     const int v = PyLong_Check(o) ? (int)std::max(-1L, std::min(PyLong_AsLong(o), (long)INT_MAX)) : -1;
@@ -269,6 +288,8 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     const Tensor &x = must(tensor(a[0], "x"), "x"), *r = tensor(a[1], "residual"), *w = tensor(a[2], "weight");
     if (!here(x, "x")) Py_RETURN_NONE;
     if (x.dim() < 1) refuse(PyExc_ValueError, "x must have at least one dimension");
+    if (eight) warn_without_gradient(a, nargs, "add_rmsnorm_e4m3", false);
+    else warn_without_gradient(a, nargs, "add_rmsnorm");
     const Call c(x);
     const float eps = as_float(a[3]);
     const Shape shape = x.sizes();
@@ -381,6 +402,7 @@ PyObject *short_conv(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     NEEDS(8);
     const Tensor &x = must(tensor(a[0], "x"), "x");
     if (!here(x, "x")) Py_RETURN_NONE;
+    warn_without_gradient(a, nargs, "short_conv");
     const Call c(x);
     const at::ScalarType t = x.scalar_type();
     const ConvIn in(c, x, tensor(a[1], "weight"), tensor(a[2], "bias"), 2);
@@ -501,6 +523,7 @@ PyObject *selective_scan(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     NEEDS(15);
     const Tensor &u = must(tensor(a[0], "u"), "u"), *given = tensor(a[14], "workspace");
     if (!here(u, "u")) Py_RETURN_NONE;
+    warn_without_gradient(a, nargs, "selective_scan");
     const Call c(u);
     const at::ScalarType t = u.scalar_type();
     const ScanIn in(c, a, 2);

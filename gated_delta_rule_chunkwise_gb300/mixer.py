@@ -11,6 +11,11 @@ wrong shapes, strides or devices ValueError, and what the C entry point refuses
 stream, or on ``stream`` (a torch.cuda.Stream) when one is given: outputs and workspaces are
 then allocated for that stream, and ordering it against the streams that made the inputs
 and read the outputs is the caller's.
+
+None of these calls records gradients: ``autograd`` has add_rmsnorm, short_conv and
+selective_scan with them.  The calls of the same names here, and add_rmsnorm_e4m3, warn
+(UserWarning) where gradients are being recorded and an argument requires one; the others,
+for single tokens and gradients, do not.
 """
 from __future__ import annotations
 

@@ -205,3 +205,35 @@ def test_wide_norm_gradients_from_several_threads():
     assert not failed
     for want, dx, dw, _, _ in calls:
         assert torch.equal(dx, want["dx"]) and torch.equal(dw, want["dweight"])
+
+
+# ---- gradients and saved tensors ----
+def test_calls_that_record_no_gradient_warn():
+    """Where an argument requires a gradient and a graph is recorded, the call without one says
+    so at the caller's line; autograd's forms, no_grad and plain tensors are quiet."""
+    import warnings
+
+    import torch
+    from gated_delta_rule_chunkwise_gb300 import autograd as ag
+    x = torch.randn(2, 9, 16, device="cuda")
+    w, taps = torch.ones(16, device="cuda"), torch.ones(16, 4, device="cuda", requires_grad=True)
+    A, m = -torch.ones(16, 8, device="cuda"), torch.randn(2, 9, 1, 8, device="cuda")
+    wp, Ap = w.clone().requires_grad_(), A.clone().requires_grad_()
+    calls = {"add_rmsnorm": lambda f: f.add_rmsnorm(x, x, wp), "short_conv": lambda f: f.short_conv(x, taps),
+             "selective_scan": lambda f: f.selective_scan(x, x, Ap, m, m)}
+    for name, f in calls.items():
+        with pytest.warns(UserWarning, match=f"autograd.{name}") as got:
+            y = f(ldn)[0]
+        assert len(got) == 1 and got[0].filename == __file__ and not y.requires_grad
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            assert f(ag)[0].requires_grad
+            with torch.no_grad():
+                assert torch.equal(f(ldn)[0], y)
+    with pytest.warns(UserWarning, match="add_rmsnorm_e4m3"):
+        ldn.add_rmsnorm_e4m3(x, x, wp)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        ldn.add_rmsnorm(x, x, w)
+        with pytest.raises(UserWarning):        # as an exception it ends the call
+            ldn.add_rmsnorm(x, x, wp)
