@@ -9,8 +9,9 @@ device checks, strides, allocation of outputs and workspaces.  Wrong types raise
 wrong shapes, strides or devices ValueError, and what the C entry point refuses
 ``LdnError``.  Every call runs on the device of its tensors, on that device's current
 stream, or on ``stream`` (a torch.cuda.Stream) when one is given: outputs and workspaces are
-then allocated for that stream, and ordering it against the streams that made the inputs
-and read the outputs is the caller's.
+then allocated for that stream, the arguments' memory is kept from reuse until it is done
+with them, and ordering it against the streams that made the inputs and read the outputs is
+the caller's.
 
 None of these calls records gradients: ``autograd`` has add_rmsnorm, short_conv and
 selective_scan with them.  The calls of the same names here, and add_rmsnorm_e4m3, warn
@@ -59,7 +60,11 @@ def _call(f, stream, x, *args):
     if not isinstance(stream, torch.cuda.Stream) or not isinstance(x, torch.Tensor) or stream.device != x.device:
         raise ValueError(f"{f.__name__}: stream must be a torch.cuda.Stream of the first tensor's device")
     with torch.cuda.stream(stream):
-        return f(x, *args)
+        r = f(x, *args)
+    for t in (x, *args):    # freed after the call, their memory waits for this stream
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+    return r
 
 
 def chunk_states_shape(B, T, D, N):

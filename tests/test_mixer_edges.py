@@ -237,3 +237,31 @@ def test_calls_that_record_no_gradient_warn():
         ldn.add_rmsnorm(x, x, w)
         with pytest.raises(UserWarning):        # as an exception it ends the call
             ldn.add_rmsnorm(x, x, wp)
+
+
+# ---- memory on another stream ----
+def test_arguments_freed_after_a_call_on_another_stream():
+    """Arguments that are dropped right after a call with stream=, while that stream is still
+    busy: tensors made next do not get their memory before the call has run."""
+    import torch
+    n = 1 << 22
+    side = torch.cuda.Stream()
+    x = torch.randn(n // 64, 64, device="cuda")
+    w, taps = torch.randn(64, device="cuda"), torch.randn(64, 4, device="cuda")
+    want_y, want_s = ldn.add_rmsnorm(x, x, w)
+    want_c = ldn.short_conv(x[None], taps)[0]
+    torch.cuda.synchronize()
+    for call in (lambda a: ldn.add_rmsnorm(a, a, w, stream=side), lambda a: ldn.short_conv(a[None], taps, stream=side)):
+        a = x.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)      # about 0.1 s
+        got = call(a)
+        del a
+        over = [torch.full((n // 64, 64), float("nan"), device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        del over
+        if got[0].dim() == 2:
+            assert torch.equal(got[0], want_y) and torch.equal(got[1], want_s)
+        else:
+            assert torch.equal(got[0], want_c)
