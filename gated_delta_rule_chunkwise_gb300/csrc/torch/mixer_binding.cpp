@@ -210,6 +210,12 @@ PyObject *dict(std::initializer_list<std::pair<const char *, const Tensor *>> it
     return d;
 }
 
+// A tensor of the caller's that the call writes: a graph that saved its values is to notice.
+void written(const Tensor &t)
+{
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // A given output, checked, or a new one; `o` becomes a new reference to it.
 template <typename T = void>
 T *output(const Call &c, PyObject *&o, const char *name, Shape shape, at::ScalarType type)
@@ -217,6 +223,7 @@ T *output(const Call &c, PyObject *&o, const char *name, Shape shape, at::Scalar
     if (o != Py_None) {
         const Tensor *t = tensor(o, name);
         T *p = address<T>(t, name, shape, type, c.dev);
+        written(*t);
         Py_INCREF(o);
         return p;
     }
@@ -433,10 +440,12 @@ PyObject *short_conv_step(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     const at::ScalarType t = x.scalar_type();
     const ConvIn in(c, x, tensor(a[1], "weight"), tensor(a[2], "bias"), 1);
     const int64_t B = x.size(0), ys[] = {B, in.C}, ss[] = {B, in.W - 1, in.C};
-    void *pst = address(tensor(a[3], "state"), "state", Shape(ss, 3), t, c.dev);
+    const Tensor *st = tensor(a[3], "state");
+    void *pst = address(st, "state", Shape(ss, 3), t, c.dev);
     void *ps = so ? address(so, "state_out", Shape(ss, 3), t, c.dev) : pst;
     PyObject *y = a[5];
     void *py = output(c, y, "out", Shape(ys, 2), t);
+    if (so || st) written(so ? *so : *st);
     THPObjectPtr hold_y(y);
     if (!done(ldn_short_conv_step(in.x.p, in.x.ld, in.w, in.b, pst, py, ps, size(B), size(in.C), size(in.W), truth(a[4]),
                                   in.code, c.stream()), "ldn_short_conv_step"))
@@ -570,8 +579,10 @@ PyObject *selective_scan_step(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     const Call c(u);
     const ScanIn in(c, a, 1);
     const int64_t nb = u.size(0), hs[] = {nb, in.Dm, in.N};
-    float *ph = address<float>(&must(tensor(a[8], "h"), "h"), "h", Shape(hs, 3), at::kFloat, c.dev);
+    const Tensor &h = must(tensor(a[8], "h"), "h");
+    float *ph = address<float>(&h, "h", Shape(hs, 3), at::kFloat, c.dev);
     float *po = ho ? address<float>(ho, "h_out", Shape(hs, 3), at::kFloat, c.dev) : ph;
+    written(ho ? *ho : h);
     PyObject *y = a[10];
     void *py = output(c, y, "out", u.sizes(), u.scalar_type());
     THPObjectPtr hold_y(y);

@@ -239,6 +239,56 @@ def test_calls_that_record_no_gradient_warn():
             ldn.add_rmsnorm(x, x, wp)
 
 
+def test_writing_into_a_saved_tensor_is_noticed():
+    """A tensor that a graph has saved and a later call writes (its sum in place, a state, an
+    output): the backward pass refuses, as after torch's own in-place operations."""
+    import torch
+    from gated_delta_rule_chunkwise_gb300 import autograd as ag
+    x, w = torch.randn(4, 64, device="cuda"), torch.ones(64, device="cuda", requires_grad=True)
+    taps = torch.randn(64, 4, device="cuda", requires_grad=True)
+    A, m = -torch.ones(64, 8, device="cuda"), torch.randn(1, 4, 1, 8, device="cuda")
+    other = torch.randn(4, 64, device="cuda")
+    state, h = torch.randn(1, 3, 64, device="cuda"), torch.randn(1, 64, 8, device="cuda")
+
+    def norm(write):
+        y, s = ag.add_rmsnorm(x, other, w)
+        if write:
+            ldn.add_rmsnorm(x, s.detach(), w.detach(), residual_out=s.detach())
+        return y
+
+    def conv(write, how):
+        st = state.clone()
+        y, _ = ag.short_conv(other[None], taps, None, st)
+        if write:
+            how(st)
+        return y
+
+    def plain(write, how):      # torch's own graph
+        hh = h.clone()
+        y = (hh * torch.ones_like(h).requires_grad_()).sum()
+        if write:
+            how(hh)
+        return y
+
+    c = taps.detach()
+    ways = [lambda write: norm(write),
+            lambda write: conv(write, lambda st: ldn.short_conv(x[None], c, None, st, state_out=st)),
+            lambda write: conv(write, lambda st: ldn.short_conv_step(x[:1], c, None, st)),
+            lambda write: conv(write, lambda st: ldn.short_conv_step(x[:1], c, None, st.clone(), state_out=st)),
+            lambda write: plain(write, lambda hh: ldn.selective_scan_step(x[:1], x[:1], A, m[:, 0], m[:, 0], None, None,
+                                                                          None, hh)),
+            lambda write: plain(write, lambda hh: ldn.selective_scan(x[None], x[None], A, m, m, h_final=hh))]
+    for f in ways:
+        f(False).sum().backward()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            f(True).sum().backward()
+    with torch.inference_mode():        # such tensors have no versions
+        st = torch.randn(1, 3, 64, device="cuda")
+    before = st.clone()
+    ldn.short_conv_step(x[:1], c, None, st)
+    assert not torch.equal(st, before)
+
+
 # ---- memory on another stream ----
 def test_arguments_freed_after_a_call_on_another_stream():
     """Arguments that are dropped right after a call with stream=, while that stream is still
