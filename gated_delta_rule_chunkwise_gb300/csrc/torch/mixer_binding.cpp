@@ -117,6 +117,7 @@ void check(const Tensor &t, const char *name, Shape shape, at::ScalarType type, 
     if (!t.is_cuda() || t.layout() != at::kStrided) refuse(PyExc_TypeError, "%s must be a CUDA tensor", name);
     if (t.get_device() != dev)
         refuse(PyExc_ValueError, "%s is on cuda:%d, expected cuda:%d", name, (int)t.get_device(), dev);
+    if (t.is_neg()) refuse(PyExc_ValueError, "%s is a negated view: its memory holds the other sign", name);
     if (t.scalar_type() != type)
         refuse(PyExc_TypeError, "%s has dtype %s, expected %s", name, c10::toString(t.scalar_type()), c10::toString(type));
     if (t.sizes() != shape)

@@ -289,6 +289,25 @@ def test_writing_into_a_saved_tensor_is_noticed():
     assert not torch.equal(st, before)
 
 
+def test_negated_views_are_refused():
+    """The imaginary part of a conjugate is a view whose memory holds the other sign."""
+    import torch
+    z = torch.randn(2, 9, 16, dtype=torch.complex64, device="cuda")
+    neg = z.conj().imag
+    assert neg.is_neg()
+    w, taps, plain = torch.ones(16, device="cuda"), torch.ones(16, 4, device="cuda"), torch.randn(2, 9, 16, device="cuda")
+    A, m = -torch.ones(16, 8, device="cuda"), torch.randn(2, 9, 1, 8, device="cuda")
+    same = torch._neg_view(plain)
+    for bad in (neg, same):
+        for f in (lambda: ldn.add_rmsnorm(plain, bad, w), lambda: ldn.add_rmsnorm(bad, None, w),
+                  lambda: ldn.short_conv(bad, taps), lambda: ldn.selective_scan(plain, bad, A, m, m),
+                  lambda: ldn.short_conv(plain, taps, out=bad)):
+            with pytest.raises(ValueError):
+                f()
+    with pytest.raises(ValueError, match="negated"):
+        ldn.short_conv(same, taps)
+
+
 # ---- memory on another stream ----
 def test_arguments_freed_after_a_call_on_another_stream():
     """Arguments that are dropped right after a call with stream=, while that stream is still
