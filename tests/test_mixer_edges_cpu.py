@@ -106,3 +106,49 @@ def test_the_c_library_is_in_place_where_the_torch_layer_fails(made, monkeypatch
     assert made == ["libldn.so", "libldn_diag.so", "_ldn_torch.so"]
     ldn_build.build()
     assert len(made) == 3
+
+
+# ---- the batched references against those that go token by token ----
+@pytest.mark.parametrize("act", [True, False])
+@pytest.mark.parametrize("W,state,bias", [(1, False, False), (4, True, True), (8, True, False), (3, False, True)])
+def test_batched_convolution_reference(act, W, state, bias):
+    import numpy as np
+    from tests import _mixer_ref as ref, _mixer_vec as vec
+    r = np.random.default_rng(W)
+    B, T, C, lens = 4, 11, 5, [11, 0, 2, 7]
+    x, w = r.normal(size=(B, T, C)), r.normal(size=(C, W))
+    b, st = r.normal(size=C) if bias else None, r.normal(size=(B, W - 1, C)) if state else None
+    dy, dl = r.normal(size=(B, T, C)), r.normal(size=(B, W - 1, C))
+    args = (x, w, b, st, lens, act)
+    pairs = [(ref.conv(*args), vec.conv(*args)), (ref.conv_bwd(*args, dy, dl), vec.conv_bwd(*args, dy, dl)),
+             (ref.conv_bounds(*args, "bf16", dy, dl), vec.conv_bounds(*args, "bf16", dy, dl))]
+    inside = (np.arange(T) < np.array(lens)[:, None])[:, :, None]
+    for want, got in pairs:
+        for a, c in zip(want, got):
+            if a.shape == (B, T, C):
+                a, c = a * inside, c * inside
+            assert np.allclose(a, c, rtol=1e-12, atol=1e-15)
+
+
+def test_bounds_of_every_state():
+    import numpy as np
+    from tests import _mixer_ref as ref, _mixer_vec as vec
+    r = np.random.default_rng(3)
+    B, T, D, G, N, lens = 2, 9, 6, 2, 4, [9, 5]
+    p = dict(u=r.normal(size=(B, T, D)), delta=r.normal(size=(B, T, D)), A=-np.abs(r.normal(size=(D, N))),
+             B=r.normal(size=(B, T, G, N)), C=r.normal(size=(B, T, G, N)), D=None, z=None, bias=None,
+             h0=r.normal(size=(B, D, N)), softplus=True)
+    h, e = vec.state_bounds(p, lens)
+    assert np.array_equal(h, ref.scan(p, lens)[1])
+    assert np.allclose(e[:, -1], ref.scan_bounds(p, lens, "f32")["h"], rtol=1e-12, atol=1e-30)
+
+
+def test_runs_of_the_convolution_emulated():
+    """The launch's run lengths, by the gradient's workspace (it holds a row of sums a block)."""
+    from tests import _mixer_vec as vec
+    for B, T, C, W in ((1, 1, 1, 1), (4, 2048, 2048, 4), (300, 150, 8, 4), (300, 150, 8, 8), (24, 200, 1100, 4),
+                       (3, 3000, 2560, 4), (7, 777, 1028, 3), (2000, 40, 4, 6)):
+        cblocks, blocks_sm = -(-C // 128), 4 if W <= 4 else 2
+        run = vec.conv_run(B * cblocks, T, W, 4, blocks_sm)
+        rblocks = -(-(-(-T // run)) // 4)
+        assert ldn.ldn_short_conv_backward_workspace_size(B, T, C, W) == B * rblocks * (W + 1) * C * 4
