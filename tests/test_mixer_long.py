@@ -234,3 +234,38 @@ def test_segments_on_streams_and_in_graphs():
                     g.replay()
         torch.cuda.synchronize()
         assert all(same(want, o) for o in outs)
+
+
+def test_infinite_rates_and_steps_over_segments():
+    """Rates of -infinity among ordinary ones in a scan of segments and in its gradient (a rate of
+    -1e30 in 64 bits is one that forgets as well); a step of -infinity (a masked token) keeps the
+    state, NaN stays in its channel; one sequence ends in an early segment."""
+    import torch
+    case = (2, 700, 8, 16, 1, "f32", {})
+    p, n = long_memory(case), [700, 350]
+    p["A"][3], p["A"][5, 2] = -1e30, -1e30
+    assert ldn.ldn_ssm_scan_workspace_size(*case[:5]) > 0
+    t, gl, h0 = scan_tensors(p, n, "f32"), dev(np.array(n)), dev(p["h0"])
+    t[2][3], t[2][5, 2] = -float("inf"), -float("inf")
+    r = np.random.default_rng(8)
+    dy, dh = rounded(r.normal(size=(2, 700, 8)), "f32"), rounded(r.normal(size=(2, 8, 16)), "f32")
+    bound, grads = ref.scan_bounds(p, n, "f32", dy, dh)
+    wh, eh = vec.state_bounds(p, n)
+    y, h, states = ldn.selective_scan(*t, h0, lens=gl, save_states=True)
+    within(y, ref.scan(p, n)[0], bound["y"] + 1e-30, "y")
+    within(h, wh[:, -1], bound["h"], "h_final")
+    within(states, wh[:, :-1:32], eh[:, :-1:32], "states")
+    g = ldn.selective_scan_backward(*t, states, dev(dy), dev(dh), lens=gl)
+    for k, want in grads.items():
+        within(g[k], want, bound[k], k)
+    # masked tokens and NaN
+    t[1][:, 40:700:3, 1] = -float("inf")
+    t[0][0, 300, 6] = float("nan")
+    q = dict(p, delta=p["delta"].copy())
+    q["delta"][:, 40:700:3, 1] = -1e4        # a step of e^-10000 is zero in 64 bits as well
+    y, h = ldn.selective_scan(*t, h0, lens=gl)
+    keep = [c for c in range(8) if c != 6]
+    bound, wh = ref.scan_bounds(q, n, "f32"), ref.scan(q, n)[1]
+    within(h[:, keep], wh[:, -1][:, keep], bound["h"][:, keep], "h_final over masked tokens")
+    assert torch.isnan(h[0, 6]).all() and torch.isfinite(h[1]).all() and torch.isnan(y[0, 300:, 6]).all()
+    assert torch.isfinite(y[0, :300]).all() and torch.isfinite(y[1]).all() and torch.isfinite(y[0][:, keep]).all()
