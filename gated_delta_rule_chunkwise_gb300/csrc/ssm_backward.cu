@@ -247,6 +247,8 @@ ssm_backward_kernel(const SsmBwdArgs a, const Plan pl, const Work wk)
                             const float4 q = *reinterpret_cast<const float4 *>(&sm.red[k][row][n]);
                             s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
                         }
+                        // past the end sums of zeros, but where a state is NaN or infinite
+                        if (row >= rows) s = make_float4(0.f, 0.f, 0.f, 0.f);
                         *reinterpret_cast<float4 *>(bc + (size_t)row * a.G * (2 * N) + n) = s;
                     }
                 // the rows' du, ddelta, dz

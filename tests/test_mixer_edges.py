@@ -167,6 +167,27 @@ def test_scan_with_a_small_workspace_beside_its_outputs():
         ldn.selective_scan(*t, h0, out=y, h_final=h, workspace=arena.view(torch.uint8))
 
 
+# ---- rows past a sequence's end ----
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+def test_scan_gradients_past_the_end_are_zero_whatever_the_state(dtype, N):
+    """A NaN in one token's input makes a channel's state NaN from there on; the gradients of the
+    rows past the sequence's end stay zero, and those before the token are what they are."""
+    import torch
+    n = [37, 64]
+    p = scan_inputs(2, 70, 24, N, 2, dtype)
+    t, gl = scan_tensors(p, n, dtype), dev(np.array(n))
+    t[0][0, 30, 5] = float("nan")
+    dy = dev(np.random.default_rng(1).normal(size=(2, 70, 24)), dtype)
+    states = ldn.selective_scan(*t, dev(p["h0"]), lens=gl, save_states=True)[2]
+    g = ldn.selective_scan_backward(*t, states, dy, None, lens=gl)
+    for k in ("du", "ddelta", "dz", "dB", "dC"):
+        for i in range(2):
+            assert (g[k][i, n[i]:] == 0).all(), k
+    assert torch.isnan(g["dC"][0, 30:37, 0]).all() and torch.isfinite(g["dC"][0, :30]).all()
+    assert torch.isfinite(g["dC"][:, :, 1]).all() and all(torch.isfinite(g[k][1]).all() for k in ("du", "dB", "dC"))
+
+
 # ---- several host threads ----
 def test_wide_norm_gradients_from_several_threads():
     """The C entry points are re-entrant: threads that call the gradient of rows of different
