@@ -291,7 +291,7 @@ short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
                     if (EDGE && t + k >= len) d = dup(0.f);   // nothing flows from past the end, whatever p is
                     now[i] = d.x;
                     now[i + 1] = d.y;
-                    if (!EDGE || t + k < t1) {
+                    if (!EDGE || t + k < min(t1, len)) {   // past the end d is 0, but a row of the window may be infinite
 #pragma unroll
                         for (int j = 0; j < W; ++j) {
                             const float2 q = __ffma2_rn(d, make_float2(win[k + j][i], win[k + j][i + 1]),
@@ -319,6 +319,7 @@ short_conv_bwd_kernel(const ConvBwdArgs a, int run, int runs, int cblocks)
                         for (int j = 0; j < W; ++j)
                             q = __ffma2_rn(make_float2(wt[W - 1 - j][i], wt[W - 1 - j][i + 1]),
                                            make_float2(dp[k + j][i], dp[k + j][i + 1]), q);
+                        if (EDGE && r >= len) q = dup(0.f);   // whatever the weights are
                         d[i] = q.x;
                         d[i + 1] = q.y;
                     }

@@ -188,6 +188,37 @@ def test_scan_gradients_past_the_end_are_zero_whatever_the_state(dtype, N):
     assert torch.isfinite(g["dC"][:, :, 1]).all() and all(torch.isfinite(g[k][1]).all() for k in ("du", "dB", "dC"))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C,W", [(8, 4), (7, 3), (12, 8)])
+def test_conv_gradients_of_a_padded_batch_are_those_without_padding(dtype, C, W):
+    """Infinite inputs at a sequence's end and an infinite weight: the gradients of a padded batch
+    are the same as of the sequence alone, and zero past its end."""
+    import torch
+    r = np.random.default_rng(W)
+    n, T = 21, 40
+    x, dy = dev(r.normal(size=(1, T, C)), dtype), dev(r.normal(size=(1, T, C)), dtype)
+    w = dev(r.normal(size=(C, W)))
+    x[0, n - 1, 2] = float("inf")
+    w[5, 1] = float("inf")
+    for act in (False, True):
+        g = ldn.short_conv_backward(x, w, None, dy, lens=torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                    activation=act)
+        cut = lambda m: m[:, :n].contiguous()  # noqa: E731
+        want = ldn.short_conv_backward(cut(x), w, None, cut(dy), activation=act)
+        assert (g["dx"][0, n:] == 0).all()
+        same = lambda a, b: bool(((a == b) | (torch.isnan(a) & torch.isnan(b))).all())  # noqa: E731
+        assert same(g["dx"][:, :n], want["dx"])
+        # the tokens of one sequence may be cut into other runs: sums to rounding, infinities and NaN alike
+        a, b = host(g["dweight"]), host(want["dweight"])
+        assert np.array_equal(np.isnan(a), np.isnan(b)) and np.array_equal(np.isinf(a), np.isinf(b))
+        # |silu'| <= 1.1, |x| < 5, n roundings on either side
+        mag = np.broadcast_to((np.abs(host(dy[0, :n])) * 1.1).sum(0)[:, None] * 5, a.shape)
+        ok = np.isfinite(b)
+        assert (np.abs(a[ok] - b[ok]) <= mag[ok] * 2 * n * U).all()
+        if not act:
+            assert np.isinf(b[2]).any()
+
+
 # ---- several host threads ----
 def test_wide_norm_gradients_from_several_threads():
     """The C entry points are re-entrant: threads that call the gradient of rows of different
