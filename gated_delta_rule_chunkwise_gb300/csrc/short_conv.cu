@@ -27,7 +27,10 @@ constexpr int kWarps = 4;   // runs per block, one warp each; all warps take the
 // measured fastest of 2, 3, 4 rows and 4 to 10 blocks at 4 x 2048 x 4096 (forward: 28 us, 33 at
 // two rows, 42 with 16-byte loads and twice the registers).
 constexpr int kBatch = 4, kBwdBatch = 3;
-// Single elements (a word each on their way) leave room for fewer blocks.
+// Single elements (a word each on their way) leave room for fewer blocks.  More than four taps take
+// registers: of 3, 4, 5, 6 blocks forward at 4 x 2048 x 4096 in bf16 W = 5 takes 36, 32, 31, 37 us and
+// W = 8 39, 36, 54, 76; of 1, 2, 3, 4 in the gradient 123, 63, 63, 72 and 128, 92, 144, 254 (fp32, half
+// the channels, W = 6: 61, 54, 46, 105).
 constexpr int fwd_blocks(int W, bool vec) { return W > 4 ? 4 : vec ? 7 : 5; }
 constexpr int bwd_blocks(int W, bool vec) { return W > 4 ? 2 : vec ? 4 : 3; }
 

@@ -13,7 +13,7 @@
 // again into registers and the gradients follow.  A lane owns two channels x 4 states, so the
 // channel sums of dB and dC start in registers; the rest goes by halving exchanges, over the
 // lanes of a channel for q, sum A w and sum C h (four tokens together), over the channels of a
-// warp for dB and dC.  An update costs 15 fp32 operations and two exponentials (108 us for
+// warp for dB and dC.  An update costs 15 fp32 operations and two exponentials (100 us for
 // 2 x 2048 tokens of 4096 x 16 on the fp32 pipes alone) and takes 24 instructions, packed pairs
 // counted once: the sums' shuffles, selections and additions are a quarter of them, broadcasts
 // into pairs, loads and the elementwise work another.  350 us: two warps a scheduler run the

@@ -7,10 +7,13 @@
 // One update costs four fp32 operations (dt A, dt u B, a h + ., C h + .) and one exponential
 // for every state of every channel and token: at N = 16 that outweighs the eight bytes a
 // channel and token of traffic.  Per SM and cycle the GPU makes 128 fp32 results and 32
-// exponentials (measured), so 32 updates: 58 us for 4 x 2048 tokens of 4096 x 16, against 40 us
-// for their bytes.  What stands above that is everything else an update needs in registers --
-// each register written, by arithmetic or by a load, takes its turn at the register file, and
-// at five results an update the operands' loads add two -- and the elementwise work.
+// exponentials (measured), so 32 updates: 54 us for 4 x 2048 tokens of 4096 x 16 at 2,060 MHz,
+// against 40 us for their bytes.  What stands above that is everything else an update needs in
+// registers -- each register written, by arithmetic or by a load, takes its turn at the register
+// file, and at five results an update the operands' loads add two: a loop of the update alone, eight
+// warps an SM as here, runs at 7.8 to 8.0 cycles an update and scheduler (7.3 to 7.5 with sixteen),
+// which is 125 us on the SMs that hold two blocks -- and the elementwise work, the exchanges and the
+// barriers, which are the other 59 us.
 //
 // L = N / S neighbouring lanes own one channel, S states each, in registers over the whole run;
 // exponentials take e^x = 2^{x log2 e} with log2 e folded into A; products are packed pairs.

@@ -67,11 +67,6 @@ def _call(f, stream, x, *args):
     return r
 
 
-def chunk_states_shape(B, T, D, N):
-    """The shape of the states a scan of these sizes saves for its gradient."""
-    return B, (T + 31) // 32, D, N
-
-
 # ---- RMS norm with the residual's addition ----
 def add_rmsnorm(x, residual, weight, *, eps=1e-6, out=None, residual_out=None, stream=None):
     """y = rmsnorm(s) * weight with s = x + residual (ldn_add_rmsnorm).
