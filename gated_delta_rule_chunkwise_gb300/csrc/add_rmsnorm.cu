@@ -3,8 +3,8 @@
 //   s = x + r (stored in the residual's type),  rstd = 1 / sqrt(mean_c s_c^2 + eps),
 //   y = s rstd w,   as the element type or in e4m3 with scales:
 //   scale = max(max_group |y|, 2^-100) / 448,  q = e4m3(y / scale), saturating;
-//   a group is 128 consecutive channels or the whole row.  y and scale are fp32: one result in
-//   1.5 million lies so near a border of e4m3 that 64 bits would round it to the other side.
+//   a group is 128 consecutive channels or the whole row.  y and scale are fp32; q is rounded as the
+//   quotient in 64 bits, stored in fp32, would be.
 // The norm is taken of s AS STORED: a bf16 residual stream rounds the sum once, and that
 // value is what the next block adds to and what the gradient reads back.
 //
@@ -12,10 +12,10 @@
 //
 // Both directions move every byte once and are bound by HBM: a row lives in registers (8
 // channels a thread and vector), two block sums a row.  Arithmetic is fp32.  16384 x 4096 in
-// bf16 to e4m3 takes 72 us by rows and 73 by 128 (6,480 and 6,420 GB/s), 8192 x 2048 with an fp32
+// bf16 to e4m3 takes 72.5 us by rows and 75.6 by 128 (6,480 and 6,240 GB/s), 8192 x 2048 with an fp32
 // residual stream 31.5 and the gradient 43.8 (6,380 and 6,130 GB/s).  Rows past 8192 channels have
 // more vectors a thread than registers for a next row, and at eight some spill: 4096 x 16384 94 us
-// (5,690 GB/s; e4m3 102 and 109), 2048 x 32768 94, and the gradient, with nothing on its way, 265
+// (5,690 GB/s; e4m3 83 and 107), 2048 x 32768 92, and the gradient, with nothing on its way, 265
 // (2,030 GB/s).
 #include <cuda_fp8.h>
 
@@ -26,10 +26,12 @@ namespace {
 
 constexpr int kE = 8;   // channels per thread and vector
 constexpr int kMostThreads = 512;
-// An SM's threads in the row walk (16384 x 4096 to e4m3: 71.5 us at 768, 75.6 at 1024, 79.7 at
-// 1536, 75.2 at 2048).
-constexpr int kNormThreads = 768;
-constexpr float kE4m3Max = 448.f;
+// An SM's threads in the row walk: 1024 to e4m3 by rows, where a row near a border holds its block
+// up (16384 x 4096: 89 us at 512, 75.6 at 768, 72.5 at 1024, 93 at 1280; 8192 x 8192 73 for 93 at
+// 768), 768 otherwise (16384 x 4096 by 128: 75.6 us, 92 at 1024 with the registers it has; as the
+// element type 84, 88 at 1024).
+constexpr int norm_threads_sm(int eight) { return eight == 1 ? 1024 : 768; }
+constexpr float kE4m3Max = 448.f, kLeast = 0x1p-100f;   // kLeast: of a group's largest |y|
 
 // Sums and the largest value over the block, to every thread, through sm[32 NV].
 template <int NV>
@@ -53,14 +55,20 @@ __device__ __forceinline__ void block_sum(float *v, float *sm, int nwarps)
     }
 }
 
-__device__ __forceinline__ float block_max(float v, float *sm, int nwarps)
+// `at` gets every warp's lane that holds its largest value.
+__device__ __forceinline__ float block_max(float v, float *sm, int *at, int nwarps)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float t = v;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if (lane == 0) sm[warp] = v;
+    for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+    const unsigned holds = __ballot_sync(0xffffffffu, v == t);
+    if (lane == 0) {
+        sm[warp] = t;
+        at[warp] = __ffs(holds) - 1;
+    }
     __syncthreads();
-    float t = lane < nwarps ? sm[lane] : 0.f;
+    t = lane < nwarps ? sm[lane] : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
     return t;
@@ -92,10 +100,135 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float *v, int valid
 // channels and its single elements are neighbours (5000 x 777 in bf16: 9.8 us for 22.5 with
 // consecutive ones, gradient 13.4 for 18.2).
 template <bool VEC> constexpr int kStep = VEC ? 1 : 32;
-template <bool VEC> __device__ __forceinline__ int place(int k)
+template <bool VEC> __device__ __forceinline__ int place(int k, int t)
 {
-    const int t = (int)threadIdx.x;
     return k * (int)blockDim.x * kE + (VEC ? t * kE : (t & ~31) * kE + (t & 31));
+}
+
+template <bool VEC> __device__ __forceinline__ int place(int k) { return place<VEC>(k, (int)threadIdx.x); }
+
+// ---- e4m3 ----
+// y / scale = 448 |s w| / max |s w|: rstd drops out, but where the group's largest |y| is below the
+// least.  m is the largest |s w|.
+__device__ __forceinline__ float scale_up(float m, float rstd)
+{
+    return m * rstd > kLeast ? kE4m3Max / m : kE4m3Max / kLeast * rstd;   // NaN where rstd is
+}
+
+// In fp32 that quotient is off by up to four roundings (both products', the division's, the last
+// product's).  They matter only where it lies so near the middle of two neighbours in e4m3: the 20 bits
+// that are rounded away are then within kNear steps of their half (one value in 95,000, and every value
+// that is halfway exactly: rows of equal weights have such).  There it is decided as a quotient in 64
+// bits, stored in fp32, would be: 448 |s w| against the middle times max |s w|, both as exact sums of two
+// floats.  Values below e4m3's normal numbers stay with fp32.
+constexpr uint32_t kNear = 5;
+__device__ __forceinline__ uint32_t from_border(float v)   // up to 2 kNear << 12 where near
+{
+    return (__float_as_uint(v) << 12) + (0x80000000u + (kNear << 12));
+}
+__device__ __forceinline__ bool near_border(uint32_t t) { return t <= kNear << 13; }
+
+struct Pair { float hi, lo; };   // a sum of two floats, hi the nearest to it
+__device__ __forceinline__ Pair product(float a, float b)
+{
+    const float p = __fmul_rn(fabsf(a), fabsf(b));
+    return {p, __fmaf_rn(fabsf(a), fabsf(b), -p)};
+}
+__device__ __forceinline__ Pair larger(Pair a, Pair b)
+{
+    return b.hi > a.hi || (b.hi == a.hi && b.lo > a.lo) ? b : a;
+}
+__device__ __forceinline__ Pair largest(Pair a, int lanes)   // over groups of lanes
+{
+    for (int o = lanes / 2; o > 0; o >>= 1)
+        a = larger(a, {__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)});
+    return a;
+}
+// v moved to its side of the border that it is near: the middle, or a step of fp32 beside it, where
+// p is |s w| and `top` the largest.
+__device__ __forceinline__ float settled(float v, Pair p, Pair top)
+{
+    const uint32_t bits = __float_as_uint(v), middle = (bits & 0xfff00000u) | 0x80000u;
+    const float b = fabsf(__uint_as_float(middle)), c = b * top.hi;
+    const float half = __uint_as_float(bits & 0x7f800000u) * 0x1p-24f * top.hi;   // half a step of fp32
+    // the first two differences are exact: what they are of is equal to 20 bits
+    const float d = (fmaf(kE4m3Max, p.hi, -c) - fmaf(b, top.hi, -c)) + fmaf(kE4m3Max, p.lo, -b * top.lo);
+    if (!(p.hi > 0x1p-90f && top.hi < 0x1p90f)) return v;   // no ordinary numbers
+    return __uint_as_float(middle + (d > half) - (d < -half));
+}
+
+// The thread's values of a row near a border, once all are stored (a warp together; s: the row as
+// stored).  Everything is formed again from memory: registers kept for one row in twenty would cost
+// every row a third of its warps.  EIGHT = 1: the row's largest |s w| is `top`, of thread `owner`.
+template <typename T, int EIGHT, bool VEC, int STEP>
+__device__ __forceinline__ void settle_row(const T *s, const float *w, uint8_t *q, int vectors, int D, float rstd,
+                                           float top, int owner)
+{
+    constexpr int N = EIGHT == 2 && !VEC ? 4 : kE, LANES = VEC ? 16 : 32;   // a lane's channels of a group, its lanes
+    auto value = [](float a, float g, float up) { return __fmul_rn(__fmul_rn(a, g), up); };   // as in the walk
+    Pair most{0.f, 0.f};
+    bool found = false;
+#pragma unroll 1
+    for (int k = 0; k < vectors * (kE / N); ++k) {
+        const int c = place<VEC>(k / (kE / N)) + k % (kE / N) * N * STEP;
+        float a[N], g[N];
+        load_n<N, VEC, STEP>(s + c, a, D - c);
+        load_n<N, VEC, STEP>(w + c, g, D - c);
+        if constexpr (EIGHT == 2) {
+            top = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(__fmul_rn(a[i], g[i])));
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
+        const float up = scale_up(top, rstd);
+        unsigned near = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) near |= (unsigned)near_border(from_border(value(a[i], g[i], up))) << i;
+        if (!__any_sync(0xffffffffu, near != 0)) continue;
+        if constexpr (EIGHT == 2) {
+            most = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < N; ++i) most = larger(most, product(a[i], g[i]));
+            most = largest(most, LANES);
+        } else if (!found) {
+            // the largest is the owner's, unless another rounds to the same
+#pragma unroll 1
+            for (int i = threadIdx.x & 31; i < vectors * kE; i += 32) {
+                const int at = place<VEC>(i / kE, owner) + i % kE * STEP;
+                if (at < D) {
+                    const Pair p = product((float)s[at], w[at]);
+                    if (p.hi == top) most = larger(most, p);
+                }
+            }
+            most = largest(most, 32);
+            found = true;
+        }
+        if (!(top * rstd > kLeast)) continue;
+#pragma unroll 1
+        for (; near; near &= near - 1) {
+            const int at = c + (__ffs(near) - 1) * STEP;
+            const float x = (float)s[at], f = w[at], v = value(x, f, up);
+            if (fabsf(v) < 2.f * kE4m3Max)
+                q[at] = (uint8_t)__nv_cvt_float_to_fp8(settled(v, product(x, f), most), __NV_SATFINITE, __NV_E4M3);
+        }
+    }
+}
+
+// In the walk's own code where a row's neighbours are in registers meanwhile; where none are, a call
+// leaves more of them to the walk (2000 x 20001 by rows: 188 us inlined, 155 called).
+template <typename T, int EIGHT, bool VEC, int STEP>
+__device__ __noinline__ void settle_called(const T *s, const float *w, uint8_t *q, int vectors, int D, float rstd,
+                                           float top, int owner)
+{
+    settle_row<T, EIGHT, VEC, STEP>(s, w, q, vectors, D, rstd, top, owner);
+}
+template <typename T, int EIGHT, bool VEC, int STEP, bool INLINE>
+__device__ __forceinline__ void settle(const T *s, const float *w, uint8_t *q, int vectors, int D, float rstd, float top,
+                                       int owner)
+{
+    if constexpr (INLINE) settle_row<T, EIGHT, VEC, STEP>(s, w, q, vectors, D, rstd, top, owner);
+    else settle_called<T, EIGHT, VEC, STEP>(s, w, q, vectors, D, rstd, top, owner);
 }
 
 // Rounds to the stored type and back.
@@ -113,6 +246,7 @@ add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__rest
                    float *__restrict__ scale, TRes *r_out, long long rows, int D, float eps)
 {
     __shared__ float sm[2][64];
+    __shared__ int at[EIGHT == 1 ? 2 : 1][EIGHT == 1 ? 16 : 1];
     const int nt = blockDim.x, nwarps = nt >> 5;
     constexpr bool KEEP = VPT <= 2;   // the weights stay in registers, the next row comes ahead
     float g[KEEP ? VPT : 1][kE];
@@ -154,12 +288,14 @@ add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__rest
         block_sum<1>(&ss, sm[turn], nwarps);   // two buffers: the next row's sums pass no reader of these
         const float rstd = rsqrtf(ss / (float)D + eps);
         float top = 0.f;
+        uint32_t near = 0xffffffffu;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = place<VEC>(k), valid = D - c;
             if constexpr (!KEEP) load_n<kE, VEC, kStep<VEC>>(w + c, g[0], valid);
 #pragma unroll
-            for (int i = 0; i < kE; ++i) v[k][i] *= rstd * g[KEEP ? k : 0][i];
+            for (int i = 0; i < kE; ++i)
+                v[k][i] = EIGHT ? __fmul_rn(v[k][i], g[KEEP ? k : 0][i]) : v[k][i] * (rstd * g[KEEP ? k : 0][i]);
             if constexpr (EIGHT == 0) {
                 store_n<kE, VEC, kStep<VEC>>((TIn *)y + row * D + c, v[k], valid);
             } else {
@@ -171,46 +307,60 @@ add_rmsnorm_kernel(const TIn *__restrict__ x, const TRes *r, const float *__rest
                     // 128 channels are four of every lane's
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        m = 0x1p-100f;
+                        m = 0.f;
 #pragma unroll
                         for (int i = 4 * h; i < 4 * h + 4; ++i) m = fmaxf(m, fabsf(v[k][i]));
 #pragma unroll
                         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        const float up = kE4m3Max / m;
+                        const float up = scale_up(m, rstd);
 #pragma unroll
-                        for (int i = 4 * h; i < 4 * h + 4; ++i) v[k][i] *= up;
+                        for (int i = 4 * h; i < 4 * h + 4; ++i) near = min(near, from_border(v[k][i] = __fmul_rn(v[k][i], up)));
                         if ((threadIdx.x & 31) == 0 && valid > 128 * h)
-                            scale[row * (long long)((D + 127) / 128) + c / 128 + h] = m / kE4m3Max;
+                            scale[row * (long long)((D + 127) / 128) + c / 128 + h] = fmaxf(m * rstd, kLeast) / kE4m3Max;
                     }
                     store_e4m3<kE, VEC, kStep<VEC>>((uint8_t *)y + row * D + c, v[k], valid);
                 } else if constexpr (EIGHT == 2) {
                     // 128 channels are the 8-channel vectors of 16 neighbouring lanes
 #pragma unroll
                     for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    m = fmaxf(m, 0x1p-100f);
-                    const float up = kE4m3Max / m;
+                    const float up = scale_up(m, rstd);
 #pragma unroll
-                    for (int i = 0; i < kE; ++i) v[k][i] *= up;
+                    for (int i = 0; i < kE; ++i) near = min(near, from_border(v[k][i] = __fmul_rn(v[k][i], up)));
                     store_e4m3<kE, VEC, kStep<VEC>>((uint8_t *)y + row * D + c, v[k], valid);
                     if ((threadIdx.x & 15) == 0 && valid > 0)
-                        scale[row * (long long)((D + 127) / 128) + c / 128] = m / kE4m3Max;
+                        scale[row * (long long)((D + 127) / 128) + c / 128] = fmaxf(m * rstd, kLeast) / kE4m3Max;
                 } else {
                     top = fmaxf(top, m);
                 }
             }
         }
         if constexpr (EIGHT == 1) {
-            top = fmaxf(block_max(top, sm[turn] + 32, nwarps), 0x1p-100f);
-            const float up = kE4m3Max / top;
+            top = block_max(top, sm[turn] + 32, at[turn], nwarps);
+            const float up = scale_up(top, rstd);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int c = place<VEC>(k);
 #pragma unroll
-                for (int i = 0; i < kE; ++i) v[k][i] *= up;
+                for (int i = 0; i < kE; ++i) near = min(near, from_border(v[k][i] = __fmul_rn(v[k][i], up)));
                 store_e4m3<kE, VEC, kStep<VEC>>((uint8_t *)y + row * D + c, v[k], D - c);
             }
-            if (threadIdx.x == 0) scale[row] = top / kE4m3Max;
+            if (threadIdx.x == 0) scale[row] = fmaxf(top * rstd, kLeast) / kE4m3Max;
         }
+        if constexpr (EIGHT != 0)
+            if (__any_sync(0xffffffffu, near_border(near))) {
+                uint8_t *q = (uint8_t *)y + row * D;
+                int owner = 0;
+                if constexpr (EIGHT == 1) {
+                    const int lane = threadIdx.x & 31;
+                    const unsigned holds = __ballot_sync(0xffffffffu, lane < nwarps && sm[turn][32 + lane] == top);
+                    owner = holds ? (__ffs(holds) - 1) * 32 + at[turn][__ffs(holds) - 1] : 0;
+                }
+                if (std::is_same_v<TIn, TRes> || r)
+                    settle<TRes, EIGHT, VEC, kStep<VEC>, KEEP>(r ? r_out + row * D : (const TRes *)x + row * D, w, q, VPT, D,
+                                                               rstd, top, owner);
+                else
+                    settle<TIn, EIGHT, VEC, kStep<VEC>, KEEP>(x + row * D, w, q, VPT, D, rstd, top, owner);
+            }
         if constexpr (!KEEP) fetch(row + gridDim.x);
     }
 }
@@ -361,8 +511,8 @@ add_rmsnorm_bwd_wide_kernel(const TIn *__restrict__ dy, const TRes *__restrict__
 }
 
 // Vectors per thread: the fewest that fit 512 threads, but two from 4096 channels on (16384 x 4096
-// with a bf16 residual: 84 us for 110 with one, to e4m3 73 for 109, gradient 89 for 110).  Two would
-// pay from 2048 channels on as well: 16384 rows take 41 us for the 47 of one, 38 for 44 and 49 for 55.
+// with a bf16 residual: 84 us for 110 with one, gradient 89 for 110).  Two would pay from 2048
+// channels on as well: 16384 rows take 41 us for the 47 of one, gradient 49 for 55.
 int norm_vpt(int D) { return D < 4096 ? 1 : D <= 8192 ? 2 : D <= 16384 ? 4 : 8; }
 // The gradient's rows past this are wide (8192 x 8192 in registers 91 us, as wide rows 264).
 constexpr int kWide = 8192;
@@ -374,7 +524,7 @@ template <typename TIn, typename TRes, int EIGHT, int VPT>
 void norm_run(const AddNormArgs &a, bool vec, cudaStream_t st)
 {
     const int nt = norm_threads(a.D, VPT);
-    const dim3 grid((unsigned)std::min<long long>(a.rows, 152LL * std::max(1, kNormThreads / nt))), block(nt);
+    const dim3 grid((unsigned)std::min<long long>(a.rows, 152LL * std::max(1, norm_threads_sm(EIGHT) / nt))), block(nt);
     if (vec)
         add_rmsnorm_kernel<TIn, TRes, EIGHT, VPT, true><<<grid, block, 0, st>>>(
             (const TIn *)a.x, (const TRes *)a.residual, a.weight, a.y, a.scale, (TRes *)a.residual_out, a.rows, a.D,

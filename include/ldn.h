@@ -488,7 +488,9 @@ int ldn_add_rmsnorm(const void *x, const void *residual, const float *weight, vo
 
 /* ldn_add_rmsnorm with y in 8 bits (e4m3) and fp32 scales, y ~ q * scale:
  *   scale = max(max |y| over the group, 2^-100) / 448,  q = e4m3(y / scale),
- * to nearest even, saturating.  `group` is 0 (one scale per row, scale [rows]) or
+ * to nearest even, saturating.  The quotient is rounded as if it were formed in 64 bits
+ * and stored in fp32, whatever the roundings of y and scale (below e4m3's normal numbers:
+ * as formed in fp32).  `group` is 0 (one scale per row, scale [rows]) or
  * 128 (scale [rows][ceil(D / 128)], the last group of a row may be short).
  *   q [rows][D] bytes.  A NaN in y is a NaN in q. */
 int ldn_add_rmsnorm_e4m3(const void *x, const void *residual, const float *weight, void *q, float *scale,

@@ -386,3 +386,71 @@ def test_arguments_freed_after_a_call_on_another_stream():
             assert torch.equal(got[0], want_y) and torch.equal(got[1], want_s)
         else:
             assert torch.equal(got[0], want_c)
+
+
+# ---- e4m3 next to a border ----
+def settled_e4m3(s, w, group):
+    """What 448 |s w| / max |s w| is in e4m3: the quotient in 64 bits, stored in fp32, rounded to
+    nearest even; and the quotient."""
+    rows, D = s.shape
+    p, g = s * w, group or D
+    n = -(-D // g)
+    pad = np.zeros((rows, n * g))
+    pad[:, :D] = np.abs(p)
+    top = np.repeat(pad.reshape(rows, n, g).max(-1), g, axis=1)[:, :D]
+    v = (p * (448.0 / top)).astype(np.float32).astype(np.float64)
+    return ref.e4m3(v), v
+
+
+@pytest.mark.parametrize("D", [2048, 1001, 4096, 5001, 9008, 9001, 20000, 20001])
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("dtype,res", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_e4m3_borders_are_decided_as_in_64_bits(D, group, dtype, res):
+    """No value falls to the other side of the middle of two e4m3 numbers than in 64 bits, and what
+    is in the middle goes to the even one: weights drawn, and equal ones, whose quotients of two
+    short numbers are often in the middle."""
+    import torch
+    r = np.random.default_rng(D + group)
+    rows = max(300, 3_000_000 // D)
+    x, rr = r.normal(size=(rows, D)), 3 * r.normal(size=(rows, D))
+    # rows on a grid of a sixteenth have many values in the middle in fp32 too
+    x[::2], rr[::2] = np.round(x[::2] * 16) / 16, np.round(rr[::2] * 16) / 16
+    gx, gr = dev(x, dtype), dev(rr, res)
+    for w in (rounded(1 + 0.1 * r.normal(size=D), "f32"), np.ones(D), np.full(D, -0.75)):
+        q, scale, s = ldn.add_rmsnorm_e4m3(gx, gr, dev(w), group=group)
+        want, v = settled_e4m3(host(s), w, group)
+        normal = np.abs(v) >= 2.0 ** -6             # below, borders stay with fp32
+        got = host(q)
+        assert np.array_equal(got[normal], want[normal]), (got != want)[normal].sum()
+        assert (np.abs(got - v)[~normal] <= 2.0 ** -10 + 2.0 ** -26).all()
+        again = ldn.add_rmsnorm_e4m3(gx, gr, dev(w), group=group)
+        assert torch.equal(q.view(torch.uint8), again[0].view(torch.uint8)) and torch.equal(scale, again[1])
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_e4m3_of_rows_that_are_not_ordinary(group):
+    """Groups below the least magnitude, zeros, infinite and NaN rows among ordinary ones."""
+    import torch
+    r = np.random.default_rng(5)
+    x = dev(r.normal(size=(6, 256)))
+    w = torch.ones(256, device="cuda")
+    tiny = w * 1e-33
+    q, scale, _ = ldn.add_rmsnorm_e4m3(x, None, tiny, group=group)
+    assert torch.equal(scale, torch.full_like(scale, 2.0 ** -100 / 448))
+    y = ref.norm(host(x), host(tiny), 1e-6) * 448 * 2.0 ** 100
+    within(q, y, np.maximum(np.abs(y) * 2.0 ** -4, 2.0 ** -10) + np.abs(y) * 40 * U, "tiny")
+    x[1], x[2, 7], x[3, 200], x[4] = 0, float("nan"), float("inf"), 3e-20
+    q, scale, _ = ldn.add_rmsnorm_e4m3(x, None, w, group=group)
+    f = q.float()
+    assert (f[1] == 0).all() and torch.isnan(f[2]).all() and torch.isnan(f[3, 200]) and torch.isfinite(f[3, :200]).all()
+    # |y| = 3e-17 in every channel of row 4
+    assert (f[4] == 448).all() and torch.isfinite(scale[[0, 1, 4, 5]]).all()
+    # without a residual the type of one does not matter
+    b = dev(host(x), "bf16")
+    want = ldn.add_rmsnorm_e4m3(b, None, w, group=group)
+    out, sc = torch.empty_like(want[0]), torch.empty_like(want[1])
+    st = ldn.ldn_add_rmsnorm_e4m3(ptr(b), None, ptr(w), ptr(out), ptr(sc), None, 6, 256, group, ldn.LDN_BF16, ldn.LDN_F32,
+                                  1e-6, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == ldn.LDN_OK and torch.equal(out.view(torch.uint8), want[0].view(torch.uint8))
+    assert torch.equal(sc, want[1])
