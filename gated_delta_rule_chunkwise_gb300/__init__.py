@@ -3,7 +3,8 @@ DeltaNet, KDA and Gated DeltaNet-2 forward, the backward, Residual Linear
 Attention / Residual DeltaNet, plus the single-token recurrent decode step.
 
 Around them: the RMS norm with the residual's addition (also in 8 bits), the
-short causal convolution with a carried state and the selective state space scan, for
+short causal convolution with a carried state, the selective state space scan, the norms
+between two blocks with the block's gate, and the projections into and out of a block, for
 sequences, single tokens and gradients (``mixer``).
 
 The computation lives in CUDA kernels behind the C ABI of include/ldn.h
@@ -24,8 +25,14 @@ from ._native import (  # noqa: F401
     ldn_short_conv, ldn_short_conv_backward, ldn_short_conv_backward_workspace_size, ldn_short_conv_step,
     ldn_ssm_backward, ldn_ssm_backward_workspace_size, ldn_ssm_scan, ldn_ssm_scan_workspace_size, ldn_ssm_step,
 )
-_MIXER = ("add_rmsnorm", "add_rmsnorm_backward", "add_rmsnorm_e4m3", "selective_scan", "selective_scan_backward",
-          "selective_scan_step", "short_conv", "short_conv_backward", "short_conv_step")
+from ._native import (  # noqa: F401
+    LDN_ACT_GELU, LDN_ACT_NONE, LDN_ACT_SILU, ldn_gated_add_rmsnorm, ldn_gated_add_rmsnorm_backward,
+    ldn_gated_add_rmsnorm_backward_workspace_size, ldn_linear, ldn_linear_backward,
+    ldn_linear_backward_workspace_size, ldn_linear_e4m3, ldn_linear_e4m3_workspace_size, ldn_linear_workspace_size,
+)
+_MIXER = ("add_rmsnorm", "add_rmsnorm_backward", "add_rmsnorm_e4m3", "gated_add_rmsnorm",
+          "gated_add_rmsnorm_backward", "linear", "linear_backward", "linear_e4m3", "selective_scan",
+          "selective_scan_backward", "selective_scan_step", "short_conv", "short_conv_backward", "short_conv_step")
 
 
 def __getattr__(name):

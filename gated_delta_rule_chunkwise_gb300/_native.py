@@ -11,11 +11,12 @@ Two layers:
     ``ldn_backward_workspace_size``, ``ldn_rla_fwd``, ``ldn_rla_fwd_ws``,
     ``ldn_rla_fwd_workspace_size``, ``ldn_prologue``,
     ``ldn_rmsnorm_gated``, ``ldn_add_rmsnorm*``, ``ldn_short_conv*``, ``ldn_ssm_*``,
-    ``ldn_get_device_status``, ``ldn_status_string``, ``ldn_version``: the C
+    ``ldn_gated_add_rmsnorm*``, ``ldn_linear*``, ``ldn_get_device_status``, ``ldn_status_string``, ``ldn_version``: the C
     entry points under the same names, taking raw integer pointers;
   * ``chunk_fwd``, ``decode_step``, ``chunk_fwd_gdn2``, ``decode_step_gdn2``, ``backward`` and
     ``rla_fwd``, and (module ``mixer``) ``add_rmsnorm``, ``add_rmsnorm_e4m3``, ``short_conv``,
-    ``short_conv_step``, ``selective_scan``, ``selective_scan_step`` and their ``*_backward``:
+    ``short_conv_step``, ``selective_scan``, ``selective_scan_step``, ``gated_add_rmsnorm``,
+    ``linear``, ``linear_e4m3`` and their ``*_backward``:
     the same calls on torch CUDA tensors,
     with shape / dtype checks and allocation of outputs and of the split
     variant's workspace (torch is used for device memory and the current
@@ -32,6 +33,7 @@ LIB_PATH = os.path.join(_HERE, "lib", "libldn.so")
 
 LDN_DELTANET, LDN_GDN, LDN_KDA, LDN_GDN2 = 0, 1, 2, 3
 LDN_F32, LDN_BF16 = 0, 1
+LDN_ACT_NONE, LDN_ACT_SILU, LDN_ACT_GELU = 0, 1, 2
 LDN_OK, LDN_ERR_INVALID_ARG, LDN_ERR_UNSUPPORTED, LDN_ERR_CUDA, LDN_ERR_TIMEOUT = 0, 1, 2, 3, 4
 LDN_VARIANT_AUTO, LDN_VARIANT_SIMT, LDN_VARIANT_TENSOR, LDN_VARIANT_SPLIT, LDN_VARIANT_PAIR = 0, 1, 2, 3, 4
 LDN_VARIANT_PRESOLVED = 5
@@ -87,6 +89,16 @@ _SIGNATURES = {
     "ldn_ssm_backward": ([_P, _L, _P, _L, _P, _P, _L, _P, _L, _P, _P, _L] + [_P] * 14 + [_I] * 7 +
                          [_P, ctypes.c_size_t, _P], _I),
     "ldn_ssm_backward_workspace_size": ([_I] * 5, ctypes.c_size_t),
+    "ldn_gated_add_rmsnorm": ([_P] * 7 + [_L, _I, _L, _I, _I, ctypes.c_float, _I, _I, ctypes.c_float, _P], _I),
+    "ldn_gated_add_rmsnorm_backward": ([_P] * 12 + [_L, _I, _L, _I, _I, ctypes.c_float, _I, _I, ctypes.c_float, _P,
+                                                    ctypes.c_size_t, _P], _I),
+    "ldn_gated_add_rmsnorm_backward_workspace_size": ([_L, _I, _L], ctypes.c_size_t),
+    "ldn_linear": ([_P, _L, _P, _L] + [_P] * 4 + [_L] + [_I] * 5 + [_P, ctypes.c_size_t, _P], _I),
+    "ldn_linear_workspace_size": ([_P, _L, _P, _L, _L] + [_I] * 3, ctypes.c_size_t),
+    "ldn_linear_e4m3": ([_P, _L, _P, _P, _L] + [_P] * 4 + [_L] + [_I] * 4 + [_P, ctypes.c_size_t, _P], _I),
+    "ldn_linear_e4m3_workspace_size": ([_P, _L, _P, _L, _L] + [_I] * 2, ctypes.c_size_t),
+    "ldn_linear_backward": ([_P, _P, _L, _P, _L] + [_P] * 4 + [_L] + [_I] * 5 + [_P, ctypes.c_size_t, _P], _I),
+    "ldn_linear_backward_workspace_size": ([_P, _P, _L, _P, _L, _L] + [_I] * 6, ctypes.c_size_t),
     "ldn_get_device_status": ([_P], _I),
     "ldn_status_string": ([_I], ctypes.c_char_p),
     "ldn_version": ([], _I),
@@ -274,6 +286,56 @@ def ldn_ssm_backward(u, ldu, delta, ld_delta, A, Bm, ldb, Cm, ldc, Dskip, z, ldz
 
 def ldn_ssm_backward_workspace_size(B, T, D, N, G):
     return load().ldn_ssm_backward_workspace_size(B, T, D, N, G)
+
+
+def ldn_gated_add_rmsnorm(x, residual, gate, post_weight, weight, y, residual_out, rows, D, gate_rows, gate_dtype,
+                          gate_sigmoid, residual_scale, dtype, residual_dtype, eps, stream):
+    return load().ldn_gated_add_rmsnorm(x, residual, gate, post_weight, weight, y, residual_out, rows, D, gate_rows,
+                                        gate_dtype, gate_sigmoid, residual_scale, dtype, residual_dtype, eps, stream)
+
+
+def ldn_gated_add_rmsnorm_backward(dy, x, s, dsum, gate, post_weight, weight, dx, dresidual, dgate, dpost_weight,
+                                   dweight, rows, D, gate_rows, gate_dtype, gate_sigmoid, residual_scale, dtype,
+                                   residual_dtype, eps, workspace, workspace_bytes, stream):
+    return load().ldn_gated_add_rmsnorm_backward(dy, x, s, dsum, gate, post_weight, weight, dx, dresidual, dgate,
+                                                 dpost_weight, dweight, rows, D, gate_rows, gate_dtype, gate_sigmoid,
+                                                 residual_scale, dtype, residual_dtype, eps, workspace,
+                                                 workspace_bytes, stream)
+
+
+def ldn_gated_add_rmsnorm_backward_workspace_size(rows, D, gate_rows):
+    return load().ldn_gated_add_rmsnorm_backward_workspace_size(rows, D, gate_rows)
+
+
+def ldn_linear(x, ldx, weight, ldw, bias, residual, y, z, rows, K, N, activation, dtype, out_dtype, workspace,
+               workspace_bytes, stream):
+    return load().ldn_linear(x, ldx, weight, ldw, bias, residual, y, z, rows, K, N, activation, dtype, out_dtype,
+                             workspace, workspace_bytes, stream)
+
+
+def ldn_linear_workspace_size(x, ldx, weight, ldw, rows, K, N, dtype):
+    return load().ldn_linear_workspace_size(x, ldx, weight, ldw, rows, K, N, dtype)
+
+
+def ldn_linear_e4m3(x, ldx, x_scale, weight, ldw, weight_scale, bias, residual, y, rows, K, N, activation, out_dtype,
+                    workspace, workspace_bytes, stream):
+    return load().ldn_linear_e4m3(x, ldx, x_scale, weight, ldw, weight_scale, bias, residual, y, rows, K, N,
+                                  activation, out_dtype, workspace, workspace_bytes, stream)
+
+
+def ldn_linear_e4m3_workspace_size(x, ldx, weight, ldw, rows, K, N):
+    return load().ldn_linear_e4m3_workspace_size(x, ldx, weight, ldw, rows, K, N)
+
+
+def ldn_linear_backward(dy, x, ldx, weight, ldw, z, dx, dweight, dbias, rows, K, N, activation, dtype, dy_dtype,
+                        workspace, workspace_bytes, stream):
+    return load().ldn_linear_backward(dy, x, ldx, weight, ldw, z, dx, dweight, dbias, rows, K, N, activation, dtype,
+                                      dy_dtype, workspace, workspace_bytes, stream)
+
+
+def ldn_linear_backward_workspace_size(dy, x, ldx, weight, ldw, rows, K, N, activation, dtype, dy_dtype, want):
+    return load().ldn_linear_backward_workspace_size(dy, x, ldx, weight, ldw, rows, K, N, activation, dtype, dy_dtype,
+                                                     want)
 
 
 def ldn_get_device_status(stream):

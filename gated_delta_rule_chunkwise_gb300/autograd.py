@@ -1,14 +1,15 @@
 """torch.autograd binding of the forward (ldn_chunk_fwd) and the backward
 (ldn_backward): ``delta_rule(q, k, v, beta, gate, S0, mode=...)`` returns
 (out, S_final) with gradients for q, k, v, beta, gate and S0; and of the operators
-around it: ``add_rmsnorm``, ``short_conv`` and ``selective_scan``.  Argument
+around it: ``add_rmsnorm``, ``short_conv``, ``selective_scan``, ``gated_add_rmsnorm`` and
+``linear``.  Argument
 marshalling only: both directions run in the CUDA kernels of libldn.so.
 
 Capturing a backward pass into a CUDA graph follows torch's rules for leaves: no
 eager graph of the same leaves may be alive, since their gradient accumulators are
 tied to the stream that made them.  The ``*_backward`` calls of ``mixer`` have no
-such state and are captured freely.  The gradients of add_rmsnorm, short_conv and
-selective_scan have no gradients of their own: asking for them raises.
+such state and are captured freely.  The gradients of add_rmsnorm, short_conv,
+selective_scan, gated_add_rmsnorm and linear have no gradients of their own: asking for them raises.
 
 The gradients of q, k and v are returned in their dtype (the kernel computes
 them in fp32); beta, gate and S0 are fp32 throughout.  The output's gradient
@@ -133,3 +134,65 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, h0=None, 
     """``mixer.selective_scan`` with gradients for every tensor but lens; returns (y, h_final).
     The forward keeps the state entering every 32 tokens for the gradient."""
     return _SelectiveScan.apply(u, delta, A, B, C, D, z, delta_bias, h0, lens, delta_softplus)
+
+
+class _GatedAddRmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, post_weight, gate, residual_scale, gate_sigmoid, eps):
+        y, s = _mixer().gated_add_rmsnorm(x, residual, weight, post_weight, gate, residual_scale=residual_scale,
+                                          gate_sigmoid=gate_sigmoid, eps=eps)
+        ctx.set_materialize_grads(False)
+        ctx.how = dict(residual_scale=residual_scale, gate_sigmoid=gate_sigmoid, eps=eps)
+        ctx.save_for_backward(x, s, weight, post_weight, gate)
+        return s if y is None else (y, s)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        x, s, weight, post_weight, gate = ctx.saved_tensors
+        dy, ds = grads if weight is not None else (None, *grads)
+        ds = None if ds is None else ds.contiguous()
+        if weight is not None and dy is None:   # only the sum was used
+            if ds is None:
+                return (None,) * 8
+            dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+        g = _mixer().gated_add_rmsnorm_backward(None if dy is None else dy.contiguous(), x, s, weight, post_weight,
+                                                gate, ds, **ctx.how)
+        return g["dx"], g["dresidual"], g["dweight"], g["dpost_weight"], g["dgate"], None, None, None
+
+
+def gated_add_rmsnorm(x, residual, weight=None, post_weight=None, gate=None, *, residual_scale=1.0,
+                      gate_sigmoid=False, eps=1e-6):
+    """``mixer.gated_add_rmsnorm`` with gradients for every tensor; returns (y, s).  The gradient
+    that reaches s joins y's in one kernel."""
+    r = _GatedAddRmsNorm.apply(x, residual, weight, post_weight, gate, residual_scale, gate_sigmoid, eps)
+    return (None, r) if weight is None else r
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, activation):
+        ctx.activation = activation
+        if activation is None:
+            y, z = _mixer().linear(x, weight, bias, residual), None
+        else:
+            y, z = _mixer().linear(x, weight, bias, residual, activation=activation, save_z=True)
+        ctx.save_for_backward(x, weight, z)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, z = ctx.saved_tensors
+        wants = ctx.needs_input_grad
+        g = {"dx": None, "dweight": None, "dbias": None}
+        if any(wants[:3]):
+            g = _mixer().linear_backward(dy.contiguous(), x, weight, z, activation=ctx.activation, bias=wants[2],
+                                         dx=wants[0], dweight=wants[1])
+        return g["dx"], g["dweight"], g["dbias"], dy if wants[3] else None, None
+
+
+def linear(x, weight, bias=None, residual=None, *, activation=None):
+    """``mixer.linear`` with gradients for x, weight, bias and residual.  With an activation the
+    forward keeps z, in x's type, for the gradient."""
+    return _Linear.apply(x, weight, bias, residual, activation)

@@ -19,13 +19,11 @@
 // (2,030 GB/s).
 #include <cuda_fp8.h>
 
-#include "mixer_common.cuh"
+#include "norm_common.cuh"
 
 namespace ldn {
 namespace {
 
-constexpr int kE = 8;   // channels per thread and vector
-constexpr int kMostThreads = 512;
 // An SM's threads in the row walk: 1024 to e4m3 by rows, where a row near a border holds its block
 // up (16384 x 4096: 89 us at 512, 75.6 at 768, 72.5 at 1024, 93 at 1280; 8192 x 8192 73 for 93 at
 // 768), 768 otherwise (16384 x 4096 by 128: 75.6 us, 92 at 1024 with the registers it has; as the
@@ -33,29 +31,8 @@ constexpr int kMostThreads = 512;
 constexpr int norm_threads_sm(int eight) { return eight == 1 ? 1024 : 768; }
 constexpr float kE4m3Max = 448.f, kLeast = 0x1p-100f;   // kLeast: of a group's largest |y|
 
-// Sums and the largest value over the block, to every thread, through sm[32 NV].
-template <int NV>
-__device__ __forceinline__ void block_sum(float *v, float *sm, int nwarps)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    if (lane == 0)
-#pragma unroll
-        for (int i = 0; i < NV; ++i) sm[i * 32 + warp] = v[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float t = lane < nwarps ? sm[i * 32 + lane] : 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        v[i] = t;
-    }
-}
-
-// `at` gets every warp's lane that holds its largest value.
+// The largest value over the block, to every thread, through sm[32]; `at` gets every warp's lane that
+// holds its largest.
 __device__ __forceinline__ float block_max(float v, float *sm, int *at, int nwarps)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -94,18 +71,6 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float *v, int valid
             if (i * STEP < valid) p[i * STEP] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
     }
 }
-
-// A thread's place in a vector of the block's, and the distance of its 8 channels: consecutive
-// where rows are whole 16-byte vectors; otherwise 32 apart, so that a warp takes the same 256
-// channels and its single elements are neighbours (5000 x 777 in bf16: 9.8 us for 22.5 with
-// consecutive ones, gradient 13.4 for 18.2).
-template <bool VEC> constexpr int kStep = VEC ? 1 : 32;
-template <bool VEC> __device__ __forceinline__ int place(int k, int t)
-{
-    return k * (int)blockDim.x * kE + (VEC ? t * kE : (t & ~31) * kE + (t & 31));
-}
-
-template <bool VEC> __device__ __forceinline__ int place(int k) { return place<VEC>(k, (int)threadIdx.x); }
 
 // ---- e4m3 ----
 // y / scale = 448 |s w| / max |s w|: rstd drops out, but where the group's largest |y| is below the
@@ -229,13 +194,6 @@ __device__ __forceinline__ void settle(const T *s, const float *w, uint8_t *q, i
 {
     if constexpr (INLINE) settle_row<T, EIGHT, VEC, STEP>(s, w, q, vectors, D, rstd, top, owner);
     else settle_called<T, EIGHT, VEC, STEP>(s, w, q, vectors, D, rstd, top, owner);
-}
-
-// Rounds to the stored type and back.
-__device__ __forceinline__ float as_stored(float x, const float *) { return x; }
-__device__ __forceinline__ float as_stored(float x, const __nv_bfloat16 *)
-{
-    return __bfloat162float(__float2bfloat16_rn(x));
 }
 
 // EIGHT: 0 = y in TIn, 1 = e4m3 with a scale per row, 2 = per 128 channels.  A block walks rows
@@ -517,9 +475,6 @@ int norm_vpt(int D) { return D < 4096 ? 1 : D <= 8192 ? 2 : D <= 16384 ? 4 : 8; 
 // The gradient's rows past this are wide (8192 x 8192 in registers 91 us, as wide rows 264).
 constexpr int kWide = 8192;
 constexpr int kWidest = 32768;   // channels that the entry points accept
-// Threads for D channels at vpt vectors of 8 each, in whole warps.
-int norm_threads(int D, int vpt) { return std::min(kMostThreads, (((D + kE * vpt - 1) / (kE * vpt) + 31) / 32) * 32); }
-
 template <typename TIn, typename TRes, int EIGHT, int VPT>
 void norm_run(const AddNormArgs &a, bool vec, cudaStream_t st)
 {
@@ -546,8 +501,6 @@ void norm_pick(const AddNormArgs &a, bool vec, cudaStream_t st)
     if (e == 2) v == 1 ? LDN_NORM(2, 1) : v == 2 ? LDN_NORM(2, 2) : v == 4 ? LDN_NORM(2, 4) : LDN_NORM(2, 8);
 #undef LDN_NORM
 }
-
-bool vec16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 template <typename TIn, typename TRes, int VPT>
 void norm_bwd_run(const AddNormBwdArgs &a, int grid, bool vec, cudaStream_t st)

@@ -83,6 +83,30 @@ struct AddNormBwdArgs {
     int D, dtype, res_dtype;
     float eps;
 };
+struct GatedNormArgs {
+    const void *x, *residual, *gate;
+    const float *post_weight, *weight;
+    void *y, *residual_out;
+    long long rows, gate_rows;
+    int D, gate_dtype, gate_sigmoid, dtype, res_dtype;
+    float residual_scale, eps;
+};
+
+struct GatedNormBwdArgs {
+    const void *dy, *x, *s, *dsum, *gate;
+    const float *post_weight, *weight;
+    void *dx, *dresidual, *dgate;
+    float *dpost_weight, *dweight, *part, *part_post, *part_gate;
+    long long rows, gate_rows;
+    int D, gate_dtype, gate_sigmoid, dtype, res_dtype;
+    float residual_scale, eps;
+};
+
+cudaError_t launch_gated_add_rmsnorm(const GatedNormArgs &a, cudaStream_t stream);
+cudaError_t launch_gated_add_rmsnorm_bwd(const GatedNormBwdArgs &a, cudaStream_t stream);
+// fp32 numbers of its workspace (gate_rows 0: no gate)
+size_t gated_add_rmsnorm_bwd_floats(long long rows, int D, long long gate_rows);
+
 cudaError_t launch_add_rmsnorm(const AddNormArgs &a, cudaStream_t stream);
 cudaError_t launch_add_rmsnorm_bwd(const AddNormBwdArgs &a, cudaStream_t stream);
 int add_rmsnorm_bwd_blocks(long long rows, int D);

@@ -1,50 +1,8 @@
 // C ABI of the operators around a token mixer: argument validation and dispatch of
 // ldn_add_rmsnorm*, ldn_short_conv* and ldn_ssm_* (documented in include/ldn.h).
-#include "ldn_internal.cuh"
+#include "api_common.cuh"
 
 using namespace ldn;
-
-namespace {
-
-constexpr long long kMostElements = 1LL << 40;
-
-bool at(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-bool known(int dtype) { return dtype == LDN_F32 || dtype == LDN_BF16; }
-size_t size_of(int dtype) { return dtype == LDN_BF16 ? 2 : 4; }
-int status_of(cudaError_t e) { return e == cudaSuccess ? LDN_OK : LDN_ERR_CUDA; }
-
-// A stretch of device memory (bytes 0: absent).
-struct Span {
-    const void *p;
-    size_t bytes;
-    bool hits(const Span &o) const
-    {
-        if (!p || !o.p || !bytes || !o.bytes) return false;
-        const uintptr_t a = (uintptr_t)p, b = (uintptr_t)o.p;
-        return a < b + o.bytes && b < a + bytes;
-    }
-};
-
-// Whether some output overlaps an input or another output.
-template <size_t NI, size_t NO>
-bool overlapping(const Span (&in)[NI], const Span (&out)[NO])
-{
-    for (size_t i = 0; i < NO; ++i) {
-        for (size_t j = 0; j < NI; ++j)
-            if (out[i].hits(in[j])) return true;
-        for (size_t j = 0; j < i; ++j)
-            if (out[i].hits(out[j])) return true;
-    }
-    return false;
-}
-
-// Bytes from the first to the last element of `rows` rows of `width`, `ld` apart.
-Span rows_span(const void *p, long long rows, long long ld, long long width, int dtype)
-{
-    return {p, p && rows > 0 ? (size_t)((rows - 1) * ld + width) * size_of(dtype) : 0};
-}
-
-}  // namespace
 
 // ---- RMS norm with the residual's addition ----
 
@@ -348,4 +306,85 @@ extern "C" int ldn_ssm_backward(const void *u, long long ldu, const void *delta,
                        dh_final, du, ddelta, dB, dC, dz, dA, dD, ddelta_bias, dh0, (float *)workspace, B, T, D, N, G,
                        delta_softplus, dtype};
     return status_of(launch_ssm_backward(a, (cudaStream_t)stream));
+}
+
+// ---- Norms around a block with its gate and the residual's scale ----
+
+static int check_gated(long long rows, int D, const void *gate, long long gate_rows, int gate_dtype, int gate_sigmoid,
+                       float scale, int dtype, int res_dtype, float eps)
+{
+    if (!known(dtype) || !known(res_dtype) || rows < 0 || D < 1) return LDN_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || eps > 1e30f || !(scale >= -1e30f && scale <= 1e30f)) return LDN_ERR_INVALID_ARG;
+    if (gate_sigmoid != 0 && gate_sigmoid != 1) return LDN_ERR_INVALID_ARG;
+    if (gate && (!known(gate_dtype) || gate_rows < 0 || (rows > 0 && (gate_rows < 1 || rows % gate_rows != 0))))
+        return LDN_ERR_INVALID_ARG;
+    if (dtype == LDN_F32 && (res_dtype != LDN_F32 || (gate && gate_dtype != LDN_F32))) return LDN_ERR_UNSUPPORTED;
+    if (D > 16384 || rows > 0x7fffffffLL || rows * D > kMostElements) return LDN_ERR_UNSUPPORTED;
+    if (gate && (gate_rows > 0x7fffffffLL || gate_rows * D > kMostElements)) return LDN_ERR_UNSUPPORTED;
+    return LDN_OK;
+}
+
+extern "C" int ldn_gated_add_rmsnorm(const void *x, const void *residual, const void *gate, const float *post_weight,
+                                     const float *weight, void *y, void *residual_out, long long rows, int D,
+                                     long long gate_rows, int gate_dtype, int gate_sigmoid, float residual_scale,
+                                     int dtype, int residual_dtype, float eps, void *stream)
+{
+    const int st = check_gated(rows, D, gate, gate_rows, gate_dtype, gate_sigmoid, residual_scale, dtype,
+                               residual_dtype, eps);
+    if (st != LDN_OK) return st;
+    if (rows == 0) return LDN_OK;
+    if (!x || !residual || !residual_out || !weight != !y) return LDN_ERR_INVALID_ARG;
+    const size_t es = size_of(dtype), rs = size_of(residual_dtype), gs = gate ? size_of(gate_dtype) : 1,
+                 n = (size_t)rows * D;
+    if (!at(x, es) || !at(y, es) || !at(residual, rs) || !at(residual_out, rs) || !at(gate, gs) ||
+        !at(post_weight, 4) || !at(weight, 4))
+        return LDN_ERR_INVALID_ARG;
+    const Span in[] = {{x, n * es}, {gate, gate ? (size_t)gate_rows * D * gs : 0}, {post_weight, (size_t)D * 4},
+                       {weight, (size_t)D * 4},
+                       {residual == residual_out ? nullptr : residual, n * rs}};   // the sum may replace the residual
+    const Span out[] = {{y, n * es}, {residual_out, n * rs}};
+    if (overlapping(in, out)) return LDN_ERR_INVALID_ARG;
+    const GatedNormArgs a{x, residual, gate, post_weight, weight, y, residual_out, rows, gate_rows, D, gate_dtype,
+                          gate_sigmoid, dtype, residual_dtype, residual_scale, eps};
+    return status_of(launch_gated_add_rmsnorm(a, (cudaStream_t)stream));
+}
+
+extern "C" size_t ldn_gated_add_rmsnorm_backward_workspace_size(long long rows, int D, long long gate_rows)
+{
+    if (rows < 1 || gate_rows < 0 || (gate_rows && rows % gate_rows) ||
+        check_gated(rows, D, nullptr, 0, 0, 0, 1.f, LDN_BF16, LDN_BF16, 0.f) != LDN_OK)
+        return 0;
+    return gated_add_rmsnorm_bwd_floats(rows, D, gate_rows) * sizeof(float);
+}
+
+extern "C" int ldn_gated_add_rmsnorm_backward(const void *dy, const void *x, const void *s, const void *dsum,
+                                              const void *gate, const float *post_weight, const float *weight,
+                                              void *dx, void *dresidual, void *dgate, float *dpost_weight,
+                                              float *dweight, long long rows, int D, long long gate_rows,
+                                              int gate_dtype, int gate_sigmoid, float residual_scale, int dtype,
+                                              int residual_dtype, float eps, void *workspace, size_t workspace_bytes,
+                                              void *stream)
+{
+    const int st = check_gated(rows, D, gate, gate_rows, gate_dtype, gate_sigmoid, residual_scale, dtype,
+                               residual_dtype, eps);
+    if (st != LDN_OK) return st;
+    if (!weight != !dweight || !post_weight != !dpost_weight || (dgate && !gate)) return LDN_ERR_INVALID_ARG;
+    const size_t need = ldn_gated_add_rmsnorm_backward_workspace_size(rows, D, gate ? gate_rows : 0);
+    if (rows > 0 && (!x || !s || !weight != !dy || !workspace || workspace_bytes < need || !at(workspace, 16)))
+        return LDN_ERR_INVALID_ARG;
+    const size_t es = size_of(dtype), rs = size_of(residual_dtype), gs = gate ? size_of(gate_dtype) : 1,
+                 n = (size_t)rows * D, ng = gate ? (size_t)gate_rows * D * gs : 0, np = (size_t)D * 4;
+    if (!at(dy, es) || !at(x, es) || !at(dx, es) || !at(s, rs) || !at(dsum, rs) || !at(dresidual, rs) ||
+        !at(gate, gs) || !at(dgate, gs) || !at(post_weight, 4) || !at(weight, 4) || !at(dpost_weight, 4) ||
+        !at(dweight, 4))
+        return LDN_ERR_INVALID_ARG;
+    const Span in[] = {{dy, n * es}, {x, n * es}, {s, n * rs}, {dsum, n * rs}, {gate, ng}, {post_weight, np},
+                       {weight, np}};
+    const Span out[] = {{dx, n * es}, {dresidual, n * rs}, {dgate, ng}, {dpost_weight, np}, {dweight, np},
+                        {workspace, need}};
+    if (overlapping(in, out)) return LDN_ERR_INVALID_ARG;
+    const GatedNormBwdArgs a{dy, x, s, dsum, gate, post_weight, weight, dx, dresidual, dgate, dpost_weight, dweight,
+                             (float *)workspace, nullptr, nullptr, rows, gate_rows, D, gate_dtype, gate_sigmoid,
+                             dtype, residual_dtype, residual_scale, eps};
+    return status_of(launch_gated_add_rmsnorm_bwd(a, (cudaStream_t)stream));
 }

@@ -43,4 +43,23 @@ inline bool make_tmap_bf16_4d(CUtensorMap *map, const void *base, uint64_t d0, u
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// `planes` matrices [rows][width] of 16-bit (bf16) or 8-bit elements, rows `ld` and planes
+// `plane` elements apart (multiples of 16 bytes), viewed through boxes of `box` rows of 128 bytes
+// with 128-byte swizzle.  What lies past a row's width or the rows reads as zero.
+inline bool make_tmap_rows(CUtensorMap *map, const void *base, uint64_t width, uint64_t rows, uint64_t planes,
+                           uint64_t ld, uint64_t plane, uint32_t box, bool bytes)
+{
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return false;
+    const uint64_t es = bytes ? 1 : 2;
+    const cuuint64_t dims[3] = {width, rows, planes};
+    const cuuint64_t strides[2] = {ld * es, plane * es};
+    const cuuint32_t boxes[3] = {(cuuint32_t)(128 / es), box, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+               const_cast<void *>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace ldn

@@ -1,5 +1,6 @@
 // Native half of mixer.py: checks torch tensors, allocates outputs and workspaces, and calls
-// the C entry points of include/ldn.h (ldn_add_rmsnorm*, ldn_short_conv*, ldn_ssm_*) on the
+// the C entry points of include/ldn.h (ldn_add_rmsnorm*, ldn_short_conv*, ldn_ssm_*,
+// ldn_gated_add_rmsnorm*, ldn_linear*) on the
 // current stream of the tensors' device.  No computation.  A call for a single token is a few
 // microseconds of GPU work, and the same steps taken in Python cost several times that.
 //
@@ -631,6 +632,243 @@ PyObject *selective_scan_backward(PyObject *, PyObject *const *a, Py_ssize_t nar
     LEAVE
 }
 
+// ---- Norms around a block with its gate and the residual's scale ----
+// Rows of a gate that is [D], or as large as x up to some dimension and 1 from there to the last.
+int64_t gate_rows(const Tensor &g, Shape x)
+{
+    const int64_t n = (int64_t)x.size();
+    const Shape s = g.sizes();
+    if (g.dim() == 1 && s[0] == x.back()) return 1;
+    int64_t rows = 1, i = 0;
+    if (g.dim() == n && s[n - 1] == x.back()) {
+        for (; i < n - 1 && s[i] == x[i]; ++i) rows *= s[i];
+        while (i < n - 1 && s[i] == 1) ++i;
+        if (i == n - 1) return rows;
+    }
+    refuse(PyExc_ValueError, "gate has shape %s: for x %s it is [D], or x's sizes up to some dimension, 1 from there "
+           "on and D last", text(s).c_str(), text(x).c_str());
+}
+
+struct GatedIn {
+    Shape shape;
+    int64_t D, n, groups = 0;
+    int code, gcode = 0;
+    void *x, *gate = nullptr;
+    float *w, *post;
+    GatedIn(const Call &c, const Tensor &t, const Tensor *weight, const Tensor *post_weight, const Tensor *g)
+        : shape(t.sizes())
+    {
+        if (t.dim() < 1) refuse(PyExc_ValueError, "x must have at least one dimension");
+        D = shape.back();
+        n = D ? t.numel() / D : 0;
+        code = ::code(t, "x");
+        const int64_t ws[] = {D};
+        x = address(&t, "x", shape, t.scalar_type(), c.dev);
+        w = address<float>(weight, "weight", Shape(ws, 1), at::kFloat, c.dev);
+        post = address<float>(post_weight, "post_weight", Shape(ws, 1), at::kFloat, c.dev);
+        if (g) {
+            gcode = ::code(*g, "gate");
+            groups = gate_rows(*g, shape);
+            gate = address(g, "gate", g->sizes(), g->scalar_type(), c.dev);
+            if (!gate) gate = (void *)16;   // an empty one is not a missing one
+        }
+    }
+};
+
+// (x, residual, weight, post_weight, gate, residual_scale, gate_sigmoid, eps, out, residual_out) -> (y, s)
+PyObject *gated_add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t nargs)
+{
+    ENTRY
+    NEEDS(10);
+    const Tensor &x = must(tensor(a[0], "x"), "x"), &r = must(tensor(a[1], "residual"), "residual");
+    if (!here(x, "x")) Py_RETURN_NONE;
+    warn_without_gradient(a, nargs, "gated_add_rmsnorm");
+    const Call c(x);
+    const GatedIn in(c, x, tensor(a[2], "weight"), tensor(a[3], "post_weight"), tensor(a[4], "gate"));
+    const float scale = as_float(a[5]), eps = as_float(a[7]);
+    const int sigmoid = truth(a[6]), cr = code(r, "residual");
+    void *pr = address(&r, "residual", in.shape, r.scalar_type(), c.dev);
+    PyObject *y = a[8], *s = a[9];
+    THPObjectPtr hold_y, hold_s;
+    void *py = nullptr;
+    if (in.w || !in.D) {
+        py = output(c, y, "out", in.shape, x.scalar_type());
+    } else {
+        if (y != Py_None) refuse(PyExc_ValueError, "out without weight");
+        kept(y);
+    }
+    hold_y = y;
+    void *ps = output(c, s, "residual_out", in.shape, r.scalar_type());
+    hold_s = s;
+    if (!done(ldn_gated_add_rmsnorm(in.x, pr, in.gate, in.post, in.w, py, ps, in.n, size(in.D), in.groups, in.gcode,
+                                    sigmoid, scale, in.code, cr, eps, c.stream()), "ldn_gated_add_rmsnorm"))
+        return nullptr;
+    return tuple({hold_y.release(), hold_s.release()});
+    LEAVE
+}
+
+// (x, dy, s, weight, post_weight, gate, dsum, residual_scale, gate_sigmoid, eps) -> dict
+PyObject *gated_add_rmsnorm_backward(PyObject *, PyObject *const *a, Py_ssize_t nargs)
+{
+    ENTRY
+    NEEDS(10);
+    const Tensor &x = must(tensor(a[0], "x"), "x"), *dy = tensor(a[1], "dy"), &s = must(tensor(a[2], "s"), "s"),
+                 *w = tensor(a[3], "weight"), *post = tensor(a[4], "post_weight"), *gate = tensor(a[5], "gate");
+    if (!here(x, "x")) Py_RETURN_NONE;
+    const Call c(x);
+    const GatedIn in(c, x, w, post, gate);
+    if (!dy != !w) refuse(PyExc_ValueError, "dy is given exactly where weight is");
+    const float scale = as_float(a[7]), eps = as_float(a[9]);
+    const int sigmoid = truth(a[8]), cr = code(s, "s");
+    void *pdy = address(dy, "dy", in.shape, x.scalar_type(), c.dev),
+         *ps = address(&s, "s", in.shape, s.scalar_type(), c.dev),
+         *pd = address(tensor(a[6], "dsum"), "dsum", in.shape, s.scalar_type(), c.dev);
+    const size_t need = ldn_gated_add_rmsnorm_backward_workspace_size(in.n, size(in.D), in.groups);
+    const int64_t nws[] = {(int64_t)(need ? need : 16)}, ws_[] = {in.D};
+    const Tensor dx = c.make(in.shape, x.scalar_type()), dr = c.make(in.shape, s.scalar_type()),
+                 ws = c.make(Shape(nws, 1), at::kByte);
+    Tensor dg, dp, dw;
+    if (gate) dg = c.make(gate->sizes(), gate->scalar_type());
+    if (post) dp = c.make(Shape(ws_, 1), at::kFloat);
+    if (w) dw = c.make(Shape(ws_, 1), at::kFloat);
+    auto p = [](const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
+    if (!done(ldn_gated_add_rmsnorm_backward(pdy, in.x, ps, pd, in.gate, in.post, in.w, p(dx), p(dr), p(dg),
+                                             (float *)p(dp), (float *)p(dw), in.n, size(in.D), in.groups, in.gcode,
+                                             sigmoid, scale, in.code, cr, eps, ws.data_ptr(), need, c.stream()),
+              "ldn_gated_add_rmsnorm_backward"))
+        return nullptr;
+    return dict({{"dx", &dx}, {"dresidual", &dr}, {"dgate", &dg}, {"dpost_weight", &dp}, {"dweight", &dw}});
+    LEAVE
+}
+
+// ---- Projections ----
+// A tensor for a workspace of n bytes; undefined for none.
+Tensor bytes(const Call &c, size_t n)
+{
+    const int64_t s[] = {(int64_t)n};
+    return n ? c.make(Shape(s, 1), at::kByte) : Tensor();
+}
+
+struct LinearIn {
+    Rows x, w;
+    int64_t K, N, n;
+    std::vector<int64_t> yshape, xshape;
+    LinearIn(const Call &c, const Tensor &t, const Tensor &weight)
+    {
+        if (t.dim() < 1) refuse(PyExc_ValueError, "x must have at least one dimension");
+        if (weight.dim() != 2) refuse(PyExc_ValueError, "weight must have 2 dimensions, got %d", (int)weight.dim());
+        K = t.sizes().back();
+        N = weight.size(0);
+        n = 1;
+        for (int64_t i = 0; i + 1 < t.dim(); ++i) n *= t.size(i);
+        const int64_t ws[] = {N, K};
+        x = rows(t, "x", t.sizes(), t.scalar_type(), c.dev, t.dim() - 1);
+        w = rows(weight, "weight", Shape(ws, 2), t.scalar_type(), c.dev, 1);
+        xshape.assign(t.sizes().begin(), t.sizes().end());
+        yshape = xshape;
+        yshape.back() = N;
+    }
+};
+
+// (x, weight, bias, residual, activation, save_z, out) -> y or (y, z)
+PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t nargs)
+{
+    ENTRY
+    NEEDS(7);
+    const Tensor &x = must(tensor(a[0], "x"), "x"), &w = must(tensor(a[1], "weight"), "weight"),
+                 *b = tensor(a[2], "bias"), *r = tensor(a[3], "residual");
+    if (!here(x, "x")) Py_RETURN_NONE;
+    warn_without_gradient(a, nargs, "linear");
+    const Call c(x);
+    const int cx = code(x, "x"), act = as_int(a[4]), save = truth(a[5]);
+    const at::ScalarType t = x.scalar_type(), ty = r ? r->scalar_type() : t;
+    const LinearIn in(c, x, w);
+    const int64_t bs[] = {in.N};
+    void *pb = address(b, "bias", Shape(bs, 1), t, c.dev);
+    const int cy = r ? code(*r, "residual") : cx;
+    void *pr = address(r, "residual", in.yshape, ty, c.dev);
+    PyObject *y = a[6];
+    void *py = output(c, y, "out", in.yshape, ty);
+    THPObjectPtr hold_y(y);
+    Tensor z;
+    if (save) z = c.make(in.yshape, t);
+    const size_t need = ldn_linear_workspace_size(in.x.p, in.x.ld, in.w.p, in.w.ld, in.n, size(in.K), size(in.N), cx);
+    const Tensor ws = bytes(c, need);
+    if (!done(ldn_linear(in.x.p, in.x.ld, in.w.p, in.w.ld, pb, pr, py, save ? z.data_ptr() : nullptr, in.n, size(in.K),
+                         size(in.N), act, cx, cy, need ? ws.data_ptr() : nullptr, need, c.stream()), "ldn_linear"))
+        return nullptr;
+    if (save) return tuple({hold_y.release(), wrap(z)});
+    return hold_y.release();
+    LEAVE
+}
+
+// (x, x_scale, weight, weight_scale, bias, residual, activation, out) -> y
+PyObject *linear_e4m3(PyObject *, PyObject *const *a, Py_ssize_t nargs)
+{
+    ENTRY
+    NEEDS(8);
+    const Tensor &x = must(tensor(a[0], "x"), "x"), &w = must(tensor(a[2], "weight"), "weight"),
+                 *b = tensor(a[4], "bias"), *r = tensor(a[5], "residual");
+    if (!here(x, "x")) Py_RETURN_NONE;
+    if (x.scalar_type() != at::kFloat8_e4m3fn)
+        refuse(PyExc_TypeError, "x must be float8_e4m3fn, got %s", c10::toString(x.scalar_type()));
+    warn_without_gradient(a, nargs, "linear_e4m3", false);
+    const Call c(x);
+    const int act = as_int(a[6]);
+    const LinearIn in(c, x, w);
+    const int64_t bs[] = {in.N};
+    const Shape xs(in.xshape.data(), in.xshape.size() - 1);
+    float *psx = address<float>(&must(tensor(a[1], "x_scale"), "x_scale"), "x_scale", xs, at::kFloat, c.dev),
+          *psw = address<float>(&must(tensor(a[3], "weight_scale"), "weight_scale"), "weight_scale", Shape(bs, 1),
+                                at::kFloat, c.dev);
+    void *pb = address(b, "bias", Shape(bs, 1), at::kBFloat16, c.dev);
+    const int cy = r ? code(*r, "residual") : LDN_BF16;
+    const at::ScalarType ty = r ? r->scalar_type() : at::kBFloat16;
+    void *pr = address(r, "residual", in.yshape, ty, c.dev);
+    PyObject *y = a[7];
+    void *py = output(c, y, "out", in.yshape, ty);
+    THPObjectPtr hold_y(y);
+    const size_t need = ldn_linear_e4m3_workspace_size(in.x.p, in.x.ld, in.w.p, in.w.ld, in.n, size(in.K), size(in.N));
+    const Tensor ws = bytes(c, need);
+    if (!done(ldn_linear_e4m3(in.x.p, in.x.ld, psx, in.w.p, in.w.ld, psw, pb, pr, py, in.n, size(in.K), size(in.N), act,
+                              cy, need ? ws.data_ptr() : nullptr, need, c.stream()), "ldn_linear_e4m3"))
+        return nullptr;
+    return hold_y.release();
+    LEAVE
+}
+
+// (x, dy, weight, z, activation, dx, dweight, dbias) -> dict
+PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t nargs)
+{
+    ENTRY
+    NEEDS(8);
+    const Tensor &x = must(tensor(a[0], "x"), "x"), &dy = must(tensor(a[1], "dy"), "dy"),
+                 &w = must(tensor(a[2], "weight"), "weight"), *z = tensor(a[3], "z");
+    if (!here(x, "x")) Py_RETURN_NONE;
+    const Call c(x);
+    const at::ScalarType t = x.scalar_type();
+    const int cx = code(x, "x"), cy = code(dy, "dy"), act = as_int(a[4]);
+    const LinearIn in(c, x, w);
+    void *pdy = address(&dy, "dy", in.yshape, dy.scalar_type(), c.dev), *pz = address(z, "z", in.yshape, t, c.dev);
+    if (act != LDN_ACT_NONE && !z) refuse(PyExc_TypeError, "z is needed with an activation");
+    const int64_t ws_[] = {in.N, in.K};
+    Tensor dx, dw, db;
+    if (truth(a[5])) dx = c.make(in.xshape, t);
+    if (truth(a[6])) dw = c.make(Shape(ws_, 2), t);
+    if (truth(a[7])) db = c.make(Shape(ws_, 1), t);
+    auto p = [](const Tensor &v) { return v.defined() ? v.data_ptr() : nullptr; };
+    const int want = (dx.defined() ? 1 : 0) | (dw.defined() ? 2 : 0) | (db.defined() ? 4 : 0);
+    const size_t need = ldn_linear_backward_workspace_size(pdy, in.x.p, in.x.ld, in.w.p, in.w.ld, in.n, size(in.K),
+                                                           size(in.N), act, cx, cy, want);
+    const Tensor ws = bytes(c, need);
+    if (!done(ldn_linear_backward(pdy, in.x.p, in.x.ld, in.w.p, in.w.ld, pz, p(dx), p(dw), p(db), in.n, size(in.K),
+                                  size(in.N), act, cx, cy, need ? ws.data_ptr() : nullptr, need, c.stream()),
+              "ldn_linear_backward"))
+        return nullptr;
+    return dict({{"dx", &dx}, {"dweight", &dw}, {"dbias", &db}});
+    LEAVE
+}
+
 // (t, lead) -> elements between rows, or -1
 PyObject *py_row_distance(PyObject *, PyObject *const *a, Py_ssize_t nargs)
 {
@@ -658,6 +896,11 @@ PyMethodDef methods[] = {FAST("add_rmsnorm", add_rmsnorm),
                          FAST("selective_scan", selective_scan),
                          FAST("selective_scan_step", selective_scan_step),
                          FAST("selective_scan_backward", selective_scan_backward),
+                         FAST("gated_add_rmsnorm", gated_add_rmsnorm),
+                         FAST("gated_add_rmsnorm_backward", gated_add_rmsnorm_backward),
+                         FAST("linear", linear),
+                         FAST("linear_e4m3", linear_e4m3),
+                         FAST("linear_backward", linear_backward),
                          FAST("row_distance", py_row_distance),
                          FAST("set_error", set_error),
                          {nullptr, nullptr, 0, nullptr}};

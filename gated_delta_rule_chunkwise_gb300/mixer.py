@@ -1,8 +1,9 @@
 """The operators around a recurrent token mixer on torch CUDA tensors: ``add_rmsnorm``,
 ``add_rmsnorm_e4m3``, ``short_conv``, ``short_conv_step``, ``selective_scan``,
-``selective_scan_step`` and the gradients ``add_rmsnorm_backward``,
-``short_conv_backward``, ``selective_scan_backward`` (the C entry points ldn_add_rmsnorm*,
-ldn_short_conv* and ldn_ssm_* of include/ldn.h).
+``selective_scan_step``, ``gated_add_rmsnorm``, ``linear``, ``linear_e4m3`` and the gradients
+``add_rmsnorm_backward``, ``short_conv_backward``, ``selective_scan_backward``,
+``gated_add_rmsnorm_backward``, ``linear_backward`` (the C entry points ldn_add_rmsnorm*,
+ldn_short_conv*, ldn_ssm_*, ldn_gated_add_rmsnorm* and ldn_linear* of include/ldn.h).
 
 Argument marshalling only, in native code (csrc/torch/, lib/_ldn_torch.so): shape, type and
 device checks, strides, allocation of outputs and workspaces.  Wrong types raise TypeError,
@@ -13,9 +14,9 @@ then allocated for that stream, the arguments' memory is kept from reuse until i
 with them, and ordering it against the streams that made the inputs and read the outputs is
 the caller's.
 
-None of these calls records gradients: ``autograd`` has add_rmsnorm, short_conv and
-selective_scan with them.  The calls of the same names here, and add_rmsnorm_e4m3, warn
-(UserWarning) where gradients are being recorded and an argument requires one; the others,
+None of these calls records gradients: ``autograd`` has add_rmsnorm, short_conv,
+selective_scan, gated_add_rmsnorm and linear with them.  The calls of the same names here, and
+add_rmsnorm_e4m3 and linear_e4m3, warn (UserWarning) where gradients are being recorded and an argument requires one; the others,
 for single tokens and gradients, do not.
 """
 from __future__ import annotations
@@ -46,6 +47,9 @@ def _load():
 _core = _load()
 _norm, _norm_bwd = _core.add_rmsnorm, _core.add_rmsnorm_backward
 _conv, _conv_step, _conv_bwd = _core.short_conv, _core.short_conv_step, _core.short_conv_backward
+_gated, _gated_bwd = _core.gated_add_rmsnorm, _core.gated_add_rmsnorm_backward
+_linear, _linear_e4m3, _linear_bwd = _core.linear, _core.linear_e4m3, _core.linear_backward
+_ACTIVATIONS = {None: _n.LDN_ACT_NONE, "silu": _n.LDN_ACT_SILU, "gelu": _n.LDN_ACT_GELU}
 _scan, _scan_step, _scan_bwd = _core.selective_scan, _core.selective_scan_step, _core.selective_scan_backward
 
 
@@ -148,3 +152,64 @@ def selective_scan_backward(u, delta, A, B, C, D, z, delta_bias, states, dy, dh_
     dz, dB, dC in u's type; dA, dD, ddelta_bias, dh0 float32; None in the place of a
     gradient whose input is None."""
     return _call(_scan_bwd, stream, u, delta, A, B, C, D, z, delta_bias, states, dy, dh_final, delta_softplus, lens)
+
+
+# ---- Norms around a block with its gate and the residual's scale ----
+def gated_add_rmsnorm(x, residual, weight=None, post_weight=None, gate=None, *, residual_scale=1.0,
+                      gate_sigmoid=False, eps=1e-6, out=None, residual_out=None, stream=None):
+    """From a block's output to the next block's input (ldn_gated_add_rmsnorm):
+    s = residual_scale * residual + g * n with n = rmsnorm(x) * post_weight (x without one) and
+    g = gate or, with gate_sigmoid, sigmoid(gate) (1 without one); y = rmsnorm(s) * weight.
+
+    x [..., D] float32 or bfloat16; residual of x's shape, in x's type or float32; weight,
+    post_weight [D] float32 or None; gate in x's type or float32: [D], or x's number of
+    dimensions, as large as x's up to some dimension, 1 from there on and D last ([B, 1, D] for
+    x [B, T, D] is one per sequence), or None.  Returns (y, s): y None without weight; s is
+    `residual_out` (which may be `residual`: in place) or a new tensor of residual's type."""
+    return _call(_gated, stream, x, residual, weight, post_weight, gate, residual_scale, gate_sigmoid, eps, out,
+                 residual_out)
+
+
+def gated_add_rmsnorm_backward(dy, x, s, weight=None, post_weight=None, gate=None, dsum=None, *, residual_scale=1.0,
+                               gate_sigmoid=False, eps=1e-6, stream=None):
+    """Gradients of gated_add_rmsnorm (ldn_gated_add_rmsnorm_backward).  dy: y's gradient in x's
+    type, None exactly where weight is; s: what gated_add_rmsnorm returned; dsum: the gradient
+    that reaches s from elsewhere, or None.  Returns a dict: dx in x's type, dresidual in s's,
+    dgate in gate's type and shape, dweight, dpost_weight [D] float32; None in the place of a
+    gradient whose input is None."""
+    return _call(_gated_bwd, stream, x, dy, s, weight, post_weight, gate, dsum, residual_scale, gate_sigmoid, eps)
+
+
+# ---- Projections ----
+def _activation(name):
+    try:
+        return _ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"activation must be None, 'silu' or 'gelu', got {name!r}") from None
+
+
+def linear(x, weight, bias=None, residual=None, *, activation=None, save_z=False, out=None, stream=None):
+    """y = act(x weight^T + bias) + residual (ldn_linear); act None, 'silu' or 'gelu' (z Phi(z)).
+
+    x [..., K] float32 or bfloat16 (rows may be a slice of wider ones); weight [N, K] of x's
+    type (rows likewise); bias [N] of x's type or None; residual [..., N] in x's type or float32,
+    or None.  y [..., N] is `out` (which may be `residual`: in place) or a new tensor, in
+    residual's type, x's without one.  With save_z=True returns (y, z), z = x weight^T + bias in
+    x's type for linear_backward."""
+    return _call(_linear, stream, x, weight, bias, residual, _activation(activation), save_z, out)
+
+
+def linear_e4m3(x, x_scale, weight, weight_scale, bias=None, residual=None, *, activation=None, out=None, stream=None):
+    """linear from 8 bits (ldn_linear_e4m3): x [..., K] and weight [N, K] float8_e4m3fn with
+    x_scale [...] and weight_scale [N] float32, one scale a row (add_rmsnorm_e4m3's with
+    group=0); bias [N] bfloat16 or None; residual [..., N] bfloat16 or float32, or None.  y in
+    residual's type, bfloat16 without one."""
+    return _call(_linear_e4m3, stream, x, x_scale, weight, weight_scale, bias, residual, _activation(activation), out)
+
+
+def linear_backward(dy, x, weight, z=None, *, activation=None, bias=False, dx=True, dweight=True, stream=None):
+    """Gradients of linear (ldn_linear_backward) for y's gradient dy [..., N], in x's type or
+    float32; the residual's gradient is dy itself.  z: what linear(save_z=True) returned, needed
+    with an activation.  Returns a dict: dx, dweight, dbias in x's type; dbias None where `bias`
+    is false, dx and dweight likewise."""
+    return _call(_linear_bwd, stream, x, dy, weight, z, _activation(activation), dx, dweight, bias)

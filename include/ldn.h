@@ -34,6 +34,11 @@
  *       the short causal convolution with a carried state;
  *   ldn_ssm_scan, _scan_workspace_size, _step, _backward, _backward_workspace_size
  *       the selective state space scan;
+ *   ldn_gated_add_rmsnorm, _backward, _backward_workspace_size
+ *       the norms after a block and before the next one, with the block's gate and the
+ *       residual's scale;
+ *   ldn_linear, _e4m3, _backward and their _workspace_size
+ *       the projections into and out of a block;
  *   ldn_get_device_status, ldn_status_string, ldn_version.
  *
  * Conventions shared by every entry point
@@ -612,6 +617,108 @@ int ldn_ssm_backward(const void *u, long long ldu, const void *delta, long long 
                      float *ddelta_bias, float *dh0, int B, int T, int D, int N, int G, int delta_softplus, int dtype,
                      void *workspace, size_t workspace_bytes, void *stream);
 size_t ldn_ssm_backward_workspace_size(int B, int T, int D, int N, int G);
+
+/*
+ * ldn_gated_add_rmsnorm -- from a block's output x to the next block's input:
+ *   n = x / sqrt(mean_c x_c^2 + eps) * post_weight   (post_weight NULL: n = x),
+ *   g = gate, or sigma(gate) with gate_sigmoid = 1   (gate NULL: 1),
+ *   s = residual_scale * residual + g n              (stored in the residual's type),
+ *   y = s / sqrt(mean_c s_c^2 + eps) * weight        (weight NULL: no y).
+ * The second norm is taken of s as stored, as in ldn_add_rmsnorm.  Arithmetic is fp32.
+ *   x, y         [rows][D] of `dtype` (y given exactly when weight is)
+ *   residual, residual_out [rows][D] of `residual_dtype` (LDN_F32, or `dtype`);
+ *                residual_out may be residual (in place)
+ *   gate         [gate_rows][D] of `gate_dtype` (LDN_F32, or `dtype`): row t's is
+ *                gate[t / (rows / gate_rows)], so 1 is a gate per channel, `rows` one per
+ *                token; gate_rows divides rows.  gate NULL: gate_rows and gate_dtype are not read
+ *   post_weight, weight [D] fp32;  rows >= 0, 1 <= D <= 16384 (multiples of 8 with 16-byte
+ *   aligned pointers move in 16-byte vectors); eps >= 0; residual_scale finite.
+ * Pointers are aligned to their element.  One launch.
+ */
+int ldn_gated_add_rmsnorm(const void *x, const void *residual, const void *gate, const float *post_weight,
+                          const float *weight, void *y, void *residual_out, long long rows, int D,
+                          long long gate_rows, int gate_dtype, int gate_sigmoid, float residual_scale, int dtype,
+                          int residual_dtype, float eps, void *stream);
+
+/*
+ * ldn_gated_add_rmsnorm_backward -- gradients of ldn_gated_add_rmsnorm for y's gradient dy
+ * (given exactly when weight is) and the one that reaches s from elsewhere, dsum (NULL: zero).
+ *   x, s         the forward's x and residual_out;  dy of `dtype`, dsum of `residual_dtype`
+ *   dx [rows][D] of `dtype`, dresidual [rows][D] of `residual_dtype`; either may be NULL
+ *   dgate        [gate_rows][D] of `gate_dtype`, summed over the rows that share it, or NULL
+ *   dpost_weight, dweight [D] fp32, given exactly when post_weight and weight are
+ *   workspace: ldn_gated_add_rmsnorm_backward_workspace_size bytes (gate_rows 0: no gate),
+ *   16-byte aligned.
+ * The result is the same bit for bit on every call.  Two launches.
+ */
+int ldn_gated_add_rmsnorm_backward(const void *dy, const void *x, const void *s, const void *dsum, const void *gate,
+                                   const float *post_weight, const float *weight, void *dx, void *dresidual,
+                                   void *dgate, float *dpost_weight, float *dweight, long long rows, int D,
+                                   long long gate_rows, int gate_dtype, int gate_sigmoid, float residual_scale,
+                                   int dtype, int residual_dtype, float eps, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+size_t ldn_gated_add_rmsnorm_backward_workspace_size(long long rows, int D, long long gate_rows);
+
+/*
+ * ldn_linear -- a projection with its epilogue, on the tensor cores:
+ *   z = x weight^T + bias,   y = act(z) + residual,   act: none, SiLU z sigma(z), or
+ *   GELU z Phi(z) (Phi the normal distribution's integral).
+ *   x            [rows][K] of `dtype`, rows ldx elements apart
+ *   weight       [N][K] of `dtype`, rows ldw elements apart
+ *   bias         [N] of `dtype` or NULL
+ *   residual     [rows][N] of `out_dtype` or NULL;  y [rows][N] of `out_dtype` (LDN_F32, or
+ *                `dtype`), contiguous; y may be residual (in place)
+ *   z            [rows][N] of `dtype` or NULL: what ldn_linear_backward needs where there is
+ *                an activation
+ *   activation   LDN_ACT_NONE, LDN_ACT_SILU, LDN_ACT_GELU.  rows >= 0, K >= 1, N >= 1.
+ * Products are exact and summed in fp32.  bf16 enters the tensor cores as it is; fp32 as three
+ * bf16 numbers whose sum it is, six of their nine products taken (the others are below 2^-25 of
+ * the product): an infinity or a NaN gives what it gives in fp32, and numbers below 2^-110 keep
+ * fewer digits.
+ * workspace: ldn_linear_workspace_size bytes, 256-byte aligned (0: none is used): what the
+ * tensor cores cannot take as it lies in memory is laid out there, fp32 operands and rows that
+ * do not start at 16-byte boundaries.  One launch, and one for each operand so laid out.
+ * The result is the same bit for bit on every call.
+ */
+typedef enum { LDN_ACT_NONE = 0, LDN_ACT_SILU = 1, LDN_ACT_GELU = 2 } ldn_activation;
+int ldn_linear(const void *x, long long ldx, const void *weight, long long ldw, const void *bias,
+               const void *residual, void *y, void *z, long long rows, int K, int N, int activation, int dtype,
+               int out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+/* Reads the pointers' alignment, not what they point at.  Pure host function; 0 also for
+ * arguments that are rejected. */
+size_t ldn_linear_workspace_size(const void *x, long long ldx, const void *weight, long long ldw, long long rows,
+                                 int K, int N, int dtype);
+
+/* ldn_linear from 8 bits (e4m3), as ldn_add_rmsnorm_e4m3 leaves them with group = 0:
+ *   z[t][n] = x_scale[t] weight_scale[n] sum_k x[t][k] weight[n][k] + bias[n].
+ *   x [rows][K] and weight [N][K] bytes, rows ldx and ldw bytes apart; x_scale [rows] and
+ *   weight_scale [N] fp32; bias [N] bf16 or NULL; residual and y [rows][N] of `out_dtype`
+ *   (LDN_BF16 or LDN_F32).  Products are exact and summed in fp32 on the tensor cores. */
+int ldn_linear_e4m3(const void *x, long long ldx, const float *x_scale, const void *weight, long long ldw,
+                    const float *weight_scale, const void *bias, const void *residual, void *y, long long rows, int K,
+                    int N, int activation, int out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+size_t ldn_linear_e4m3_workspace_size(const void *x, long long ldx, const void *weight, long long ldw, long long rows,
+                                      int K, int N);
+
+/*
+ * ldn_linear_backward -- gradients of ldn_linear for y's gradient dy [rows][N] of `dy_dtype`
+ * (LDN_F32, or `dtype`), contiguous; the residual's is dy itself:
+ *   dz = dy act'(z),  dx = dz weight,  dweight = dz^T x,  dbias = sum over rows of dz.
+ *   z            [rows][N] of `dtype`, what the forward stored (not read, and may be NULL,
+ *                with LDN_ACT_NONE)
+ *   dx [rows][K], dweight [N][K], dbias [N] of `dtype`, contiguous; each may be NULL.
+ * With bf16, dz is rounded to bf16 for its two products, and not for dbias; sums are fp32.
+ * workspace: ldn_linear_backward_workspace_size bytes for these arguments (want: 1 for dx,
+ * 2 for dweight, 4 for dbias, added), 256-byte aligned.  The result is the same bit for bit on
+ * every call.
+ */
+int ldn_linear_backward(const void *dy, const void *x, long long ldx, const void *weight, long long ldw,
+                        const void *z, void *dx, void *dweight, void *dbias, long long rows, int K, int N,
+                        int activation, int dtype, int dy_dtype, void *workspace, size_t workspace_bytes,
+                        void *stream);
+size_t ldn_linear_backward_workspace_size(const void *dy, const void *x, long long ldx, const void *weight,
+                                          long long ldw, long long rows, int K, int N, int activation, int dtype,
+                                          int dy_dtype, int want);
 
 /* Synchronises `stream`, then reads and clears the device status word on the
  * current device.  Returns LDN_OK, LDN_ERR_TIMEOUT (a kernel abandoned a
