@@ -19,6 +19,7 @@ struct Walk {
     long long groups, cuts;
 };
 
+constexpr int kRingLeast = 1024;   // channels from which a row is worth its bulk copies
 int bwd_vpt(int D) { return D <= 4096 ? 1 : D <= 8192 ? 2 : 4; }
 
 Walk walk_of(long long rows, int D, long long gate_rows, bool dgate)
@@ -35,182 +36,240 @@ Walk walk_of(long long rows, int D, long long gate_rows, bool dgate)
     return w;
 }
 
-template <typename TIn, typename TRes, typename TG, int VPT, bool VEC>
+// RING: the rows come through a ring in shared memory, a stage being refilled once every thread has
+// its values in registers, behind the first sums' barrier.
+template <typename TIn, typename TRes, typename TG, int VPT, bool VEC, bool RING>
 __global__ void __launch_bounds__(kMostThreads)
-gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk)
+gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
 {
-    constexpr int ST = kStep<VEC>;
+    static_assert(VPT == 1 || !RING, "the sums have the dynamic shared memory");
     // one vector a thread: its weights and its columns' sums in registers, the next row on its way;
     // more: the sums in shared memory, each its thread's own
     constexpr bool ONE = VPT == 1;
     extern __shared__ float acc_sm[];
-    __shared__ float sm[2][4 * 32];
+    __shared__ __align__(16) Sums<3> sm[2];
+    __shared__ __align__(16) Sums<1> sm_x[2];
     const int D = a.D, nt = blockDim.x, nwarps = nt >> 5;
     const TIn *x = (const TIn *)a.x, *dy = (const TIn *)a.dy;
     const TRes *s = (const TRes *)a.s, *dsum = (const TRes *)a.dsum;
     const TG *gate = (const TG *)a.gate;
     const bool post = a.post_weight != nullptr, pre = a.weight != nullptr, wants_gate = a.dgate != nullptr;
-    const long long per = a.rows / walk.groups, shared = gate ? a.rows / a.gate_rows : 1;
+    const long long per = a.rows / walk.groups;
+    const unsigned shared = gate ? (unsigned)(a.rows / a.gate_rows) : 1u;
+    const bool own_gate = gate && shared == 1;
+    __shared__ uint64_t full[kRingMost];
+    __shared__ int fail;
+    RowRing<5> ring((uint8_t *)acc_sm, full, &fail, plan);
+    int at_dy = 0, at_x = 0, at_d = 0, at_g = 0;
+    if constexpr (RING) {
+        ring.add<0>(s, pre ? D * sizeof(TRes) : 0);
+        at_dy = ring.add<1>(dy, pre ? D * sizeof(TIn) : 0);
+        at_x = ring.add<2>(x, D * sizeof(TIn));
+        at_d = ring.add<3>(dsum, dsum ? D * sizeof(TRes) : 0);
+        at_g = ring.add<4>(gate, own_gate ? D * sizeof(TG) : 0);
+        __syncthreads();
+    }
 
-    // the columns' sums: dweight, dpost_weight, dgate
-    float acc[ONE ? 3 : 1][kE];
-    auto add = [&](int which, int k, int i, float v) {
-        if constexpr (ONE) acc[which][i] += v;
-        else acc_sm[((which * VPT + k) * kE + i) * nt + threadIdx.x] += v;
+    const float inv_D = 1.f / (float)D;
+
+    // the columns' sums over rows: of dy s rho_s (dweight), of dn x rho_x (dpost_weight) and of
+    // dS x rho_x (dgate without its factor post_weight)
+    V8 acc[ONE ? 3 : 1];
+    auto kept = [&](int which, int k) -> float4 * {   // a thread's own 8 in shared memory
+        return (float4 *)acc_sm + ((which * VPT + k) * 2) * nt + threadIdx.x;
     };
-    auto sum_of = [&](int which, int k, float *v) {
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-            if constexpr (ONE) v[i] = acc[which][i];
-            else v[i] = acc_sm[((which * VPT + k) * kE + i) * nt + threadIdx.x];
+    auto add = [&](int which, int k, const V8 &v, float f) {
+        if constexpr (ONE) {
+            acc[which] = fma(v, f, acc[which]);
+        } else {
+            float4 *at = kept(which, k);
+            V8 t{{{at[0].x, at[0].y}, {at[0].z, at[0].w}, {at[nt].x, at[nt].y}, {at[nt].z, at[nt].w}}};
+            t = fma(v, f, t);
+            at[0] = make_float4(t.p[0].x, t.p[0].y, t.p[1].x, t.p[1].y);
+            at[nt] = make_float4(t.p[2].x, t.p[2].y, t.p[3].x, t.p[3].y);
         }
     };
+    auto sum_of = [&](int which, int k) {
+        if constexpr (ONE) return acc[which];
+        const float4 *at = kept(which, k);
+        return V8{{{at[0].x, at[0].y}, {at[0].z, at[0].w}, {at[nt].x, at[nt].y}, {at[nt].z, at[nt].w}}};
+    };
     auto clear = [&](int which) {
+        if constexpr (ONE) acc[which] = filled(0.f);
+        else
 #pragma unroll
-        for (int k = 0; k < VPT; ++k)
-#pragma unroll
-            for (int i = 0; i < kE; ++i) {
-                if constexpr (ONE) acc[which][i] = 0.f;
-                else acc_sm[((which * VPT + k) * kE + i) * nt + threadIdx.x] = 0.f;
-            }
+            for (int k = 0; k < VPT; ++k) kept(which, k)[0] = kept(which, k)[nt] = make_float4(0.f, 0.f, 0.f, 0.f);
     };
     clear(0);
     clear(1);
+    for (int i = 0; i < 2; ++i) {
+        clear_sums<3>(sm[i]);
+        clear_sums<1>(sm_x[i]);
+    }
+    __syncthreads();
 
-    float w[ONE ? VPT : 1][kE], wp[ONE ? VPT : 1][kE];
+    V8 w[1], wp[1];
     auto weights = [&](int k) {
         const int c = place<VEC>(k);
-        load_n<kE, VEC, ST>(a.weight + c, w[ONE ? k : 0], pre ? D - c : 0);
-        load_n<kE, VEC, ST>(a.post_weight + c, wp[ONE ? k : 0], post ? D - c : 0);
+        w[0] = load8<VEC>(a.weight + c, pre ? D - c : 0);
+        wp[0] = load8<VEC>(a.post_weight + c, post ? D - c : 0);
     };
-    if constexpr (ONE) weights(0);
+    if constexpr (ONE) {
+        weights(0);
+        if (!post) wp[0] = filled(1.f);
+    }
 
     Raw<TRes, kE, VEC> rs[VPT], rd[VPT];
     Raw<TIn, kE, VEC> ry[VPT], rx[VPT];
     Raw<TG, kE, VEC> rg[VPT];
     auto fetch = [&](int k, long long row) {   // row < 0: none
         const int c = place<VEC>(k), valid = row >= 0 ? D - c : 0;
-        rs[k].template load<VEC, ST>(s + row * D + c, pre ? valid : 0);
-        ry[k].template load<VEC, ST>(dy + row * D + c, pre ? valid : 0);
-        rx[k].template load<VEC, ST>(x + row * D + c, valid);
-        rd[k].template load<VEC, ST>(dsum + row * D + c, dsum ? valid : 0);
-        rg[k].template load<VEC, ST>(gate + row / shared * D + c, gate ? valid : 0);
+        take8<VEC>(rs[k], s + row * D + c, pre ? valid : 0);
+        take8<VEC>(ry[k], dy + row * D + c, pre ? valid : 0);
+        take8<VEC>(rx[k], x + row * D + c, valid);
+        take8<VEC>(rd[k], dsum + row * D + c, dsum ? valid : 0);
+        if (gate && row >= 0) take8<VEC>(rg[k], gate + (unsigned)row / shared * (long long)D + c, D - c);
+    };
+    long long held = -1;   // RING: the gate's row in rg
+    auto take = [&](int k, long long row) {   // from the ring
+        const int c = place<VEC>(k);
+        const uint8_t *in = ring.row();
+        take8<VEC>(rs[k], (const TRes *)in + c, pre ? D - c : 0);
+        take8<VEC>(ry[k], (const TIn *)(in + at_dy) + c, pre ? D - c : 0);
+        take8<VEC>(rx[k], (const TIn *)(in + at_x) + c, D - c);
+        take8<VEC>(rd[k], (const TRes *)(in + at_d) + c, dsum ? D - c : 0);
+        if (own_gate) take8<VEC>(rg[k], (const TG *)(in + at_g) + c, D - c);
+        else if (gate && (unsigned)row / shared != held) {
+            held = (unsigned)row / shared;
+            take8<VEC>(rg[k], gate + held * D + c, D - c);
+        }
     };
 
-    const long long runs = walk.groups * walk.cuts;
-    long long run = blockIdx.x, row = 0, end = 0;
-    auto open = [&]() {   // the run's rows
-        const long long g = run / walk.cuts, q = run - g * walk.cuts;
-        row = g * per + per * q / walk.cuts;
-        end = g * per + per * (q + 1) / walk.cuts;
+    // This block's rows one after another; `row` < 0 behind the last.
+    struct Rows {
+        long long run, row, end;
     };
-    open();
-    if constexpr (ONE) fetch(0, row);
+    const long long runs = walk.groups * walk.cuts;
+    auto open = [&](long long run) {
+        const long long g = run / walk.cuts, q = run - g * walk.cuts;
+        return run < runs ? Rows{run, g * per + per * q / walk.cuts, g * per + per * (q + 1) / walk.cuts}
+                          : Rows{run, -1, -1};
+    };
+    auto after = [&](Rows r) {
+        if (r.row >= 0 && ++r.row == r.end) r = open(r.run + gridDim.x);
+        return r;
+    };
+    Rows at = open(blockIdx.x), ahead = at;   // ahead: the next to go into the ring, in thread 0
+    if constexpr (RING) {
+        if (threadIdx.x == 0)
+            for (int i = 0; i < plan.stages && ahead.row >= 0; ++i, ahead = after(ahead)) ring.fill(i, ahead.row);
+    } else if constexpr (ONE) {
+        fetch(0, at.row);
+    }
     int turn = 0;
-    while (run < runs) {
+    while (at.row >= 0) {
         if (walk.summed) clear(2);
-        for (; row < end; ++row, turn ^= 1) {
-            if constexpr (!ONE)
+        const long long run = at.run;
+        for (; at.run == run && at.row >= 0; at = after(at), turn ^= 1) {
+            const long long row = at.row;
+            if constexpr (RING) take(0, row);
+            else if constexpr (!ONE)
 #pragma unroll
                 for (int k = 0; k < VPT; ++k) fetch(k, row);
-            float sums[3] = {0.f, 0.f, 0.f}, d[VPT][kE], xv[VPT][kE], sv[VPT][kE], gy[VPT][kE], gv[VPT][kE];
+            V8 d[VPT], xv[VPT], sv[VPT], gy[VPT], gv[VPT];
+            float2 ss = dup(0.f), sy = dup(0.f), xx = dup(0.f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 if constexpr (!ONE) weights(k);
-                rs[k].widen(sv[k]);
-                ry[k].widen(gy[k]);
-                rx[k].widen(xv[k]);
-                rd[k].widen(d[k]);
-                rg[k].widen(gv[k]);
-#pragma unroll
-                for (int i = 0; i < kE; ++i) {
-                    sums[0] = fmaf(sv[k][i], sv[k][i], sums[0]);
-                    sums[1] = fmaf(w[ONE ? k : 0][i] * gy[k][i], sv[k][i], sums[1]);
-                    sums[2] = fmaf(xv[k][i], xv[k][i], sums[2]);
-                    if (!gate) gv[k][i] = 1.f;
-                    else if (a.gate_sigmoid) gv[k][i] = sigmoid_fast(gv[k][i]);
+                xv[k] = widened(rx[k]);
+                d[k] = widened(rd[k]);
+                if (pre) {
+                    sv[k] = widened(rs[k]);
+                    gy[k] = widened(ry[k]);
+                    ss = dot(sv[k], sv[k], ss);
+                    sy = dot(w[0] * gy[k], sv[k], sy);
+                }
+                if (post) xx = dot(xv[k], xv[k], xx);
+                if (gate) {
+                    gv[k] = widened(rg[k]);
+                    if (a.gate_sigmoid) gv[k] = sigmoid(gv[k]);
                 }
             }
-            if constexpr (ONE) {
-                long long next = row + 1;
-                if (next == end) {   // the first row of this block's next run
-                    const long long u = run + gridDim.x, g = u / walk.cuts, q = u - g * walk.cuts;
-                    next = u < runs ? g * per + per * q / walk.cuts : -1;
+            float sums[3] = {ss.x + ss.y, sy.x + sy.y, xx.x + xx.y};
+            if constexpr (ONE && !RING) fetch(0, after(at).row);
+            row_sums<3>(sums, sm[turn], nwarps);   // two buffers: the next row's sums pass no reader of these
+            if constexpr (RING) {
+                if (threadIdx.x == 0 && ahead.row >= 0) {
+                    ring.fill(ring.s, ahead.row);
+                    ahead = after(ahead);
                 }
-                fetch(0, next);
+                ring.step();
             }
-            block_sum<3>(sums, sm[turn], nwarps);   // two buffers: the next row's sums pass no reader of these
-            const float rho_s = root(sums[0] / (float)D + a.eps), m_s = rho_s * rho_s * (sums[1] / (float)D);
-            const float rho_x = post ? root(sums[2] / (float)D + a.eps) : 1.f;
-            float dot = 0.f;
+            const float rho_s = root(fmaf(sums[0], inv_D, a.eps)), m_s = rho_s * rho_s * rho_s * (sums[1] * inv_D);
+            const float rho_x = post ? root(fmaf(sums[2], inv_D, a.eps)) : 1.f;
+            float2 dots = dup(0.f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int c = place<VEC>(k), at = ONE ? k : 0;
-                if constexpr (!ONE) weights(k);
-                float out[kE];
-#pragma unroll
-                for (int i = 0; i < kE; ++i) {
-                    if (pre) {
-                        add(0, k, i, gy[k][i] * (sv[k][i] * rho_s));
-                        d[k][i] = fmaf(rho_s, w[at][i] * gy[k][i] - sv[k][i] * m_s, d[k][i]);
-                    }
-                    out[i] = a.residual_scale * d[k][i];
+                const int c = place<VEC>(k);
+                if constexpr (!ONE) {
+                    weights(k);
+                    if (!post) wp[0] = filled(1.f);
                 }
-                if (a.dresidual) store_n<kE, VEC, ST>((TRes *)a.dresidual + row * D + c, out, D - c);
-#pragma unroll
-                for (int i = 0; i < kE; ++i) {
-                    const float xh = xv[k][i] * rho_x, n = post ? xh * wp[at][i] : xh;
-                    if (wants_gate) {
-                        const float dg = d[k][i] * n;
-                        if (walk.summed) add(2, k, i, dg);
-                        else out[i] = a.gate_sigmoid ? dg * (gv[k][i] * (1.f - gv[k][i])) : dg;
-                    }
-                    d[k][i] *= gv[k][i];
-                    if (post) {
-                        add(1, k, i, d[k][i] * xh);
-                        d[k][i] *= wp[at][i];
-                        dot = fmaf(d[k][i], xv[k][i], dot);
+                if (pre) {
+                    add(0, k, gy[k] * sv[k], rho_s);
+                    d[k] = fma(sv[k], -m_s, fma(w[0] * gy[k], rho_s, d[k]));
+                }
+                if (a.dresidual) store8<VEC>((TRes *)a.dresidual + row * D + c, d[k] * a.residual_scale, D - c);
+                V8 e = d[k] * xv[k];
+                if (wants_gate) {
+                    if (walk.summed) {
+                        add(2, k, e, rho_x);
+                    } else {
+                        V8 out = e * (wp[0] * rho_x);
+                        if (a.gate_sigmoid) out = out * (gv[k] * fma(gv[k], -1.f, filled(1.f)));
+                        store8<VEC>((TG *)a.dgate + row * D + c, out, D - c);
                     }
                 }
-                if (wants_gate && !walk.summed) store_n<kE, VEC, ST>((TG *)a.dgate + row * D + c, out, D - c);
+                if (gate) {
+                    e = e * gv[k];
+                    d[k] = d[k] * gv[k];
+                }
+                if (post) {
+                    add(1, k, e, rho_x);
+                    dots = dot(e, wp[0], dots);
+                    d[k] = d[k] * (wp[0] * rho_x);
+                }
             }
             float m_x = 0.f;
             if (post) {
-                block_sum<1>(&dot, sm[turn] + 96, nwarps);
-                m_x = rho_x * rho_x * (dot / (float)D);
+                m_x = dots.x + dots.y;
+                row_sums<1>(&m_x, sm_x[turn], nwarps);
+                m_x = rho_x * rho_x * rho_x * (m_x * inv_D);
             }
             if (a.dx)
 #pragma unroll
                 for (int k = 0; k < VPT; ++k) {
                     const int c = place<VEC>(k);
-#pragma unroll
-                    for (int i = 0; i < kE; ++i) d[k][i] = rho_x * (d[k][i] - xv[k][i] * m_x);
-                    store_n<kE, VEC, ST>((TIn *)a.dx + row * D + c, d[k], D - c);
+                    store8<VEC>((TIn *)a.dx + row * D + c, post ? fma(xv[k], -m_x, d[k]) : d[k], D - c);
                 }
         }
         if (walk.summed)
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                float v[kE];
-                sum_of(2, k, v);
                 const int c = place<VEC>(k);
-                store_n<kE, VEC, ST>(a.part_gate + run * D + c, v, D - c);
+                if constexpr (!ONE) {
+                    weights(k);
+                    if (!post) wp[0] = filled(1.f);
+                }
+                store8<VEC>(a.part_gate + run * D + c, sum_of(2, k) * wp[0], D - c);
             }
-        run += gridDim.x;
-        if (run < runs) open();
     }
+    if constexpr (RING) ring.close(a.status);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        float v[kE];
         const int c = place<VEC>(k);
-        if (pre) {
-            sum_of(0, k, v);
-            store_n<kE, VEC, ST>(a.part + (size_t)blockIdx.x * D + c, v, D - c);
-        }
-        if (post) {
-            sum_of(1, k, v);
-            store_n<kE, VEC, ST>(a.part_post + (size_t)blockIdx.x * D + c, v, D - c);
-        }
+        if (pre) store8<VEC>(a.part + (size_t)blockIdx.x * D + c, sum_of(0, k), D - c);
+        if (post) store8<VEC>(a.part_post + (size_t)blockIdx.x * D + c, sum_of(1, k), D - c);
     }
 }
 
@@ -256,16 +315,31 @@ template <typename TIn, typename TRes, typename TG, int VPT, bool VEC>
 cudaError_t bwd_run(const GatedNormBwdArgs &a, const Walk &walk, cudaStream_t st)
 {
     const int nt = norm_threads(a.D, VPT);
-    auto *k = gated_bwd_kernel<TIn, TRes, TG, VPT, VEC>;
+    cudaError_t e = cudaSuccess;
+    if constexpr (VPT == 1 && VEC)
+        if (a.D >= kRingLeast && a.rows > 2LL * walk.blocks) {
+            const bool own = a.gate && a.gate_rows == a.rows;
+            const RingPlan plan = ring_plan(a.D * (int)((a.weight ? sizeof(TRes) + sizeof(TIn) : 0) + sizeof(TIn) +
+                                                        (a.dsum ? sizeof(TRes) : 0) + (own ? sizeof(TG) : 0)),
+                                            kMostThreads / nt);
+            if (plan.stages) {
+                auto *k = gated_bwd_kernel<TIn, TRes, TG, 1, true, true>;
+                // always the most: the attribute is the kernel's, shared by all host threads
+                e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+                if (e != cudaSuccess) return e;
+                k<<<walk.blocks, nt, plan.stages * plan.stage, st>>>(a, walk, plan);
+                return cudaGetLastError();
+            }
+        }
+    auto *k = gated_bwd_kernel<TIn, TRes, TG, VPT, VEC, false>;
     size_t smem = 0;
     if constexpr (VPT > 1) {
-        // always the most: the attribute is the kernel's, shared by all host threads
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   3 * VPT * kE * kMostThreads * (int)sizeof(float));
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 3 * VPT * kE * kMostThreads * (int)sizeof(float));
         if (e != cudaSuccess) return e;
         smem = (size_t)3 * VPT * kE * nt * sizeof(float);
     }
-    k<<<walk.blocks, nt, smem, st>>>(a, walk);
+    k<<<walk.blocks, nt, smem, st>>>(a, walk, RingPlan{0, 0});
     return cudaGetLastError();
 }
 

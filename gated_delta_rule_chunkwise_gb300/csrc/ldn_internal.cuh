@@ -90,6 +90,7 @@ struct GatedNormArgs {
     long long rows, gate_rows;
     int D, gate_dtype, gate_sigmoid, dtype, res_dtype;
     float residual_scale, eps;
+    int *status;
 };
 
 struct GatedNormBwdArgs {
@@ -100,6 +101,7 @@ struct GatedNormBwdArgs {
     long long rows, gate_rows;
     int D, gate_dtype, gate_sigmoid, dtype, res_dtype;
     float residual_scale, eps;
+    int *status;
 };
 
 cudaError_t launch_gated_add_rmsnorm(const GatedNormArgs &a, cudaStream_t stream);

@@ -48,14 +48,21 @@ Source source(const void *p, long long ld, long long rows, int width, int dtype,
     return s;
 }
 
-cudaError_t prepare(const Source &s, int dtype, int es, char *ws, cudaStream_t st)
+// Lays out what is not taken where it lies.
+cudaError_t prepare(const Source &a, const Source &b, int dtype, int es, char *ws, cudaStream_t st)
 {
-    if (!s.copied) return cudaSuccess;
     if (dtype == LDN_F32) {
-        const long long ld = padded(s.width, 2);
-        return linear::split_rows((const float *)s.p, s.ld, ws + s.place, ld, ld * s.rows, s.rows, s.width, st);
+        auto split = [&](const Source &s) {
+            return linear::Split{(const float *)s.p, ws + s.place, s.ld, padded(s.width, 2), s.copied ? s.rows : 0, s.width};
+        };
+        return a.copied || b.copied ? linear::split_rows(split(a), split(b), st) : cudaSuccess;
     }
-    return linear::copy_rows(s.p, s.ld, ws + s.place, padded(s.width, es), s.rows, s.width, es, st);
+    for (const Source *s : {&a, &b}) {
+        if (!s->copied) continue;
+        const cudaError_t e = linear::copy_rows(s->p, s->ld, ws + s->place, padded(s->width, es), s->rows, s->width, es, st);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 Operand operand(const Source &s, int dtype, int es, const char *ws)
@@ -134,9 +141,7 @@ int forward(const void *x, long long ldx, const float *x_scale, const void *weig
     if (overlapping(in, out)) return LDN_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     char *ws = (char *)workspace;
-    cudaError_t e = prepare(f.x, dtype, es, ws, s);
-    if (e == cudaSuccess) e = prepare(f.w, dtype, es, ws, s);
-    if (e != cudaSuccess) return LDN_ERR_CUDA;
+    if (prepare(f.x, f.w, dtype, es, ws, s) != cudaSuccess) return LDN_ERR_CUDA;
     linear::Args a = product(N, rows, K, dtype, es);
     a.out = y;
     a.z = z;
@@ -256,15 +261,14 @@ extern "C" int ldn_linear_backward(const void *dy, const void *x, long long ldx,
     }
     const Operand dz = b.form ? Operand{ws + b.dz, N, rows, b.ld_dz, plane, planes ? linear::kPlanes : 1}
                               : Operand{dy, N, rows, N, 0, 1};
+    if (prepare(b.x, b.w, dtype, es, ws, s) != cudaSuccess) return LDN_ERR_CUDA;
     if (dx) {
-        if (prepare(b.w, dtype, es, ws, s) != cudaSuccess) return LDN_ERR_CUDA;
         linear::Args a = product(K, rows, N, dtype, es);
         a.out = dx;
         a.out_f32 = planes;
         if (linear_product_dx(operand(b.w, dtype, es, ws), dz, a, s) != cudaSuccess) return LDN_ERR_CUDA;
     }
     if (dweight) {
-        if (prepare(b.x, dtype, es, ws, s) != cudaSuccess) return LDN_ERR_CUDA;
         linear::Args a = product(K, N, rows, dtype, es);
         a.out = dweight;
         a.out_f32 = planes;

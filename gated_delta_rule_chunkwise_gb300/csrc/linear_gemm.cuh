@@ -41,8 +41,11 @@ template <int BN> struct Tile {
     static constexpr int kTmemCols = 2 * BN;   // two accumulators, a power of two of at least 32
 };
 
-// x Phi(x): Phi the normal distribution's integral.
-__device__ __forceinline__ float gelu(float x) { return x * fmaf(0.5f, erff(x * 0.70710678f), 0.5f); }
+__device__ __forceinline__ float gelu(float z)
+{
+    float bell;
+    return z * normal_integral(z, bell);
+}
 
 __device__ __forceinline__ float widened(float x) { return x; }
 __device__ __forceinline__ float widened(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -193,7 +196,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     // this block's k blocks: all, or its share
     const int b0 = (int)((long long)a.kblocks * rank / split), b1 = (int)((long long)a.kblocks * (rank + 1) / split);
 
-    if (threadIdx.x == 0) {
+    const bool one = elect_one();   // one thread of a warp, the same throughout
+    if (warp == 0 && one) {
         fail = 0;
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -205,6 +209,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         }
         mbar_init(&drain, 1);
         fence_mbar_init();
+    }
+    if (warp == 2 && one) {
         tma_prefetch_desc(&map_a);
         tma_prefetch_desc(&map_b);
     }
@@ -218,8 +224,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     const uint32_t tbase = tmem;
     Ring<S::kStages> ring;   // of this thread's loads or products
 
-    // one thread of a warp, the same throughout
-    const bool one = elect_one();
     if (warp == 0 && one) {
         // ---- loads
         bool go = true;

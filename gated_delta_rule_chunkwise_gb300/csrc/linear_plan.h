@@ -8,10 +8,10 @@ namespace linear {
 
 struct Plan { int bn, split; };
 
-// The cheapest of the cuts by a model of one block's time in cycles: a k block costs its products (2 a
-// column) or its loads (128-byte rows of both operands at 48 bytes a cycle and SM), whichever is
-// longer; a tile its pipeline's filling and, where the last one's epilogue is not covered, 12 a column;
-// the exchange of a split 3000.
+// The cheapest of the cuts by a model of one block's time in cycles, fitted to both sides of each choice
+// over 12 sizes from 1 x 4096 x 4096 to 2048 x 2048 x 2048: a k block costs its products (2 a column) and
+// 100, and 290 at least (its loads); a tile its pipeline's filling and 12 a column of epilogue that no
+// other tile's products cover; the exchange of a split 4500.
 inline Plan plan_for(long long ni, long long nj, int kblocks, int npairs, int narrowest, int sms)
 {
     Plan best{0, 1};
@@ -23,8 +23,8 @@ inline Plan plan_for(long long ni, long long nj, int kblocks, int npairs, int na
             if (split > 1 && (tiles * split > sms || split > kblocks)) break;
             const long long waves = split > 1 ? 1 : (tiles + sms - 1) / sms;
             const int blocks = (kblocks + split - 1) / split * npairs;
-            const double each = std::max(2.0 * bn, (128.0 + bn) * 128 / 48);
-            const double cost = waves * (blocks * each + 200) + 2000 + 12.0 * bn / split + (split > 1 ? 3000 : 0);
+            const double each = std::max(2.0 * bn + 100, 290.0);
+            const double cost = waves * (blocks * each + 200) + 12.0 * bn / split + (split > 1 ? 4500 : 0);
             if (cost < least) {
                 least = cost;
                 best = {bn, split};

@@ -22,7 +22,8 @@ copy_rows_kernel(const T *__restrict__ src, long long ld, T *__restrict__ dst, l
 // the nearest one to it, to what is left, and the rest.  What would round past the largest bf16 is cut
 // off instead.  What is not finite is in the fourth plane alone, the one that only the largest parts'
 // product reads: an infinity then meets no zero of the other operand's smaller planes.
-__device__ __forceinline__ void split_f32(float x, __nv_bfloat16 *p, long long plane)
+struct Parts { float hi, mid, lo, all; };
+__device__ __forceinline__ Parts parts(float x)
 {
     const float size = fabsf(x);
     const bool finite = size <= 3.402823466e38f;
@@ -30,19 +31,39 @@ __device__ __forceinline__ void split_f32(float x, __nv_bfloat16 *p, long long p
     const float hi = size < 3.38e38f ? __bfloat162float(__float2bfloat16_rn(v))
                                      : __uint_as_float(__float_as_uint(v) & 0xffff0000u);
     const float mid = __bfloat162float(__float2bfloat16_rn(v - hi));
-    p[0] = __float2bfloat16_rn(hi);
-    p[plane] = __float2bfloat16_rn(mid);
-    p[2 * plane] = __float2bfloat16_rn(v - hi - mid);
-    p[3 * plane] = __float2bfloat16_rn(finite ? hi : x);
+    return {hi, mid, v - hi - mid, finite ? hi : x};
 }
 
-__global__ void __launch_bounds__(kThreadsPrep)
-split_rows_kernel(const float *__restrict__ src, long long ld, __nv_bfloat16 *__restrict__ dst, long long ld_dst,
-                  long long plane, long long rows, int width)
+// N neighbours of a row into its planes (N = 4, 8: as vectors).
+template <int N> __device__ __forceinline__ void put_planes(const float *x, __nv_bfloat16 *p, long long plane)
 {
-    const int c = blockIdx.x * kThreadsPrep + threadIdx.x;
-    if (c >= width) return;
-    for (long long r = blockIdx.y; r < rows; r += gridDim.y) split_f32(src[r * ld + c], dst + r * ld_dst + c, plane);
+    float v[4][N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const Parts q = parts(x[i]);
+        v[0][i] = q.hi; v[1][i] = q.mid; v[2][i] = q.lo; v[3][i] = q.all;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) store_n<N, N != 1>(p + k * plane, v[k]);
+}
+
+// A block takes the rows that `rows_of` blocks share, 4 neighbours a thread where every row of src
+// begins at a 16-byte boundary.
+template <int N>
+__global__ void __launch_bounds__(kThreadsPrep)
+split_rows_kernel(const Split a, const Split b, int blocks_a)
+{
+    const bool first = (int)blockIdx.y < blocks_a;
+    const Split &s = first ? a : b;
+    const int c = (blockIdx.x * kThreadsPrep + threadIdx.x) * N;
+    const long long plane = s.ld_dst * s.rows;
+    if (c >= s.width) return;
+    for (long long r = first ? blockIdx.y : blockIdx.y - blocks_a; r < s.rows;
+         r += first ? blocks_a : gridDim.y - blocks_a) {
+        float v[N];
+        load_n<N, N != 1>(s.src + r * s.ld + c, v);
+        put_planes<N>(v, (__nv_bfloat16 *)s.dst + r * s.ld_dst + c, plane);
+    }
 }
 
 // act'(z)
@@ -52,32 +73,57 @@ __device__ __forceinline__ float slope(float z, int activation)
         const float g = sigmoid_fast(z);
         return g * fmaf(z, 1.f - g, 1.f);
     }
-    // Phi(z) + z phi(z)
-    return fmaf(0.5f, erff(z * 0.70710678f), 0.5f) + z * 0.39894228f * ex2(-0.5f * kLog2e * z * z);
+    float bell;   // Phi(z) + z phi(z)
+    const float phi = normal_integral(z, bell);
+    return fmaf(z * 0.39894228f, bell, phi);
 }
 
 // dz = dy act'(z), as bf16 rows or planes of them, and each run of rows' share of its column sums.
 // dz is rounded to bf16 for the tensor cores; the sums take it before.
-template <typename TY, typename TZ, bool PLANES>
+// N neighbours a thread (8 where rows are whole vectors, 1 otherwise); a block takes 32 N columns and 8
+// rows at a time, and adds the sums of its eight warps in a fixed order.
+template <typename TY, typename TZ, bool PLANES, int N>
 __global__ void __launch_bounds__(kThreadsPrep)
 dz_kernel(const TY *__restrict__ dy, const TZ *__restrict__ z, __nv_bfloat16 *__restrict__ dz, long long ld_dz,
           long long plane, float *__restrict__ part, long long rows, int n, int activation, long long run)
 {
-    const int c = blockIdx.x * kThreadsPrep + threadIdx.x;
-    if (c >= n) return;
+    constexpr int WARPS = kThreadsPrep / 32;
+    constexpr bool VEC = N != 1;
+    __shared__ float sm[WARPS][32 * N + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = (blockIdx.x * 32 + lane) * N;
     const long long r0 = blockIdx.y * run, r1 = min(rows, r0 + run);
-    float sum = 0.f;
-#pragma unroll 4
-    for (long long r = r0; r < r1; ++r) {
-        float v = (float)dy[r * n + c];
-        if (z) v *= slope((float)z[r * n + c], activation);
-        sum += v;
-        if (dz) {
-            if constexpr (PLANES) split_f32(v, dz + r * ld_dz + c, plane);
-            else dz[r * ld_dz + c] = __float2bfloat16_rn(v);
+    float sum[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum[i] = 0.f;
+    if (c < n)
+#pragma unroll 2
+        for (long long r = r0 + warp; r < r1; r += WARPS) {
+            float v[N];
+            load_n<N, VEC>(dy + r * n + c, v);
+            if (z) {
+                float q[N];
+                load_n<N, VEC>(z + r * n + c, q);
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] *= slope(q[i], activation);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) sum[i] += v[i];
+            if (dz) {
+                if constexpr (PLANES) put_planes<N>(v, dz + r * ld_dz + c, plane);
+                else store_n<N, VEC>(dz + r * ld_dz + c, v);
+            }
         }
+    if (!part) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sm[warp][lane * N + i] = sum[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * N; i += kThreadsPrep) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) t += sm[w][i];
+        const int at = blockIdx.x * 32 * N + i;
+        if (at < n) part[(long long)blockIdx.y * n + at] = t;
     }
-    if (part) part[(long long)blockIdx.y * n + c] = sum;
 }
 
 constexpr int kSumRows = 32;
@@ -118,42 +164,55 @@ cudaError_t copy_rows(const void *src, long long ld, void *dst, long long ld_dst
     return cudaGetLastError();
 }
 
-cudaError_t split_rows(const float *src, long long ld, void *dst, long long ld_dst, long long plane, long long rows,
-                       int width, cudaStream_t st)
+cudaError_t split_rows(const Split &a, const Split &b, cudaStream_t st)
 {
-    split_rows_kernel<<<grid_for(rows, width), kThreadsPrep, 0, st>>>(src, ld, (__nv_bfloat16 *)dst, ld_dst, plane, rows,
-                                                                      width);
+    auto vec = [](const Split &s) {
+        return s.rows == 0 || (((uintptr_t)s.src & 15) == 0 && s.width % 4 == 0 && (s.ld % 4 == 0 || s.rows == 1));
+    };
+    const int n = vec(a) && vec(b) ? 4 : 1, widest = std::max(a.rows ? a.width : 1, b.rows ? b.width : 1);
+    const int strips = (widest + kThreadsPrep * n - 1) / (kThreadsPrep * n);
+    // a few rows a block, so that the card is full and no block ends at once
+    auto blocks = [&](const Split &s) { return (int)std::min<long long>(s.rows, std::max(1, 152 * 16 / strips)); };
+    const dim3 grid(strips, blocks(a) + blocks(b));
+    if (n == 4) split_rows_kernel<4><<<grid, kThreadsPrep, 0, st>>>(a, b, blocks(a));
+    else split_rows_kernel<1><<<grid, kThreadsPrep, 0, st>>>(a, b, blocks(a));
     return cudaGetLastError();
 }
 
 // Rows of a run, so that the blocks fill the card a few times and the sums' last step stays short.
 static long long dz_run(long long rows, int n)
 {
-    const long long strips = (n + kThreadsPrep - 1) / kThreadsPrep;
-    const long long runs = std::max(1LL, std::min(1024LL, 152 * 8 / strips));
-    return std::max(8LL, (rows + runs - 1) / runs);
+    const long long strips = (n + 255) / 256;   // of columns, of a vectored block
+    const long long runs = std::max(1LL, std::min(256LL, 152 * 8 / strips));
+    return std::max(32LL, (rows + runs - 1) / runs);
 }
 long long dz_runs(long long rows, int n) { return rows ? (rows + dz_run(rows, n) - 1) / dz_run(rows, n) : 0; }
+
+template <typename TY, typename TZ, bool PLANES>
+static void run_dz(const void *dy, const void *z, __nv_bfloat16 *dz, long long ld_dz, long long plane, float *part,
+                   long long rows, int n, int activation, cudaStream_t st)
+{
+    const long long run = dz_run(rows, n);
+    const unsigned runs = (unsigned)dz_runs(rows, n);
+    const bool vec = n % 8 == 0 && (((uintptr_t)dy | (uintptr_t)z) & 15) == 0;
+    if (vec)
+        dz_kernel<TY, TZ, PLANES, 8><<<dim3((n + 255) / 256, runs), kThreadsPrep, 0, st>>>(
+            (const TY *)dy, (const TZ *)z, dz, ld_dz, plane, part, rows, n, activation, run);
+    else
+        dz_kernel<TY, TZ, PLANES, 1><<<dim3((n + 31) / 32, runs), kThreadsPrep, 0, st>>>(
+            (const TY *)dy, (const TZ *)z, dz, ld_dz, plane, part, rows, n, activation, run);
+}
 
 cudaError_t form_dz(const void *dy, int dy_f32, const void *z, int activation, void *dz, long long ld_dz, long long plane,
                     bool planes, float *part, void *dbias, int bias_f32, long long rows, int n, cudaStream_t st)
 {
-    const int runs = (int)dz_runs(rows, n);
-    const long long run = dz_run(rows, n);
-    const dim3 grid((n + kThreadsPrep - 1) / kThreadsPrep, runs);
     __nv_bfloat16 *d = (__nv_bfloat16 *)dz;
-    if (planes)
-        dz_kernel<float, float, true><<<grid, kThreadsPrep, 0, st>>>((const float *)dy, (const float *)z, d, ld_dz, plane,
-                                                                     part, rows, n, activation, run);
-    else if (dy_f32)
-        dz_kernel<float, __nv_bfloat16, false><<<grid, kThreadsPrep, 0, st>>>(
-            (const float *)dy, (const __nv_bfloat16 *)z, d, ld_dz, plane, part, rows, n, activation, run);
-    else
-        dz_kernel<__nv_bfloat16, __nv_bfloat16, false><<<grid, kThreadsPrep, 0, st>>>(
-            (const __nv_bfloat16 *)dy, (const __nv_bfloat16 *)z, d, ld_dz, plane, part, rows, n, activation, run);
-    cudaError_t e = cudaGetLastError();
+    if (planes) run_dz<float, float, true>(dy, z, d, ld_dz, plane, part, rows, n, activation, st);
+    else if (dy_f32) run_dz<float, __nv_bfloat16, false>(dy, z, d, ld_dz, plane, part, rows, n, activation, st);
+    else run_dz<__nv_bfloat16, __nv_bfloat16, false>(dy, z, d, ld_dz, plane, part, rows, n, activation, st);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !part) return e;
-    bias_sum_kernel<<<(n + 31) / 32, dim3(32, kSumRows), 0, st>>>(part, dbias, bias_f32, runs, n);
+    bias_sum_kernel<<<(n + 31) / 32, dim3(32, kSumRows), 0, st>>>(part, dbias, bias_f32, (int)dz_runs(rows, n), n);
     return cudaGetLastError();
 }
 

@@ -345,7 +345,8 @@ extern "C" int ldn_gated_add_rmsnorm(const void *x, const void *residual, const 
     const Span out[] = {{y, n * es}, {residual_out, n * rs}};
     if (overlapping(in, out)) return LDN_ERR_INVALID_ARG;
     const GatedNormArgs a{x, residual, gate, post_weight, weight, y, residual_out, rows, gate_rows, D, gate_dtype,
-                          gate_sigmoid, dtype, residual_dtype, residual_scale, eps};
+                          gate_sigmoid, dtype, residual_dtype, residual_scale, eps, status_word_ptr()};
+    if (!a.status) return LDN_ERR_CUDA;
     return status_of(launch_gated_add_rmsnorm(a, (cudaStream_t)stream));
 }
 
@@ -385,6 +386,7 @@ extern "C" int ldn_gated_add_rmsnorm_backward(const void *dy, const void *x, con
     if (overlapping(in, out)) return LDN_ERR_INVALID_ARG;
     const GatedNormBwdArgs a{dy, x, s, dsum, gate, post_weight, weight, dx, dresidual, dgate, dpost_weight, dweight,
                              (float *)workspace, nullptr, nullptr, rows, gate_rows, D, gate_dtype, gate_sigmoid,
-                             dtype, residual_dtype, residual_scale, eps};
+                             dtype, residual_dtype, residual_scale, eps, status_word_ptr()};
+    if (!a.status) return LDN_ERR_CUDA;
     return status_of(launch_gated_add_rmsnorm_bwd(a, (cudaStream_t)stream));
 }

@@ -677,7 +677,7 @@ size_t ldn_gated_add_rmsnorm_backward_workspace_size(long long rows, int D, long
  * fewer digits.
  * workspace: ldn_linear_workspace_size bytes, 256-byte aligned (0: none is used): what the
  * tensor cores cannot take as it lies in memory is laid out there, fp32 operands and rows that
- * do not start at 16-byte boundaries.  One launch, and one for each operand so laid out.
+ * do not start at 16-byte boundaries.  One launch, and one or two for what is so laid out.
  * The result is the same bit for bit on every call.
  */
 typedef enum { LDN_ACT_NONE = 0, LDN_ACT_SILU = 1, LDN_ACT_GELU = 2 } ldn_activation;
