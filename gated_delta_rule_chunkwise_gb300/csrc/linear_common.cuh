@@ -19,12 +19,13 @@ struct Args {
     int chunk;                 // k blocks that are summed in tensor memory before they join the sum in registers
     int npairs;                // pairs of planes, four bits each: plane of A, plane of B
     uint32_t pairs_a, pairs_b;
-    int split;
+    int bn, split, stages;     // the cut (linear_plan.h) and the stages of its ring
     // epilogue
     void *out, *z;             // [nj][ni]
     const void *bias, *residual;
     const float *scale_i, *scale_j;
     int out_f32, z_f32, bias_f32, activation;
+    int staged;                // bf16 results leave through shared memory (linear_gemm.cuh)
     int *status;
 };
 

@@ -9,14 +9,21 @@
 // full lanes, and the weight streams through once.  For the gradients A is the weight or x transposed
 // and B dz: "MN-major" operands, whose contiguous index is i or j, are taken as they lie in memory.
 //
-// A block takes 128 x BN of the output: one warp issues the TMA loads of 128-byte wide k blocks, one
+// A block takes 128 x bn of the output: one warp issues the TMA loads of 128-byte wide k blocks, one
 // thread the products, eight warps the epilogue of the tile before, out of the other half of tensor
-// memory.  Few tiles: `split` blocks of a cluster share a tile's k blocks, add their parts through
-// distributed shared memory in a fixed order and take a share of the columns each.
+// memory.  Many tiles (PAIR): two blocks of a cluster take 256 x bn together, each loading its half of
+// either operand, so that a product's operands cross into an SM once for twice the output.  Few tiles:
+// `split` blocks of a cluster share a tile's k blocks; each writes its part of every column to the block
+// whose share the column is, which adds the parts in a fixed order.
 //
 // The tensor cores cut off what an addition to their accumulators rounds away (an fp32 sum over 4096
 // was 4.5e-6 of its norm off, twice that over 8192).  Where the output keeps such digits (PROMOTE: fp32
 // outputs) the sum is taken over chunks of k, whose results are added in registers, rounded to nearest.
+//
+// bf16 results leave through shared memory (`staged`): fragments of 8 x 8 are written there transposed,
+// 128 lanes x 32 columns at a time, and one TMA store takes them.  Written by the lanes, 2 bytes each, they
+// hold the products up, whose operands pass the same memory port (8192 x 512 to 4096: 44 us; 21 without
+// any stores).  A bf16 residual comes in the same way, into the place of the results.
 //
 // fp32 inputs come as planes of bf16 (linear_prep.cu): a chunk then runs over pairs of planes, the
 // smallest products first.
@@ -33,13 +40,13 @@ using namespace sm100;
 constexpr int kLanes = 128, kEpilogue = 256, kThreads = 64 + kEpilogue;
 constexpr long long kWaitCycles = 4000000000ll;   // 2 s
 
-// A tile's place in shared memory: 128-byte wide blocks of A, then of B.
-template <int BN> struct Tile {
-    static constexpr int kABytes = kLanes * 128, kBBytes = BN * 128, kStage = kABytes + kBBytes;
-    static constexpr int kStages = 204800 / kStage < 10 ? 204800 / kStage : 10;
-    static constexpr int kSmem = kStages * kStage + 1024;
-    static constexpr int kTmemCols = 2 * BN;   // two accumulators, a power of two of at least 32
-};
+// A block's stages in shared memory: 128-byte wide blocks of A, then of B, at multiples of 1024 bytes.
+constexpr int kABytes = kLanes * 128, kMostStages = 10, kStageBytes = 224 * 1024;   // with what follows them
+__host__ __device__ inline int stage_bytes(int columns) { return kABytes + columns * 128; }   // of B in this block
+// Two buffers for each half of the epilogue's warps: 32 columns of 128 lanes in bf16, as two boxes of 64.
+constexpr int kBuffer = 32 * kLanes * 2, kStaging = 4 * kBuffer;
+// Room for the parts of a split tile: bn columns of 128 lanes.
+__host__ __device__ inline int part_bytes(int bn, int split) { return split > 1 ? bn * kLanes * 4 : 0; }
 
 __device__ __forceinline__ float gelu(float z)
 {
@@ -118,24 +125,24 @@ __device__ __forceinline__ void finish(const Args &a, float *v, long long i, lon
     else finish_as<EPI, F8, N, false>(a, v, i, j, (int)min(a.nj - j, (long long)most));
 }
 
-// Tiles in the order that blocks take them: groups of 16 tiles of lanes, through all columns, so that
+// Tiles in the order that blocks take them: groups of about 2048 lanes, through all columns, so that
 // the tiles in flight share operands in L2.
+// (A product of at most 2^40 elements has fewer than 2^30 tiles: 32-bit divisions, 64-bit ones of three
+// roles took a call 1 us.)
 struct Place { int mi, nj; };
-__device__ __forceinline__ Place place_of(long long t, int mt, int nt)
+__device__ __forceinline__ Place place_of(unsigned t, unsigned mt, unsigned nt, unsigned group)
 {
-    constexpr int G = 16;
-    const long long per = (long long)G * nt;
-    const int g = (int)(t / per), rest = (int)(t - g * per), width = min(G, mt - g * G);
-    return {g * G + rest % width, rest / width};
+    const unsigned per = group * nt, g = t / per, width = min(group, mt - g * group), rest = t - g * per;
+    return {(int)(g * group + rest % width), (int)(rest / width)};
 }
 
 // A place in the ring of stages, and how often it went round.
-template <int STAGES> struct Ring {
-    int s = 0;
+struct Ring {
+    int stages, s = 0;
     uint32_t round = 0;
     __device__ __forceinline__ void step()
     {
-        if (++s == STAGES) {
+        if (++s == stages) {
             s = 0;
             ++round;
         }
@@ -170,42 +177,48 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity)
 // Columns c, c + 1, ... of this warp's lanes of tensor memory.
 template <int C> __device__ __forceinline__ void load_columns(uint32_t at, float *v)
 {
-    if constexpr (C == 8) tmem_ld8(at, v);
-    else
 #pragma unroll
-        for (int q = 0; q < C; q += 16) tmem_ld16(at + q, v + q);
+    for (int q = 0; q < C; q += 16) tmem_ld16(at + q, v + q);
     tmem_ld_wait();
 }
 
-template <int BN, bool AMN, bool BMN, bool F8, bool EPI, bool PROMOTE>
+template <bool AMN, bool BMN, bool F8, bool EPI, bool PROMOTE, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Args a)
+gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+            const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_z,
+            const __grid_constant__ CUtensorMap map_residual, const Args a)
 {
-    using S = Tile<BN>;
     extern __shared__ uint8_t raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[S::kStages], empty[S::kStages], done[2], drained[2], drain;
+    __shared__ uint64_t full[kMostStages], empty[kMostStages], done[2], drained[2], loaded[2], drain;
     __shared__ uint32_t tmem;
     __shared__ int fail;
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-    const int split = a.split;
-    const uint32_t rank = split > 1 ? cluster_ctarank() : 0;
-    constexpr int kElems = F8 ? 128 : 64;   // elements of a k block
-    const int mt = (int)((a.ni + kLanes - 1) / kLanes), nt = (int)((a.nj + BN - 1) / BN);
-    const long long tiles = (long long)mt * nt, first = blockIdx.x / split, step = gridDim.x / split;
-    // this block's k blocks: all, or its share
-    const int b0 = (int)((long long)a.kblocks * rank / split), b1 = (int)((long long)a.kblocks * (rank + 1) / split);
-
     const bool one = elect_one();   // one thread of a warp, the same throughout
+    const int split = PAIR ? 1 : a.split, bn = a.bn, stages = a.stages, cols = PAIR ? bn / 2 : bn,
+              stage = stage_bytes(cols);
+    const uint32_t rank = PAIR || split > 1 ? cluster_ctarank() : 0;
+    constexpr int kElems = F8 ? 128 : 64;                  // elements of a k block
+    constexpr int kTileLanes = PAIR ? 2 * kLanes : kLanes;
+    const int mt = (int)((a.ni + kTileLanes - 1) / kTileLanes), nt = (int)((a.nj + bn - 1) / bn);
+    constexpr int kGroup = 2048 / kTileLanes;
+    const int blocks = PAIR ? 2 : split;                   // that share a tile
+    const unsigned tiles = (unsigned)mt * nt, first = blockIdx.x / (unsigned)blocks, step = gridDim.x / (unsigned)blocks;
+    // this block's k blocks: all, or its share
+    const int b0 = PAIR ? 0 : (int)((unsigned)a.kblocks * rank / split),
+              b1 = PAIR ? a.kblocks : (int)((unsigned)a.kblocks * (rank + 1) / split);
+    const uint32_t tcols = bn <= 16 ? 32 : bn <= 32 ? 64 : bn <= 64 ? 128 : bn <= 128 ? 256 : 512;   // two accumulators
+
     if (warp == 0 && one) {
         fail = 0;
-        for (int s = 0; s < S::kStages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&done[i], 1);
-            mbar_init(&drained[i], kEpilogue);
+            mbar_init(&drained[i], (PAIR ? 2 : 1) * (kEpilogue / 32));
+            mbar_init(&loaded[i], 1);
         }
         mbar_init(&drain, 1);
         fence_mbar_init();
@@ -215,20 +228,34 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         tma_prefetch_desc(&map_b);
     }
     if (warp == 1) {
-        tmem_alloc(&tmem, S::kTmemCols);
-        tmem_relinquish();
+        if constexpr (PAIR) {
+            tmem_alloc_pair(&tmem, tcols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(&tmem, tcols);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    if constexpr (PAIR) {
+        cluster_sync();   // the other block's barriers are there
+    } else {
+        // the loads need nothing but the barriers, which their own thread made
+        __syncwarp();
+        if (warp == 0) named_arrive(1, kThreads);
+        else named_sync(1, kThreads);
+        if (split > 1) cluster_arrive_relaxed();
+    }
     tc_fence_after();
-    const uint32_t tbase = tmem;
-    Ring<S::kStages> ring;   // of this thread's loads or products
+    const uint32_t tbase = warp == 0 ? 0 : tmem;
+    Ring ring{stages};   // of this thread's loads or products
 
     if (warp == 0 && one) {
         // ---- loads
         bool go = true;
-        for (long long t = first; go && t < tiles; t += step) {
-            const Place p = place_of(t, mt, nt);
+        for (unsigned t = first; go && t < tiles; t += step) {
+            const Place p = place_of(t, mt, nt, kGroup);
+            const int ia = p.mi * kTileLanes + (PAIR ? rank * kLanes : 0), jb = p.nj * bn + (PAIR ? rank * cols : 0);
             for (int c0 = b0; go && c0 < b1; c0 += a.chunk) {
                 const int c1 = min(b1, c0 + a.chunk);
                 for (int pair = 0; go && pair < a.npairs; ++pair) {
@@ -240,35 +267,42 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                             go = false;
                             break;
                         }
-                        uint8_t *da = sm + s * S::kStage, *db = da + S::kABytes;
-                        mbar_arrive_expect_tx(&full[s], S::kStage);
+                        uint8_t *da = sm + s * stage, *db = da + kABytes;
+                        // a pair's bytes are all counted on the first block's barrier
+                        if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * stage);
+                        const uint32_t bar = PAIR ? mapa_shared(smem_u32(&full[s]), 0) : 0;
+                        auto load = [&](uint8_t *d, const CUtensorMap *m, int c, int r, int plane) {
+                            if constexpr (PAIR) tma_load_3d_pair(d, m, bar, c, r, plane);
+                            else tma_load_3d(d, m, &full[s], c, r, plane);
+                        };
                         if constexpr (AMN) {
 #pragma unroll
-                            for (int b = 0; b < kLanes / 64; ++b)
-                                tma_load_3d(da + b * 8192, &map_a, &full[s], p.mi * kLanes + 64 * b, at, pa);
+                            for (int b = 0; b < kLanes / 64; ++b) load(da + b * 8192, &map_a, ia + 64 * b, at, pa);
                         } else {
-                            tma_load_3d(da, &map_a, &full[s], at, p.mi * kLanes, pa);
+                            load(da, &map_a, at, ia, pa);
                         }
                         if constexpr (BMN) {
-#pragma unroll
-                            for (int b = 0; b < BN / 64; ++b)
-                                tma_load_3d(db + b * 8192, &map_b, &full[s], p.nj * BN + 64 * b, at, pb);
+                            for (int b = 0; b < cols / 64; ++b) load(db + b * 8192, &map_b, jb + 64 * b, at, pb);
                         } else {
-                            tma_load_3d(db, &map_b, &full[s], at, p.nj * BN, pb);
+                            load(db, &map_b, at, jb, pb);
                         }
                     }
                 }
             }
         }
-    } else if (warp == 1 && one) {
+    } else if (warp == 1 && one && (!PAIR || rank == 0)) {
         // ---- products
-        constexpr uint32_t idesc = idesc_f16kind_f32(kLanes, BN, AMN, BMN, F8 ? kMmaE4M3 : kMmaBF16);
+        const uint32_t idesc = idesc_f16kind_f32(kTileLanes, bn, AMN, BMN, F8 ? kMmaE4M3 : kMmaBF16);
         const uint32_t at = smem_u32(sm);
         const uint64_t desc_a = AMN ? mnmajor_desc(at, 64, 0) : kmajor_desc(at, kLanes, 0),
-                       desc_b = BMN ? mnmajor_desc(at + S::kABytes, 64, 0) : kmajor_desc(at + S::kABytes, BN, 0);
+                       desc_b = BMN ? mnmajor_desc(at + kABytes, 64, 0) : kmajor_desc(at + kABytes, cols, 0);
+        auto commit = [&](uint64_t *bar) {
+            if constexpr (PAIR) umma_commit_pair(bar);
+            else umma_commit(bar);
+        };
         int turn = 0;
         bool go = true;
-        for (long long t = first; go && t < tiles; t += step)
+        for (unsigned t = first; go && t < tiles; t += step)
             for (int c0 = b0; go && c0 < b1; c0 += a.chunk, ++turn) {
                 const int acc = turn & 1, n = (min(b1, c0 + a.chunk) - c0) * a.npairs;
                 if (!wait(&drained[acc], ((uint32_t)(turn >> 1) & 1u) ^ 1u)) {
@@ -277,7 +311,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tbase + acc * BN;
+                const uint32_t d = tbase + acc * (tcols / 2);
                 for (int k = 0; k < n; ++k, ring.step()) {
                     const int s = ring.s;
                     if (!wait(&full[s], ring.round & 1u)) {
@@ -287,40 +321,173 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     }
                     tc_fence_after();
                     // a stage and a step of 32 bytes of k further: 16-byte units in the low bits
-                    const uint64_t sa = desc_a + s * (S::kStage / 16), sb = desc_b + s * (S::kStage / 16);
+                    const uint64_t sa = desc_a + (uint32_t)(s * stage) / 16, sb = desc_b + (uint32_t)(s * stage) / 16;
 #pragma unroll
                     for (uint32_t q = 0; q < 4; ++q) {
                         const uint64_t da = sa + q * (AMN ? 128 : 2), db = sb + q * (BMN ? 128 : 2);
-                        if constexpr (F8) umma_f8(d, da, db, idesc, k > 0 || q > 0);
-                        else umma_bf16(d, da, db, idesc, k > 0 || q > 0);
+                        const uint32_t more = k > 0 || q > 0;
+                        if constexpr (PAIR && F8) umma_f8_pair(d, da, db, idesc, more);
+                        else if constexpr (PAIR) umma_bf16_pair(d, da, db, idesc, more);
+                        else if constexpr (F8) umma_f8(d, da, db, idesc, more);
+                        else umma_bf16(d, da, db, idesc, more);
                     }
-                    umma_commit(&empty[s]);
+                    commit(&empty[s]);
                 }
-                if (go) umma_commit(&done[acc]);
+                if (go) commit(&done[acc]);
             }
+    } else if (!PROMOTE && warp >= 2 && a.staged) {
+        // ---- epilogue through shared memory: this warp's 32 lanes, and every other 32 columns
+        const uint32_t quad = warp & 3, half = (uint32_t)(warp - 2) >> 2, bar = 2 + half, row = lane >> 2;
+        const bool leader = quad == 2 && one;   // warps 2 and 6
+        uint8_t *buffers = sm + stages * stage + half * 2 * kBuffer;
+        // where a lane's row of a matrix lies: token lane % 8 (of 8), features 8 (lane / 8) on of this warp's
+        const uint32_t chunk = (quad & 1) * 4 + (lane >> 3), at_row = (quad >> 1) * (kBuffer / 2) + (lane & 7) * 128 +
+                                                                      ((chunk ^ (lane & 7)) << 4);
+        int turn = 0, used = 0, late = 0;
+        uint32_t loads = 0;
+        for (unsigned t = first; t < tiles; t += step, ++turn) {
+            const int acc = turn & 1;
+            const Place p = place_of(t, mt, nt, kGroup);
+            const int i0 = p.mi * kTileLanes + (PAIR ? rank * kLanes : 0), j0 = p.nj * bn;
+            float bias[4], si[4];
+            if constexpr (EPI)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const long long i = i0 + (long long)(quad * 32 + 8 * g + row);
+                    bias[g] = a.bias && i < a.ni ? __bfloat162float(((const __nv_bfloat16 *)a.bias)[i]) : 0.f;
+                    if constexpr (F8) si[g] = i < a.ni ? a.scale_i[i] : 0.f;
+                }
+            // a wait that ran out ends no loop whose barriers other warps are in: what follows is not waited for
+            if (!late && !wait(&done[acc], (uint32_t)(turn >> 1) & 1u)) fail = late = 1;
+            tc_fence_after();
+            const uint32_t from = tbase + (quad << 21) + acc * (tcols / 2);
+            for (int c = half * 32; c < bn && j0 + c < a.nj; c += 64) {
+                uint8_t *buf = buffers + (used & 1) * kBuffer;
+                const int j = j0 + c;
+                if (leader) {
+                    bulk_wait_read_but_one();   // what last left this buffer has been read
+                    if (EPI && a.residual) {
+                        uint8_t *to = buf;
+                        if (a.z) {   // z takes this one
+                            bulk_wait_read_all();
+                            to = buffers + (~used & 1) * kBuffer;
+                        }
+                        mbar_arrive_expect_tx(&loaded[half], kBuffer);
+                        tma_load_3d(to, &map_residual, &loaded[half], i0, j, 0);
+                        tma_load_3d(to + kBuffer / 2, &map_residual, &loaded[half], i0 + 64, j, 0);
+                    }
+                }
+                float v[32];   // [16 lanes][8 columns][..]: as tmem_ld_frag32 has them
+                tmem_ld_frag32(from + c, v);
+                tmem_ld_frag32(from + (16u << 16) + c, v + 16);
+                tmem_ld_wait();
+                // register r is of columns 8 (r / 4 % 4) + 2 (lane % 4) + r % 2 and features 8 (2 (r / 16) + r / 2 % 2)
+                auto send = [&](const CUtensorMap *m, uint8_t *b) {
+                    const uint32_t to = smem_u32(b) + at_row;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            w[g] = bf16x2_pack(v[16 * (g >> 1) + 4 * q + 2 * (g & 1)], v[16 * (g >> 1) + 4 * q + 2 * (g & 1) + 1]);
+                        stsm_x4_trans(to + q * 1024, w);
+                    }
+                    fence_proxy_async_smem();
+                    named_sync(bar, kEpilogue / 2);
+                    if (leader) {
+                        tma_store_3d(m, b, i0, j, 0);
+                        tma_store_3d(m, b + kBuffer / 2, i0 + 64, j, 0);
+                        bulk_commit();
+                    }
+                    ++used;
+                };
+                if constexpr (EPI) {
+                    if constexpr (F8)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const long long col = j + 8 * q + 2 * (lane & 3) + e;
+                                const float sj = col < a.nj ? a.scale_j[col] : 0.f;
+#pragma unroll
+                                for (int g = 0; g < 4; ++g) v[16 * (g >> 1) + 4 * q + 2 * (g & 1) + e] *= si[g] * sj;
+                            }
+                    if (a.bias)
+#pragma unroll
+                        for (int r = 0; r < 32; ++r) v[r] += bias[2 * (r / 16) + r / 2 % 2];
+                    if (a.z) {
+                        named_sync(bar, kEpilogue / 2);   // the buffer is free
+                        send(&map_z, buf);
+                        buf = buffers + (used & 1) * kBuffer;
+                        if (leader) bulk_wait_read_but_one();
+                    }
+                    if (a.activation == LDN_ACT_SILU) {
+#pragma unroll
+                        for (int r = 0; r < 32; ++r) v[r] *= sigmoid_fast(v[r]);
+                    } else if (a.activation == LDN_ACT_GELU) {
+#pragma unroll
+                        for (int r = 0; r < 32; ++r) v[r] = gelu(v[r]);
+                    }
+                    if (a.residual) {
+                        if (!late && !wait(&loaded[half], loads & 1u)) fail = late = 1;
+                        ++loads;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t w[4];
+                            ldsm_x4_trans(w, buf + at_row + q * 1024);
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                float f[2];
+                                bf16x2_widen(w[g], f);
+                                v[16 * (g >> 1) + 4 * q + 2 * (g & 1)] += f[0];
+                                v[16 * (g >> 1) + 4 * q + 2 * (g & 1) + 1] += f[1];
+                            }
+                        }
+                    }
+                }
+                if (!EPI || !a.residual) named_sync(bar, kEpilogue / 2);   // the buffer is free
+                send(&map_out, buf);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (one) {
+                if constexpr (PAIR) mbar_remote_arrive(mapa_shared(smem_u32(&drained[acc]), 0));
+                else mbar_arrive(&drained[acc]);
+            }
+        }
+        if (leader) bulk_wait_all();   // nothing is left in the buffers
     } else if (warp >= 2) {
-        // ---- epilogue: this warp's 32 lanes and half of the columns
-        constexpr int H = BN / 2, C = H < 32 ? H : 32;
+        // ---- epilogue: this warp's 32 lanes and half of the columns, in units of 16
         const uint32_t quad = warp & 3, half = (uint32_t)(warp - 2) >> 2;
-        float *part = (float *)sm;   // a split tile's parts, once every stage is free
+        const int per = (bn / 2 + 15) & ~15, h0 = half * per, h = min(per, bn - h0), share = bn / split;
+        // a split tile's parts: of each block, its columns of this block's share
+        const uint32_t part = smem_u32(sm) + stages * stage + (rank * share * kLanes + quad * 32 + lane) * 4;
         int turn = 0;
-        bool go = true;
-        for (long long t = first; go && t < tiles; t += step) {
-            const Place p = place_of(t, mt, nt);
-            const long long i = (long long)p.mi * kLanes + quad * 32 + lane, j = (long long)p.nj * BN + half * H;
-            // columns [c, c + C) of this half, done
-            auto leave = [&](float *v, int c) {
+        bool go = true, met = false;
+        for (unsigned t = first; go && t < tiles; t += step) {
+            const Place p = place_of(t, mt, nt, kGroup);
+            const long long i = (long long)p.mi * kTileLanes + (PAIR ? rank * kLanes : 0) + quad * 32 + lane,
+                            j = (long long)p.nj * bn + h0;
+            // C columns from c on, done
+            auto leave = [&](auto n, float *v, int c) {
+                constexpr int C = decltype(n)::value;
                 if (split == 1) {
                     finish<EPI, F8, C>(a, v, i, j + c);
                 } else {
-#pragma unroll
-                    for (int q = 0; q < C; ++q) part[(half * H + c + q) * kLanes + quad * 32 + lane] = v[q];
+                    if (!met) cluster_wait();   // the other blocks have started
+                    met = true;
+                    for (int q = 0; q < C; ++q) {
+                        const int col = h0 + c + q, to = col / share;
+                        st_shared_cluster(mapa_shared(part, to) + (col - to * share) * kLanes * 4, v[q]);
+                    }
                 }
             };
-            float sum[PROMOTE ? H : 1];
+            using C32 = std::integral_constant<int, 32>;
+            using C16 = std::integral_constant<int, 16>;
+            float sum[PROMOTE ? 128 : 16];
             if constexpr (PROMOTE)
 #pragma unroll
-                for (int c = 0; c < H; ++c) sum[c] = 0.f;
+                for (int c = 0; c < 128; ++c) sum[c] = 0.f;
             for (int c0 = b0; c0 < b1; c0 += a.chunk, ++turn) {
                 const int acc = turn & 1;
                 if (!wait(&done[acc], (uint32_t)(turn >> 1) & 1u)) {
@@ -329,81 +496,97 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     break;
                 }
                 tc_fence_after();
-                const uint32_t row = tbase + (quad << 21) + acc * BN + half * H;
+                const uint32_t row = tbase + (quad << 21) + acc * (tcols / 2) + h0;
                 if constexpr (PROMOTE) {
 #pragma unroll
-                    for (int c = 0; c < H; c += C) {
-                        float v[C];
-                        load_columns<C>(row + c, v);
+                    for (int c = 0; c < 128; c += 16)
+                        if (c < h) {
+                            float v[16];
+                            load_columns<16>(row + c, v);
 #pragma unroll
-                        for (int q = 0; q < C; ++q) sum[c + q] += v[q];
-                    }
+                            for (int q = 0; q < 16; ++q) sum[c + q] += v[q];
+                        }
                 } else {
+                    int c = 0;
 #pragma unroll 1
-                    for (int c = 0; c < H; c += C) {
-                        float v[C];
-                        load_columns<C>(row + c, v);
-                        leave(v, c);
+                    for (; c + 32 <= h; c += 32) {
+                        float v[32];
+                        load_columns<32>(row + c, v);
+                        leave(C32(), v, c);
+                    }
+                    if (c < h) {
+                        float v[16];
+                        load_columns<16>(row + c, v);
+                        leave(C16(), v, c);
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(&drained[acc]);
+                __syncwarp();
+                if (one) {
+                    if constexpr (PAIR) mbar_remote_arrive(mapa_shared(smem_u32(&drained[acc]), 0));
+                    else mbar_arrive(&drained[acc]);
+                }
             }
             if constexpr (PROMOTE)
                 if (go)
+#pragma unroll 1
+                    for (int c = 0; c < h; c += 16) {   // the first 16, and the others move up
+                        leave(C16(), sum, c);
 #pragma unroll
-                    for (int c = 0; c < H; c += C) leave(sum + c, c);
+                        for (int q = 0; q < 112; ++q) sum[q] = sum[q + 16];
+                    }
         }
+        if (split > 1 && !met) cluster_wait();
     }
     __syncwarp();
-    if (split > 1) {
-        cluster_sync();
-        constexpr int U = 8;   // columns at a time: as many reads of each block are on their way together
-        const uint32_t quad = warp & 3, half = (uint32_t)(warp - 2) >> 2;
-        const int mine = BN / 2 / split;   // columns of a half of this block's share
-        const Place p = place_of(first, mt, nt);
-        const long long i = (long long)p.mi * kLanes + quad * 32 + lane, j = (long long)p.nj * BN;
-        const uint32_t at = smem_u32(sm) + (quad * 32 + lane) * 4;
-        const int c0 = (rank * 2 + half) * mine, c1 = warp >= 2 ? (int)min((long long)c0 + mine, a.nj - j) : c0;
-        // Only what is stored is read: a store waits for its value, so no read is under way when this
-        // block says that the others may leave.
-        if (i < a.ni)
+    if (!PAIR && split > 1) {
+        if (warp < 2) cluster_wait();
+        cluster_sync();   // every part is where it is added
+        if (warp >= 2) {
+            constexpr int U = 4;   // columns at a time
+            const uint32_t quad = warp & 3, half = (uint32_t)(warp - 2) >> 2;
+            const int share = bn / split;
+            const Place p = place_of(first, mt, nt, kGroup);
+            const long long i = (long long)p.mi * kLanes + quad * 32 + lane,
+                            j = (long long)p.nj * bn + rank * share;
+            const float *part = (const float *)(sm + stages * stage) + quad * 32 + lane;
 #pragma unroll 1
-            for (int c = c0; c < c1; c += U) {
+            for (int c = half * U; c < share; c += 2 * U) {
                 float v[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) v[u] = 0.f;
 #pragma unroll 2
-                for (int q = 0; q < split; ++q) {
-                    const uint32_t from = mapa_shared(at, q);
+                for (int q = 0; q < split; ++q)
 #pragma unroll
                     for (int u = 0; u < U; ++u)
-                        if (c + u < c1) v[u] += __uint_as_float(ld_shared_cluster_u32(from + (c + u) * kLanes * 4));
-                }
-                finish<EPI, F8, U>(a, v, i, j + c, c1 - c);
+                        if (c + u < share) v[u] += part[(q * share + c + u) * kLanes];
+                finish<EPI, F8, U>(a, v, i, j + c, share - c);
             }
-        __syncwarp();
-        cluster_sync();
+        }
     }
     tc_fence_before();
     __syncthreads();
     if (fail) {
         // what is under way ends before the memory it uses is given back (bounded)
-        if (warp == 1 && one) {
-            umma_commit(&drain);
+        if (warp == 1 && one && (!PAIR || rank == 0)) {
+            if constexpr (PAIR) umma_commit_pair(&drain);
+            else umma_commit(&drain);
             wait(&drain, 0);
         }
         if (warp == 0 && one) {
             atomicOr(a.status, 1 << LDN_ERR_TIMEOUT);
-            for (int s = 0; s < S::kStages; ++s)
-            {
+            for (int s = 0; s < stages; ++s) {
                 const uint32_t loads = ring.round + (s < ring.s);   // that went into stage s
-                if (loads) wait(&full[s], (loads - 1) & 1u);
+                if (loads && (!PAIR || rank == 0)) wait(&full[s], (loads - 1) & 1u);
             }
         }
         __syncthreads();
     }
-    if (warp == 1) tmem_dealloc(tbase, S::kTmemCols);
+    if constexpr (PAIR) cluster_sync();   // neither block's barriers or memory are used any more
+    if (warp == 1) {
+        if constexpr (PAIR) tmem_dealloc_pair(tbase, tcols);
+        else tmem_dealloc(tbase, tcols);
+    }
 }
 
 }  // namespace linear

@@ -19,34 +19,47 @@ inline int sm_count()
     return n[dev];
 }
 
-template <int BN, bool AMN, bool BMN, bool F8, bool EPI, bool PROMOTE>
-cudaError_t launch(const Operand &A, const Operand &B, const Args &a, int sms, cudaStream_t st)
+template <bool AMN, bool BMN, bool F8, bool EPI, bool PROMOTE, bool PAIR>
+cudaError_t launch(const Operand &A, const Operand &B, Args a, int sms, cudaStream_t st)
 {
-    using S = Tile<BN>;
-    CUtensorMap ma, mb;
+    const long long n = a.ni;
+    auto vectors = [n](const void *p) { return ((uintptr_t)p & 15) == 0 && n % 8 == 0; };   // or null
+    a.staged = !PROMOTE && !a.out_f32 && a.split == 1 && a.bn % 32 == 0 && a.nj >= 32 && vectors(a.out) &&
+               vectors(a.residual) && vectors(a.z);
+    const int cols = PAIR ? a.bn / 2 : a.bn, stage = stage_bytes(cols),
+              beside = a.staged ? kStaging : part_bytes(a.bn, a.split);
+    a.stages = std::min(kMostStages, (kStageBytes - beside) / stage);
+    CUtensorMap ma, mb, mo, mz, mr;
     // one row has no distance to a next one: any multiple of 16 bytes will do
     auto ld = [](const Operand &o) { return (uint64_t)(o.rows == 1 ? (o.width + 15) / 16 * 16 : o.ld); };
     auto plane = [&](const Operand &o) { return (uint64_t)(o.planes == 1 ? ld(o) : o.plane); };
     if (!make_tmap_rows(&ma, A.p, A.width, A.rows, A.planes, ld(A), plane(A), AMN ? 64 : kLanes, F8) ||
-        !make_tmap_rows(&mb, B.p, B.width, B.rows, B.planes, ld(B), plane(B), BMN ? 64 : BN, F8))
+        !make_tmap_rows(&mb, B.p, B.width, B.rows, B.planes, ld(B), plane(B), BMN ? 64 : cols, F8))
         return cudaErrorInvalidValue;
-    auto *k = gemm_kernel<BN, AMN, BMN, F8, EPI, PROMOTE>;
-    // always the same value: a call between another's two lines changes nothing
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    mo = mz = mr = ma;   // where they are not used
+    auto result = [&](CUtensorMap *m, const void *p) {
+        return !p || make_tmap_rows(m, p, a.ni, a.nj, 1, a.ni, a.ni, 32, false);
+    };
+    if (a.staged && (!result(&mo, a.out) || !result(&mz, a.z) || !result(&mr, a.residual))) return cudaErrorInvalidValue;
+    auto *k = gemm_kernel<AMN, BMN, F8, EPI, PROMOTE, PAIR>;
+    // always the most: a call between another's two lines changes nothing
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageBytes + 1024);
     if (e != cudaSuccess) return e;
-    const long long tiles = ((a.ni + kLanes - 1) / kLanes) * ((a.nj + BN - 1) / BN);
+    constexpr int kTileLanes = PAIR ? 2 * kLanes : kLanes;
+    const long long tiles = ((a.ni + kTileLanes - 1) / kTileLanes) * ((a.nj + a.bn - 1) / a.bn);
+    const int blocks = PAIR ? 2 : a.split;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.split > 1 ? tiles * a.split : std::min<long long>(tiles, sms)));
+    cfg.gridDim = dim3((unsigned)(blocks * (a.split > 1 ? tiles : std::min<long long>(tiles, sms / blocks))));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.dynamicSmemBytes = a.stages * stage + beside + 1024;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = a.split;
+    attr[0].val.clusterDim.x = blocks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = a.split > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, k, ma, mb, a);
+    cfg.numAttrs = blocks > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, k, ma, mb, mo, mz, mr, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -57,16 +70,12 @@ cudaError_t run(const Operand &A, const Operand &B, Args a, cudaStream_t st)
     const int sms = sm_count();
     a.status = status_word_ptr();
     if (!sms || !a.status) return cudaErrorUnknown;
-    const Plan p = plan_for(a.ni, a.nj, a.kblocks, a.npairs, BMN ? 64 : 16, sms);
+    const Plan p = plan_for(a.ni, a.nj, a.kblocks, a.npairs, BMN, sms);
+    a.bn = p.bn;
     a.split = p.split;
     if (!PROMOTE) a.chunk = a.kblocks;
-    if constexpr (!BMN) {
-        if (p.bn == 16) return launch<16, AMN, BMN, F8, EPI, PROMOTE>(A, B, a, sms, st);
-        if (p.bn == 32) return launch<32, AMN, BMN, F8, EPI, PROMOTE>(A, B, a, sms, st);
-    }
-    if (p.bn == 64) return launch<64, AMN, BMN, F8, EPI, PROMOTE>(A, B, a, sms, st);
-    if (p.bn == 128) return launch<128, AMN, BMN, F8, EPI, PROMOTE>(A, B, a, sms, st);
-    return launch<256, AMN, BMN, F8, EPI, PROMOTE>(A, B, a, sms, st);
+    if (p.pair) return launch<AMN, BMN, F8, EPI, PROMOTE, true>(A, B, a, sms, st);
+    return launch<AMN, BMN, F8, EPI, PROMOTE, false>(A, B, a, sms, st);
 }
 
 // k blocks of a chunk: 512 elements of 16 bits keep the sum within 5e-7 of its norm, and with fp32's six

@@ -141,21 +141,25 @@ def test_plans_fill_their_tiles(tmp_path):
     src.write_text('#include <cstdio>\n#include "linear_plan.h"\nint main(){ long long i, j; int k, p, n;\n'
                    'while (scanf("%lld %lld %d %d %d", &i, &j, &k, &p, &n) == 5) {\n'
                    'ldn::linear::Plan q = ldn::linear::plan_for(i, j, k, p, n, 152);\n'
-                   'printf("%d %d\\n", q.bn, q.split); } }\n')
+                   'printf("%d %d %d\\n", q.bn, q.split, q.pair); } }\n')
     exe = str(tmp_path / "plan")
     subprocess.run(["g++", "-std=c++17", "-I", csrc, str(src), "-o", exe], check=True)
     r = np.random.default_rng(0)
     cases = [(int(np.exp(r.uniform(0, np.log(20000)))), int(np.exp(r.uniform(0, np.log(20000)))),
-              int(np.exp(r.uniform(0, np.log(300)))), int(r.choice([1, 6])), int(r.choice([16, 64]))) for _ in range(3000)]
-    cases += [(1, 1, 1, 1, 16), (MOST, 1, 1, 1, 16), (1, MOST, 1, 1, 64), (1, 1, 1 << 25, 6, 16)]
+              int(np.exp(r.uniform(0, np.log(300)))), int(r.choice([1, 6])), int(r.integers(2))) for _ in range(3000)]
+    cases += [(1, 1, 1, 1, 0), (MOST, 1, 1, 1, 0), (1, MOST, 1, 1, 1), (1, 1, 1 << 25, 6, 0)]
     out = subprocess.run([exe], input="\n".join(" ".join(map(str, c)) for c in cases), capture_output=True, text=True,
                          check=True).stdout.split()
-    assert len(out) == 2 * len(cases)
-    for (i, j, k, p, n), bn, split in zip(cases, map(int, out[::2]), map(int, out[1::2])):
-        assert bn in (16, 32, 64, 128, 256) and bn >= n and split in (1, 2, 4, 8)
-        tiles = -(-i // 128) * -(-j // bn)
+    assert len(out) == 3 * len(cases)
+    for (i, j, k, p, mn), bn, split, pair in zip(cases, *(map(int, out[q::3]) for q in range(3))):
+        assert 16 <= bn <= 256 and bn % (64 if mn else 32 if bn > 16 else 16) == 0 and split in (1, 2, 4, 8)
+        stage = 128 * (128 + (bn // 2 if pair else bn))
+        parts = bn * 512 if split > 1 else 0
+        assert stage % 1024 == 0 and 3 <= (200 * 1024 - parts) // stage     # a ring beside the parts
         if split > 1:
-            assert split <= k and tiles * split <= 152 and bn // 2 >= split
+            assert not pair and split <= k and -(-i // 128) * -(-j // bn) * split <= 152 and bn % (2 * split) == 0
+        if pair:
+            assert bn % (128 if mn else 32) == 0
 
 
 # ---- the references' gradients ----
