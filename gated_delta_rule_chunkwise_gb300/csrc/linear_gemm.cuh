@@ -43,8 +43,9 @@ constexpr long long kWaitCycles = 4000000000ll;   // 2 s
 // A block's stages in shared memory: 128-byte wide blocks of A, then of B, at multiples of 1024 bytes.
 constexpr int kABytes = kLanes * 128, kMostStages = 10, kStageBytes = 224 * 1024;   // with what follows them
 __host__ __device__ inline int stage_bytes(int columns) { return kABytes + columns * 128; }   // of B in this block
-// Two buffers for each half of the epilogue's warps: 32 columns of 128 lanes in bf16, as two boxes of 64.
-constexpr int kBuffer = 32 * kLanes * 2, kStaging = 4 * kBuffer;
+// Two pairs of buffers for each half of the epilogue's warps, one filled while the other is read: 32
+// columns of 128 lanes in bf16, as two boxes of 64.
+constexpr int kBuffer = 32 * kLanes * 2, kStaging = 8 * kBuffer;
 // Room for the parts of a split tile: bn columns of 128 lanes.
 __host__ __device__ inline int part_bytes(int bn, int split) { return split > 1 ? bn * kLanes * 4 : 0; }
 
@@ -339,12 +340,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         // ---- epilogue through shared memory: this warp's 32 lanes, and every other 32 columns
         const uint32_t quad = warp & 3, half = (uint32_t)(warp - 2) >> 2, bar = 2 + half, row = lane >> 2;
         const bool leader = quad == 2 && one;   // warps 2 and 6
-        uint8_t *buffers = sm + stages * stage + half * 2 * kBuffer;
+        uint8_t *const both = sm + stages * stage + half * 4 * kBuffer;
         // where a lane's row of a matrix lies: token lane % 8 (of 8), features 8 (lane / 8) on of this warp's
         const uint32_t chunk = (quad & 1) * 4 + (lane >> 3), at_row = (quad >> 1) * (kBuffer / 2) + (lane & 7) * 128 +
                                                                       ((chunk ^ (lane & 7)) << 4);
-        int turn = 0, used = 0, late = 0;
+        int turn = 0, late = 0, used = 0;
         uint32_t loads = 0;
+        // a pair of buffers is filled between two barriers: with 64 columns, or with z and y of 32
+        const int width = EPI && a.z ? 32 : 64;
         for (unsigned t = first; t < tiles; t += step, ++turn) {
             const int acc = turn & 1;
             const Place p = place_of(t, mt, nt, kGroup);
@@ -361,92 +364,101 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             if (!late && !wait(&done[acc], (uint32_t)(turn >> 1) & 1u)) fail = late = 1;
             tc_fence_after();
             const uint32_t from = tbase + (quad << 21) + acc * (tcols / 2);
-            for (int c = half * 32; c < bn && j0 + c < a.nj; c += 64) {
-                uint8_t *buf = buffers + (used & 1) * kBuffer;
-                const int j = j0 + c;
+#pragma unroll 1
+            for (int c0 = half * width; c0 < bn && j0 + c0 < a.nj; c0 += 2 * width, used ^= 1) {
+                uint8_t *buffers = both + used * 2 * kBuffer;
+                const int slices = width == 64 && c0 + 32 < bn ? 2 : 1;
+                // 8 KB for 32 columns from j on, as two boxes of 64 lanes
+                auto store = [&](const CUtensorMap *m, uint8_t *b, int j) {
+                    tma_store_3d(m, b, i0, j, 0);
+                    tma_store_3d(m, b + kBuffer / 2, i0 + 64, j, 0);
+                };
                 if (leader) {
-                    bulk_wait_read_but_one();   // what last left this buffer has been read
+                    bulk_wait_read_but_one();   // what last left these buffers has been read
                     if (EPI && a.residual) {
-                        uint8_t *to = buf;
-                        if (a.z) {   // z takes this one
-                            bulk_wait_read_all();
-                            to = buffers + (~used & 1) * kBuffer;
+                        mbar_arrive_expect_tx(&loaded[half], slices * kBuffer);
+                        for (int q = 0; q < slices; ++q) {
+                            uint8_t *b = buffers + q * kBuffer;
+                            tma_load_3d(b, &map_residual, &loaded[half], i0, j0 + c0 + 32 * q, 0);
+                            tma_load_3d(b + kBuffer / 2, &map_residual, &loaded[half], i0 + 64, j0 + c0 + 32 * q, 0);
                         }
-                        mbar_arrive_expect_tx(&loaded[half], kBuffer);
-                        tma_load_3d(to, &map_residual, &loaded[half], i0, j, 0);
-                        tma_load_3d(to + kBuffer / 2, &map_residual, &loaded[half], i0 + 64, j, 0);
                     }
                 }
-                float v[32];   // [16 lanes][8 columns][..]: as tmem_ld_frag32 has them
-                tmem_ld_frag32(from + c, v);
-                tmem_ld_frag32(from + (16u << 16) + c, v + 16);
-                tmem_ld_wait();
-                // register r is of columns 8 (r / 4 % 4) + 2 (lane % 4) + r % 2 and features 8 (2 (r / 16) + r / 2 % 2)
-                auto send = [&](const CUtensorMap *m, uint8_t *b) {
-                    const uint32_t to = smem_u32(b) + at_row;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            w[g] = bf16x2_pack(v[16 * (g >> 1) + 4 * q + 2 * (g & 1)], v[16 * (g >> 1) + 4 * q + 2 * (g & 1) + 1]);
-                        stsm_x4_trans(to + q * 1024, w);
-                    }
-                    fence_proxy_async_smem();
-                    named_sync(bar, kEpilogue / 2);
-                    if (leader) {
-                        tma_store_3d(m, b, i0, j, 0);
-                        tma_store_3d(m, b + kBuffer / 2, i0 + 64, j, 0);
-                        bulk_commit();
-                    }
-                    ++used;
-                };
-                if constexpr (EPI) {
-                    if constexpr (F8)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const long long col = j + 8 * q + 2 * (lane & 3) + e;
-                                const float sj = col < a.nj ? a.scale_j[col] : 0.f;
-#pragma unroll
-                                for (int g = 0; g < 4; ++g) v[16 * (g >> 1) + 4 * q + 2 * (g & 1) + e] *= si[g] * sj;
-                            }
-                    if (a.bias)
-#pragma unroll
-                        for (int r = 0; r < 32; ++r) v[r] += bias[2 * (r / 16) + r / 2 % 2];
-                    if (a.z) {
-                        named_sync(bar, kEpilogue / 2);   // the buffer is free
-                        send(&map_z, buf);
-                        buf = buffers + (used & 1) * kBuffer;
-                        if (leader) bulk_wait_read_but_one();
-                    }
-                    if (a.activation == LDN_ACT_SILU) {
-#pragma unroll
-                        for (int r = 0; r < 32; ++r) v[r] *= sigmoid_fast(v[r]);
-                    } else if (a.activation == LDN_ACT_GELU) {
-#pragma unroll
-                        for (int r = 0; r < 32; ++r) v[r] = gelu(v[r]);
-                    }
-                    if (a.residual) {
-                        if (!late && !wait(&loaded[half], loads & 1u)) fail = late = 1;
-                        ++loads;
+#pragma unroll 1
+                for (int slice = 0; slice < slices; ++slice) {
+                    const int c = c0 + 32 * slice;
+                    const uint32_t to = smem_u32(buffers + slice * kBuffer) + at_row;
+                    // v[r]: column 8 (r / 4 % 4) + 2 (lane % 4) + r % 2, feature 8 (2 (r / 16) + r / 2 % 2) + lane / 4
+                    float v[32];
+                    tmem_ld_frag32(from + c, v);
+                    tmem_ld_frag32(from + (16u << 16) + c, v + 16);
+                    tmem_ld_wait();
+                    auto put32 = [&](uint32_t at) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint32_t w[4];
-                            ldsm_x4_trans(w, buf + at_row + q * 1024);
 #pragma unroll
                             for (int g = 0; g < 4; ++g) {
-                                float f[2];
-                                bf16x2_widen(w[g], f);
-                                v[16 * (g >> 1) + 4 * q + 2 * (g & 1)] += f[0];
-                                v[16 * (g >> 1) + 4 * q + 2 * (g & 1) + 1] += f[1];
+                                const float *f = v + 16 * (g >> 1) + 4 * q + 2 * (g & 1);
+                                w[g] = bf16x2_pack(f[0], f[1]);
+                            }
+                            stsm_x4_trans(at + q * 1024, w);
+                        }
+                    };
+                    if constexpr (EPI) {
+                        if constexpr (F8)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const long long col = j0 + (long long)c + 8 * q + 2 * (lane & 3) + e;
+                                    const float sj = col < a.nj ? a.scale_j[col] : 0.f;
+#pragma unroll
+                                    for (int g = 0; g < 4; ++g) v[16 * (g >> 1) + 4 * q + 2 * (g & 1) + e] *= si[g] * sj;
+                                }
+                        if (a.bias)
+#pragma unroll
+                            for (int r = 0; r < 32; ++r) v[r] += bias[2 * (r / 16) + r / 2 % 2];
+                    }
+                    if (slice == 0 && !(EPI && a.residual)) named_sync(bar, kEpilogue / 2);   // the buffers are free
+                    if constexpr (EPI) {
+                        if (__builtin_expect(a.z != nullptr, 0)) put32(to + kBuffer);
+                        if (__builtin_expect(a.activation == LDN_ACT_SILU, 0)) {
+#pragma unroll
+                            for (int r = 0; r < 32; ++r) v[r] *= sigmoid_fast(v[r]);
+                        } else if (__builtin_expect(a.activation == LDN_ACT_GELU, 0)) {
+#pragma unroll
+                            for (int r = 0; r < 32; ++r) v[r] = gelu(v[r]);
+                        }
+                        if (__builtin_expect(a.residual != nullptr, 0)) {
+                            if (slice == 0) {
+                                if (!late && !wait(&loaded[half], loads & 1u)) fail = late = 1;
+                                ++loads;
+                            }
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint32_t w[4];
+                                ldsm_x4_trans(w, buffers + slice * kBuffer + at_row + q * 1024);
+#pragma unroll
+                                for (int g = 0; g < 4; ++g) {
+                                    float f[2];
+                                    bf16x2_widen(w[g], f);
+                                    v[16 * (g >> 1) + 4 * q + 2 * (g & 1)] += f[0];
+                                    v[16 * (g >> 1) + 4 * q + 2 * (g & 1) + 1] += f[1];
+                                }
                             }
                         }
                     }
+                    put32(to);
                 }
-                if (!EPI || !a.residual) named_sync(bar, kEpilogue / 2);   // the buffer is free
-                send(&map_out, buf);
+                fence_proxy_async_smem();
+                named_sync(bar, kEpilogue / 2);
+                if (leader) {
+                    store(&map_out, buffers, j0 + c0);
+                    if (slices == 2) store(&map_out, buffers + kBuffer, j0 + c0 + 32);
+                    if (EPI && a.z) store(&map_z, buffers + kBuffer, j0 + c0);
+                    bulk_commit();
+                }
             }
             tc_fence_before();
             __syncwarp();

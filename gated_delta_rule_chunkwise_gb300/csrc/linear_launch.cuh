@@ -24,7 +24,7 @@ cudaError_t launch(const Operand &A, const Operand &B, Args a, int sms, cudaStre
 {
     const long long n = a.ni;
     auto vectors = [n](const void *p) { return ((uintptr_t)p & 15) == 0 && n % 8 == 0; };   // or null
-    a.staged = !PROMOTE && !a.out_f32 && a.split == 1 && a.bn % 32 == 0 && a.nj >= 32 && vectors(a.out) &&
+    a.staged = !PROMOTE && !a.out_f32 && a.split == 1 && a.bn % 32 == 0 && !(a.z && a.residual) && vectors(a.out) &&
                vectors(a.residual) && vectors(a.z);
     const int cols = PAIR ? a.bn / 2 : a.bn, stage = stage_bytes(cols),
               beside = a.staged ? kStaging : part_bytes(a.bn, a.split);
