@@ -53,6 +53,8 @@ gated_kernel(const GatedNormArgs a, const RingPlan plan)
         at_g = ring.add<2>(gate, own_gate ? D * sizeof(TG) : 0);
     }
     for (int i = 0; i < 4; ++i) clear_sums<1>(sm[i >> 1][i & 1]);
+    sm100::griddep_wait();   // before any memory of another kernel
+    sm100::griddep_launch_dependents();
     V8 wp[KEEP ? VPT : 1], w[KEEP ? VPT : 1];
     if constexpr (KEEP)
 #pragma unroll
@@ -178,13 +180,11 @@ cudaError_t gated_run(const GatedNormArgs &a, bool vec, cudaStream_t st)
                 // always the most: the attribute is the kernel's, shared by all host threads
                 const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
                 if (e != cudaSuccess) return e;
-                k<<<grid, block, plan.stages * plan.stage, st>>>(a, plan);
-                return cudaGetLastError();
+                return launch_after(k, grid, block, plan.stages * plan.stage, st, a, plan);
             }
         }
-    if (vec) gated_kernel<TIn, TRes, TG, VPT, true, false><<<grid, block, 0, st>>>(a, RingPlan{0, 0});
-    else gated_kernel<TIn, TRes, TG, VPT, false, false><<<grid, block, 0, st>>>(a, RingPlan{0, 0});
-    return cudaGetLastError();
+    return launch_after(vec ? gated_kernel<TIn, TRes, TG, VPT, true, false> : gated_kernel<TIn, TRes, TG, VPT, false, false>,
+                        grid, block, 0, st, a, RingPlan{0, 0});
 }
 
 template <typename TIn, typename TRes, typename TG>

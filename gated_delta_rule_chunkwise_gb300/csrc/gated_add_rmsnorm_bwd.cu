@@ -100,6 +100,8 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
 #pragma unroll
             for (int k = 0; k < VPT; ++k) kept(which, k)[0] = kept(which, k)[nt] = make_float4(0.f, 0.f, 0.f, 0.f);
     };
+    sm100::griddep_wait();   // before any memory of another kernel
+    sm100::griddep_launch_dependents();
     clear(0);
     clear(1);
     for (int i = 0; i < 2; ++i) {
@@ -281,6 +283,8 @@ __global__ void __launch_bounds__(32 * kSumRows)
 gated_sum_kernel(const GatedNormBwdArgs a, const Walk walk)
 {
     __shared__ float sm[kSumRows][33];
+    sm100::griddep_wait();
+    sm100::griddep_launch_dependents();
     const int c = blockIdx.x * 32 + threadIdx.x, y = threadIdx.y, D = a.D;
     const long long which = blockIdx.y;
     for (long long u = which; u < 2 + (walk.summed ? walk.groups : 0); u += gridDim.y) {
@@ -327,8 +331,7 @@ cudaError_t bwd_run(const GatedNormBwdArgs &a, const Walk &walk, cudaStream_t st
                 // always the most: the attribute is the kernel's, shared by all host threads
                 e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
                 if (e != cudaSuccess) return e;
-                k<<<walk.blocks, nt, plan.stages * plan.stage, st>>>(a, walk, plan);
-                return cudaGetLastError();
+                return launch_after(k, walk.blocks, nt, plan.stages * plan.stage, st, a, walk, plan);
             }
         }
     auto *k = gated_bwd_kernel<TIn, TRes, TG, VPT, VEC, false>;
@@ -339,8 +342,7 @@ cudaError_t bwd_run(const GatedNormBwdArgs &a, const Walk &walk, cudaStream_t st
         if (e != cudaSuccess) return e;
         smem = (size_t)3 * VPT * kE * nt * sizeof(float);
     }
-    k<<<walk.blocks, nt, smem, st>>>(a, walk, RingPlan{0, 0});
-    return cudaGetLastError();
+    return launch_after(k, walk.blocks, nt, smem, st, a, walk, RingPlan{0, 0});
 }
 
 template <typename TIn, typename TRes, typename TG>
@@ -356,9 +358,8 @@ cudaError_t bwd_pick(GatedNormBwdArgs a, const Walk &walk, bool vec, cudaStream_
         if (e != cudaSuccess) return e;
     }
     const long long sums = 2 + (walk.summed ? walk.groups : 0);
-    gated_sum_kernel<TG><<<dim3((a.D + 31) / 32, (unsigned)std::min<long long>(sums, 65535)), dim3(32, kSumRows), 0, st>>>(
-        a, walk);
-    return cudaGetLastError();
+    return launch_after(gated_sum_kernel<TG>, dim3((a.D + 31) / 32, (unsigned)std::min<long long>(sums, 65535)),
+                        dim3(32, kSumRows), 0, st, a, walk);
 }
 
 }  // namespace

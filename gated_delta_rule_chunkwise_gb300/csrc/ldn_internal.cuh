@@ -83,6 +83,26 @@ struct AddNormBwdArgs {
     int D, dtype, res_dtype;
     float eps;
 };
+// Launches a kernel that begins with griddep_wait(): its blocks may start while the grid before it on the
+// stream drains, and wait there for its end and its memory.  A kernel so launched calls
+// griddep_launch_dependents() after that, once its blocks hold all they need, so that the next one may.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*k)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A &&...a)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k, P(a)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 struct GatedNormArgs {
     const void *x, *residual, *gate;
     const float *post_weight, *weight;

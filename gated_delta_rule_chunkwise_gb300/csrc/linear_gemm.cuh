@@ -13,8 +13,9 @@
 // thread the products, eight warps the epilogue of the tile before, out of the other half of tensor
 // memory.  Many tiles (PAIR): two blocks of a cluster take 256 x bn together, each loading its half of
 // either operand, so that a product's operands cross into an SM once for twice the output.  Few tiles:
-// `split` blocks of a cluster share a tile's k blocks; each writes its part of every column to the block
-// whose share the column is, which adds the parts in a fixed order.
+// `split` blocks of a cluster share a tile's k blocks; each sends its part of every column to the block
+// whose share the column is, by bulk copies between their shared memories, and that one adds the parts in a
+// fixed order (128 columns among 4 blocks: 5 us by single stores there, 3 by single reads).
 //
 // The tensor cores cut off what an addition to their accumulators rounds away (an fp32 sum over 4096
 // was 4.5e-6 of its norm off, twice that over 8192).  Where the output keeps such digits (PROMOTE: fp32
@@ -55,75 +56,65 @@ __device__ __forceinline__ float gelu(float z)
     return z * normal_integral(z, bell);
 }
 
-__device__ __forceinline__ float widened(float x) { return x; }
-__device__ __forceinline__ float widened(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
-
-// f(type) with the element type of `f32`: a branch for the whole warp around N accesses.
-template <typename F> __device__ __forceinline__ void with_type(int f32, F f)
-{
-    if (f32) f(float());
-    else f(__nv_bfloat16());
-}
-
-// N columns of lane i, from column j on, of which `valid` are there (WHOLE: all, and no access waits
-// for a comparison).
-template <bool EPI, bool F8, int N, bool WHOLE>
-__device__ __forceinline__ void finish_as(const Args &a, float *v, long long i, long long j, int valid)
+// 16 columns of lane i, from column j on, of which `valid` are there.  There is one copy of this code in a
+// kernel and no other for whole chunks: what a small product executes once comes from a cold instruction
+// cache, and with six unrolled copies a tile's end took 3 us.
+template <bool EPI, bool F8>
+__device__ __forceinline__ void finish16(const Args &a, float *v, long long i, long long j, int valid)
 {
     const long long at = j * a.ni + i;
+    const auto last = [&](int c) { return min(c, valid - 1); };   // in place of a column that is not there
     if constexpr (EPI) {
-        float r[N];
-        if (a.residual)   // on its way while the rest is formed
-            with_type(a.out_f32, [&](auto e) {
-                const decltype(e) *p = (const decltype(e) *)a.residual + at;
+        float r[16];
+        if (a.residual) {   // on its way while the rest is formed
+            if (a.out_f32)
 #pragma unroll
-                for (int c = 0; c < N; ++c, p += a.ni) r[c] = WHOLE || c < valid ? widened(*p) : 0.f;
-            });
+                for (int c = 0; c < 16; ++c) r[c] = ((const float *)a.residual)[at + last(c) * a.ni];
+            else
+#pragma unroll
+                for (int c = 0; c < 16; ++c) r[c] = __bfloat162float(((const __nv_bfloat16 *)a.residual)[at + last(c) * a.ni]);
+        }
         if constexpr (F8) {
             const float si = a.scale_i[i];
 #pragma unroll
-            for (int c = 0; c < N; ++c) v[c] *= si * a.scale_j[j + (WHOLE ? c : min(c, valid - 1))];
+            for (int c = 0; c < 16; ++c) v[c] *= si * a.scale_j[j + last(c)];
         }
         if (a.bias) {
-            float b;
-            with_type(a.bias_f32, [&](auto e) { b = widened(((const decltype(e) *)a.bias)[i]); });
+            const float b = a.bias_f32 ? ((const float *)a.bias)[i] : __bfloat162float(((const __nv_bfloat16 *)a.bias)[i]);
 #pragma unroll
-            for (int c = 0; c < N; ++c) v[c] += b;
+            for (int c = 0; c < 16; ++c) v[c] += b;
         }
-        if (a.z)
-            with_type(a.z_f32, [&](auto e) {
-                decltype(e) *p = (decltype(e) *)a.z + at;
+        if (a.z) {
+            if (a.z_f32)
 #pragma unroll
-                for (int c = 0; c < N; ++c, p += a.ni)
-                    if (WHOLE || c < valid) put(p, v[c]);
-            });
+                for (int c = 0; c < 16; ++c) {
+                    if (c < valid) ((float *)a.z)[at + c * a.ni] = v[c];
+                }
+            else
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    if (c < valid) ((__nv_bfloat16 *)a.z)[at + c * a.ni] = __float2bfloat16_rn(v[c]);
+        }
         if (a.activation == LDN_ACT_SILU) {
 #pragma unroll
-            for (int c = 0; c < N; ++c) v[c] *= sigmoid_fast(v[c]);
+            for (int c = 0; c < 16; ++c) v[c] *= sigmoid_fast(v[c]);
         } else if (a.activation == LDN_ACT_GELU) {
 #pragma unroll
-            for (int c = 0; c < N; ++c) v[c] = gelu(v[c]);
+            for (int c = 0; c < 16; ++c) v[c] = gelu(v[c]);
         }
         if (a.residual)
 #pragma unroll
-            for (int c = 0; c < N; ++c) v[c] += r[c];
+            for (int c = 0; c < 16; ++c) v[c] += r[c];
     }
-    with_type(a.out_f32, [&](auto e) {
-        decltype(e) *p = (decltype(e) *)a.out + at;
+    if (a.out_f32) {
 #pragma unroll
-        for (int c = 0; c < N; ++c, p += a.ni)
-            if (WHOLE || c < valid) put(p, v[c]);
-    });
-}
-
-template <bool EPI, bool F8, int N>
-__device__ __forceinline__ void finish(const Args &a, float *v, long long i, long long j, int most = N)
-{
-    if (i >= a.ni || j >= a.nj || most <= 0) return;
-    if (most >= N && a.nj - j >= N) finish_as<EPI, F8, N, true>(a, v, i, j, N);
-    else finish_as<EPI, F8, N, false>(a, v, i, j, (int)min(a.nj - j, (long long)most));
+        for (int c = 0; c < 16; ++c)
+            if (c < valid) ((float *)a.out)[at + c * a.ni] = v[c];
+    } else {
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c < valid) ((__nv_bfloat16 *)a.out)[at + c * a.ni] = __float2bfloat16_rn(v[c]);
+    }
 }
 
 // Tiles in the order that blocks take them: groups of about 2048 lanes, through all columns, so that
@@ -191,7 +182,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 {
     extern __shared__ uint8_t raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[kMostStages], empty[kMostStages], done[2], drained[2], loaded[2], drain;
+    __shared__ uint64_t full[kMostStages], empty[kMostStages], done[2], drained[2], loaded[2], met, drain;
     __shared__ uint32_t tmem;
     __shared__ int fail;
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -222,7 +213,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             mbar_init(&loaded[i], 1);
         }
         mbar_init(&drain, 1);
+        mbar_init(&met, 1);
         fence_mbar_init();
+        if (!PAIR && split > 1) mbar_arrive_expect_tx(&met, part_bytes(bn, split));
     }
     if (warp == 2 && one) {
         tma_prefetch_desc(&map_a);
@@ -249,7 +242,24 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
     tc_fence_after();
     const uint32_t tbase = warp == 0 ? 0 : tmem;
+    griddep_wait();   // what was set up so far touches no memory of another kernel
+    griddep_launch_dependents();
     Ring ring{stages};   // of this thread's loads or products
+    // this warp has read accumulator acc
+    auto drained_by = [&](int acc) {
+        tc_fence_before();
+        __syncwarp();
+        if (one) {
+            if constexpr (PAIR) mbar_remote_arrive(mapa_shared(smem_u32(&drained[acc]), 0));
+            else mbar_arrive(&drained[acc]);
+        }
+    };
+    // a half's columns of a split tile's share: multiples of 16, or all for the first
+    auto per_half = [](int share, uint32_t half, int &h0, int &h) {
+        const int per = (share / 2 + 15) & ~15;
+        h0 = half * per;
+        h = max(0, min(per, share - h0));
+    };
 
     if (warp == 0 && one) {
         // ---- loads
@@ -460,121 +470,116 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     bulk_commit();
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (one) {
-                if constexpr (PAIR) mbar_remote_arrive(mapa_shared(smem_u32(&drained[acc]), 0));
-                else mbar_arrive(&drained[acc]);
-            }
+            drained_by(acc);
         }
         if (leader) bulk_wait_all();   // nothing is left in the buffers
     } else if (warp >= 2) {
         // ---- epilogue: this warp's 32 lanes and half of the columns, in units of 16
         const uint32_t quad = warp & 3, half = (uint32_t)(warp - 2) >> 2;
-        const int per = (bn / 2 + 15) & ~15, h0 = half * per, h = min(per, bn - h0), share = bn / split;
-        // a split tile's parts: of each block, its columns of this block's share
-        const uint32_t part = smem_u32(sm) + stages * stage + (rank * share * kLanes + quad * 32 + lane) * 4;
+        const int per = (bn / 2 + 15) & ~15;
+        uint8_t *const got = sm + stages * stage;   // split: [block][its columns of this block's share][lanes]
         int turn = 0;
-        bool go = true, met = false;
+        bool go = true;
         for (unsigned t = first; go && t < tiles; t += step) {
             const Place p = place_of(t, mt, nt, kGroup);
-            const long long i = (long long)p.mi * kTileLanes + (PAIR ? rank * kLanes : 0) + quad * 32 + lane,
-                            j = (long long)p.nj * bn + h0;
-            // C columns from c on, done
-            auto leave = [&](auto n, float *v, int c) {
-                constexpr int C = decltype(n)::value;
-                if (split == 1) {
-                    finish<EPI, F8, C>(a, v, i, j + c);
-                } else {
-                    if (!met) cluster_wait();   // the other blocks have started
-                    met = true;
-                    for (int q = 0; q < C; ++q) {
-                        const int col = h0 + c + q, to = col / share;
-                        st_shared_cluster(mapa_shared(part, to) + (col - to * share) * kLanes * 4, v[q]);
-                    }
-                }
-            };
-            using C32 = std::integral_constant<int, 32>;
-            using C16 = std::integral_constant<int, 16>;
-            float sum[PROMOTE ? 128 : 16];
+            const long long i = (long long)p.mi * kTileLanes + (PAIR ? rank * kLanes : 0) + quad * 32 + lane;
+            int h0 = half * per, h = min(per, bn - h0), acc = 0;
+            uint32_t row = 0;
+            constexpr int kMostSums = PROMOTE ? (PAIR ? 128 : 64) : 16;   // of a half: bn is 256 or 128 at most
+            float sum[kMostSums];
             if constexpr (PROMOTE)
 #pragma unroll
-                for (int c = 0; c < 128; ++c) sum[c] = 0.f;
-            for (int c0 = b0; c0 < b1; c0 += a.chunk, ++turn) {
-                const int acc = turn & 1;
+                for (int c = 0; c < kMostSums; ++c) sum[c] = 0.f;
+            for (int c0 = b0; c0 < b1; c0 += a.chunk, turn += PROMOTE) {
+                acc = turn & 1;
                 if (!wait(&done[acc], (uint32_t)(turn >> 1) & 1u)) {
                     fail = 1;
                     go = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t row = tbase + (quad << 21) + acc * (tcols / 2) + h0;
+                row = tbase + (quad << 21) + acc * (tcols / 2) + h0;
                 if constexpr (PROMOTE) {
 #pragma unroll
-                    for (int c = 0; c < 128; c += 16)
-                        if (c < h) {
-                            float v[16];
-                            load_columns<16>(row + c, v);
+                    for (int c = 0; c < kMostSums; c += 32)
+                        if (c < h) {   // of 16 columns the second half is another tile's, and not used
+                            float v[32];
+                            load_columns<32>(row + c, v);
 #pragma unroll
-                            for (int q = 0; q < 16; ++q) sum[c + q] += v[q];
+                            for (int q = 0; q < 32; ++q) sum[c + q] += v[q];
                         }
-                } else {
-                    int c = 0;
-#pragma unroll 1
-                    for (; c + 32 <= h; c += 32) {
-                        float v[32];
-                        load_columns<32>(row + c, v);
-                        leave(C32(), v, c);
-                    }
-                    if (c < h) {
-                        float v[16];
-                        load_columns<16>(row + c, v);
-                        leave(C16(), v, c);
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (one) {
-                    if constexpr (PAIR) mbar_remote_arrive(mapa_shared(smem_u32(&drained[acc]), 0));
-                    else mbar_arrive(&drained[acc]);
+                    drained_by(acc);
                 }
             }
-            if constexpr (PROMOTE)
-                if (go)
-#pragma unroll 1
-                    for (int c = 0; c < h; c += 16) {   // the first 16, and the others move up
-                        leave(C16(), sum, c);
+            // the first 16 sums; the others move up
+            auto next = [&](int c) {
+                if constexpr (PROMOTE) {
+                    if (c > 0)
 #pragma unroll
-                        for (int q = 0; q < 112; ++q) sum[q] = sum[q + 16];
+                        for (int q = 0; q < kMostSums - 16; ++q) sum[q] = sum[q + 16];
+                } else {
+                    load_columns<16>(row + c, sum);
+                }
+            };
+            if (!PAIR && split > 1) {
+                if (go) {
+                    float *const part = (float *)sm + quad * 32 + lane;   // in the ring, whose stages are all free
+#pragma unroll 1
+                    for (int c = 0; c < h; c += 16) {
+                        next(c);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) part[(h0 + c + q) * kLanes] = sum[q];
                     }
+                }
+                __syncwarp();
+                cluster_wait();   // the other blocks have started
+                fence_proxy_async_smem();
+                named_sync(2, kEpilogue);
+                const int share = bn / split, bytes = share * kLanes * 4;
+                if (warp == 2 && one)
+                    for (int to = 0; to < split; ++to)
+                        bulk_copy_to_peer(mapa_shared(smem_u32(got + rank * bytes), to), sm + to * bytes, bytes,
+                                          mapa_shared(smem_u32(&met), to));
+                if (!wait(&met, 0)) fail = 1;
+                __syncwarp();
+                cluster_arrive_relaxed();   // nothing comes here any more
+                per_half(share, half, h0, h);
+            }
+            const long long j = (long long)p.nj * bn + (!PAIR && split > 1 ? rank * (bn / split) : 0) + h0;
+            if (go)
+#pragma unroll 1
+                for (int c = 0; c < h; c += 16) {
+                    if (!PAIR && split > 1) {
+                        const int share = bn / split;
+                        const float *from = (const float *)got + (h0 + c) * kLanes + quad * 32 + lane;
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) sum[q] = 0.f;
+#pragma unroll 1
+                        for (int b = 0; b < split; ++b, from += share * kLanes)
+#pragma unroll
+                            for (int q = 0; q < 16; ++q)
+                                if (c + q < h) sum[q] += from[q * kLanes];
+                    } else {
+                        next(c);
+                    }
+                    const int valid = (int)min((long long)min(16, h - c), a.nj - j - c);
+                    if (i < a.ni && valid > 0) finish16<EPI, F8>(a, sum, i, j + c, valid);
+                }
+            if (!PROMOTE) {
+                ++turn;
+                drained_by(acc);
+            }
         }
-        if (split > 1 && !met) cluster_wait();
+        if (!PAIR && split > 1) {
+            __syncwarp();
+            cluster_wait();   // nothing leaves from here any more: the others have all parts
+        }
     }
     __syncwarp();
-    if (!PAIR && split > 1) {
-        if (warp < 2) cluster_wait();
-        cluster_sync();   // every part is where it is added
-        if (warp >= 2) {
-            constexpr int U = 4;   // columns at a time
-            const uint32_t quad = warp & 3, half = (uint32_t)(warp - 2) >> 2;
-            const int share = bn / split;
-            const Place p = place_of(first, mt, nt, kGroup);
-            const long long i = (long long)p.mi * kLanes + quad * 32 + lane,
-                            j = (long long)p.nj * bn + rank * share;
-            const float *part = (const float *)(sm + stages * stage) + quad * 32 + lane;
-#pragma unroll 1
-            for (int c = half * U; c < share; c += 2 * U) {
-                float v[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) v[u] = 0.f;
-#pragma unroll 2
-                for (int q = 0; q < split; ++q)
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (c + u < share) v[u] += part[(q * share + c + u) * kLanes];
-                finish<EPI, F8, U>(a, v, i, j + c, share - c);
-            }
-        }
+    if (!PAIR && split > 1 && warp < 2) {
+        cluster_wait();
+        cluster_arrive_relaxed();
+        cluster_wait();
     }
     tc_fence_before();
     __syncthreads();

@@ -53,12 +53,14 @@ cudaError_t launch(const Operand &A, const Operand &B, Args a, int sms, cudaStre
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = a.stages * stage + beside + 1024;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = blocks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // as launch_after
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = blocks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = blocks > 1 ? 1 : 0;
+    cfg.numAttrs = blocks > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, k, ma, mb, mo, mz, mr, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -70,7 +72,7 @@ cudaError_t run(const Operand &A, const Operand &B, Args a, cudaStream_t st)
     const int sms = sm_count();
     a.status = status_word_ptr();
     if (!sms || !a.status) return cudaErrorUnknown;
-    const Plan p = plan_for(a.ni, a.nj, a.kblocks, a.npairs, BMN, sms);
+    const Plan p = plan_for(a.ni, a.nj, a.kblocks, a.npairs, BMN, PROMOTE, sms);
     a.bn = p.bn;
     a.split = p.split;
     if (!PROMOTE) a.chunk = a.kblocks;

@@ -2,6 +2,7 @@
 // TMA cannot start at (16-byte boundaries), fp32 as planes of bf16, and dz of the gradients.
 // Each moves its bytes once and is bound by HBM.
 #include "linear_common.cuh"
+#include "sm100_ptx.cuh"
 
 namespace ldn {
 namespace linear {
@@ -9,10 +10,18 @@ namespace {
 
 constexpr int kThreadsPrep = 256;
 
+// Once in every kernel, before it touches memory.
+__device__ __forceinline__ void begin()
+{
+    sm100::griddep_wait();
+    sm100::griddep_launch_dependents();
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreadsPrep)
 copy_rows_kernel(const T *__restrict__ src, long long ld, T *__restrict__ dst, long long ld_dst, long long rows, int width)
 {
+    begin();
     const int c = blockIdx.x * kThreadsPrep + threadIdx.x;
     if (c >= width) return;
     for (long long r = blockIdx.y; r < rows; r += gridDim.y) dst[r * ld_dst + c] = src[r * ld + c];
@@ -53,6 +62,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreadsPrep)
 split_rows_kernel(const Split a, const Split b, int blocks_a)
 {
+    begin();
     const bool first = (int)blockIdx.y < blocks_a;
     const Split &s = first ? a : b;
     const int c = (blockIdx.x * kThreadsPrep + threadIdx.x) * N;
@@ -87,6 +97,7 @@ __global__ void __launch_bounds__(kThreadsPrep)
 dz_kernel(const TY *__restrict__ dy, const TZ *__restrict__ z, __nv_bfloat16 *__restrict__ dz, long long ld_dz,
           long long plane, float *__restrict__ part, long long rows, int n, int activation, long long run)
 {
+    begin();
     constexpr int WARPS = kThreadsPrep / 32;
     constexpr bool VEC = N != 1;
     __shared__ float sm[WARPS][32 * N + 1];
@@ -131,6 +142,7 @@ __global__ void __launch_bounds__(32 * kSumRows)
 bias_sum_kernel(const float *__restrict__ part, void *__restrict__ out, int out_f32, int runs, int n)
 {
     __shared__ float sm[kSumRows][33];
+    begin();
     const int c = blockIdx.x * 32 + threadIdx.x, y = threadIdx.y;
     float t = 0.f;
     if (c < n)
@@ -155,13 +167,12 @@ dim3 grid_for(long long rows, int width)
 cudaError_t copy_rows(const void *src, long long ld, void *dst, long long ld_dst, long long rows, int width, int bytes,
                       cudaStream_t st)
 {
+    const dim3 grid = grid_for(rows, width);
     if (bytes == 1)
-        copy_rows_kernel<<<grid_for(rows, width), kThreadsPrep, 0, st>>>((const uint8_t *)src, ld, (uint8_t *)dst, ld_dst,
-                                                                         rows, width);
-    else
-        copy_rows_kernel<<<grid_for(rows, width), kThreadsPrep, 0, st>>>((const uint16_t *)src, ld, (uint16_t *)dst,
-                                                                         ld_dst, rows, width);
-    return cudaGetLastError();
+        return launch_after(copy_rows_kernel<uint8_t>, grid, kThreadsPrep, 0, st, (const uint8_t *)src, ld, (uint8_t *)dst,
+                            ld_dst, rows, width);
+    return launch_after(copy_rows_kernel<uint16_t>, grid, kThreadsPrep, 0, st, (const uint16_t *)src, ld, (uint16_t *)dst,
+                        ld_dst, rows, width);
 }
 
 cudaError_t split_rows(const Split &a, const Split &b, cudaStream_t st)
@@ -174,9 +185,7 @@ cudaError_t split_rows(const Split &a, const Split &b, cudaStream_t st)
     // a few rows a block, so that the card is full and no block ends at once
     auto blocks = [&](const Split &s) { return (int)std::min<long long>(s.rows, std::max(1, 152 * 16 / strips)); };
     const dim3 grid(strips, blocks(a) + blocks(b));
-    if (n == 4) split_rows_kernel<4><<<grid, kThreadsPrep, 0, st>>>(a, b, blocks(a));
-    else split_rows_kernel<1><<<grid, kThreadsPrep, 0, st>>>(a, b, blocks(a));
-    return cudaGetLastError();
+    return launch_after(n == 4 ? split_rows_kernel<4> : split_rows_kernel<1>, grid, kThreadsPrep, 0, st, a, b, blocks(a));
 }
 
 // Rows of a run, so that the blocks fill the card a few times and the sums' last step stays short.
@@ -189,31 +198,28 @@ static long long dz_run(long long rows, int n)
 long long dz_runs(long long rows, int n) { return rows ? (rows + dz_run(rows, n) - 1) / dz_run(rows, n) : 0; }
 
 template <typename TY, typename TZ, bool PLANES>
-static void run_dz(const void *dy, const void *z, __nv_bfloat16 *dz, long long ld_dz, long long plane, float *part,
+static cudaError_t run_dz(const void *dy, const void *z, __nv_bfloat16 *dz, long long ld_dz, long long plane, float *part,
                    long long rows, int n, int activation, cudaStream_t st)
 {
     const long long run = dz_run(rows, n);
     const unsigned runs = (unsigned)dz_runs(rows, n);
     const bool vec = n % 8 == 0 && (((uintptr_t)dy | (uintptr_t)z) & 15) == 0;
-    if (vec)
-        dz_kernel<TY, TZ, PLANES, 8><<<dim3((n + 255) / 256, runs), kThreadsPrep, 0, st>>>(
-            (const TY *)dy, (const TZ *)z, dz, ld_dz, plane, part, rows, n, activation, run);
-    else
-        dz_kernel<TY, TZ, PLANES, 1><<<dim3((n + 31) / 32, runs), kThreadsPrep, 0, st>>>(
-            (const TY *)dy, (const TZ *)z, dz, ld_dz, plane, part, rows, n, activation, run);
+    return launch_after(vec ? dz_kernel<TY, TZ, PLANES, 8> : dz_kernel<TY, TZ, PLANES, 1>,
+                        dim3(vec ? (n + 255) / 256 : (n + 31) / 32, runs), kThreadsPrep, 0, st, (const TY *)dy,
+                        (const TZ *)z, dz, ld_dz, plane, part, rows, n, activation, run);
 }
 
 cudaError_t form_dz(const void *dy, int dy_f32, const void *z, int activation, void *dz, long long ld_dz, long long plane,
                     bool planes, float *part, void *dbias, int bias_f32, long long rows, int n, cudaStream_t st)
 {
     __nv_bfloat16 *d = (__nv_bfloat16 *)dz;
-    if (planes) run_dz<float, float, true>(dy, z, d, ld_dz, plane, part, rows, n, activation, st);
-    else if (dy_f32) run_dz<float, __nv_bfloat16, false>(dy, z, d, ld_dz, plane, part, rows, n, activation, st);
-    else run_dz<__nv_bfloat16, __nv_bfloat16, false>(dy, z, d, ld_dz, plane, part, rows, n, activation, st);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        planes ? run_dz<float, float, true>(dy, z, d, ld_dz, plane, part, rows, n, activation, st)
+        : dy_f32 ? run_dz<float, __nv_bfloat16, false>(dy, z, d, ld_dz, plane, part, rows, n, activation, st)
+                 : run_dz<__nv_bfloat16, __nv_bfloat16, false>(dy, z, d, ld_dz, plane, part, rows, n, activation, st);
     if (e != cudaSuccess || !part) return e;
-    bias_sum_kernel<<<(n + 31) / 32, dim3(32, kSumRows), 0, st>>>(part, dbias, bias_f32, (int)dz_runs(rows, n), n);
-    return cudaGetLastError();
+    return launch_after(bias_sum_kernel, dim3((n + 31) / 32), dim3(32, kSumRows), 0, st, part, dbias, bias_f32,
+                        (int)dz_runs(rows, n), n);
 }
 
 }  // namespace linear

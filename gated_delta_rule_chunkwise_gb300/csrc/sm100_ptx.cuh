@@ -246,11 +246,6 @@ __device__ __forceinline__ void cluster_sync()
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void st_shared_cluster(uint32_t addr, float v)
-{
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
 // Arrive on an mbarrier of any CTA of the cluster, for what this thread did in tensor memory: it orders
 // no memory of the cluster (a release at that scope takes 2500 cycles while stores are under way).
 __device__ __forceinline__ void mbar_remote_arrive(uint32_t remote_bar)

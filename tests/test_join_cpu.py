@@ -138,23 +138,24 @@ def test_plans_fill_their_tiles(tmp_path):
     together, and gives each half of a split block's share a column at least."""
     csrc = ldn_build.CSRC
     src = tmp_path / "plan.cpp"
-    src.write_text('#include <cstdio>\n#include "linear_plan.h"\nint main(){ long long i, j; int k, p, n;\n'
-                   'while (scanf("%lld %lld %d %d %d", &i, &j, &k, &p, &n) == 5) {\n'
-                   'ldn::linear::Plan q = ldn::linear::plan_for(i, j, k, p, n, 152);\n'
+    src.write_text('#include <cstdio>\n#include "linear_plan.h"\nint main(){ long long i, j; int k, p, n, r;\n'
+                   'while (scanf("%lld %lld %d %d %d %d", &i, &j, &k, &p, &n, &r) == 6) {\n'
+                   'ldn::linear::Plan q = ldn::linear::plan_for(i, j, k, p, n, r, 152);\n'
                    'printf("%d %d %d\\n", q.bn, q.split, q.pair); } }\n')
     exe = str(tmp_path / "plan")
     subprocess.run(["g++", "-std=c++17", "-I", csrc, str(src), "-o", exe], check=True)
     r = np.random.default_rng(0)
     cases = [(int(np.exp(r.uniform(0, np.log(20000)))), int(np.exp(r.uniform(0, np.log(20000)))),
-              int(np.exp(r.uniform(0, np.log(300)))), int(r.choice([1, 6])), int(r.integers(2))) for _ in range(3000)]
-    cases += [(1, 1, 1, 1, 0), (MOST, 1, 1, 1, 0), (1, MOST, 1, 1, 1), (1, 1, 1 << 25, 6, 0)]
+              int(np.exp(r.uniform(0, np.log(300)))), int(r.choice([1, 6])), int(r.integers(2)), int(r.integers(2))) for _ in range(3000)]
+    cases += [(1, 1, 1, 1, 0, 0), (MOST, 1, 1, 1, 0, 1), (1, MOST, 1, 1, 1, 0), (1, 1, 1 << 25, 6, 0, 1)]
     out = subprocess.run([exe], input="\n".join(" ".join(map(str, c)) for c in cases), capture_output=True, text=True,
                          check=True).stdout.split()
     assert len(out) == 3 * len(cases)
-    for (i, j, k, p, mn), bn, split, pair in zip(cases, *(map(int, out[q::3]) for q in range(3))):
+    for (i, j, k, p, mn, promote), bn, split, pair in zip(cases, *(map(int, out[q::3]) for q in range(3))):
         assert 16 <= bn <= 256 and bn % (64 if mn else 32 if bn > 16 else 16) == 0 and split in (1, 2, 4, 8)
         stage = 128 * (128 + (bn // 2 if pair else bn))
         parts = bn * 512 if split > 1 else 0
+        assert not promote or bn <= (256 if pair else 128)                  # sums that fit a thread's registers
         assert stage % 1024 == 0 and 3 <= (200 * 1024 - parts) // stage     # a ring beside the parts
         if split > 1:
             assert not pair and split <= k and -(-i // 128) * -(-j // bn) * split <= 152 and bn % (2 * split) == 0
