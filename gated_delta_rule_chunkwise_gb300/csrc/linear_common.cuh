@@ -25,7 +25,7 @@ struct Args {
     const void *bias, *residual;
     const float *scale_i, *scale_j;
     int out_f32, z_f32, bias_f32, activation;
-    int staged;                // bf16 results leave through shared memory (linear_gemm.cuh)
+    int staged;                // results leave through shared memory (linear_gemm.cuh)
     int *status;
 };
 

@@ -21,10 +21,10 @@
 // was 4.5e-6 of its norm off, twice that over 8192).  Where the output keeps such digits (PROMOTE: fp32
 // outputs) the sum is taken over chunks of k, whose results are added in registers, rounded to nearest.
 //
-// bf16 results leave through shared memory (`staged`): fragments of 8 x 8 are written there transposed,
-// 128 lanes x 32 columns at a time, and one TMA store takes them.  Written by the lanes, 2 bytes each, they
-// hold the products up, whose operands pass the same memory port (8192 x 512 to 4096: 44 us; 21 without
-// any stores).  A bf16 residual comes in the same way, into the place of the results.
+// Results leave through shared memory (`staged`), 128 lanes x 32 columns at a time, by TMA stores; bf16
+// ones are written there transposed, as fragments of 8 x 8.  Written by the lanes, 2 bytes each, they hold
+// the products up (8192 x 512 to 4096: 44 us for 31).  A residual comes in the same way, into the place of
+// the results, while the products run (as loads of the lanes: 8192 x 4096 to 4096 with fp32, 220 us).
 //
 // fp32 inputs come as planes of bf16 (linear_prep.cu): a chunk then runs over pairs of planes, the
 // smallest products first.
@@ -44,8 +44,8 @@ constexpr long long kWaitCycles = 4000000000ll;   // 2 s
 // A block's stages in shared memory: 128-byte wide blocks of A, then of B, at multiples of 1024 bytes.
 constexpr int kABytes = kLanes * 128, kMostStages = 10, kStageBytes = 224 * 1024;   // with what follows them
 __host__ __device__ inline int stage_bytes(int columns) { return kABytes + columns * 128; }   // of B in this block
-// Two pairs of buffers for each half of the epilogue's warps, one filled while the other is read: 32
-// columns of 128 lanes in bf16, as two boxes of 64.
+// Two pairs of buffers for each half of the epilogue's warps, one filled while the other is read.  A buffer
+// is 32 columns of 128 lanes in bf16, as two boxes of 64, or half of 32 columns in fp32.
 constexpr int kBuffer = 32 * kLanes * 2, kStaging = 8 * kBuffer;
 // Room for the parts of a split tile: bn columns of 128 lanes.
 __host__ __device__ inline int part_bytes(int bn, int split) { return split > 1 ? bn * kLanes * 4 : 0; }
@@ -58,26 +58,17 @@ __device__ __forceinline__ float gelu(float z)
 
 // 16 columns of lane i, from column j on, of which `valid` are there.  There is one copy of this code in a
 // kernel and no other for whole chunks: what a small product executes once comes from a cold instruction
-// cache, and with six unrolled copies a tile's end took 3 us.
+// cache.
+// z, stored where it is wanted, and the activation.
 template <bool EPI, bool F8>
-__device__ __forceinline__ void finish16(const Args &a, float *v, long long i, long long j, int valid)
+__device__ __forceinline__ void apply16(const Args &a, float *v, long long i, long long j, int valid)
 {
-    const long long at = j * a.ni + i;
-    const auto last = [&](int c) { return min(c, valid - 1); };   // in place of a column that is not there
     if constexpr (EPI) {
-        float r[16];
-        if (a.residual) {   // on its way while the rest is formed
-            if (a.out_f32)
-#pragma unroll
-                for (int c = 0; c < 16; ++c) r[c] = ((const float *)a.residual)[at + last(c) * a.ni];
-            else
-#pragma unroll
-                for (int c = 0; c < 16; ++c) r[c] = __bfloat162float(((const __nv_bfloat16 *)a.residual)[at + last(c) * a.ni]);
-        }
+        if (valid <= 0 || i >= a.ni) return;
         if constexpr (F8) {
             const float si = a.scale_i[i];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] *= si * a.scale_j[j + last(c)];
+            for (int c = 0; c < 16; ++c) v[c] *= si * a.scale_j[j + min(c, valid - 1)];
         }
         if (a.bias) {
             const float b = a.bias_f32 ? ((const float *)a.bias)[i] : __bfloat162float(((const __nv_bfloat16 *)a.bias)[i]);
@@ -85,6 +76,7 @@ __device__ __forceinline__ void finish16(const Args &a, float *v, long long i, l
             for (int c = 0; c < 16; ++c) v[c] += b;
         }
         if (a.z) {
+            const long long at = j * a.ni + i;
             if (a.z_f32)
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
@@ -102,9 +94,25 @@ __device__ __forceinline__ void finish16(const Args &a, float *v, long long i, l
 #pragma unroll
             for (int c = 0; c < 16; ++c) v[c] = gelu(v[c]);
         }
-        if (a.residual)
+    }
+}
+// The residual, and the result.
+template <bool EPI>
+__device__ __forceinline__ void store16(const Args &a, float *v, long long i, long long j, int valid)
+{
+    if (valid <= 0 || i >= a.ni) return;
+    const long long at = j * a.ni + i;
+    if (EPI && a.residual) {
+        float r[16];
+        if (a.out_f32)
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] += r[c];
+            for (int c = 0; c < 16; ++c) r[c] = ((const float *)a.residual)[at + min(c, valid - 1) * a.ni];
+        else
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                r[c] = __bfloat162float(((const __nv_bfloat16 *)a.residual)[at + min(c, valid - 1) * a.ni]);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) v[c] += r[c];
     }
     if (a.out_f32) {
 #pragma unroll
@@ -182,7 +190,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 {
     extern __shared__ uint8_t raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[kMostStages], empty[kMostStages], done[2], drained[2], loaded[2], met, drain;
+    __shared__ uint64_t full[kMostStages], empty[kMostStages], done[2], drained[2], loaded[4], met, drain;
     __shared__ uint32_t tmem;
     __shared__ int fail;
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -211,6 +219,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             mbar_init(&done[i], 1);
             mbar_init(&drained[i], (PAIR ? 2 : 1) * (kEpilogue / 32));
             mbar_init(&loaded[i], 1);
+            mbar_init(&loaded[2 + i], 1);
         }
         mbar_init(&drain, 1);
         mbar_init(&met, 1);
@@ -346,7 +355,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 }
                 if (go) commit(&done[acc]);
             }
-    } else if (!PROMOTE && warp >= 2 && a.staged) {
+    } else if (!PROMOTE && warp >= 2 && a.staged && !a.out_f32) {
         // ---- epilogue through shared memory: this warp's 32 lanes, and every other 32 columns
         const uint32_t quad = warp & 3, half = (uint32_t)(warp - 2) >> 2, bar = 2 + half, row = lane >> 2;
         const bool leader = quad == 2 && one;   // warps 2 and 6
@@ -355,13 +364,30 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         const uint32_t chunk = (quad & 1) * 4 + (lane >> 3), at_row = (quad >> 1) * (kBuffer / 2) + (lane & 7) * 128 +
                                                                       ((chunk ^ (lane & 7)) << 4);
         int turn = 0, late = 0, used = 0;
-        uint32_t loads = 0;
+        uint32_t loads = 0;   // parities of the loads into either pair of buffers
         // a pair of buffers is filled between two barriers: with 64 columns, or with z and y of 32
         const int width = EPI && a.z ? 32 : 64;
         for (unsigned t = first; t < tiles; t += step, ++turn) {
             const int acc = turn & 1;
             const Place p = place_of(t, mt, nt, kGroup);
             const int i0 = p.mi * kTileLanes + (PAIR ? rank * kLanes : 0), j0 = p.nj * bn;
+            // the columns from c0 on of the residual, into the pair of buffers `to` (the leader)
+            auto request = [&](int c0, int to) {
+                if (c0 >= bn || j0 + c0 >= a.nj) return;
+                const int slices = c0 + 32 < bn ? 2 : 1;
+                uint64_t *arrived = &loaded[half * 2 + to];
+                mbar_arrive_expect_tx(arrived, slices * kBuffer);
+                for (int q = 0; q < slices; ++q) {
+                    uint8_t *b = both + (to * 2 + q) * kBuffer;
+                    tma_load_3d(b, &map_residual, arrived, i0, j0 + c0 + 32 * q, 0);
+                    tma_load_3d(b + kBuffer / 2, &map_residual, arrived, i0 + 64, j0 + c0 + 32 * q, 0);
+                }
+            };
+            if (EPI && a.residual && leader) {   // the tile's first two, while its products run
+                bulk_wait_read_all();
+                request(half * width, used);
+                request(half * width + 2 * width, used ^ 1);
+            }
             float bias[4], si[4];
             if constexpr (EPI)
 #pragma unroll
@@ -383,17 +409,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     tma_store_3d(m, b, i0, j, 0);
                     tma_store_3d(m, b + kBuffer / 2, i0 + 64, j, 0);
                 };
-                if (leader) {
-                    bulk_wait_read_but_one();   // what last left these buffers has been read
-                    if (EPI && a.residual) {
-                        mbar_arrive_expect_tx(&loaded[half], slices * kBuffer);
-                        for (int q = 0; q < slices; ++q) {
-                            uint8_t *b = buffers + q * kBuffer;
-                            tma_load_3d(b, &map_residual, &loaded[half], i0, j0 + c0 + 32 * q, 0);
-                            tma_load_3d(b + kBuffer / 2, &map_residual, &loaded[half], i0 + 64, j0 + c0 + 32 * q, 0);
-                        }
-                    }
-                }
+                if (leader && !(EPI && a.residual)) bulk_wait_read_but_one();   // what last left these buffers has been read
 #pragma unroll 1
                 for (int slice = 0; slice < slices; ++slice) {
                     const int c = c0 + 32 * slice;
@@ -442,8 +458,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         }
                         if (__builtin_expect(a.residual != nullptr, 0)) {
                             if (slice == 0) {
-                                if (!late && !wait(&loaded[half], loads & 1u)) fail = late = 1;
-                                ++loads;
+                                if (!late && !wait(&loaded[half * 2 + used], loads >> used & 1u)) fail = late = 1;
+                                loads ^= 1u << used;
                             }
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
@@ -468,6 +484,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     if (slices == 2) store(&map_out, buffers + kBuffer, j0 + c0 + 32);
                     if (EPI && a.z) store(&map_z, buffers + kBuffer, j0 + c0);
                     bulk_commit();
+                    // (no tile has more than two of 64 columns for a half, so none waits for these here)
+                    if (EPI && a.residual && c0 + 4 * width < bn) {
+                        bulk_wait_read_all();
+                        request(c0 + 4 * width, used);
+                    }
                 }
             }
             drained_by(acc);
@@ -478,13 +499,33 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         const uint32_t quad = warp & 3, half = (uint32_t)(warp - 2) >> 2;
         const int per = (bn / 2 + 15) & ~15;
         uint8_t *const got = sm + stages * stage;   // split: [block][its columns of this block's share][lanes]
-        int turn = 0;
+        // staged: [2][32 columns][lanes] for this half
+        uint8_t *const both = sm + stages * stage + half * 4 * kBuffer;
+        const uint32_t bar = 2 + half;
+        const bool leader = quad == 2 && one;   // warps 2 and 6
+        int turn = 0, used = 0, late = 0;
+        uint32_t loads = 0;   // parities of the loads into either
         bool go = true;
         for (unsigned t = first; go && t < tiles; t += step) {
             const Place p = place_of(t, mt, nt, kGroup);
             const long long i = (long long)p.mi * kTileLanes + (PAIR ? rank * kLanes : 0) + quad * 32 + lane;
             int h0 = half * per, h = min(per, bn - h0), acc = 0;
             uint32_t row = 0;
+            const int i0 = p.mi * kTileLanes + (PAIR ? rank * kLanes : 0);
+            const int there = (int)min((long long)h, a.nj - ((long long)p.nj * bn + h0));   // staged: of this half
+            auto request = [&](int c, int to) {   // columns c to c + 31 of the residual (the leader)
+                if (c >= there) return;
+                const int boxes = c + 16 < there ? 2 : 1;
+                mbar_arrive_expect_tx(&loaded[half * 2 + to], boxes * kBuffer);
+                for (int q = 0; q < boxes; ++q)
+                    tma_load_3d(both + (to * 2 + q) * kBuffer, &map_residual, &loaded[half * 2 + to], i0,
+                                p.nj * bn + h0 + c + 16 * q, 0);
+            };
+            if (EPI && a.staged && a.residual && leader) {   // the tile's first 64, while its products run
+                bulk_wait_read_all();
+                request(0, used);
+                request(32, used ^ 1);
+            }
             constexpr int kMostSums = PROMOTE ? (PAIR ? 128 : 64) : 16;   // of a half: bn is 256 or 128 at most
             float sum[kMostSums];
             if constexpr (PROMOTE)
@@ -492,11 +533,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 for (int c = 0; c < kMostSums; ++c) sum[c] = 0.f;
             for (int c0 = b0; c0 < b1; c0 += a.chunk, turn += PROMOTE) {
                 acc = turn & 1;
-                if (!wait(&done[acc], (uint32_t)(turn >> 1) & 1u)) {
-                    fail = 1;
-                    go = false;
-                    break;
+                // a wait that ran out ends no loop whose barriers other warps are in
+                if (!late && !wait(&done[acc], (uint32_t)(turn >> 1) & 1u)) {
+                    fail = late = 1;
+                    go = a.staged;
                 }
+                if (!go) break;
                 tc_fence_after();
                 row = tbase + (quad << 21) + acc * (tcols / 2) + h0;
                 if constexpr (PROMOTE) {
@@ -563,13 +605,54 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         next(c);
                     }
                     const int valid = (int)min((long long)min(16, h - c), a.nj - j - c);
-                    if (i < a.ni && valid > 0) finish16<EPI, F8>(a, sum, i, j + c, valid);
+                    apply16<EPI, F8>(a, sum, i, j + c, valid);
+                    if (!a.staged) {
+                        store16<EPI>(a, sum, i, j + c, valid);
+                        continue;
+                    }
+                    // fp32 results: 32 columns of a buffer, 16 at a time
+                    float *mine = (float *)(both + used * 2 * kBuffer) + (c & 16) * kLanes + quad * 32 + lane;
+                    if ((c & 16) == 0) {
+                        if (EPI && a.residual) {
+                            if (c < there) {
+                                if (!late && !wait(&loaded[half * 2 + used], loads >> used & 1u)) fail = late = 1;
+                                loads ^= 1u << used;
+                            }
+                        } else {
+                            if (leader) bulk_wait_read_but_one();   // what last left this buffer has been read
+                            named_sync(bar, kEpilogue / 2);
+                        }
+                    }
+                    if (c < there) {   // behind the last column nothing was loaded, and the buffer may be in use
+                        if (EPI && a.residual)
+#pragma unroll
+                            for (int q = 0; q < 16; ++q) sum[q] += mine[q * kLanes];
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) mine[q * kLanes] = sum[q];
+                    }
+                    if ((c & 16) || c + 16 >= h) {
+                        fence_proxy_async_smem();
+                        named_sync(bar, kEpilogue / 2);
+                        if (leader) {
+                            const int c32 = c & ~31;
+                            for (int q = c32; q <= c && q < there; q += 16)
+                                tma_store_3d(&map_out, both + used * 2 * kBuffer + (q & 16) / 16 * kBuffer, i0,
+                                             p.nj * bn + h0 + q, 0);
+                            bulk_commit();
+                            if (EPI && a.residual) {
+                                bulk_wait_read_all();
+                                request(c32 + 64, used);
+                            }
+                        }
+                        used ^= 1;
+                    }
                 }
             if (!PROMOTE) {
                 ++turn;
                 drained_by(acc);
             }
         }
+        if (leader) bulk_wait_all();   // nothing is left in the buffers
         if (!PAIR && split > 1) {
             __syncwarp();
             cluster_wait();   // nothing leaves from here any more: the others have all parts

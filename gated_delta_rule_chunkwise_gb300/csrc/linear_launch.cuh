@@ -22,10 +22,11 @@ inline int sm_count()
 template <bool AMN, bool BMN, bool F8, bool EPI, bool PROMOTE, bool PAIR>
 cudaError_t launch(const Operand &A, const Operand &B, Args a, int sms, cudaStream_t st)
 {
-    const long long n = a.ni;
-    auto vectors = [n](const void *p) { return ((uintptr_t)p & 15) == 0 && n % 8 == 0; };   // or null
-    a.staged = !PROMOTE && !a.out_f32 && a.split == 1 && a.bn % 32 == 0 && !(a.z && a.residual) && vectors(a.out) &&
-               vectors(a.residual) && vectors(a.z);
+    // rows of whole 16-byte vectors; fp32 z leaves by the lanes
+    const long long row = a.ni * (a.out_f32 ? 4 : 2);
+    auto vectors = [row](const void *p) { return ((uintptr_t)p & 15) == 0 && row % 16 == 0; };   // or null
+    a.staged = a.split == 1 && vectors(a.out) && vectors(a.residual) &&
+               (a.out_f32 ? !a.z : a.bn % 32 == 0 && !(a.z && a.residual) && vectors(a.z));
     const int cols = PAIR ? a.bn / 2 : a.bn, stage = stage_bytes(cols),
               beside = a.staged ? kStaging : part_bytes(a.bn, a.split);
     a.stages = std::min(kMostStages, (kStageBytes - beside) / stage);
@@ -38,7 +39,7 @@ cudaError_t launch(const Operand &A, const Operand &B, Args a, int sms, cudaStre
         return cudaErrorInvalidValue;
     mo = mz = mr = ma;   // where they are not used
     auto result = [&](CUtensorMap *m, const void *p) {
-        return !p || make_tmap_rows(m, p, a.ni, a.nj, 1, a.ni, a.ni, 32, false);
+        return !p || (a.out_f32 ? make_tmap_f32(m, p, a.ni, a.nj, 16) : make_tmap_rows(m, p, a.ni, a.nj, 1, a.ni, a.ni, 32, false));
     };
     if (a.staged && (!result(&mo, a.out) || !result(&mz, a.z) || !result(&mr, a.residual))) return cudaErrorInvalidValue;
     auto *k = gemm_kernel<AMN, BMN, F8, EPI, PROMOTE, PAIR>;

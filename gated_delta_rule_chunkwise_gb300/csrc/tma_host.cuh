@@ -62,4 +62,18 @@ inline bool make_tmap_rows(CUtensorMap *map, const void *base, uint64_t width, u
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A matrix [rows][width] of fp32, contiguous, viewed through boxes of `box` rows of 128, unswizzled.
+inline bool make_tmap_f32(CUtensorMap *map, const void *base, uint64_t width, uint64_t rows, uint32_t box)
+{
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {width, rows, 1};
+    const cuuint64_t strides[2] = {width * 4, width * 4};
+    const cuuint32_t boxes[3] = {128, box, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(base), dims, strides, boxes, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace ldn
