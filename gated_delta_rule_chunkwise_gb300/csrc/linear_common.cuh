@@ -29,21 +29,26 @@ struct Args {
     int *status;
 };
 
-// Phi(z), the normal distribution's integral, and phi(z) sqrt(2 pi) = e^(-z^2 / 2), from which both it
-// and its slope come: the rational approximation 7.1.26 of Abramowitz and Stegun's handbook, within
-// 0.8e-7 of Phi, and a few steps of fp32 at 1.
-__device__ __forceinline__ float normal_integral(float z, float &bell)
+// Phi(z), the normal distribution's integral, and e^(-z^2 / 2), from which both it and its slope come, of
+// two values in packed arithmetic: the rational approximation 7.1.26 of Abramowitz and Stegun's handbook
+// (its coefficients halved: the tail of Phi is half of erfc's), within 0.8e-7 of Phi, and a few steps of
+// fp32 at 1.
+__device__ __forceinline__ float2 normal_integral(float2 z, float2 &bell)
 {
-    const float x = fabsf(z) * 0.70710678f;
-    bell = ex2(-0.5f * kLog2e * (z * z));
-    const float t = rcp(fmaf(0.3275911f, x, 1.f));
-    float q = 1.061405429f;
-    q = fmaf(q, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f);
-    const float tail = 0.5f * (q * t) * bell;   // Phi(-|z|)
-    return z > 0.f ? 1.f - tail : tail;         // NaN where z is
+    bell = ex2(__fmul2_rn(__fmul2_rn(z, z), dup(-0.5f * kLog2e)));
+    const float2 t = rcp(__ffma2_rn(make_float2(fabsf(z.x), fabsf(z.y)), dup(0.3275911f * 0.70710678f), dup(1.f)));
+    float2 q = dup(0.5f * 1.061405429f);
+    q = __ffma2_rn(q, t, dup(0.5f * -1.453152027f));
+    q = __ffma2_rn(q, t, dup(0.5f * 1.421413741f));
+    q = __ffma2_rn(q, t, dup(0.5f * -0.284496736f));
+    q = __ffma2_rn(q, t, dup(0.5f * 0.254829592f));
+    const float2 tail = __fmul2_rn(__fmul2_rn(q, t), bell);   // Phi(-|z|); NaN where z is
+    return make_float2(z.x > 0.f ? 1.f - tail.x : tail.x, z.y > 0.f ? 1.f - tail.y : tail.y);
+}
+__device__ __forceinline__ float2 gelu(float2 z)
+{
+    float2 bell;
+    return __fmul2_rn(z, normal_integral(z, bell));
 }
 
 // Planes of an fp32 operand (split_rows): the largest part, the next, the last, and the largest with

@@ -50,10 +50,24 @@ constexpr int kBuffer = 32 * kLanes * 2, kStaging = 8 * kBuffer;
 // Room for the parts of a split tile: bn columns of 128 lanes.
 __host__ __device__ inline int part_bytes(int bn, int split) { return split > 1 ? bn * kLanes * 4 : 0; }
 
-__device__ __forceinline__ float gelu(float z)
+// N values through an activation.
+template <int N> __device__ __forceinline__ void activate(float *v, int activation)
 {
-    float bell;
-    return z * normal_integral(z, bell);
+    if (__builtin_expect(activation == LDN_ACT_SILU, 0)) {
+#pragma unroll
+        for (int c = 0; c < N; c += 2) {
+            const float2 y = silu_fast(make_float2(v[c], v[c + 1]));
+            v[c] = y.x;
+            v[c + 1] = y.y;
+        }
+    } else if (__builtin_expect(activation == LDN_ACT_GELU, 0)) {
+#pragma unroll
+        for (int c = 0; c < N; c += 2) {
+            const float2 y = gelu(make_float2(v[c], v[c + 1]));
+            v[c] = y.x;
+            v[c + 1] = y.y;
+        }
+    }
 }
 
 // 16 columns of lane i, from column j on, of which `valid` are there.  There is one copy of this code in a
@@ -87,13 +101,7 @@ __device__ __forceinline__ void apply16(const Args &a, float *v, long long i, lo
                 for (int c = 0; c < 16; ++c)
                     if (c < valid) ((__nv_bfloat16 *)a.z)[at + c * a.ni] = __float2bfloat16_rn(v[c]);
         }
-        if (a.activation == LDN_ACT_SILU) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] *= sigmoid_fast(v[c]);
-        } else if (a.activation == LDN_ACT_GELU) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = gelu(v[c]);
-        }
+        activate<16>(v, a.activation);
     }
 }
 // The residual, and the result.
@@ -449,13 +457,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     if (slice == 0 && !(EPI && a.residual)) named_sync(bar, kEpilogue / 2);   // the buffers are free
                     if constexpr (EPI) {
                         if (__builtin_expect(a.z != nullptr, 0)) put32(to + kBuffer);
-                        if (__builtin_expect(a.activation == LDN_ACT_SILU, 0)) {
-#pragma unroll
-                            for (int r = 0; r < 32; ++r) v[r] *= sigmoid_fast(v[r]);
-                        } else if (__builtin_expect(a.activation == LDN_ACT_GELU, 0)) {
-#pragma unroll
-                            for (int r = 0; r < 32; ++r) v[r] = gelu(v[r]);
-                        }
+                        activate<32>(v, a.activation);
                         if (__builtin_expect(a.residual != nullptr, 0)) {
                             if (slice == 0) {
                                 if (!late && !wait(&loaded[half * 2 + used], loads >> used & 1u)) fail = late = 1;

@@ -77,15 +77,15 @@ split_rows_kernel(const Split a, const Split b, int blocks_a)
 }
 
 // act'(z)
-__device__ __forceinline__ float slope(float z, int activation)
+__device__ __forceinline__ float2 slope(float2 z, int activation)
 {
-    if (activation == LDN_ACT_SILU) {
-        const float g = sigmoid_fast(z);
-        return g * fmaf(z, 1.f - g, 1.f);
+    if (activation == LDN_ACT_SILU) {   // g (1 + z (1 - g))
+        const float2 g = rcp(__fadd2_rn(ex2(__fmul2_rn(z, dup(-kLog2e))), dup(1.f)));
+        return __fmul2_rn(g, __ffma2_rn(z, __ffma2_rn(g, dup(-1.f), dup(1.f)), dup(1.f)));
     }
-    float bell;   // Phi(z) + z phi(z)
-    const float phi = normal_integral(z, bell);
-    return fmaf(z * 0.39894228f, bell, phi);
+    float2 bell;   // Phi(z) + z phi(z)
+    const float2 phi = normal_integral(z, bell);
+    return __ffma2_rn(__fmul2_rn(z, dup(0.39894228f)), bell, phi);
 }
 
 // dz = dy act'(z), as bf16 rows or planes of them, and each run of rows' share of its column sums.
@@ -107,7 +107,7 @@ dz_kernel(const TY *__restrict__ dy, const TZ *__restrict__ z, __nv_bfloat16 *__
 #pragma unroll
     for (int i = 0; i < N; ++i) sum[i] = 0.f;
     if (c < n)
-#pragma unroll 2
+#pragma unroll 4
         for (long long r = r0 + warp; r < r1; r += WARPS) {
             float v[N];
             load_n<N, VEC>(dy + r * n + c, v);
@@ -115,7 +115,11 @@ dz_kernel(const TY *__restrict__ dy, const TZ *__restrict__ z, __nv_bfloat16 *__
                 float q[N];
                 load_n<N, VEC>(z + r * n + c, q);
 #pragma unroll
-                for (int i = 0; i < N; ++i) v[i] *= slope(q[i], activation);
+                for (int i = 0; i < N; i += 2) {
+                    const float2 f = slope(make_float2(q[i], q[N == 1 ? i : i + 1]), activation);
+                    v[i] *= f.x;
+                    if (N > 1) v[N == 1 ? i : i + 1] *= f.y;
+                }
             }
 #pragma unroll
             for (int i = 0; i < N; ++i) sum[i] += v[i];
