@@ -141,9 +141,9 @@ def linear_bwd(dy, x, w, z, name):
 def summed(mag, k, kept):
     """Bound of a sum over k products of magnitude sum `mag` in tensor memory: 16 products a step,
     each step and the tree within it cut off at up to a step of fp32.  kept: an fp32 result, of chunks
-    of at most 512 that are added in registers, rounded to nearest, and of fp32 factors without the
+    of at most 1024 that are added in registers, rounded to nearest, and of fp32 factors without the
     smallest three of their nine products (2^-25)."""
-    steps = min(k, 512) / 16 if kept else k / 16
+    steps = min(k, 1024) / 16 if kept else k / 16
     return mag * ((steps + 32) * 2 * U + (k / 256 * U + U if kept else 0))
 
 

@@ -171,8 +171,9 @@ def test_linear_and_backward(M, K, N, dtype, res, act, bias):
 @pytest.mark.parametrize("M,K,N", [(5, 20000, 130), (300, 8200, 40)])
 @pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16")])
 def test_linear_long_sums(M, K, N, dtype, out):
-    """Over many chunks of k; the norm of the difference within 1e-6 where sums are kept: chunks of 512
-    products are cut off by at most 64 steps of 2^-23 of a partial sum, the mean of which is far below."""
+    """Over many chunks of k.  Where sums are kept the norm of the difference is within 64 steps of 2^-23 of
+    the result's: a chunk of 1024 products has 64 additions in tensor memory, each cut off by a step of its
+    partial sum at most."""
     import torch
     p = linear_inputs(M, K, N, dtype, out, False)
     r = dev(p["r"], out)
