@@ -13,10 +13,17 @@ struct Plan {
 };
 
 // The cheapest of the cuts by a model of one block's time in cycles, fitted to both sides of each choice
-// over 12 sizes from 1 x 4096 x 4096 to 2048 x 2048 x 2048: a k block costs its products (2 a column) and
-// 100 (a pair 20, having half as much to load), and 290 at least; a tile its pipeline's filling and 12 a
-// column of epilogue that no other tile's products cover; the exchange of a split 3500 and 16 a column.
-// promote: sums in registers.  b_mn: the columns lie along memory, are loaded 64 at a time, and both operands come at 56 bytes a cycle.
+// over 17 sizes from 1 x 4096 x 4096 to 8192 x 4096 x 4096:
+// - a k block costs its products (2 a column) and 100 (a pair 20, having half as much to load), and 290 at
+//   least: the 128 lanes of A are read in 70 cycles for each of four steps, however few the columns;
+// - b_mn, columns that lie along memory: both operands come at 56 bytes a cycle and SM, 64 columns a load;
+// - what every cut reads of HBM comes at 3250 bytes a cycle;
+// - a tile's end that no other tile's products cover takes 12 a column, and a split one's exchange 190 a
+//   column of a block's share and 250 a block (256 x 4096 to 4096: 64 columns 15.2 us, 128 in two halves
+//   16.7; 64 x 4096 to 4096: 64 columns in quarters 10.9, in halves 11.6, whole 13.6);
+// - eight blocks of a cluster find room for 13 clusters at once (fp32 64 x 1024 to 1024 in 16 of them 18.5 us,
+//   in 8 of twice the columns 12.1).
+// promote: sums stay in registers, of 128 columns where no pair shares them.
 inline Plan plan_for(long long ni, long long nj, int kblocks, int npairs, bool b_mn, bool promote, int sms)
 {
     const int widths[] = {16, 32, 64, 96, 128, 160, 192, 224, 256};
@@ -28,14 +35,18 @@ inline Plan plan_for(long long ni, long long nj, int kblocks, int npairs, bool b
         for (int blocks = 1; blocks <= 8; blocks *= 2)
             for (int pair = 0; pair <= (blocks == 2 && bn % (b_mn ? 128 : 32) == 0); ++pair) {
                 const int split = pair ? 1 : blocks, lanes = pair ? 256 : 128;
-                if (promote && !pair && bn > 128) continue;   // the sums of half a tile stay in registers
+                if (promote && !pair && bn > 128) continue;
                 const long long tiles = ((ni + lanes - 1) / lanes) * ((nj + bn - 1) / bn);
-                if (split > 1 && (tiles * split > sms || split > kblocks || bn > 128 || bn % (2 * split))) continue;
-                const long long waves = (tiles * blocks + sms - 1) / sms;
+                if (split > 1 && (tiles * split > (split == 8 ? sms * 2 / 3 : sms) || split > kblocks || bn > 128 ||
+                                  bn % (2 * split)))
+                    continue;
+                const double waves = (double)((tiles * blocks + sms - 1) / sms);
                 const double loads = b_mn ? (128 + (pair ? bn / 2 : bn)) * 128 / 56.0 : 290.0;
                 const double each = std::max(2.0 * bn + (pair ? 20 : 100), loads);
-                const double cost = waves * ((kblocks + split - 1) / split * npairs * each + 200) +
-                                    12.0 * bn / split + (split > 1 ? 3500 + 16 * bn : 0) + (pair ? 500 : 0);
+                const double products = waves * ((kblocks + split - 1) / split * npairs * each + 200);
+                const double stream = ((double)ni + nj) * kblocks * 128 / 3250;
+                const double cost = std::max(products, stream) + (split > 1 ? 190.0 * bn / split + 250 * split : 12.0 * bn) +
+                                    (pair ? 500 : 0);
                 if (cost < least) {
                     least = cost;
                     best = {bn, split, pair != 0};
