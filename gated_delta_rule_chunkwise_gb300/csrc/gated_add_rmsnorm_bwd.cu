@@ -7,7 +7,10 @@
 // Both roots and the first mean are one round of block sums, the second mean another.  The columns'
 // sums stay on chip over all rows that a block walks and are joined by a second launch in a fixed
 // order.  A block walks runs of rows that share a gate's row, so that the gate's sum is a column's too.
-// Bound by HBM.
+// 8192 x 2048 in bf16 with an fp32 residual stream and a gate per sequence: 70 us (4,330 GB/s; 80 before
+// packed arithmetic).  Its registers (three columns' sums, two weights, a row's five arrays) leave 16 warps
+// an SM, and the two rounds of sums a row bind them.  Single elements, where rows are no whole vectors:
+// 3333 x 777 in fp32 31 us, bound by issue.
 #include "norm_common.cuh"
 
 namespace ldn {

