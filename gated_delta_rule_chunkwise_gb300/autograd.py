@@ -173,8 +173,8 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, residual, activation):
         ctx.activation = activation
-        if activation is None:
-            y, z = _mixer().linear(x, weight, bias, residual), None
+        if activation is None or not any(ctx.needs_input_grad[:3]):
+            y, z = _mixer().linear(x, weight, bias, residual, activation=activation), None
         else:
             y, z = _mixer().linear(x, weight, bias, residual, activation=activation, save_z=True)
         ctx.save_for_backward(x, weight, z)

@@ -199,3 +199,49 @@ def test_a_chain_of_calls_sees_what_each_wrote():
     a, b = chain(True), chain(False)
     torch.cuda.synchronize()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@gpu
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("shifted", ["y", "residual", "z", "all"])
+def test_linear_results_at_any_address(out, shifted):
+    """y, residual and z that start at odd elements: the same values bit for bit as at aligned ones, and
+    nothing written around y."""
+    import torch
+    M, K, N = 2049, 264, 1032
+    p = linear_inputs(M, K, N, "bf16", out, True, seed=9)
+    x, w, b, r = (dev(p[k], d) for k, d in (("x", "bf16"), ("w", "bf16"), ("b", "bf16"), ("r", out)))
+    want = ldn.linear(x, w, b, r, activation="silu")
+    _, wz = ldn.linear(x, w, b, activation="silu", save_z=True)
+
+    def at(t, move):
+        flat = torch.full((t.numel() + 16,), 7.0, dtype=t.dtype, device="cuda")
+        v = flat[move:move + t.numel()].view(t.shape)
+        v.copy_(t)
+        return v, flat
+    y, flat = at(torch.zeros_like(want), int(shifted in ("y", "all")))
+    r2, _ = at(r, int(shifted in ("residual", "all")))
+    z, _ = at(torch.zeros_like(wz), int(shifted in ("z", "all")))
+    st = ldn.ldn_linear(x.data_ptr(), K, w.data_ptr(), K, b.data_ptr(), r2.data_ptr(), y.data_ptr(), z.data_ptr(), M, K, N,
+                        ldn.LDN_ACT_SILU, ldn.LDN_BF16, ldn.LDN_F32 if out == "f32" else ldn.LDN_BF16, None, 0,
+                        torch.cuda.current_stream().cuda_stream)
+    assert st == ldn.LDN_OK
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(z, wz)
+    move = int(shifted in ("y", "all"))
+    assert (flat[:move] == 7.0).all() and (flat[move + y.numel():] == 7.0).all()
+
+
+@gpu
+def test_autograd_linear_keeps_z_only_for_a_gradient():
+    import torch
+    from gated_delta_rule_chunkwise_gb300 import autograd as ag
+    x, w = torch.randn(64, 256, device="cuda"), torch.randn(4096, 256, device="cuda")
+    torch.cuda.synchronize()
+
+    def grown(*a):
+        base = torch.cuda.memory_allocated()
+        y = ag.linear(*a, activation="gelu")
+        return torch.cuda.memory_allocated() - base, y
+    size = 64 * 4096 * 4
+    assert grown(x, w)[0] == size and grown(x, w.requires_grad_())[0] == 2 * size
