@@ -23,12 +23,14 @@ struct Walk {
 };
 
 constexpr int kRingLeast = 1024;   // channels from which a row is worth its bulk copies
+constexpr int kRingThreads = 256;  // of two vectors each: they have the registers of 512 of one
 int bwd_vpt(int D) { return D <= 4096 ? 1 : D <= 8192 ? 2 : 4; }
 
 Walk walk_of(long long rows, int D, long long gate_rows, bool dgate)
 {
     if (rows == 0) return {0, dgate, gate_rows, 0};   // sums of nothing
-    const int per = std::max(1, kMostThreads / norm_threads(D, bwd_vpt(D)));
+    int per = std::max(1, kMostThreads / norm_threads(D, bwd_vpt(D)));
+    if (D >= kRingLeast && D % kE == 0 && D <= 4096) per = std::min(per, kRingThreads / norm_threads(D, 2));
     const long long most = std::min<long long>(rows, 152LL * per);
     Walk w{(int)most, dgate && gate_rows < rows, 1, most};
     if (w.summed) {
@@ -42,13 +44,12 @@ Walk walk_of(long long rows, int D, long long gate_rows, bool dgate)
 // RING: the rows come through a ring in shared memory, a stage being refilled once every thread has
 // its values in registers, behind the first sums' barrier.
 template <typename TIn, typename TRes, typename TG, int VPT, bool VEC, bool RING>
-__global__ void __launch_bounds__(kMostThreads)
+__global__ void __launch_bounds__(RING ? kRingThreads : kMostThreads, 1)
 gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
 {
-    static_assert(VPT == 1 || !RING, "the sums have the dynamic shared memory");
-    // one vector a thread: its weights and its columns' sums in registers, the next row on its way;
-    // more: the sums in shared memory, each its thread's own
-    constexpr bool ONE = VPT == 1;
+    // one vector a thread, or a ring: the weights and the columns' sums in registers, and the next row on its
+    // way; more without one: the sums in shared memory, each its thread's own
+    constexpr bool KEEP = VPT == 1 || RING;
     extern __shared__ float acc_sm[];
     __shared__ __align__(16) Sums<3> sm[2];
     __shared__ __align__(16) Sums<1> sm_x[2];
@@ -77,13 +78,13 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
 
     // the columns' sums over rows: of dy s rho_s (dweight), of dn x rho_x (dpost_weight) and of
     // dS x rho_x (dgate without its factor post_weight)
-    V8 acc[ONE ? 3 : 1];
+    V8 acc[KEEP ? 3 * VPT : 1];
     auto kept = [&](int which, int k) -> float4 * {   // a thread's own 8 in shared memory
         return (float4 *)acc_sm + ((which * VPT + k) * 2) * nt + threadIdx.x;
     };
     auto add = [&](int which, int k, const V8 &v, float f) {
-        if constexpr (ONE) {
-            acc[which] = fma(v, f, acc[which]);
+        if constexpr (KEEP) {
+            acc[which * VPT + k] = fma(v, f, acc[which * VPT + k]);
         } else {
             float4 *at = kept(which, k);
             V8 t{{{at[0].x, at[0].y}, {at[0].z, at[0].w}, {at[nt].x, at[nt].y}, {at[nt].z, at[nt].w}}};
@@ -93,15 +94,16 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
         }
     };
     auto sum_of = [&](int which, int k) {
-        if constexpr (ONE) return acc[which];
+        if constexpr (KEEP) return acc[which * VPT + k];
         const float4 *at = kept(which, k);
         return V8{{{at[0].x, at[0].y}, {at[0].z, at[0].w}, {at[nt].x, at[nt].y}, {at[nt].z, at[nt].w}}};
     };
     auto clear = [&](int which) {
-        if constexpr (ONE) acc[which] = filled(0.f);
-        else
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) kept(which, k)[0] = kept(which, k)[nt] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < VPT; ++k) {
+            if constexpr (KEEP) acc[which * VPT + k] = filled(0.f);
+            else kept(which, k)[0] = kept(which, k)[nt] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
     };
     sm100::griddep_wait();   // before any memory of another kernel
     sm100::griddep_launch_dependents();
@@ -113,16 +115,16 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
     }
     __syncthreads();
 
-    V8 w[1], wp[1];
+    V8 w[KEEP ? VPT : 1], wp[KEEP ? VPT : 1];
     auto weights = [&](int k) {
-        const int c = place<VEC>(k);
-        w[0] = load8<VEC>(a.weight + c, pre ? D - c : 0);
-        wp[0] = load8<VEC>(a.post_weight + c, post ? D - c : 0);
+        const int c = place<VEC>(k), at = KEEP ? k : 0;
+        w[at] = load8<VEC>(a.weight + c, pre ? D - c : 0);
+        wp[at] = load8<VEC>(a.post_weight + c, post ? D - c : 0);
+        if (!post) wp[at] = filled(1.f);
     };
-    if constexpr (ONE) {
-        weights(0);
-        if (!post) wp[0] = filled(1.f);
-    }
+    if constexpr (KEEP)
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) weights(k);
 
     Raw<TRes, kE, VEC> rs[VPT], rd[VPT];
     Raw<TIn, kE, VEC> ry[VPT], rx[VPT];
@@ -136,7 +138,7 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
         if (gate && row >= 0) take8<VEC>(rg[k], gate + (unsigned)row / shared * (long long)D + c, D - c);
     };
     long long held = -1;   // RING: the gate's row in rg
-    auto take = [&](int k, long long row) {   // from the ring
+    auto take = [&](int k, long long at_gate) {   // from the ring
         const int c = place<VEC>(k);
         const uint8_t *in = ring.row();
         take8<VEC>(rs[k], (const TRes *)in + c, pre ? D - c : 0);
@@ -144,10 +146,7 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
         take8<VEC>(rx[k], (const TIn *)(in + at_x) + c, D - c);
         take8<VEC>(rd[k], (const TRes *)(in + at_d) + c, dsum ? D - c : 0);
         if (own_gate) take8<VEC>(rg[k], (const TG *)(in + at_g) + c, D - c);
-        else if (gate && (unsigned)row / shared != held) {
-            held = (unsigned)row / shared;
-            take8<VEC>(rg[k], gate + held * D + c, D - c);
-        }
+        else if (gate && at_gate != held) take8<VEC>(rg[k], gate + at_gate * D + c, D - c);
     };
 
     // This block's rows one after another; `row` < 0 behind the last.
@@ -168,7 +167,7 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
     if constexpr (RING) {
         if (threadIdx.x == 0)
             for (int i = 0; i < plan.stages && ahead.row >= 0; ++i, ahead = after(ahead)) ring.fill(i, ahead.row);
-    } else if constexpr (ONE) {
+    } else if constexpr (KEEP) {
         fetch(0, at.row);
     }
     int turn = 0;
@@ -177,22 +176,28 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
         const long long run = at.run;
         for (; at.run == run && at.row >= 0; at = after(at), turn ^= 1) {
             const long long row = at.row;
-            if constexpr (RING) take(0, row);
-            else if constexpr (!ONE)
+            if constexpr (RING) {
+                const long long at_gate = (unsigned)row / shared;
+#pragma unroll
+                for (int k = 0; k < VPT; ++k) take(k, at_gate);
+                held = at_gate;
+            } else if constexpr (!KEEP) {
 #pragma unroll
                 for (int k = 0; k < VPT; ++k) fetch(k, row);
+            }
             V8 d[VPT], xv[VPT], sv[VPT], gy[VPT], gv[VPT];
             float2 ss = dup(0.f), sy = dup(0.f), xx = dup(0.f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                if constexpr (!ONE) weights(k);
+                const int at_w = KEEP ? k : 0;
+                if constexpr (!KEEP) weights(k);
                 xv[k] = widened(rx[k]);
                 d[k] = widened(rd[k]);
                 if (pre) {
                     sv[k] = widened(rs[k]);
                     gy[k] = widened(ry[k]);
                     ss = dot(sv[k], sv[k], ss);
-                    sy = dot(w[0] * gy[k], sv[k], sy);
+                    sy = dot(w[at_w] * gy[k], sv[k], sy);
                 }
                 if (post) xx = dot(xv[k], xv[k], xx);
                 if (gate) {
@@ -201,7 +206,7 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
                 }
             }
             float sums[3] = {ss.x + ss.y, sy.x + sy.y, xx.x + xx.y};
-            if constexpr (ONE && !RING) fetch(0, after(at).row);
+            if constexpr (KEEP && !RING) fetch(0, after(at).row);
             row_sums<3>(sums, sm[turn], nwarps);   // two buffers: the next row's sums pass no reader of these
             if constexpr (RING) {
                 if (threadIdx.x == 0 && ahead.row >= 0) {
@@ -215,14 +220,11 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
             float2 dots = dup(0.f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int c = place<VEC>(k);
-                if constexpr (!ONE) {
-                    weights(k);
-                    if (!post) wp[0] = filled(1.f);
-                }
+                const int c = place<VEC>(k), at_w = KEEP ? k : 0;
+                if constexpr (!KEEP) weights(k);
                 if (pre) {
                     add(0, k, gy[k] * sv[k], rho_s);
-                    d[k] = fma(sv[k], -m_s, fma(w[0] * gy[k], rho_s, d[k]));
+                    d[k] = fma(sv[k], -m_s, fma(w[at_w] * gy[k], rho_s, d[k]));
                 }
                 if (a.dresidual) store8<VEC>((TRes *)a.dresidual + row * D + c, d[k] * a.residual_scale, D - c);
                 V8 e = d[k] * xv[k];
@@ -230,7 +232,7 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
                     if (walk.summed) {
                         add(2, k, e, rho_x);
                     } else {
-                        V8 out = e * (wp[0] * rho_x);
+                        V8 out = e * (wp[at_w] * rho_x);
                         if (a.gate_sigmoid) out = out * (gv[k] * fma(gv[k], -1.f, filled(1.f)));
                         store8<VEC>((TG *)a.dgate + row * D + c, out, D - c);
                     }
@@ -241,8 +243,8 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
                 }
                 if (post) {
                     add(1, k, e, rho_x);
-                    dots = dot(e, wp[0], dots);
-                    d[k] = d[k] * (wp[0] * rho_x);
+                    dots = dot(e, wp[at_w], dots);
+                    d[k] = d[k] * (wp[at_w] * rho_x);
                 }
             }
             float m_x = 0.f;
@@ -262,11 +264,8 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int c = place<VEC>(k);
-                if constexpr (!ONE) {
-                    weights(k);
-                    if (!post) wp[0] = filled(1.f);
-                }
-                store8<VEC>(a.part_gate + run * D + c, sum_of(2, k) * wp[0], D - c);
+                if constexpr (!KEEP) weights(k);
+                store8<VEC>(a.part_gate + run * D + c, sum_of(2, k) * wp[KEEP ? k : 0], D - c);
             }
     }
     if constexpr (RING) ring.close(a.status);
@@ -328,13 +327,13 @@ cudaError_t bwd_run(const GatedNormBwdArgs &a, const Walk &walk, cudaStream_t st
             const bool own = a.gate && a.gate_rows == a.rows;
             const RingPlan plan = ring_plan(a.D * (int)((a.weight ? sizeof(TRes) + sizeof(TIn) : 0) + sizeof(TIn) +
                                                         (a.dsum ? sizeof(TRes) : 0) + (own ? sizeof(TG) : 0)),
-                                            kMostThreads / nt);
+                                            kRingThreads / norm_threads(a.D, 2));
             if (plan.stages) {
-                auto *k = gated_bwd_kernel<TIn, TRes, TG, 1, true, true>;
+                auto *k = gated_bwd_kernel<TIn, TRes, TG, 2, true, true>;
                 // always the most: the attribute is the kernel's, shared by all host threads
                 e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
                 if (e != cudaSuccess) return e;
-                return launch_after(k, walk.blocks, nt, plan.stages * plan.stage, st, a, walk, plan);
+                return launch_after(k, walk.blocks, norm_threads(a.D, 2), plan.stages * plan.stage, st, a, walk, plan);
             }
         }
     auto *k = gated_bwd_kernel<TIn, TRes, TG, VPT, VEC, false>;
