@@ -93,7 +93,7 @@ gated_kernel(const GatedNormArgs a, const RingPlan plan)
     };
     const long long ahead = (long long)plan.stages * gridDim.x;
     if constexpr (RING) {
-        if (threadIdx.x == 0)
+        if (ring.issues())
             for (int i = 0; i < plan.stages; ++i)
                 if (blockIdx.x + (long long)i * gridDim.x < rows) ring.fill(i, blockIdx.x + (long long)i * gridDim.x);
     } else {
@@ -137,7 +137,7 @@ gated_kernel(const GatedNormArgs a, const RingPlan plan)
             __syncthreads();
         }
         if constexpr (RING) {   // every thread has read the stage
-            if (threadIdx.x == 0 && row + ahead < rows) ring.fill(ring.s, row + ahead);
+            if (ring.issues() && row + ahead < rows) ring.fill(ring.s, row + ahead);
             ring.step();
         }
         sum2 = dup(0.f);

@@ -7,38 +7,40 @@
 // Both roots and the first mean are one round of block sums, the second mean another.  The columns'
 // sums stay on chip over all rows that a block walks and are joined by a second launch in a fixed
 // order.  A block walks runs of rows that share a gate's row, so that the gate's sum is a column's too.
-// 8192 x 2048 in bf16 with an fp32 residual stream and a gate per sequence: 70 us (4,330 GB/s; 80 before
-// packed arithmetic).  Its registers (three columns' sums, two weights, a row's five arrays) leave 16 warps
-// an SM, and the two rounds of sums a row bind them.  Single elements, where rows are no whole vectors:
-// 3333 x 777 in fp32 31 us, bound by issue.
+// A row costs its latencies, of two rounds of sums and of the work between, with as few warps as the registers
+// leave (three columns' sums, two weights, a row's five arrays): behind a ring a thread has two vectors and twice
+// the registers, so that half the warps do as much between the sums.  8192 x 2048 in bf16 with an fp32 residual
+// stream and a gate per sequence: 56 us (5,370 GB/s; 71 with one vector a thread, 64 with one thread to issue
+// the copies and 64-bit rows), fp32 8192 x 4096 131 (6,140 GB/s; 255 with one vector).  One round of six sums in
+// place of two took 65 for 64.  Single elements, where rows are no whole vectors: 3333 x 777 in fp32 25 us,
+// bound by issue.
 #include "norm_common.cuh"
 
 namespace ldn {
 namespace {
 
 // How the rows are walked: `groups` of them, each cut into `cuts` runs; block b takes runs b, b + blocks, ...
+// A group's run q has base rows, the first `extra` runs one more.
 struct Walk {
     int blocks, summed;   // summed: the gate's gradient is a sum over each group
-    long long groups, cuts;
+    unsigned groups, cuts, per, base, extra;
 };
 
-constexpr int kRingLeast = 1024;   // channels from which a row is worth its bulk copies
-constexpr int kRingThreads = 256;  // of two vectors each: they have the registers of 512 of one
+constexpr int kRingLeast = 1024;    // channels from which a row is worth its bulk copies
+constexpr int kRingThreads = 256;   // of two vectors each: they have the registers of 512 of one
 int bwd_vpt(int D) { return D <= 4096 ? 1 : D <= 8192 ? 2 : 4; }
 
 Walk walk_of(long long rows, int D, long long gate_rows, bool dgate)
 {
-    if (rows == 0) return {0, dgate, gate_rows, 0};   // sums of nothing
+    if (rows == 0) return {0, dgate, (unsigned)gate_rows, 0, 0, 0, 0};   // sums of nothing
     int per = std::max(1, kMostThreads / norm_threads(D, bwd_vpt(D)));
     if (D >= kRingLeast && D % kE == 0 && D <= 4096) per = std::min(per, kRingThreads / norm_threads(D, 2));
     const long long most = std::min<long long>(rows, 152LL * per);
-    Walk w{(int)most, dgate && gate_rows < rows, 1, most};
-    if (w.summed) {
-        w.groups = gate_rows;
-        w.cuts = std::max(1LL, std::min(most / gate_rows, rows / gate_rows));
-        w.blocks = (int)std::min(most, w.groups * w.cuts);
-    }
-    return w;
+    const bool summed = dgate && gate_rows < rows;
+    const long long groups = summed ? gate_rows : 1, of = rows / groups,
+                    cuts = summed ? std::max(1LL, std::min(most / groups, of)) : most;
+    return {(int)std::min(most, groups * cuts), summed, (unsigned)groups, (unsigned)cuts, (unsigned)of,
+            (unsigned)(of / cuts), (unsigned)(of % cuts)};
 }
 
 // RING: the rows come through a ring in shared memory, a stage being refilled once every thread has
@@ -58,7 +60,6 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
     const TRes *s = (const TRes *)a.s, *dsum = (const TRes *)a.dsum;
     const TG *gate = (const TG *)a.gate;
     const bool post = a.post_weight != nullptr, pre = a.weight != nullptr, wants_gate = a.dgate != nullptr;
-    const long long per = a.rows / walk.groups;
     const unsigned shared = gate ? (unsigned)(a.rows / a.gate_rows) : 1u;
     const bool own_gate = gate && shared == 1;
     __shared__ uint64_t full[kRingMost];
@@ -131,10 +132,11 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
     Raw<TG, kE, VEC> rg[VPT];
     auto fetch = [&](int k, long long row) {   // row < 0: none
         const int c = place<VEC>(k), valid = row >= 0 ? D - c : 0;
-        take8<VEC>(rs[k], s + row * D + c, pre ? valid : 0);
-        take8<VEC>(ry[k], dy + row * D + c, pre ? valid : 0);
-        take8<VEC>(rx[k], x + row * D + c, valid);
-        take8<VEC>(rd[k], dsum + row * D + c, dsum ? valid : 0);
+        const long long o = row * D + c;
+        take8<VEC>(rs[k], s + o, pre ? valid : 0);
+        take8<VEC>(ry[k], dy + o, pre ? valid : 0);
+        take8<VEC>(rx[k], x + o, valid);
+        take8<VEC>(rd[k], dsum + o, dsum ? valid : 0);
         if (gate && row >= 0) take8<VEC>(rg[k], gate + (unsigned)row / shared * (long long)D + c, D - c);
     };
     long long held = -1;   // RING: the gate's row in rg
@@ -150,22 +152,24 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
     };
 
     // This block's rows one after another; `row` < 0 behind the last.
+    // (int outside a ring spills more: 3333 x 777 in fp32 33 us, 28 with 64 bits)
+    using Index = std::conditional_t<RING, int, long long>;
     struct Rows {
-        long long run, row, end;
+        unsigned run;
+        Index row, end;
     };
-    const long long runs = walk.groups * walk.cuts;
-    auto open = [&](long long run) {
-        const long long g = run / walk.cuts, q = run - g * walk.cuts;
-        return run < runs ? Rows{run, g * per + per * q / walk.cuts, g * per + per * (q + 1) / walk.cuts}
-                          : Rows{run, -1, -1};
+    const unsigned runs = walk.groups * walk.cuts;   // fewer than 2^31, as rows
+    auto open = [&](unsigned run) {
+        const unsigned g = run / walk.cuts, q = run - g * walk.cuts, first = g * walk.per + q * walk.base + min(q, walk.extra);
+        return run < runs ? Rows{run, (Index)first, (Index)(first + walk.base + (q < walk.extra))} : Rows{run, -1, -1};
     };
     auto after = [&](Rows r) {
         if (r.row >= 0 && ++r.row == r.end) r = open(r.run + gridDim.x);
         return r;
     };
-    Rows at = open(blockIdx.x), ahead = at;   // ahead: the next to go into the ring, in thread 0
+    Rows at = open(blockIdx.x), ahead = at;   // ahead: the next to go into the ring
     if constexpr (RING) {
-        if (threadIdx.x == 0)
+        if (ring.issues())
             for (int i = 0; i < plan.stages && ahead.row >= 0; ++i, ahead = after(ahead)) ring.fill(i, ahead.row);
     } else if constexpr (KEEP) {
         fetch(0, at.row);
@@ -173,7 +177,7 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
     int turn = 0;
     while (at.row >= 0) {
         if (walk.summed) clear(2);
-        const long long run = at.run;
+        const unsigned run = at.run;
         for (; at.run == run && at.row >= 0; at = after(at), turn ^= 1) {
             const long long row = at.row;
             if constexpr (RING) {
@@ -209,7 +213,7 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
             if constexpr (KEEP && !RING) fetch(0, after(at).row);
             row_sums<3>(sums, sm[turn], nwarps);   // two buffers: the next row's sums pass no reader of these
             if constexpr (RING) {
-                if (threadIdx.x == 0 && ahead.row >= 0) {
+                if (ring.issues() && ahead.row >= 0) {
                     ring.fill(ring.s, ahead.row);
                     ahead = after(ahead);
                 }
@@ -265,7 +269,7 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
             for (int k = 0; k < VPT; ++k) {
                 const int c = place<VEC>(k);
                 if constexpr (!KEEP) weights(k);
-                store8<VEC>(a.part_gate + run * D + c, sum_of(2, k) * wp[KEEP ? k : 0], D - c);
+                store8<VEC>(a.part_gate + (long long)run * D + c, sum_of(2, k) * wp[KEEP ? k : 0], D - c);
             }
     }
     if constexpr (RING) ring.close(a.status);
@@ -279,7 +283,7 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
 
 // blockIdx.y 0: dweight, 1: dpost_weight, from every block's share; 2 + g: the gate's row g from its
 // runs'.  32 columns a block, kSumRows rows at a time.
-constexpr int kSumRows = 32;
+constexpr int kSumRows = 32, kSumAhead = 10;   // 304 blocks' shares are one round of loads
 template <typename TG>
 __global__ void __launch_bounds__(32 * kSumRows)
 gated_sum_kernel(const GatedNormBwdArgs a, const Walk walk)
@@ -288,15 +292,19 @@ gated_sum_kernel(const GatedNormBwdArgs a, const Walk walk)
     sm100::griddep_wait();
     sm100::griddep_launch_dependents();
     const int c = blockIdx.x * 32 + threadIdx.x, y = threadIdx.y, D = a.D;
-    const long long which = blockIdx.y;
-    for (long long u = which; u < 2 + (walk.summed ? walk.groups : 0); u += gridDim.y) {
+    for (long long u = blockIdx.y; u < 2 + (walk.summed ? walk.groups : 0); u += gridDim.y) {
         if ((u == 0 && !a.weight) || (u == 1 && !a.post_weight)) continue;
-        const float *part = u == 0 ? a.part : u == 1 ? a.part_post : a.part_gate + (u - 2) * walk.cuts * D;
+        const float *part = u == 0 ? a.part : u == 1 ? a.part_post : a.part_gate + (u - 2) * (long long)walk.cuts * D;
         const int n = u < 2 ? walk.blocks : (int)walk.cuts;
         float t = 0.f;
         if (c < D)
-#pragma unroll 8
-            for (int i = y; i < n; i += kSumRows) t += part[(size_t)i * D + c];
+            for (int i = y; i < n; i += kSumRows * kSumAhead) {
+                float v[kSumAhead];
+#pragma unroll
+                for (int q = 0; q < kSumAhead; ++q) v[q] = i + q * kSumRows < n ? part[(size_t)(i + q * kSumRows) * D + c] : 0.f;
+#pragma unroll
+                for (int q = 0; q < kSumAhead; ++q) t += v[q];
+            }
         sm[y][threadIdx.x] = t;
         __syncthreads();
         if (y == 0 && c < D) {
@@ -359,7 +367,7 @@ cudaError_t bwd_pick(GatedNormBwdArgs a, const Walk &walk, bool vec, cudaStream_
         else e = vec ? bwd_run<TIn, TRes, TG, 4, true>(a, walk, st) : bwd_run<TIn, TRes, TG, 4, false>(a, walk, st);
         if (e != cudaSuccess) return e;
     }
-    const long long sums = 2 + (walk.summed ? walk.groups : 0);
+    const long long sums = 2 + (walk.summed ? (long long)walk.groups : 0);
     return launch_after(gated_sum_kernel<TG>, dim3((a.D + 31) / 32, (unsigned)std::min<long long>(sums, 65535)),
                         dim3(32, kSumRows), 0, st, a, walk);
 }
@@ -369,7 +377,7 @@ cudaError_t bwd_pick(GatedNormBwdArgs a, const Walk &walk, bool vec, cudaStream_
 size_t gated_add_rmsnorm_bwd_floats(long long rows, int D, long long gate_rows)
 {
     const Walk w = walk_of(rows, D, gate_rows ? gate_rows : rows, true);
-    return ((size_t)2 * w.blocks + (w.summed ? (size_t)(w.groups * w.cuts) : 0)) * D;
+    return ((size_t)2 * w.blocks + (w.summed ? (size_t)w.groups * w.cuts : 0)) * D;
 }
 
 cudaError_t launch_gated_add_rmsnorm_bwd(const GatedNormBwdArgs &given, cudaStream_t st)

@@ -190,8 +190,8 @@ inline bool vec16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 // ---- rows through a ring in shared memory ----
 // A row of registers a thread holds too few bytes on their way for the memory's latency; a ring of rows
-// in shared memory, filled by bulk copies that one thread issues, holds as many as fit.  Each stage is
-// one row of each of several arrays.
+// in shared memory, filled by bulk copies, holds as many as fit.  Each stage is one row of each of several
+// arrays; the first warps share the copies' issue, which is between two rows' work.
 constexpr int kRingMost = 8;                  // stages
 constexpr int kRingBytes = 222 * 1024;        // of an SM, beside the kernels' static arrays
 constexpr uint64_t kRingWaitNs = 2000000000ull;
@@ -212,18 +212,19 @@ template <int ARRAYS> struct RowRing {
     uint8_t *base;
     uint64_t *full;
     int *fail;
-    int stages, stage, s = 0;
-    uint32_t phase = 0;
+    int stages, stage, issuers, s = 0;
+    uint32_t phase = 0, own = 0, mine = 0;   // arrays that this warp issues, a bit each, and their bytes of a row
     const char *from[ARRAYS];
     int bytes[ARRAYS];
 
     // Every thread; `bars`: kRingMost barriers in shared memory.  __syncthreads() before the first use.
     __device__ __forceinline__ RowRing(uint8_t *smem, uint64_t *bars, int *failed, RingPlan p)
-        : base(smem), full(bars), fail(failed), stages(p.stages), stage(p.stage)
+        : base(smem), full(bars), fail(failed), stages(p.stages), stage(p.stage),
+          issuers(min(ARRAYS, (int)blockDim.x >> 5))
     {
         if (threadIdx.x == 0) {
             *fail = 0;
-            for (int i = 0; i < stages; ++i) sm100::mbar_init(full + i, 1);
+            for (int i = 0; i < stages; ++i) sm100::mbar_init(full + i, issuers);
             sm100::fence_mbar_init();
         }
     }
@@ -236,16 +237,22 @@ template <int ARRAYS> struct RowRing {
         for (int i = 0; i < I; ++i) at += bytes[i];
         from[I] = (const char *)p;
         bytes[I] = size;
+        if (size && I % issuers == (int)(threadIdx.x >> 5)) {
+            own |= 1u << I;
+            mine += size;
+        }
         return at;
     }
-    // Thread 0: row `row` of every array into stage `to`.
+    // Whether this thread issues copies: then it calls fill, as the other issuers do.
+    __device__ __forceinline__ bool issues() const { return (threadIdx.x & 31) == 0 && (int)threadIdx.x < 32 * issuers; }
+    // Row `row` of every array into stage `to`.
     __device__ __forceinline__ void fill(int to, long long row)
     {
-        sm100::mbar_arrive_expect_tx(full + to, stage);
+        sm100::mbar_arrive_expect_tx(full + to, mine);
         uint8_t *d = base + (size_t)to * stage;
 #pragma unroll
         for (int i = 0; i < ARRAYS; ++i) {
-            if (bytes[i]) sm100::bulk_load(d, from[i] + row * bytes[i], bytes[i], full + to);
+            if (own >> i & 1) sm100::bulk_load(d, from[i] + row * bytes[i], bytes[i], full + to);
             d += bytes[i];
         }
     }
