@@ -24,6 +24,8 @@ namespace {
 struct Walk {
     int blocks, summed;   // summed: the gate's gradient is a sum over each group
     unsigned groups, cuts, per, base, extra;
+    // Rows of D floats in the workspace: two columns' sums of every block, and the gate's of every run.
+    size_t shares() const { return (size_t)2 * blocks + (summed ? (size_t)groups * cuts : 0); }
 };
 
 constexpr int kRingLeast = 1024;    // channels from which a row is worth its bulk copies
@@ -374,10 +376,12 @@ cudaError_t bwd_pick(GatedNormBwdArgs a, const Walk &walk, bool vec, cudaStream_
 
 }  // namespace
 
+// For either kind of call: without dgate a shared gate's groups do not bound the blocks, and the walk may have
+// more of them (1530 rows of 2048 with 153 gates: 608 shares, 459 with dgate).
 size_t gated_add_rmsnorm_bwd_floats(long long rows, int D, long long gate_rows)
 {
-    const Walk w = walk_of(rows, D, gate_rows ? gate_rows : rows, true);
-    return ((size_t)2 * w.blocks + (w.summed ? (size_t)w.groups * w.cuts : 0)) * D;
+    const long long gates = gate_rows ? gate_rows : rows;
+    return std::max(walk_of(rows, D, gates, true).shares(), walk_of(rows, D, gates, false).shares()) * D;
 }
 
 cudaError_t launch_gated_add_rmsnorm_bwd(const GatedNormBwdArgs &given, cudaStream_t st)

@@ -1,0 +1,87 @@
+"""The operators that join blocks at the edges of what their documentation allows: outputs that are left out,
+workspaces of exactly the stated size, the largest and smallest rows, very long sums."""
+import itertools
+
+import numpy as np
+import pytest
+
+import gated_delta_rule_chunkwise_gb300 as ldn
+from tests import _join_ref as ref
+from tests.test_join_parity import EPS, gated_inputs
+from tests.test_mixer_parity import _t, dev, host, within
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gated_delta_rule_chunkwise_gb300 import build
+    build.build()
+    ldn.load()
+
+
+# ---- the norms' gradient with outputs left out ----
+def test_gated_workspace_holds_a_call_without_dgate():
+    """Without dgate the rows are walked as without a gate: the stated size is no smaller than there."""
+    f = ldn.ldn_gated_add_rmsnorm_backward_workspace_size
+    cases = [(1530, 2048, 153), (7700, 4096, 77), (7700, 8192, 77), (5120, 4096, 80), (6400, 4096, 100),
+             (1280, 2048, 160)]
+    r = np.random.default_rng(0)
+    for _ in range(3000):
+        gates, each, D = (int(np.exp(r.uniform(0, np.log(n)))) for n in (2000, 300, 16384))
+        cases.append((gates * each, int(r.choice([D, max(8, D // 8 * 8)])), gates))
+    for rows, D, gates in cases:
+        assert f(rows, D, gates) >= f(rows, D, 0), (rows, D, gates)
+
+
+def c_backward(p, s, case, give, guard=1 << 20):
+    """ldn_gated_add_rmsnorm_backward with the outputs `give` alone, on a workspace of exactly the stated size
+    between guards; the other outputs are None."""
+    import torch
+    B, T, D, dtype, res, gate, gtype, sig, scale = case
+    rows, gates = B * T, p["gate"].size // D
+    t = dict(dy=dev(p["dy"], dtype), x=dev(p["x"], dtype), s=s, dsum=dev(p["dsum"], res), gate=dev(p["gate"], gtype),
+             wp=dev(p["wp"]), w=dev(p["w"]))
+    new = dict(dx=((B, T, D), dtype), dresidual=((B, T, D), res), dgate=(p["gate"].shape, gtype))
+    out = {k: torch.empty(shape, dtype=_t(d), device="cuda") if k in give else None for k, (shape, d) in new.items()}
+    out |= {k: torch.empty(D, device="cuda") for k in ("dpost_weight", "dweight")}
+    need = ldn.ldn_gated_add_rmsnorm_backward_workspace_size(rows, D, gates)
+    room = torch.full((guard + need + guard,), 0x5a, dtype=torch.uint8, device="cuda")
+    q = lambda v: None if v is None else v.data_ptr()  # noqa: E731
+    codes = {"f32": ldn.LDN_F32, "bf16": ldn.LDN_BF16}
+    st = ldn.ldn_gated_add_rmsnorm_backward(
+        *(q(t[k]) for k in ("dy", "x", "s", "dsum", "gate", "wp", "w")),
+        *(q(out[k]) for k in ("dx", "dresidual", "dgate", "dpost_weight", "dweight")), rows, D, gates, codes[gtype],
+        int(sig), scale, codes[dtype], codes[res], EPS, room.data_ptr() + guard, need,
+        torch.cuda.current_stream().cuda_stream)
+    assert st == ldn.LDN_OK
+    torch.cuda.synchronize()
+    assert (room[:guard] == 0x5a).all() and (room[guard + need:] == 0x5a).all()
+    return out
+
+
+@gpu
+@pytest.mark.parametrize("case", [  # B, T, D, dtype, residual, gate, gate's type, sigmoid, scale
+    (153, 10, 2048, "bf16", "bf16", "sequence", "bf16", False, 1.0),
+    (80, 11, 4096, "bf16", "f32", "sequence", "f32", True, 0.5),
+    (77, 8, 8192, "f32", "f32", "sequence", "f32", False, 1.0),
+    (160, 8, 333, "f32", "f32", "sequence", "f32", True, 1.0),
+    (2, 300, 1024, "bf16", "f32", "channel", "f32", False, 1.0),
+    (2, 400, 1024, "bf16", "bf16", "token", "bf16", True, 1.0)])
+def test_gated_backward_with_outputs_left_out(case):
+    """Each of dx, dresidual and dgate may be NULL: the others are what they are with all of them, and nothing
+    is written around the workspace."""
+    B, T, D, dtype, res, gate, gtype, sig, scale = case
+    p = gated_inputs(B, T, D, dtype, res, gate, gtype, seed=5)
+    _, s = ldn.gated_add_rmsnorm(dev(p["x"], dtype), dev(p["r"], res), dev(p["w"]), dev(p["wp"]), dev(p["gate"], gtype),
+                                 residual_scale=scale, gate_sigmoid=sig, eps=EPS)
+    hs = host(s)
+    own = {k: p[k] for k in ("x", "r", "w", "wp", "gate")}
+    b = ref.gated_bounds(*own.values(), scale, sig, EPS, hs, dtype, res, gtype, p["dy"], p["dsum"])
+    want = ref.gated_bwd(p["dy"], p["x"], hs, p["w"], p["wp"], p["gate"], p["dsum"], scale, sig, EPS)
+    names = ("dx", "dresidual", "dgate")
+    for n in range(4):
+        for give in itertools.combinations(names, n):
+            for k, v in c_backward(p, s, case, give).items():
+                if v is not None:
+                    within(v, want[k], b[k], f"{k} of {give}")
