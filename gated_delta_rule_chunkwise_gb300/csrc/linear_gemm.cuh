@@ -30,6 +30,7 @@
 // smallest products first.
 #pragma once
 #include "linear_common.cuh"
+#include "linear_plan.h"
 #include "sm100_ptx.cuh"
 #include "tma_host.cuh"
 
@@ -215,7 +216,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     // this block's k blocks: all, or its share
     const int b0 = PAIR ? 0 : (int)((unsigned)a.kblocks * rank / split),
               b1 = PAIR ? a.kblocks : (int)((unsigned)a.kblocks * (rank + 1) / split);
-    const uint32_t tcols = bn <= 16 ? 32 : bn <= 32 ? 64 : bn <= 64 ? 128 : bn <= 128 ? 256 : 512;   // two accumulators
+    const uint32_t tcols = tensor_columns(bn, PROMOTE);    // two accumulators
 
     if (warp == 0 && one) {
         fail = 0;
@@ -499,7 +500,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     } else if (warp >= 2) {
         // ---- epilogue: this warp's 32 lanes and half of the columns, in units of 16
         const uint32_t quad = warp & 3, half = (uint32_t)(warp - 2) >> 2;
-        const int per = (bn / 2 + 15) & ~15;
+        const int per = half_columns(bn);
         uint8_t *const got = sm + stages * stage;   // split: [block][its columns of this block's share][lanes]
         // staged: [2][32 columns][lanes] for this half
         uint8_t *const both = sm + stages * stage + half * 4 * kBuffer;
@@ -546,7 +547,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 if constexpr (PROMOTE) {
 #pragma unroll
                     for (int c = 0; c < kMostSums; c += 32)
-                        if (c < h) {   // of 16 columns the second half is another tile's, and not used
+                        if (c < h) {   // of 16 columns the second half is no sum, and not used (tensor_columns)
                             float v[32];
                             load_columns<32>(row + c, v);
 #pragma unroll

@@ -1,7 +1,6 @@
 // Launch of one product, for the translation units that hold its forms.
 #pragma once
 #include "linear_gemm.cuh"
-#include "linear_plan.h"
 
 namespace ldn {
 namespace linear {

@@ -1,6 +1,6 @@
 // How a product of the linear operators is cut: columns of a tile, blocks that share its k blocks, and
-// whether two blocks take a tile of twice the lanes.  Host code alone, so that the plans are checked
-// without a GPU.
+// whether two blocks take a tile of twice the lanes; and where the accumulators are read.  Host code alone, so
+// that both are checked without a GPU.
 #pragma once
 #include <algorithm>
 
@@ -11,6 +11,19 @@ struct Plan {
     int bn, split;
     bool pair;
 };
+
+// Columns of a tile whose sums the first half of the epilogue's warps takes; the other takes the rest.
+constexpr int half_columns(int bn) { return (bn / 2 + 15) & ~15; }
+
+// Columns of tensor memory that a block allocates: two accumulators, of bn columns or, promoted, of what is
+// read.  That is 32 columns at a time from each half's first on, so with 16 columns of a half (bn = 16, 32)
+// 16 more, which hold no sum and are allocated all the same.
+constexpr int tensor_columns(int bn, bool promote)
+{
+    const int first = half_columns(bn), reads = first + (bn - first + 31) / 32 * 32;
+    const int each = !promote || bn > 32 ? bn : bn - first ? reads : 32;
+    return each <= 16 ? 32 : each <= 32 ? 64 : each <= 64 ? 128 : each <= 128 ? 256 : 512;
+}
 
 // The cheapest of the cuts by a model of one block's time in cycles, fitted to both sides of each choice
 // over 17 sizes from 1 x 4096 x 4096 to 8192 x 4096 x 4096:

@@ -1,13 +1,14 @@
 """The operators that join blocks at the edges of what their documentation allows: outputs that are left out,
 workspaces of exactly the stated size, the largest and smallest rows, very long sums."""
 import itertools
+import subprocess
 
 import numpy as np
 import pytest
 
 import gated_delta_rule_chunkwise_gb300 as ldn
 from tests import _join_ref as ref
-from tests.test_join_parity import EPS, gated_inputs
+from tests.test_join_parity import EPS, gated_inputs, linear_inputs
 from tests.test_mixer_parity import _t, dev, host, within
 
 gpu = pytest.mark.gpu
@@ -85,3 +86,47 @@ def test_gated_backward_with_outputs_left_out(case):
             for k, v in c_backward(p, s, case, give).items():
                 if v is not None:
                     within(v, want[k], b[k], f"{k} of {give}")
+
+
+# ---- tensor memory ----
+def test_accumulators_are_read_where_they_are_allocated(tmp_path):
+    """Every load of the epilogue, 32 columns of promoted sums and 16 of others from where each half of a tile
+    begins, lies inside its own accumulator of the two that the block allocates."""
+    from gated_delta_rule_chunkwise_gb300 import build as ldn_build
+    src = tmp_path / "columns.cpp"
+    src.write_text('#include <cstdio>\n#include "linear_plan.h"\nint main(){ int bn, p;\n'
+                   'while (scanf("%d %d", &bn, &p) == 2)\n'
+                   'printf("%d %d\\n", ldn::linear::tensor_columns(bn, p), ldn::linear::half_columns(bn)); }\n')
+    exe = str(tmp_path / "columns")
+    subprocess.run(["g++", "-std=c++17", "-I", ldn_build.CSRC, str(src), "-o", exe], check=True)
+    asked = [(bn, p) for bn in (16, 32, 64, 96, 128, 160, 192, 224, 256) for p in (0, 1)]
+    out = subprocess.run([exe], input="\n".join(f"{b} {p}" for b, p in asked), capture_output=True, text=True,
+                         check=True).stdout.split()
+    for (bn, promote), cols, per in zip(asked, map(int, out[::2]), map(int, out[1::2])):
+        assert cols in (32, 64, 128, 256, 512) and bn <= cols // 2 and per % 16 == 0 and per <= bn
+        unit = 32 if promote else 16
+        for first, n in ((0, min(per, bn)), (per, bn - per)):
+            for c in range(0, n, unit):
+                assert first + c + unit <= cols // 2, (bn, promote, first, c)
+
+
+@gpu
+@pytest.mark.parametrize("M", [1, 16, 17, 32, 33])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_few_tokens_over_many_chunks(M, dtype):
+    """fp32 results of few tokens: narrow tiles whose sums are taken over both accumulators in turn, beside
+    another product that fills the rest of the card."""
+    import torch
+    K, N = 8192, 520
+    p = linear_inputs(M, K, N, dtype, "f32", True, seed=11)
+    x, w, b, r = dev(p["x"], dtype), dev(p["w"], dtype), dev(p["b"], dtype), dev(p["r"])
+    y = ldn.linear(x, w, b, r)
+    bound = ref.linear_bounds(p["x"], p["w"], p["b"], p["r"], None, dtype, "f32")["y"]
+    within(y, ref.linear(p["x"], p["w"], p["b"], p["r"], None)[0], bound, "y")
+    wide = torch.randn(2048, 1024, device="cuda").bfloat16()
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        ldn.linear(wide, wide, stream=other)
+        assert torch.equal(ldn.linear(x, w, b, r), y)
+    torch.cuda.synchronize()
