@@ -221,7 +221,9 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
                 }
                 ring.step();
             }
-            const float rho_s = root(fmaf(sums[0], inv_D, a.eps)), m_s = rho_s * rho_s * rho_s * (sums[1] * inv_D);
+            // rho^3 times a sum that is as large as 1 / rho is small: rho's cube alone would leave fp32's range for
+            // rows above 4e12 or, without eps, below 2e-13
+            const float rho_s = root(fmaf(sums[0], inv_D, a.eps)), m_s = rho_s * (rho_s * (rho_s * (sums[1] * inv_D)));
             const float rho_x = post ? root(fmaf(sums[2], inv_D, a.eps)) : 1.f;
             float2 dots = dup(0.f);
 #pragma unroll
@@ -257,7 +259,7 @@ gated_bwd_kernel(const GatedNormBwdArgs a, const Walk walk, const RingPlan plan)
             if (post) {
                 m_x = dots.x + dots.y;
                 row_sums<1>(&m_x, sm_x[turn], nwarps);
-                m_x = rho_x * rho_x * rho_x * (m_x * inv_D);
+                m_x = rho_x * (rho_x * (rho_x * (m_x * inv_D)));
             }
             if (a.dx)
 #pragma unroll

@@ -88,6 +88,27 @@ def test_gated_backward_with_outputs_left_out(case):
                     within(v, want[k], b[k], f"{k} of {give}")
 
 
+@gpu
+@pytest.mark.parametrize("size", [1e16, 1e-16])
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("T,D", [(3, 64), (700, 1024), (2, 8192), (5, 777)])
+def test_gated_gradient_of_large_and_small_rows(T, D, post, size):
+    """One norm alone, without eps, of rows whose squares are in fp32's range but whose cubes are not: the
+    gradient's second term, as large as the first over the root of D, is there."""
+    p = gated_inputs(1, T, D, "f32", "f32", "none", "f32", seed=6)
+    f = np.float32(size)
+    x, r, dy = (np.float64(np.float32(p[k]) * f) for k in ("x", "r", "dy"))
+    w, wp, dsum = (None, p["wp"], p["dsum"]) if post else (p["w"], None, None)
+    dy = None if post else dy
+    _, s = ldn.gated_add_rmsnorm(dev(x), dev(r), dev(w), dev(wp), eps=0.0)
+    hs = host(s)
+    g = ldn.gated_add_rmsnorm_backward(dev(dy), dev(x), s, dev(w), dev(wp), None, dev(dsum), eps=0.0)
+    b = ref.gated_bounds(x, r, w, wp, None, 1.0, False, 0.0, hs, "f32", "f32", None, dy, dsum)
+    want = ref.gated_bwd(dy, x, hs, w, wp, None, dsum, 1.0, False, 0.0)
+    for k in ("dx", "dresidual", "dpost_weight" if post else "dweight"):
+        within(g[k], want[k], b[k], k)
+
+
 # ---- tensor memory ----
 def test_accumulators_are_read_where_they_are_allocated(tmp_path):
     """Every load of the epilogue, 32 columns of promoted sums and 16 of others from where each half of a tile
