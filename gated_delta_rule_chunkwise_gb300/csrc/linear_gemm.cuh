@@ -18,8 +18,9 @@
 // fixed order (128 columns among 4 blocks: 5 us by single stores there, 3 by single reads).
 //
 // The tensor cores cut off what an addition to their accumulators rounds away (an fp32 sum over 4096
-// was 4.5e-6 of its norm off, twice that over 8192).  Where the output keeps such digits (PROMOTE: fp32
-// outputs) the sum is taken over chunks of k, whose results are added in registers, rounded to nearest.
+// was 4.5e-6 of its norm off, twice that over 8192).  Where the output would show it (PROMOTE: fp32 outputs,
+// and bf16 ones of more than 65536 products) the sum is taken over chunks of k, whose results are added in
+// registers, rounded to nearest.
 //
 // Results leave through shared memory (`staged`), 128 lanes x 32 columns at a time, by TMA stores; bf16
 // ones are written there transposed, as fragments of 8 x 8.  Written by the lanes, 2 bytes each, they hold

@@ -21,11 +21,11 @@ inline int sm_count()
 template <bool AMN, bool BMN, bool F8, bool EPI, bool PROMOTE, bool PAIR>
 cudaError_t launch(const Operand &A, const Operand &B, Args a, int sms, cudaStream_t st)
 {
-    // rows of whole 16-byte vectors; fp32 z leaves by the lanes
+    // rows of whole 16-byte vectors; fp32 z leaves by the lanes, and so do bf16 results of promoted sums
     const long long row = a.ni * (a.out_f32 ? 4 : 2);
     auto vectors = [row](const void *p) { return ((uintptr_t)p & 15) == 0 && row % 16 == 0; };   // or null
     a.staged = a.split == 1 && vectors(a.out) && vectors(a.residual) &&
-               (a.out_f32 ? !a.z : a.bn % 32 == 0 && !(a.z && a.residual) && vectors(a.z));
+               (a.out_f32 ? !a.z : !PROMOTE && a.bn % 32 == 0 && !(a.z && a.residual) && vectors(a.z));
     const int cols = PAIR ? a.bn / 2 : a.bn, stage = stage_bytes(cols),
               beside = a.staged ? kStaging : part_bytes(a.bn, a.split);
     a.stages = std::min(kMostStages, (kStageBytes - beside) / stage);
@@ -84,13 +84,16 @@ cudaError_t run(const Operand &A, const Operand &B, Args a, cudaStream_t st)
 // 1.5e-6), and while a tile's results leave, the next one's products run two chunks ahead and no further
 // (8192 x 4096 to 4096 onto an fp32 stream: 182 us, 204 with 512).  With fp32's six pairs of planes 256.
 constexpr int kChunk = 16, kChunkPlanes = 4;
+// For bf16 results, which are rounded by up to 3.9e-3: sums of one sign over 65536 elements of 16 bits come out 3.7e-4
+// too small, and so do longer ones (over a million tokens 6.6e-3 without this, in 3640 us for 3620).
+constexpr int kChunkRounded = 1024;
 
-// Sums that an fp32 output would show are promoted; the others are rounded to bf16's 8 bits anyway.
+// Sums of more than one chunk are promoted.
 template <bool AMN, bool BMN, bool F8, bool EPI>
 cudaError_t run(const Operand &A, const Operand &B, Args a, cudaStream_t st)
 {
-    a.chunk = a.npairs > 1 ? kChunkPlanes : kChunk;
-    if (a.out_f32 && a.kblocks * a.npairs > a.chunk) return run<AMN, BMN, F8, EPI, true>(A, B, a, st);
+    a.chunk = !a.out_f32 ? kChunkRounded : a.npairs > 1 ? kChunkPlanes : kChunk;
+    if ((long long)a.kblocks * a.npairs > a.chunk) return run<AMN, BMN, F8, EPI, true>(A, B, a, st);
     return run<AMN, BMN, F8, EPI, false>(A, B, a, st);
 }
 

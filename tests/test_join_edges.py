@@ -151,3 +151,70 @@ def test_few_tokens_over_many_chunks(M, dtype):
         ldn.linear(wide, wide, stream=other)
         assert torch.equal(ldn.linear(x, w, b, r), y)
     torch.cuda.synchronize()
+
+
+# ---- bf16 results of very long sums ----
+def tokens_of_one_sign(T, D, seed):
+    """dy and x, whose rows are all the same, so that dweight is the columns' sums of dy times x's row."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    column = 1 + torch.rand(D, device="cuda", generator=g)
+    x = (1 + torch.rand(D, device="cuda", generator=g)).bfloat16().repeat(T, 1)
+    dy = torch.empty(T, D, dtype=torch.bfloat16, device="cuda")
+    for part in dy.split(1 << 16):
+        part.copy_((0.5 + torch.rand(part.shape, device="cuda", generator=g)) * column)
+    return dy, x
+
+
+@gpu
+def test_dweight_over_a_million_tokens():
+    """What an addition in tensor memory cuts off is always towards zero: over sums of one sign it is the mean of
+    the results' relative errors, in which their roundings to bf16 (at most 2^-8 each, of either sign, 2.4 million
+    of them) leave 1e-5 at most.  A chunk of 65536 products is 4096 additions, and 32 more for those within one; in
+    each the 16 products and the partial sum are cut off by a step of fp32 of the largest, 17 2^-23 of a partial
+    sum that grows evenly: 4128 / 2 17 2^-23 of the chunk's at most, and as much of the whole sum."""
+    import torch
+    T, D = 1 << 20, 1536
+    dy, x = tokens_of_one_sign(T, D, 12)
+    got = ldn.linear_backward(dy, x, torch.zeros(D, D, dtype=torch.bfloat16, device="cuda"), dx=False)["dweight"]
+    want = dy.sum(0, dtype=torch.float64)[:, None] * x[0].double()
+    off = (got.double() - want) / want
+    cut = 4128 / 2 * 17 * 2.0 ** -23
+    assert off.abs().max().item() <= 2.0 ** -8 + cut
+    assert abs(off.mean().item()) <= cut + 1e-5
+
+
+@gpu
+def test_dweight_of_the_same_tokens_again():
+    """65536 tokens 16 times over: every chunk's sum is the same number P, and 16 additions of it in fp32 are
+    within 16 2^-24 of 16 P.  Both are rounded to bf16, to neighbours at most, and only where 16 P is that close
+    to the middle of two: 2 16 2^-24 of the 2^-8 or more between them, one in a thousand or so."""
+    import torch
+    D = 1536
+    dy, x = tokens_of_one_sign(1 << 16, D, 14)
+    w = torch.zeros(D, D, dtype=torch.bfloat16, device="cuda")
+    once = ldn.linear_backward(dy, x, w, dx=False)["dweight"].double()
+    got = ldn.linear_backward(dy.repeat(16, 1), x.repeat(16, 1), w, dx=False)["dweight"].double()
+    off = (got - 16 * once).abs() / (16 * once)
+    assert off.max().item() <= 2.0 ** -7 and (off > 0).double().mean().item() <= 2.0 ** -8
+
+
+@gpu
+@pytest.mark.parametrize("M,K,N,res,act,bias,save", [(40, 70400, 300, "bf16", "silu", True, True),
+                                                     (300, 66000, 520, None, "gelu", True, True),
+                                                     (130, 65600, 200, "bf16", None, False, False),
+                                                     (2060, 66000, 1030, "bf16", None, True, True)])
+def test_bf16_results_of_long_sums(M, K, N, res, act, bias, save):
+    import torch
+    p = linear_inputs(M, K, N, "bf16", "bf16", bias, seed=13)
+    r = p["r"] if res else None
+    args = dev(p["x"], "bf16"), dev(p["w"], "bf16"), dev(p["b"], "bf16"), dev(r, "bf16") if res else None
+    y = ldn.linear(*args, activation=act, save_z=save)
+    y, z = y if save else (y, None)
+    b = ref.linear_bounds(p["x"], p["w"], p["b"], r, act, "bf16", "bf16")
+    wy, wz = ref.linear(p["x"], p["w"], p["b"], r, act)
+    within(y, wy, b["y"], "y")
+    if save:
+        within(z, wz, b["z"], "z")
+    again = ldn.linear(*args, activation=act)
+    assert torch.equal(again, y)
