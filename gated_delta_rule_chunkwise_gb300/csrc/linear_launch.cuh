@@ -80,9 +80,11 @@ cudaError_t run(const Operand &A, const Operand &B, Args a, cudaStream_t st)
     return launch<AMN, BMN, F8, EPI, PROMOTE, false>(A, B, a, sms, st);
 }
 
-// k blocks of a chunk.  1024 elements of 16 bits keep the sum within 7e-7 of its norm (512 within 3.4e-7, 2048
-// 1.5e-6), and while a tile's results leave, the next one's products run two chunks ahead and no further
-// (8192 x 4096 to 4096 onto an fp32 stream: 182 us, 204 with 512).  With fp32's six pairs of planes 256.
+// k blocks of a chunk, each four additions in tensor memory: of 16 products in 16 bits, of 32 in 8.  64 additions, 1024
+// elements of 16 bits or 2048 of e4m3, keep a sum within 1.0e-6 of its norm (8.3e-7 where its products have one sign;
+// of e4m3, whose products have few digits, 1.2e-7), and while a tile's results leave, the next one's products
+// run two chunks ahead and no further (8192 x 4096 to 4096 onto an fp32 stream: 182 us, 204 with half as many).  With
+// fp32's six pairs of planes 96 additions, of which the largest pair's are 16: 2.4e-7.
 constexpr int kChunk = 16, kChunkPlanes = 4;
 // For bf16 results, which are rounded by up to 3.9e-3: sums of one sign over 65536 elements of 16 bits come out 3.7e-4
 // too small, and so do longer ones (over a million tokens 6.6e-3 without this, in 3640 us for 3620).

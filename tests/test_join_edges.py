@@ -218,3 +218,27 @@ def test_bf16_results_of_long_sums(M, K, N, res, act, bias, save):
         within(z, wz, b["z"], "z")
     again = ldn.linear(*args, activation=act)
     assert torch.equal(again, y)
+
+
+# ---- fp32 results from 8 bits, over more than one chunk ----
+@gpu
+@pytest.mark.parametrize("M,K,N,act", [(5, 20000, 130, None), (16, 8208, 520, "silu"), (40, 4112, 300, None),
+                                       (300, 8200, 40, "gelu"), (1030, 4100, 2060, None)])
+def test_linear_e4m3_long_sums(M, K, N, act):
+    """A chunk of 2048 products in 8 bits is 64 additions in tensor memory, as 1024 in 16 bits are: the norm of
+    what is off before the activation is within 64 steps of 2^-23 of the result's."""
+    import torch
+    r = np.random.default_rng(15)
+    q = dev(r.normal(size=(M, K)) * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    wq = dev(r.normal(size=(N, K)) * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    sx, sw = dev(np.exp(r.normal(size=M)) / 1e4), dev(np.exp(r.normal(size=N)) / 1e4)
+    b, re = dev(r.normal(size=N), "bf16"), dev(r.normal(size=(M, N)))
+    y = ldn.linear_e4m3(q, sx, wq, sw, b, re, activation=act)
+    x, w = host(q.float()) * host(sx)[:, None], host(wq.float()) * host(sw)[:, None]
+    want, z = ref.linear(x, w, host(b), host(re), act)
+    bound = ref.linear_bounds(x, w, host(b), host(re), act, "bf16", "f32")["y"]
+    within(y, want, bound + ref.SLOPE * 4 * ref.U * np.abs(z - host(b)), "y")
+    if act is None:
+        assert np.linalg.norm(host(y) - want) <= 64 * 2.0 ** -23 * np.linalg.norm(want)
+    same = re.clone()
+    assert torch.equal(ldn.linear_e4m3(q, sx, wq, sw, b, same, activation=act, out=same), y)
