@@ -78,15 +78,15 @@ split_rows_kernel(const Split a, const Split b, int blocks_a)
     }
 }
 
-// act'(z)
-__device__ __forceinline__ float2 slope(float2 z, int activation)
+// act'(z); FINE: of a z in fp32
+template <bool FINE> __device__ __forceinline__ float2 slope(float2 z, int activation)
 {
     if (activation == LDN_ACT_SILU) {   // g (1 + z (1 - g))
         const float2 g = rcp(__fadd2_rn(ex2(__fmul2_rn(z, dup(-kLog2e))), dup(1.f)));
         return __fmul2_rn(g, __ffma2_rn(z, __ffma2_rn(g, dup(-1.f), dup(1.f)), dup(1.f)));
     }
     float2 bell;   // Phi(z) + z phi(z)
-    const float2 phi = normal_integral(z, bell);
+    const float2 phi = normal_integral<FINE>(z, bell);
     return __ffma2_rn(__fmul2_rn(z, dup(0.39894228f)), bell, phi);
 }
 
@@ -131,7 +131,7 @@ dz_kernel(const TY *__restrict__ dy, const TZ *__restrict__ z, __nv_bfloat16 *__
                     rz[u].widen(q);
 #pragma unroll
                     for (int i = 0; i < N; i += 2) {
-                        const float2 f = slope(make_float2(q[i], q[N == 1 ? i : i + 1]), activation);
+                        const float2 f = slope<sizeof(TZ) == 4>(make_float2(q[i], q[N == 1 ? i : i + 1]), activation);
                         v[i] *= f.x;
                         if (N > 1) v[N == 1 ? i : i + 1] *= f.y;
                     }

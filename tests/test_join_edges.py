@@ -242,3 +242,30 @@ def test_linear_e4m3_long_sums(M, K, N, act):
         assert np.linalg.norm(host(y) - want) <= 64 * 2.0 ** -23 * np.linalg.norm(want)
     same = re.clone()
     assert torch.equal(ldn.linear_e4m3(q, sx, wq, sw, b, same, activation=act, out=same), y)
+
+
+# ---- GELU ----
+@gpu
+def test_gelu_and_its_slope_to_fp32s_digits():
+    """Through a product with the identity, whose z is x itself.  In steps U = 2^-24 of the tail Phi(-|z|): the
+    exponential 4, and its argument 3 z^2 / 2 (z^2, its factor and their product); t = 1 / (1 + p |z|) 3, which the
+    tail follows to the power of 2.4 at most; the polynomial's own sum 5 (its terms are 2.4 times the sum at most), two
+    products and the fit 3: 20 + 1.5 z^2 in all, and one or two more for what follows."""
+    import math
+
+    import torch
+    z = np.concatenate([np.linspace(-12, 12, 6007), [0.0, -0.0, 1e-30, -1e-30, 0.75, -0.75, 40.0, -40.0, 3e38]])
+    z = np.float32(z).reshape(-1, 64)
+    eye = torch.eye(64, device="cuda")
+    y, got = ldn.linear(dev(z), eye, activation="gelu", save_z=True)
+    assert torch.equal(got, dev(z))
+    z = z.astype(np.float64)
+    tail = np.vectorize(lambda v: math.erfc(abs(v) / math.sqrt(2)) / 2)(z)
+    phi = np.where(z > 0, 1 - tail, tail)
+    e = (20 + 1.5 * np.minimum(z * z, 200.0)) * ref.U * tail + 2.0 ** -126     # results below it are zero
+    within(y, z * phi, np.abs(z) * (e + 2 * ref.U * phi), "gelu")
+    with np.errstate(under="ignore"):
+        bell = z * np.exp(-np.minimum(z * z, 1e4) / 2) / math.sqrt(2 * math.pi)
+    g = ldn.linear_backward(torch.ones_like(y), dev(np.float32(z)), eye, got, activation="gelu")["dx"]
+    bound = e + 2 * ref.U * phi + (8 + 1.5 * np.minimum(z * z, 200.0)) * ref.U * np.abs(bell) + np.abs(z) * 2.0 ** -126
+    within(g, phi + bell, bound + 1.1e-38, "slope")
