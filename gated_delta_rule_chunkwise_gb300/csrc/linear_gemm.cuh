@@ -393,7 +393,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     tma_load_3d(b + kBuffer / 2, &map_residual, arrived, i0 + 64, j0 + c0 + 32 * q, 0);
                 }
             };
-            if (EPI && a.residual && leader) {   // the tile's first two, while its products run
+            // while the tile's products run, its residual: a half has two pairs of 64 columns at most (width is 64
+            // here, as z and a residual together are not staged)
+            if (EPI && a.residual && leader) {
                 bulk_wait_read_all();
                 request(half * width, used);
                 request(half * width + 2 * width, used ^ 1);
@@ -488,11 +490,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     if (slices == 2) store(&map_out, buffers + kBuffer, j0 + c0 + 32);
                     if (EPI && a.z) store(&map_z, buffers + kBuffer, j0 + c0);
                     bulk_commit();
-                    // (no tile has more than two of 64 columns for a half, so none waits for these here)
-                    if (EPI && a.residual && c0 + 4 * width < bn) {
-                        bulk_wait_read_all();
-                        request(c0 + 4 * width, used);
-                    }
                 }
             }
             drained_by(acc);
