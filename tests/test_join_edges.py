@@ -269,3 +269,135 @@ def test_gelu_and_its_slope_to_fp32s_digits():
     g = ldn.linear_backward(torch.ones_like(y), dev(np.float32(z)), eye, got, activation="gelu")["dx"]
     bound = e + 2 * ref.U * phi + (8 + 1.5 * np.minimum(z * z, 200.0)) * ref.U * np.abs(bell) + np.abs(z) * 2.0 ** -126
     within(g, phi + bell, bound + 1.1e-38, "slope")
+
+
+# ---- calls that the documentation allows ----
+@gpu
+@pytest.mark.parametrize("dtype,dy_dtype,act", [("bf16", "bf16", None), ("bf16", "f32", None), ("bf16", "bf16", "silu"),
+                                                ("f32", "f32", None), ("f32", "f32", "gelu")])
+@pytest.mark.parametrize("M,K,N,pad", [(300, 264, 520, 0), (1, 72, 130, 0), (1000, 65, 77, 3)])
+def test_linear_backward_with_outputs_left_out(M, K, N, pad, dtype, dy_dtype, act):
+    """Each of dx, dweight and dbias may be NULL: the others are what they are with all of them, bit for bit, on a
+    workspace of exactly the size for what is wanted, between guards."""
+    import torch
+    p = linear_inputs(M, K, N, dtype, dy_dtype, False, seed=16)
+    x, w, dy = dev(p["x"], dtype, pad=pad), dev(p["w"], dtype), dev(p["dy"], dy_dtype)
+    z = dev(linear_inputs(M, K, N, dtype, dtype, False, seed=17)["r"], dtype) if act else None
+    every = ldn.linear_backward(dy, x, w, z, activation=act, bias=True)
+    codes = {"f32": ldn.LDN_F32, "bf16": ldn.LDN_BF16}
+    how = {None: ldn.LDN_ACT_NONE, "silu": ldn.LDN_ACT_SILU, "gelu": ldn.LDN_ACT_GELU}[act]
+    q = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    for want in range(8):
+        out = [torch.empty_like(every[k]) if want >> i & 1 else None for i, k in enumerate(("dx", "dweight", "dbias"))]
+        a = (dy.data_ptr(), x.data_ptr(), x.stride(0), w.data_ptr(), w.stride(0))
+        need = ldn.ldn_linear_backward_workspace_size(*a, M, K, N, how, codes[dtype], codes[dy_dtype], want)
+        guard = 1 << 18
+        room = torch.full((guard + need + guard,), 0x5a, dtype=torch.uint8, device="cuda")
+        st = ldn.ldn_linear_backward(*a, q(z), *map(q, out), M, K, N, how, codes[dtype], codes[dy_dtype],
+                                     room.data_ptr() + guard if need else None, need,
+                                     torch.cuda.current_stream().cuda_stream)
+        assert st == ldn.LDN_OK
+        torch.cuda.synchronize()
+        assert (room[:guard] == 0x5a).all() and (room[guard + need:] == 0x5a).all()
+        for k, v in zip(("dx", "dweight", "dbias"), out):
+            assert v is None or torch.equal(v, every[k]), (want, k)
+
+
+FIRST = """
+import torch, gated_delta_rule_chunkwise_gb300 as ldn
+x, w = torch.ones(40, 64, device="cuda"), torch.ones(72, 64, device="cuda")
+n, m = torch.ones(72, device="cuda"), torch.zeros(40, 72, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    z = ldn.linear(x, w)
+    y, s = ldn.gated_add_rmsnorm(z, m, n, n, n)
+    d = ldn.gated_add_rmsnorm_backward(y, z, s, n, n, n)
+    e = ldn.linear_backward(d["dx"], x, w, bias=True)
+g.replay()
+torch.cuda.synchronize()
+assert (z == 64).all() and torch.isfinite(e["dweight"]).all()
+assert (s - 1).abs().max() < 1e-5 and (y - 1).abs().max() < 1e-5 and d["dgate"].shape == (72,)
+"""
+
+
+@gpu
+def test_first_calls_are_captured():
+    """A process whose first calls are captured into a graph."""
+    import os
+    import sys
+    r = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@gpu
+def test_calls_from_several_threads():
+    import threading
+
+    import torch
+    sets = []
+    for i, (M, D, H) in enumerate([(5, 256, 520), (300, 1024, 2056), (2100, 264, 1032), (64, 2048, 512)]):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        f = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+        sets.append((f(M, D).bfloat16(), (f(H, D) * D ** -0.5).bfloat16(), f(M, H), 1 + 0.1 * f(H), f(H)))
+
+    def steps(x, w, r, n, gate):
+        y = ldn.linear(x, w, None, r)
+        o, s = ldn.gated_add_rmsnorm(y, r, n, n, gate, gate_sigmoid=True)
+        d = ldn.gated_add_rmsnorm_backward(o, y, s, n, n, gate, r, gate_sigmoid=True)
+        e = ldn.linear_backward(d["dx"], x, w, bias=True)
+        return [y, o, s, *d.values(), *e.values()]
+    want = [steps(*s) for s in sets]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got = steps(*sets[i])
+                torch.cuda.current_stream().synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                wrong.append(i)
+        except Exception as e:  # a thread's own is lost
+            wrong.append((i, e))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+@gpu
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows are what they are alone (each row's norm is its own), and a
+    projection's last rows what plain fp32 products give, to bf16's rounding (2^-8) and what fp32 sums of 64 or
+    16384 products of a size of 1 and a row's norm of 1 or 16 leave (6e-8 and 2e-5 of it)."""
+    import torch
+    D, rows, last = 16384, (1 << 17) + 900, 400
+    x = torch.randn(last, D, device="cuda").bfloat16().repeat(-(-rows // last), 1)[:rows]
+    r, n = x.flip(1), 1 + 0.1 * torch.randn(D, device="cuda")
+    assert rows * D > 1 << 31
+    y, s = ldn.gated_add_rmsnorm(x, r, n, n, x, gate_sigmoid=True)
+    g = ldn.gated_add_rmsnorm_backward(x, x, s, n, n, x, r, gate_sigmoid=True)
+    tail = lambda t: t[-last:].contiguous()  # noqa: E731
+    y2, s2 = ldn.gated_add_rmsnorm(tail(x), tail(r), n, n, tail(x), gate_sigmoid=True)
+    g2 = ldn.gated_add_rmsnorm_backward(tail(x), tail(x), s2, n, n, tail(x), tail(r), gate_sigmoid=True)
+    assert torch.equal(tail(y), y2) and torch.equal(tail(s), s2)
+    assert all(torch.equal(tail(g[k]), g2[k]) for k in ("dx", "dresidual", "dgate"))
+    del y, s, g, r
+    w = (torch.randn(64, D, device="cuda") / 128).bfloat16()
+    wide = x[:, :64]                                    # rows 16384 apart
+    for a, b in ((x, w), (wide, w[:, :64]), (wide, (torch.randn(D, 64, device="cuda") / 8).bfloat16())):
+        y = ldn.linear(a, b, activation="silu")
+        own = torch.nn.functional.silu(a[-last:].float() @ b.float().t())
+        assert ((y[-last:].float() - own).abs() <= 2.0 ** -8 * own.abs() + 1e-4).all()
+    # y is [rows][16384] now: its gradients
+    g = ldn.linear_backward(y, wide, b, bias=True)
+    own = y[-last:].float() @ b.float()
+    assert ((g["dx"][-last:].float() - own).abs() <= 2.0 ** -8 * own.abs() + 1e-3).all()
+    want = sum(p.sum(0, dtype=torch.float64) for p in y.split(1 << 14))
+    # rounding of the result, and of at most rows / 256 + 256 sums of a column in fp32
+    size = sum(p.float().abs().sum(0, dtype=torch.float64) for p in y.split(1 << 14))
+    assert ((g["dbias"].double() - want).abs() <= 2.0 ** -8 * want.abs() + 800 * 2.0 ** -24 * size).all()
