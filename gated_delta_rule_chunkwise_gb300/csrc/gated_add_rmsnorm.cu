@@ -9,7 +9,7 @@
 // sums, and the next rows are on their way meanwhile, in a ring in shared memory where there are many:
 // two blocks of 512 threads hold 49 KB on their way in registers (16384 x 4096 in bf16 with a gate per
 // token: 131 us), with a ring of 96 KB each 119, and in packed arithmetic 104 (6,450 GB/s).  Bound by HBM;
-// 8192 x 2048 with an fp32 residual stream 34 us (5,920 GB/s), 68 % of the issue slots in use.
+// 8192 x 2048 with an fp32 residual stream 34 us (5,920 GB/s), 57 % of the issue slots in use.
 #include "norm_common.cuh"
 
 namespace ldn {

@@ -671,7 +671,9 @@ size_t ldn_gated_add_rmsnorm_backward_workspace_size(long long rows, int D, long
  *   z            [rows][N] of `dtype` or NULL: what ldn_linear_backward needs where there is
  *                an activation
  *   activation   LDN_ACT_NONE, LDN_ACT_SILU, LDN_ACT_GELU.  rows >= 0, K >= 1, N >= 1.
- * Products are exact and summed in fp32.  bf16 enters the tensor cores as it is; fp32 as three
+ * Products are exact and summed in fp32, where an addition on the tensor cores cuts off what it
+ * rounds away: fp32 results in chunks of 1024 products (1.0e-6 of the norm), bf16 ones of 65536
+ * (3.7e-4 too small where all have one sign).  bf16 enters the tensor cores as it is; fp32 as three
  * bf16 numbers whose sum it is, six of their nine products taken (the others are below 2^-25 of
  * the product): an infinity or a NaN gives what it gives in fp32, and numbers below 2^-110 keep
  * fewer digits.
